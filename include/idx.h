@@ -64,7 +64,13 @@ typedef enum {
 /* IDX_MXFP4 (the OCP MX format): e2m1 elements packed two per byte (element 2i in
  * the low nibble) with one e8m0 scale per 32 consecutive elements along D; only
  * the *_mxfp4 entry points below take it (they also take the scale arrays). */
-typedef enum { IDX_BF16 = 1, IDX_FP8_E4M3 = 2, IDX_MXFP4 = 3 } idx_dtype;
+typedef enum {
+    IDX_BF16 = 1,
+    IDX_FP8_E4M3 = 2,
+    IDX_MXFP4 = 3,
+    IDX_FP16 = 4,  /* the serving entry points below only */
+    IDX_FP32 = 5   /* idx_add_rmsnorm_quant only */
+} idx_dtype;
 
 /* Optional device-side counters (zero them before the call if you read them). */
 typedef struct idx_stats {
@@ -352,6 +358,108 @@ idx_status idx_score_materialise_mxfp4(const uint8_t* q, const uint8_t* q_sf, co
                                        long long keys, int H, int D, float* scores,
                                        long long row_stride, void* ws, size_t ws_bytes,
                                        const idx_options* opt, void* stream);
+
+/* ------------------------------------------------------------------------
+ * Serving operators around the indexer: the norm that makes its 8-bit rows, the
+ * attention of a decode batch over a paged cache, and the eviction that keeps
+ * such a cache within a budget.
+ *
+ * idx_add_rmsnorm_quant - per row of x [rows, N] (bf16, fp16 or fp32):
+ *     h = x + residual (h = x when residual is NULL)
+ *     y = h * rsqrt(mean(h^2) + eps) * weight
+ *     scale = max(max|y| / 448, 2^-100),   out = e4m3(y / scale)
+ * with one scale per row (group 0: scale [rows]; for N = D these are k and
+ * k_scale as idx_score_topk reads them) or per `group` consecutive columns
+ * (group 32, 64 or 128, N % group == 0: scale [rows, N / group]).  h is kept in
+ * fp32 up to the codes and is rounded to x's type only in residual_out.
+ *   x            rows of N elements, x_stride elements apart (x_stride >= N, so x
+ *                may be a column slice of a wider projection)
+ *   residual     [rows, N] or NULL, residual_out [rows, N] or NULL (may be
+ *                `residual` itself, not x); weight [N]; all of x's type
+ *   out [rows, N] e4m3 bytes, scale fp32
+ * 1 <= N <= 32768 (IDX_EUNSUPPORTED above).  Pointers are aligned to their
+ * element (IDX_EALIGN); rows on 16-byte boundaries with N % 8 == 0 take the
+ * vector path.  A row with no finite norm gives no meaningful codes; other rows
+ * are not affected.  No workspace.
+ * ------------------------------------------------------------------------ */
+idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* residual,
+                                 const void* weight, int rows, int N, float eps, int group,
+                                 idx_dtype dt, void* residual_out, uint8_t* out, float* scale,
+                                 const idx_options* opt, void* stream);
+
+/* ------------------------------------------------------------------------
+ * idx_prefix_attention - attention of B requests with Q new tokens each over a
+ * prefix that all of them share and a private part of each one's own, both in
+ * one paged cache.  The prefix is read once for the whole batch.
+ *
+ * Row (b, t, head) sees the prefix's slots 0 .. prefix_len - 1 and the private
+ * slots 0 .. lens[b] - (Q - 1 - t) - 1: the newest Q private slots are the new
+ * tokens in order, and a token does not see those after it.  With key head
+ * head / (Hq / Hkv), z_j = scale * q . k_j:
+ *     out = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse = log sum_j exp(z_j)
+ * A row that sees nothing gets out 0 and lse -inf.
+ *
+ *   q   [B, Q, Hq, D];  k_cache, v_cache [pages, Hkv, page_size, D]; bf16 or fp16
+ *   prefix_table [ceil(prefix_len / page_size)] int32: the prefix's pages in order
+ *                (may be NULL when prefix_len is 0)
+ *   table [B, table_stride] int32: each request's own pages; lens [B] int32
+ *   max_len  an upper bound on lens (0 = table_stride * page_size)
+ *   w, w_out [B, Hkv, slots] fp32, both NULL or both given (w_out may be w),
+ *            slots >= max_len: the weight each private slot has gathered,
+ *                w_out[b,h,j] = w[b,h,j] + sum over h's rows of exp(z_j - lse)
+ *            for j < lens[b]; the newest Q slots start from 0 whatever w holds.
+ *            Slots from lens[b] on are not written.
+ *   out [B, Q, Hq, D] of q's type;  lse [B, Q, Hq] fp32 or NULL
+ *   ws  idx_prefix_attention_workspace(...) bytes, 256-byte aligned; needs no
+ *       clearing between calls
+ * Supported: D 64 or 128; page_size 16, 32, 64 or 128; 1 <= Q <= 16; Hq a
+ * multiple of Hkv with Hq / Hkv <= 128; B * Hkv <= 65535.  Device errors
+ * (IDX_DEV_RANGE): lens[b] outside [0, max_len] is clamped; a page outside
+ * [0, pages) reads as zeros, and the results of its request (of all of them,
+ * for a page of the prefix) are meaningless.
+ * ------------------------------------------------------------------------ */
+size_t idx_prefix_attention_workspace(int B, int Q, int Hq, int Hkv, int D, int prefix_len,
+                                      int max_len, int weights);
+idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* v_cache,
+                                const int* prefix_table, const int* table, const int* lens,
+                                const float* w, int B, int Q, int Hq, int Hkv, int D, int pages,
+                                int page_size, int prefix_len, long long table_stride,
+                                int max_len, long long slots, float scale, idx_dtype dt,
+                                void* out, float* lse, float* w_out, void* ws, size_t ws_bytes,
+                                const idx_options* opt, void* stream);
+
+/* ------------------------------------------------------------------------
+ * idx_cache_evict - keeps at most `budget` of the lens[b] cached slots of each
+ * (request, key head), by the weights idx_prefix_attention gathers.
+ *
+ * Slots are ranked protected first (position < sink, or position >=
+ * next_pos[b] - recent), then by weight, ties to the lower slot; the first
+ * `budget` stay.  Kept slots below `budget` do not move; the i-th hole among
+ * them (ascending) takes the K and V rows, weight and position of the i-th kept
+ * slot from `budget` on (ascending).  The heads of a request may keep different
+ * tokens.  A request of at most `budget` slots keeps everything.
+ *
+ *   k_cache, v_cache [pages, Hkv, page_size, D] bf16 or fp16, moved in place
+ *   table [B, table_stride], lens [B], next_pos [B] int32 (next_pos: tokens the
+ *         request has seen, one past the largest position)
+ *   w fp32, positions int32 [B, Hkv, slots]; w_out, positions_out likewise: the
+ *         first min(lens[b], budget) entries are written (each may be its input,
+ *         then only the filled holes are)
+ *   lens_out [B] int32 = min(lens[b], budget); not lens itself
+ *   max_len  an upper bound on lens (0 = table_stride * page_size)
+ *   ws  idx_cache_evict_workspace(...) bytes, 256-byte aligned
+ * No two requests may share a private page.  budget >= 1, recent, sink >= 0 and
+ * recent + sink <= budget (IDX_EINVAL); D 64 or 128; page_size 16, 32, 64 or 128.
+ * Device errors (IDX_DEV_RANGE): lens[b] outside [0, max_len] is clamped; a K/V
+ * row in a page outside [0, pages) is not moved.
+ * ------------------------------------------------------------------------ */
+size_t idx_cache_evict_workspace(int B, int Hkv, int budget, int max_len);
+idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const int* lens,
+                           const float* w, const int* positions, const int* next_pos, int B,
+                           int Hkv, int D, int pages, int page_size, long long table_stride,
+                           int max_len, long long slots, int budget, int recent, int sink,
+                           idx_dtype dt, int* lens_out, float* w_out, int* positions_out,
+                           void* ws, size_t ws_bytes, const idx_options* opt, void* stream);
 
 /* Static text for a status code. */
 const char* idx_status_string(idx_status s);

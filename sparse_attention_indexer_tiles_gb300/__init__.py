@@ -13,6 +13,9 @@ Entry points (same names as the C ABI in ``include/idx.h``):
   idx_score_topk_mxfp4, idx_score_materialise_mxfp4, idx_mxfp4_to_e4m3
                             the same on MXFP4 inputs (expanded exactly to e4m3)
   idx_score_topk_workspace, idx_topk_workspace, idx_status_string
+  idx_add_rmsnorm_quant     residual add + RMS norm to e4m3 rows with scales (k and k_scale)
+  idx_prefix_attention      decode attention over a shared prefix and private paged caches
+  idx_cache_evict           keep a budget of cached slots by accumulated attention weight
 """
 from __future__ import annotations
 
@@ -28,7 +31,9 @@ __all__ = [
     "idx_status_string", "DTYPES", "STAT_FIELDS", "StageEvents", "idx_launch_count",
     "idx_score_topk_noalloc", "idx_page_table_transform", "idx_route_fused",
     "idx_score_topk_routed", "idx_score_topk_routed_workspace", "idx_mxfp4_to_e4m3",
-    "idx_score_topk_mxfp4", "idx_score_materialise_mxfp4",
+    "idx_score_topk_mxfp4", "idx_score_materialise_mxfp4", "idx_add_rmsnorm_quant",
+    "idx_prefix_attention", "idx_prefix_attention_workspace", "idx_cache_evict",
+    "idx_cache_evict_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -36,6 +41,9 @@ LIB_PATH = os.path.join(_HERE, "_build", "libidx.so")
 
 IDX_BF16, IDX_FP8_E4M3, IDX_MXFP4 = 1, 2, 3
 DTYPES = {torch.bfloat16: IDX_BF16, torch.float8_e4m3fn: IDX_FP8_E4M3}
+IDX_FP16, IDX_FP32 = 4, 5
+# the serving operators' types (the indexer's own are DTYPES)
+SERVE_DTYPES = {torch.bfloat16: IDX_BF16, torch.float16: IDX_FP16, torch.float32: IDX_FP32}
 STAT_FIELDS = ("emit_all_rows", "overflow_rows", "short_rows", "fallback_rows", "max_count",
                "split_rows", "tie_rescan_rows", "reserved")
 
@@ -129,6 +137,17 @@ def load(path: str | None = None):
     lib.idx_score_materialise_mxfp4.argtypes = [P, P, P, P, P, P, P, P, I, LL, I, I, P, LL, P,
                                                 SZ, P, P]
     lib.idx_score_materialise_mxfp4.restype = I
+    F = ctypes.c_float
+    lib.idx_add_rmsnorm_quant.argtypes = [P, LL, P, P, I, I, F, I, I, P, P, P, P, P]
+    lib.idx_add_rmsnorm_quant.restype = I
+    lib.idx_prefix_attention_workspace.argtypes = [I] * 8
+    lib.idx_prefix_attention_workspace.restype = SZ
+    lib.idx_prefix_attention.argtypes = [P] * 7 + [I] * 8 + [LL, I, LL, F, I, P, P, P, P, SZ, P, P]
+    lib.idx_prefix_attention.restype = I
+    lib.idx_cache_evict_workspace.argtypes = [I] * 4
+    lib.idx_cache_evict_workspace.restype = SZ
+    lib.idx_cache_evict.argtypes = [P] * 7 + [I] * 5 + [LL, I, LL, I, I, I, I, P, P, P, P, SZ, P, P]
+    lib.idx_cache_evict.restype = I
     lib.idx_status_string.argtypes = [I]
     lib.idx_status_string.restype = ctypes.c_char_p
     lib.idx_version.argtypes = []
@@ -476,3 +495,163 @@ def idx_score_topk_routed(q, k, k_scale, w, ks, ke, topk: int, *, max_len: int =
             topk, dt, _ptr(out), _ptr(ws), ws.numel() * ws.element_size(), _opt_ref(o),
             _stream(stream)))
         return out
+
+
+def _serve_dtype(fn: str, *ts):
+    """The one element type of the tensors, as the C ABI names it."""
+    for t in ts:
+        if t is not None and t.dtype != ts[0].dtype:
+            raise ValueError(f"{fn}: {t.dtype} and {ts[0].dtype} tensors where one type is needed")
+    if ts[0].dtype not in SERVE_DTYPES:
+        raise ValueError(f"{fn}: unsupported type {ts[0].dtype}")
+    return SERVE_DTYPES[ts[0].dtype]
+
+
+def _expect(fn: str, name: str, t, dtype, shape):
+    if t is not None and (t.dtype != dtype or tuple(t.shape) != tuple(shape)):
+        raise ValueError(f"{fn}: {name} must be {dtype} {tuple(shape)}, got {t.dtype} "
+                         f"{tuple(t.shape)}")
+
+
+def idx_add_rmsnorm_quant(x, weight, *, residual=None, residual_out=None, eps: float = 1e-6,
+                          group: int = 0, out=None, scale=None, options=None,
+                          stats: Stats | None = None, stream=None):
+    """RMS norm of x (+ residual) [rows, N] to e4m3: (out [rows, N] e4m3, scale fp32
+    [rows] or, with group 32, 64 or 128, [rows, N // group]).  x may be a column
+    slice of a wider tensor.  residual_out receives x + residual in x's type."""
+    fn = "idx_add_rmsnorm_quant"
+    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
+        raise ValueError(f"{fn}: x must be [rows, N] with adjacent columns")
+    rows, N = x.shape
+    x_stride = x.stride(0) if rows > 1 else max(N, x.stride(0))
+    dev = _dev(weight, residual, residual_out, out, scale)
+    if x.device != dev:
+        raise ValueError(f"idx: tensors on different devices ({dev} and {x.device})")
+    dt = _serve_dtype(fn, x, weight, residual, residual_out)
+    _expect(fn, "weight", weight, x.dtype, (N,))
+    _expect(fn, "residual", residual, x.dtype, (rows, N))
+    _expect(fn, "residual_out", residual_out, x.dtype, (rows, N))
+    if group < 0 or (group and N % group):
+        raise ValueError(f"{fn}: {N} columns are not whole groups of {group}")
+    scales = (rows, N // group) if group else (rows,)
+    with torch.cuda.device(dev):
+        if out is None:
+            out = torch.empty(rows, N, dtype=torch.float8_e4m3fn, device=dev)
+        if scale is None:
+            scale = torch.empty(scales, dtype=torch.float32, device=dev)
+        _expect(fn, "out", out, torch.float8_e4m3fn, (rows, N))
+        _expect(fn, "scale", scale, torch.float32, scales)
+        o = make_options(options, stats)
+        _check(fn, load().idx_add_rmsnorm_quant(
+            _ptr(x), x_stride, _ptr(residual), _ptr(weight), rows, N, eps, group, dt,
+            _ptr(residual_out), _ptr(out), _ptr(scale), _opt_ref(o), _stream(stream)))
+        return out, scale
+
+
+def idx_prefix_attention_workspace(B: int, Q: int, Hq: int, Hkv: int, D: int, prefix_len: int,
+                                   max_len: int, weights: bool) -> int:
+    return int(load().idx_prefix_attention_workspace(B, Q, Hq, Hkv, D, prefix_len, max_len,
+                                                     int(bool(weights))))
+
+
+def idx_prefix_attention(q, k_cache, v_cache, table, lens, *, prefix_table=None,
+                         prefix_len: int = 0, max_len: int = 0, scale: float | None = None,
+                         weights=None, weights_out=None, out=None, lse=None, ws=None,
+                         options=None, stats: Stats | None = None, stream=None):
+    """Decode attention of q [B, Q, Hq, D] over a shared prefix (prefix_table) and each
+    request's own pages (table [B, P], lens [B]) of k_cache, v_cache
+    [pages, Hkv, page_size, D]: (out, lse [B, Q, Hq]), and weights_out when weights
+    [B, Hkv, slots] (what each private slot has gathered) is given."""
+    fn = "idx_prefix_attention"
+    dev = _dev(q, k_cache, v_cache, table, lens, prefix_table, weights, weights_out, out, lse, ws)
+    dt = _serve_dtype(fn, q, k_cache, v_cache)
+    if q.dim() != 4 or k_cache.dim() != 4 or k_cache.shape != v_cache.shape or table.dim() != 2:
+        raise ValueError(f"{fn}: q [B, Q, Hq, D], caches [pages, Hkv, page_size, D], table [B, P]")
+    B, Q, Hq, D = q.shape
+    pages, Hkv, page_size, cache_d = k_cache.shape
+    if cache_d != D:
+        raise ValueError(f"{fn}: q has {D} dimensions, the caches {cache_d}")
+    _expect(fn, "table", table, torch.int32, (B, table.shape[1]))
+    _expect(fn, "lens", lens, torch.int32, (B,))
+    if prefix_len > 0 and (prefix_table is None or prefix_table.dtype != torch.int32 or
+                           prefix_table.numel() * page_size < prefix_len):
+        raise ValueError(f"{fn}: prefix_table must be int32 and cover prefix_len")
+    if weights is not None and (weights.dim() != 3 or weights.dtype != torch.float32 or
+                                weights.shape[:2] != (B, Hkv)):
+        raise ValueError(f"{fn}: weights must be float32 [B, Hkv, slots]")
+    if weights is None and weights_out is not None:
+        raise ValueError(f"{fn}: weights_out without weights")
+    slots = 0 if weights is None else weights.shape[2]
+    with torch.cuda.device(dev):
+        if weights is not None and weights_out is None:
+            weights_out = torch.zeros_like(weights)
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(B, Q, Hq, dtype=torch.float32, device=dev)
+        _expect(fn, "weights_out", weights_out, torch.float32, (B, Hkv, slots))
+        _expect(fn, "out", out, q.dtype, q.shape)
+        _expect(fn, "lse", lse, torch.float32, (B, Q, Hq))
+        if ws is None:
+            need = idx_prefix_attention_workspace(
+                B, Q, Hq, Hkv, D, prefix_len, max_len or table.shape[1] * page_size,
+                weights is not None) if Hq % Hkv == 0 else 0
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=dev)
+        o = make_options(options, stats)
+        _check(fn, load().idx_prefix_attention(
+            _ptr(q), _ptr(k_cache), _ptr(v_cache), _ptr(prefix_table), _ptr(table), _ptr(lens),
+            _ptr(weights), B, Q, Hq, Hkv, D, pages, page_size, prefix_len, table.shape[1],
+            max_len, slots, D ** -0.5 if scale is None else scale, dt, _ptr(out), _ptr(lse),
+            _ptr(weights_out), _ptr(ws), ws.numel() * ws.element_size(), _opt_ref(o),
+            _stream(stream)))
+        return (out, lse) if weights is None else (out, lse, weights_out)
+
+
+def idx_cache_evict_workspace(B: int, Hkv: int, budget: int, max_len: int) -> int:
+    return int(load().idx_cache_evict_workspace(B, Hkv, budget, max_len))
+
+
+def idx_cache_evict(k_cache, v_cache, table, lens, weights, positions, next_pos, budget: int, *,
+                    recent: int = 0, sink: int = 0, max_len: int = 0, lens_out=None,
+                    weights_out=None, positions_out=None, ws=None, options=None,
+                    stats: Stats | None = None, stream=None):
+    """Keep the `budget` best slots of every (request, key head) by weights
+    [B, Hkv, slots], protecting positions < sink and >= next_pos - recent; the K/V rows
+    that move do so in place.  Returns (lens_out, weights_out, positions_out);
+    weights_out and positions_out may be the inputs themselves."""
+    fn = "idx_cache_evict"
+    dev = _dev(k_cache, v_cache, table, lens, weights, positions, next_pos, lens_out, weights_out,
+               positions_out, ws)
+    dt = _serve_dtype(fn, k_cache, v_cache)
+    if k_cache.dim() != 4 or k_cache.shape != v_cache.shape or table.dim() != 2 or \
+            weights.dim() != 3:
+        raise ValueError(f"{fn}: caches [pages, Hkv, page_size, D], table [B, P], weights "
+                         "[B, Hkv, slots]")
+    pages, Hkv, page_size, D = k_cache.shape
+    B, slots = table.shape[0], weights.shape[2]
+    _expect(fn, "table", table, torch.int32, table.shape)
+    _expect(fn, "lens", lens, torch.int32, (B,))
+    _expect(fn, "next_pos", next_pos, torch.int32, (B,))
+    _expect(fn, "weights", weights, torch.float32, (B, Hkv, slots))
+    _expect(fn, "positions", positions, torch.int32, (B, Hkv, slots))
+    with torch.cuda.device(dev):
+        if lens_out is None:
+            lens_out = torch.empty_like(lens)
+        if weights_out is None:
+            weights_out = torch.zeros_like(weights)
+        if positions_out is None:
+            positions_out = torch.full_like(positions, -1)
+        _expect(fn, "lens_out", lens_out, torch.int32, (B,))
+        _expect(fn, "weights_out", weights_out, torch.float32, (B, Hkv, slots))
+        _expect(fn, "positions_out", positions_out, torch.int32, (B, Hkv, slots))
+        if ws is None:
+            ws = torch.empty(max(256, idx_cache_evict_workspace(
+                B, Hkv, budget, max_len or table.shape[1] * page_size)),
+                dtype=torch.uint8, device=dev)
+        o = make_options(options, stats)
+        _check(fn, load().idx_cache_evict(
+            _ptr(k_cache), _ptr(v_cache), _ptr(table), _ptr(lens), _ptr(weights), _ptr(positions),
+            _ptr(next_pos), B, Hkv, D, pages, page_size, table.shape[1], max_len, slots, budget,
+            recent, sink, dt, _ptr(lens_out), _ptr(weights_out), _ptr(positions_out), _ptr(ws),
+            ws.numel() * ws.element_size(), _opt_ref(o), _stream(stream)))
+        return lens_out, weights_out, positions_out

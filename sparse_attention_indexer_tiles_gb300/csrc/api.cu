@@ -11,7 +11,10 @@
 
 #include <cudaTypedefs.h>
 
+#include "attention.cuh"
+#include "evict.cuh"
 #include "mxfp4.cuh"
+#include "norm_quant.cuh"
 #include "page_table.cuh"
 #include "plan.cuh"
 #include "score.cuh"
@@ -969,6 +972,214 @@ idx_status idx_score_materialise_mxfp4(const uint8_t* q, const uint8_t* q_sf, co
     if (st != IDX_OK) return st;
     return idx_score_materialise(base + L.q8, base + L.k8, k_scale, w, ks, ke, rows, keys, H, D,
                                  IDX_FP8_E4M3, scores, row_stride, opt, stream);
+}
+
+// ------------------------------------------------- serving operators
+
+namespace {
+
+bool page_size_ok(int p) { return p == 16 || p == 32 || p == 64 || p == 128; }
+
+int page_shift(int p) { return p == 16 ? 4 : p == 32 ? 5 : p == 64 ? 6 : 7; }
+
+bool is_16bit(idx_dtype dt) { return dt == IDX_BF16 || dt == IDX_FP16; }
+
+// max_len 0 is the table's whole width; false when the bound does not fit it.
+bool private_bound(int& max_len, long long table_stride, int page_size) {
+    const long long width = table_stride * page_size;
+    if (max_len == 0) {
+        if (width > 0x3fffffffll) return false;
+        max_len = (int)width;
+    }
+    return max_len <= width && max_len <= 0x3fffffff;
+}
+
+}  // namespace
+
+idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* residual,
+                                 const void* weight, int rows, int N, float eps, int group,
+                                 idx_dtype dt, void* residual_out, uint8_t* out, float* scale,
+                                 const idx_options* opt, void* stream) {
+    if (rows < 0 || N < 1 || x_stride < N || !(eps >= 0.f)) return IDX_EINVAL;
+    if (group != 0 && group != 32 && group != 64 && group != 128) return IDX_EINVAL;
+    if (group != 0 && N % group != 0) return IDX_EINVAL;
+    if (dt != IDX_BF16 && dt != IDX_FP16 && dt != IDX_FP32) return IDX_EUNSUPPORTED;
+    if (N > kNormMaxCols) return IDX_EUNSUPPORTED;
+    if (rows == 0) return IDX_OK;
+    if (!x || !weight || !out || !scale || residual_out == x) return IDX_EINVAL;
+    const size_t es = dt == IDX_FP32 ? 4 : 2;
+    if (!aligned(x, es) || !aligned(weight, es) || !aligned(scale, 4) ||
+        (residual && !aligned(residual, es)) || (residual_out && !aligned(residual_out, es)))
+        return IDX_EALIGN;
+    if (!arch_ok()) return IDX_EUNSUPPORTED;
+    NormArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.x = x;
+    a.residual = residual;
+    a.weight = weight;
+    a.residual_out = residual_out;
+    a.out = out;
+    a.scale = scale;
+    a.x_stride = x_stride;
+    a.rows = rows;
+    a.N = N;
+    a.group = group;
+    a.eps = eps;
+    a.vec = N % 8 == 0 && x_stride * es % 16 == 0 && aligned(x, 16) && aligned(weight, 16) &&
+            aligned(out, 8) && (!residual || aligned(residual, 16)) &&
+            (!residual_out || aligned(residual_out, 16));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    record(opt, 0, s);
+    const cudaError_t e = launch_norm_quant(a, dt, sm_count(), s);
+    if (e == cudaSuccess) count_launches(1);
+    record(opt, 1, s);
+    return cuda_status(e);
+}
+
+size_t idx_prefix_attention_workspace(int B, int Q, int Hq, int Hkv, int D, int prefix_len,
+                                      int max_len, int weights) {
+    if (B <= 0 || Q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || D < 1 || prefix_len < 0 ||
+        max_len < 0)
+        return 0;
+    return attn_plan(B, Q, Hq, Hkv, D, prefix_len, max_len, weights != 0, sm_count()).total;
+}
+
+idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* v_cache,
+                                const int* prefix_table, const int* table, const int* lens,
+                                const float* w, int B, int Q, int Hq, int Hkv, int D, int pages,
+                                int page_size, int prefix_len, long long table_stride,
+                                int max_len, long long slots, float scale, idx_dtype dt,
+                                void* out, float* lse, float* w_out, void* ws, size_t ws_bytes,
+                                const idx_options* opt, void* stream) {
+    if (B < 0 || Q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || pages < 0 || prefix_len < 0 ||
+        table_stride < 0 || max_len < 0 || !std::isfinite(scale) || !w != !w_out)
+        return IDX_EINVAL;
+    if (!is_16bit(dt) || (D != 64 && D != 128) || !page_size_ok(page_size) ||
+        Q > kAttnMaxTokens || Hq / Hkv > kAttnMaxGroup || (long long)B * Hkv > 65535 ||
+        (long long)B * Q * Hq > 0x7fffff00ll || prefix_len > 0x3fffffff)
+        return IDX_EUNSUPPORTED;
+    if (!private_bound(max_len, table_stride, page_size)) return IDX_EINVAL;
+    if (w && slots < max_len) return IDX_EINVAL;
+    if (B == 0) return IDX_OK;
+    if (!q || !out || !lens || (prefix_len > 0 && !prefix_table) || (max_len > 0 && !table) ||
+        ((prefix_len > 0 || max_len > 0) && (!k_cache || !v_cache)))
+        return IDX_EINVAL;
+    if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+        !aligned(lens, 4) || !aligned(prefix_table, 4) || !aligned(table, 4) || !aligned(w, 4) ||
+        !aligned(w_out, 4) || !aligned(lse, 4))
+        return IDX_EALIGN;
+    const AttnPlan p = attn_plan(B, Q, Hq, Hkv, D, prefix_len, max_len, w != nullptr, sm_count());
+    if (p.total > 0 && (!ws || ws_bytes < p.total)) return IDX_EWORKSPACE;
+    if (!aligned(ws, 256)) return IDX_EALIGN;
+    if (!arch_ok()) return IDX_EUNSUPPORTED;
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    AttnArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k = k_cache;
+    a.v = v_cache;
+    a.prefix_table = prefix_table;
+    a.table = table;
+    a.lens = lens;
+    a.w = w;
+    a.w_out = w_out;
+    a.out = out;
+    a.lse = lse;
+    a.part = reinterpret_cast<float*>(base + p.part);
+    a.part_lse = reinterpret_cast<float*>(base + p.part_lse);
+    a.logits = w ? reinterpret_cast<float*>(base + p.logits) : nullptr;
+    a.table_stride = table_stride;
+    a.slots = slots;
+    a.logit_stride = p.logit_stride;
+    a.B = B;
+    a.Q = Q;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.D = D;
+    a.pages = pages;
+    a.page_size = page_size;
+    a.page_shift = page_shift(page_size);
+    a.prefix_len = prefix_len;
+    a.max_len = max_len;
+    a.prefix_splits = p.prefix_splits;
+    a.prefix_chunk = p.prefix_chunk;
+    a.private_splits = p.private_splits;
+    a.private_chunk = p.private_chunk;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    a.d_status = opt ? opt->d_status : nullptr;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launched = 0;
+    record(opt, 0, s);
+    const cudaError_t e = launch_attention(a, dt, sm_count(), s, &launched);
+    count_launches(launched);
+    record(opt, 1, s);
+    return cuda_status(e);
+}
+
+size_t idx_cache_evict_workspace(int B, int Hkv, int budget, int max_len) {
+    if (B <= 0 || Hkv <= 0 || budget < 1 || max_len < 0) return 0;
+    return ((size_t)B * Hkv * 2 * evict_max_moves(budget, max_len) * sizeof(int) + 255) / 256 * 256;
+}
+
+idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const int* lens,
+                           const float* w, const int* positions, const int* next_pos, int B,
+                           int Hkv, int D, int pages, int page_size, long long table_stride,
+                           int max_len, long long slots, int budget, int recent, int sink,
+                           idx_dtype dt, int* lens_out, float* w_out, int* positions_out,
+                           void* ws, size_t ws_bytes, const idx_options* opt, void* stream) {
+    if (B < 0 || Hkv < 1 || pages < 0 || table_stride < 0 || max_len < 0 || budget < 1 ||
+        recent < 0 || sink < 0 || (long long)recent + sink > budget)
+        return IDX_EINVAL;
+    if (!is_16bit(dt) || (D != 64 && D != 128) || !page_size_ok(page_size) ||
+        (long long)B * Hkv > 0x7fffffffll)
+        return IDX_EUNSUPPORTED;
+    if (!private_bound(max_len, table_stride, page_size) || slots < max_len) return IDX_EINVAL;
+    if (B == 0) return IDX_OK;
+    if (!lens || !lens_out || lens == lens_out || !next_pos) return IDX_EINVAL;
+    if (max_len > 0 && (!k_cache || !v_cache || !table || !w || !positions || !w_out || !positions_out))
+        return IDX_EINVAL;
+    if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
+        !aligned(w, 4) || !aligned(positions, 4) || !aligned(next_pos, 4) ||
+        !aligned(lens_out, 4) || !aligned(w_out, 4) || !aligned(positions_out, 4))
+        return IDX_EALIGN;
+    const size_t need = idx_cache_evict_workspace(B, Hkv, budget, max_len);
+    if (need > 0 && (!ws || ws_bytes < need)) return IDX_EWORKSPACE;
+    if (!aligned(ws, 256)) return IDX_EALIGN;
+    if (!arch_ok()) return IDX_EUNSUPPORTED;
+    EvictArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.k = static_cast<uint8_t*>(k_cache);
+    a.v = static_cast<uint8_t*>(v_cache);
+    a.table = table;
+    a.lens = lens;
+    a.w = w;
+    a.pos = positions;
+    a.next_pos = next_pos;
+    a.lens_out = lens_out;
+    a.w_out = w_out;
+    a.pos_out = positions_out;
+    a.moves = static_cast<int*>(ws);
+    a.slots = slots;
+    a.table_stride = table_stride;
+    a.B = B;
+    a.Hkv = Hkv;
+    a.page_size = page_size;
+    a.page_shift = page_shift(page_size);
+    a.pages = pages;
+    a.row_bytes = D * 2;
+    a.budget = budget;
+    a.recent = recent;
+    a.sink = sink;
+    a.max_len = max_len;
+    a.max_moves = evict_max_moves(budget, max_len);
+    a.d_status = opt ? opt->d_status : nullptr;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    record(opt, 0, s);
+    const cudaError_t e = launch_evict(a, sm_count(), s);
+    if (e == cudaSuccess) count_launches(1);
+    record(opt, 1, s);
+    return cuda_status(e);
 }
 
 }  // extern "C"

@@ -1,0 +1,480 @@
+// Decode attention of a batch over a shared prefix and private paged caches.
+//
+// For row r (one query token and head) over the prefix's keys and its request's own,
+//     o = sum_j exp(z_j) v_j / sum_j exp(z_j),   z_j = scale * q . k_j,
+//     lse = log sum_j exp(z_j).
+// The keys of a row are cut into parts.  A part's rows are the rows that read the same
+// keys: the query heads of a key head for a private part, those of the whole batch for
+// a part of the prefix, so the prefix is read once however many requests share it.
+// Each part leaves m + log2(sum) and its normalised o; the parts are joined by
+//     o = sum_p 2^(l_p - L) o_p,   L = log2 sum_p 2^(l_p).
+// All exponentials are base 2 on z * log2(e); sums, maxima and o are fp32, and the
+// weights enter the second product in the tensors' own type (a relative rounding of
+// half a step per weight, as V itself carries).
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "attention.cuh"
+#include "common.cuh"
+
+namespace idx {
+
+namespace {
+
+constexpr int kPartWarps = 4;
+constexpr int kStep = 16;    // keys a warp takes at a time; pages hold at least as many
+constexpr int kStages = 4;   // steps in flight per warp
+
+IDX_DEVI float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// 16-byte asynchronous copy; bytes = 0 writes zeros and reads nothing
+IDX_DEVI void cp_async16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+                 : "memory");
+}
+IDX_DEVI void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> IDX_DEVI void cp_async_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+IDX_DEVI void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+IDX_DEVI void ldsm4_t(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+
+template <typename T> struct Mma;
+template <> struct Mma<__nv_bfloat16> {
+    static IDX_DEVI void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static IDX_DEVI uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static IDX_DEVI __nv_bfloat16 one(float v) { return __float2bfloat16_rn(v); }
+};
+template <> struct Mma<__half> {
+    static IDX_DEVI void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+        asm volatile(
+            "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, "
+            "{%8, %9}, {%0, %1, %2, %3};"
+            : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+            : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+    }
+    static IDX_DEVI uint32_t pack(float lo, float hi) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+    static IDX_DEVI __half one(float v) { return __float2half_rn(v); }
+};
+
+// Shared memory of a block: per warp a ring of kStages steps of K and V, rows of D
+// elements whose 16-byte chunks are xor-ed with the row's low bits (ldmatrix reads
+// eight rows at one chunk without bank conflicts).  The ring is reused for the join.
+template <int D> constexpr int part_smem() { return kPartWarps * kStages * 2 * kStep * D * 2; }
+
+// One part: 16 rows against keys [lo, hi) of one page table.  The block's warps take
+// the 16-key steps in turn, each with its own softmax state; the states are joined at
+// the end.  blockIdx.x: key head, row block and split; blockIdx.y: the request (private
+// parts); the prefix's rows are the batch's.
+template <typename T, int D, bool PREFIX>
+__global__ void __launch_bounds__(kPartWarps * 32) attn_part_kernel(AttnArgs a) {
+    extern __shared__ __align__(128) uint8_t smem[];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int splits = PREFIX ? a.prefix_splits : a.private_splits;
+    const int split = blockIdx.x % splits;
+    const int hk = blockIdx.x / splits % a.Hkv, rb = blockIdx.x / splits / a.Hkv;
+    const int b = PREFIX ? 0 : blockIdx.y;
+    const int rows = (PREFIX ? a.B : 1) * a.Q * a.G;
+    const int total_splits = a.prefix_splits + a.private_splits;
+    const int slot = PREFIX ? split : a.prefix_splits + split;
+
+    int n = a.prefix_len;
+    if (!PREFIX) {
+        n = a.lens[b];
+        if ((n < 0 || n > a.max_len) && tid == 0) raise_status(a.d_status, IDX_DEV_RANGE);
+        n = min(max(n, 0), a.max_len);
+    }
+    const int chunk = PREFIX ? a.prefix_chunk : a.private_chunk;
+    const int lo = split * chunk, hi = min(n, lo + chunk);
+    const int* table = PREFIX ? a.prefix_table : a.table + (long long)b * a.table_stride;
+
+    // row i of the block: query token bt, head of the group g
+    auto query_row = [&](int i) {
+        const int r = rb * 16 + i;
+        const int bt = r / a.G;
+        return ((long long)(PREFIX ? bt : b * a.Q + bt)) * a.Hq + hk * a.G + (r - bt * a.G);
+    };
+    if (lo >= hi) {  // no keys in this part
+        for (int i = tid; i < 16 && rb * 16 + i < rows; i += kPartWarps * 32)
+            a.part_lse[query_row(i) * total_splits + slot] = -INFINITY;
+        return;
+    }
+    const int r0 = rb * 16 + lane / 4, r1 = r0 + 8;  // this thread's two rows
+    const bool live0 = r0 < rows, live1 = r1 < rows;
+    // keys a private row sees: all but the tokens after its own
+    int see0 = n, see1 = n;
+    if (!PREFIX) {
+        see0 = live0 ? n - (a.Q - 1 - r0 / a.G) : 0;
+        see1 = live1 ? n - (a.Q - 1 - r1 / a.G) : 0;
+    }
+
+    uint32_t qf[D / 16][4];
+    {
+        const T* q = static_cast<const T*>(a.q);
+        const T* p0 = q + (live0 ? query_row(lane / 4) : 0) * D + (lane % 4) * 2;
+        const T* p1 = q + (live1 ? query_row(lane / 4 + 8) : 0) * D + (lane % 4) * 2;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            qf[k][0] = live0 ? *reinterpret_cast<const uint32_t*>(p0 + k * 16) : 0u;
+            qf[k][1] = live1 ? *reinterpret_cast<const uint32_t*>(p1 + k * 16) : 0u;
+            qf[k][2] = live0 ? *reinterpret_cast<const uint32_t*>(p0 + k * 16 + 8) : 0u;
+            qf[k][3] = live1 ? *reinterpret_cast<const uint32_t*>(p1 + k * 16 + 8) : 0u;
+        }
+    }
+
+    constexpr int kRowBytes = D * 2, kChunks = D / 8, kTile = kStep * kRowBytes;
+    const uint32_t ring = smem_u32(smem) + warp * kStages * 2 * kTile;
+    const int steps = (hi - lo + kStep - 1) / kStep;
+    const int mine = warp < steps ? (steps - 1 - warp) / kPartWarps + 1 : 0;
+    bool bad = false;
+    // a warp's pages are looked up 32 steps at a time, one per lane
+    int pages_from = 0, page_of = 0;
+    auto look_up = [&](int i) {
+        pages_from = i;
+        const int at = lo + ((i + lane) * kPartWarps + warp) * kStep;
+        page_of = i + lane < mine ? table[at >> a.page_shift] : 0;
+    };
+    look_up(0);
+    auto fetch = [&](int i) {
+        if (i - pages_from >= 32) look_up(i);
+        const int page = __shfl_sync(~0u, page_of, i - pages_from);
+        const bool ok = page >= 0 && page < a.pages;
+        bad |= !ok;
+        const int key = lo + (i * kPartWarps + warp) * kStep;
+        const long long row = ((long long)(ok ? page : 0) * a.Hkv + hk) * a.page_size +
+                              (key & (a.page_size - 1));
+        const uint8_t* kp = static_cast<const uint8_t*>(a.k) + row * kRowBytes;
+        const uint8_t* vp = static_cast<const uint8_t*>(a.v) + row * kRowBytes;
+        const uint32_t dst = ring + (i % kStages) * 2 * kTile;
+#pragma unroll
+        for (int j = 0; j < kStep * kChunks / 32; ++j) {
+            const int c = j * 32 + lane, rr = c / kChunks, cc = c % kChunks;
+            const uint32_t off = rr * kRowBytes + ((cc ^ (rr & 7)) * 16);
+            const uint32_t bytes = ok && key + rr < hi ? 16u : 0u;  // zeros past the end
+            cp_async16_zfill(dst + off, kp + rr * kRowBytes + cc * 16, bytes);
+            cp_async16_zfill(dst + kTile + off, vp + rr * kRowBytes + cc * 16, bytes);
+        }
+    };
+
+    float o[D / 8][4];
+#pragma unroll
+    for (int i = 0; i < D / 8; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
+    float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
+    float* logits = nullptr;
+    if (!PREFIX && a.logits)
+        logits = a.logits + ((long long)b * a.Hkv + hk) * (a.Q * a.G) * a.logit_stride;
+
+    for (int i = 0; i < kStages - 1; ++i) {
+        if (i < mine) fetch(i);
+        cp_async_commit();
+    }
+    for (int i = 0; i < mine; ++i) {
+        if (i + kStages - 1 < mine) fetch(i + kStages - 1);
+        cp_async_commit();
+        cp_async_wait<kStages - 1>();
+        __syncwarp();
+        const uint32_t kt = ring + (i % kStages) * 2 * kTile, vt = kt + kTile;
+        const int key = lo + (i * kPartWarps + warp) * kStep;
+        float s[2][4] = {{0.f, 0.f, 0.f, 0.f}, {0.f, 0.f, 0.f, 0.f}};
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k) {
+            // matrices: keys 0-7 and 8-15, each at d 16k .. and 16k + 8 ..
+            const int rr = (lane & 7) + ((lane >> 4) & 1) * 8, cc = 2 * k + ((lane >> 3) & 1);
+            uint32_t f[4];
+            ldsm4(kt + rr * kRowBytes + ((cc ^ (rr & 7)) * 16), f);
+            Mma<T>::run(s[0], qf[k], f[0], f[1]);
+            Mma<T>::run(s[1], qf[k], f[2], f[3]);
+        }
+#pragma unroll
+        for (int t = 0; t < 2; ++t)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                const int c = key + t * 8 + (lane % 4) * 2 + j;
+                s[t][j] = c < hi && c < see0 ? s[t][j] * a.scale_log2 : -INFINITY;
+                s[t][j + 2] = c < hi && c < see1 ? s[t][j + 2] * a.scale_log2 : -INFINITY;
+            }
+        if (logits) {
+#pragma unroll
+            for (int t = 0; t < 2; ++t) {
+                const int c = key + t * 8 + (lane % 4) * 2;
+                if (live0)
+                    *reinterpret_cast<float2*>(logits + r0 * a.logit_stride + c) =
+                        make_float2(s[t][0], s[t][1]);
+                if (live1)
+                    *reinterpret_cast<float2*>(logits + r1 * a.logit_stride + c) =
+                        make_float2(s[t][2], s[t][3]);
+            }
+        }
+        float x0 = fmaxf(fmaxf(s[0][0], s[0][1]), fmaxf(s[1][0], s[1][1]));
+        float x1 = fmaxf(fmaxf(s[0][2], s[0][3]), fmaxf(s[1][2], s[1][3]));
+        x0 = fmaxf(x0, __shfl_xor_sync(~0u, x0, 1));
+        x1 = fmaxf(x1, __shfl_xor_sync(~0u, x1, 1));
+        x0 = fmaxf(x0, __shfl_xor_sync(~0u, x0, 2));
+        x1 = fmaxf(x1, __shfl_xor_sync(~0u, x1, 2));
+        if (__any_sync(~0u, x0 > m0 || x1 > m1)) {
+            const float n0 = fmaxf(m0, x0), n1 = fmaxf(m1, x1);
+            const float f0 = n0 == -INFINITY ? 1.f : exp2_approx(m0 - n0);
+            const float f1 = n1 == -INFINITY ? 1.f : exp2_approx(m1 - n1);
+            m0 = n0;
+            m1 = n1;
+            l0 *= f0;
+            l1 *= f1;
+#pragma unroll
+            for (int d = 0; d < D / 8; ++d) {
+                o[d][0] *= f0;
+                o[d][1] *= f0;
+                o[d][2] *= f1;
+                o[d][3] *= f1;
+            }
+        }
+        // rows that have seen no key yet keep m = -inf: their weights are 0
+        const float b0 = m0 == -INFINITY ? 0.f : m0, b1 = m1 == -INFINITY ? 0.f : m1;
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+            s[t][0] = exp2_approx(s[t][0] - b0);
+            s[t][1] = exp2_approx(s[t][1] - b0);
+            s[t][2] = exp2_approx(s[t][2] - b1);
+            s[t][3] = exp2_approx(s[t][3] - b1);
+            l0 += s[t][0] + s[t][1];
+            l1 += s[t][2] + s[t][3];
+        }
+        const uint32_t p[4] = {Mma<T>::pack(s[0][0], s[0][1]), Mma<T>::pack(s[0][2], s[0][3]),
+                               Mma<T>::pack(s[1][0], s[1][1]), Mma<T>::pack(s[1][2], s[1][3])};
+#pragma unroll
+        for (int d = 0; d < D / 16; ++d) {
+            // matrices: keys 0-7 and 8-15 at d 16d .., then at 16d + 8 ..
+            const int rr = lane & 15, cc = 2 * d + (lane >> 4);
+            uint32_t f[4];
+            ldsm4_t(vt + rr * kRowBytes + ((cc ^ (rr & 7)) * 16), f);
+            Mma<T>::run(o[2 * d], p, f[0], f[1]);
+            Mma<T>::run(o[2 * d + 1], p, f[2], f[3]);
+        }
+        __syncwarp();
+    }
+    if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
+    l0 += __shfl_xor_sync(~0u, l0, 1);
+    l1 += __shfl_xor_sync(~0u, l1, 1);
+    l0 += __shfl_xor_sync(~0u, l0, 2);
+    l1 += __shfl_xor_sync(~0u, l1, 2);
+
+    // join the warps' states through shared memory
+    cp_async_wait<0>();
+    __syncthreads();
+    float* so = reinterpret_cast<float*>(smem);           // [warps][16][D + 4]
+    constexpr int kPitch = D + 4;
+    float* sm = so + kPartWarps * 16 * kPitch;             // [warps][16] maxima, then sums
+    float* sl = sm + kPartWarps * 16;
+#pragma unroll
+    for (int d = 0; d < D / 8; ++d) {
+        float* p = so + (warp * 16 + lane / 4) * kPitch + d * 8 + (lane % 4) * 2;
+        *reinterpret_cast<float2*>(p) = make_float2(o[d][0], o[d][1]);
+        *reinterpret_cast<float2*>(p + 8 * kPitch) = make_float2(o[d][2], o[d][3]);
+    }
+    if (lane % 4 == 0) {
+        sm[warp * 16 + lane / 4] = m0;
+        sm[warp * 16 + lane / 4 + 8] = m1;
+        sl[warp * 16 + lane / 4] = l0;
+        sl[warp * 16 + lane / 4 + 8] = l1;
+    }
+    __syncthreads();
+    for (int i = tid; i < 16 * (D / 4); i += kPartWarps * 32) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        if (rb * 16 + r >= rows) break;
+        float m = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kPartWarps; ++w) m = fmaxf(m, sm[w * 16 + r]);
+        const float base = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kPartWarps; ++w) {
+            const float f = exp2_approx(sm[w * 16 + r] - base);
+            const float4 x = *reinterpret_cast<const float4*>(so + (w * 16 + r) * kPitch + d);
+            l += f * sl[w * 16 + r];
+            acc.x += f * x.x;
+            acc.y += f * x.y;
+            acc.z += f * x.z;
+            acc.w += f * x.w;
+        }
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const long long at = query_row(r) * total_splits + slot;
+        *reinterpret_cast<float4*>(a.part + at * D + d) =
+            make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+        if (d == 0) a.part_lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
+    }
+}
+
+// log2-sum-exp2 of a row's parts: every lane of the warp gets it
+IDX_DEVI float join_lse(const float* part_lse, int splits, int lane) {
+    float m = -INFINITY;
+    for (int i = lane; i < splits; i += 32) m = fmaxf(m, part_lse[i]);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    if (m == -INFINITY) return m;
+    float l = 0.f;
+    for (int i = lane; i < splits; i += 32) l += exp2_approx(part_lse[i] - m);
+#pragma unroll
+    for (int o = 16; o > 0; o /= 2) l += __shfl_xor_sync(~0u, l, o);
+    return m + log2f(l);
+}
+
+constexpr int kJoinWarps = 4;
+
+// One warp per query row: the join of its parts.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnArgs a) {
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+    if (row >= (long long)a.B * a.Q * a.Hq) return;
+    const int splits = a.prefix_splits + a.private_splits;
+    const float* pl = a.part_lse + row * splits;
+    const float lse = join_lse(pl, splits, lane);
+    float acc[D / 32];
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+    if (lse != -INFINITY) {
+        const float* part = a.part + row * splits * D;
+        for (int p = 0; p < splits; ++p) {
+            const float f = exp2_approx(pl[p] - lse);
+            if (pl[p] == -INFINITY) continue;  // nothing was written there
+#pragma unroll
+            for (int i = 0; i < D / 32; ++i) acc[i] += f * part[(long long)p * D + i * 32 + lane];
+        }
+    }
+    T* out = static_cast<T*>(a.out) + row * D;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) out[i * 32 + lane] = Mma<T>::one(acc[i]);
+    if (a.lse && lane == 0) a.lse[row] = lse * 0.6931471805599453f;
+}
+
+constexpr int kWeightSlots = 256;
+
+// One thread per private slot: the weight its key received from the request's rows.
+// blockIdx.x: slots, blockIdx.y: request and key head.
+__global__ void __launch_bounds__(kWeightSlots) attn_weights_kernel(AttnArgs a) {
+    extern __shared__ __align__(16) float row_lse[];
+    const int b = blockIdx.y / a.Hkv, hk = blockIdx.y % a.Hkv;
+    const int n = min(max(a.lens[b], 0), a.max_len);
+    const int first = blockIdx.x * kWeightSlots;
+    if (first >= n) return;
+    const int rows = a.Q * a.G, splits = a.prefix_splits + a.private_splits;
+    const int lane = threadIdx.x & 31;
+    for (int r = threadIdx.x / 32; r < rows; r += kWeightSlots / 32) {
+        const long long row = ((long long)b * a.Q + r / a.G) * a.Hq + hk * a.G + r % a.G;
+        const float l = join_lse(a.part_lse + row * splits, splits, lane);
+        if (lane == 0) row_lse[r] = l;
+    }
+    __syncthreads();
+    const int j = first + (int)threadIdx.x;
+    if (j >= n) return;
+    const long long at = (long long)blockIdx.y * a.slots + j;
+    const float* z = a.logits + (long long)blockIdx.y * rows * a.logit_stride + j;
+    // the newest tokens' slots have gathered nothing yet, whatever the array holds
+    float sum = 0.f;
+    for (int r = 0; r < rows; ++r)
+        if (row_lse[r] != -INFINITY) sum += exp2_approx(z[r * a.logit_stride] - row_lse[r]);
+    a.w_out[at] = (j < n - a.Q ? a.w[at] : 0.f) + sum;
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const AttnArgs& a, cudaStream_t s, int* launched) {
+    const int smem = part_smem<D>();
+    cudaError_t e = cudaSuccess;
+    if (a.prefix_splits > 0) {
+        const long long rows = (long long)a.B * a.Q * a.G;
+        const long long blocks = (rows + 15) / 16 * a.Hkv * a.prefix_splits;
+        e = cudaFuncSetAttribute(attn_part_kernel<T, D, true>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        attn_part_kernel<T, D, true><<<(unsigned)blocks, kPartWarps * 32, smem, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        ++*launched;
+    }
+    if (a.private_splits > 0) {
+        const dim3 grid((a.Q * a.G + 15) / 16 * a.Hkv * a.private_splits, a.B);
+        e = cudaFuncSetAttribute(attn_part_kernel<T, D, false>,
+                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        if (e != cudaSuccess) return e;
+        attn_part_kernel<T, D, false><<<grid, kPartWarps * 32, smem, s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        ++*launched;
+    }
+    const long long rows = (long long)a.B * a.Q * a.Hq;
+    attn_join_kernel<T, D><<<(unsigned)((rows + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, s>>>(a);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    ++*launched;
+    if (a.w_out && a.max_len > 0) {
+        const dim3 grid((a.max_len + kWeightSlots - 1) / kWeightSlots, a.B * a.Hkv);
+        attn_weights_kernel<<<grid, kWeightSlots, a.Q * a.G * sizeof(float), s>>>(a);
+        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        ++*launched;
+    }
+    return e;
+}
+
+}  // namespace
+
+AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max_len, bool weights,
+                   int sm_count) {
+    AttnPlan p;
+    const int G = Hq / Hkv;
+    auto cut = [&](long long items, int len, int& splits, int& chunk) {
+        splits = chunk = 0;
+        if (len <= 0) return;
+        // about four blocks per SM, at least 256 keys each
+        long long want = (4ll * sm_count + items - 1) / items;
+        const long long most = (len + 255) / 256;
+        want = want < most ? want : most;
+        chunk = (int)(((len + want - 1) / want + 63) / 64 * 64);
+        splits = (len + chunk - 1) / chunk;
+    };
+    cut(((long long)B * Q * G + 15) / 16 * Hkv, prefix_len, p.prefix_splits, p.prefix_chunk);
+    cut((long long)(Q * G + 15) / 16 * Hkv * B, max_len, p.private_splits, p.private_chunk);
+    const size_t rows = (size_t)B * Q * Hq, splits = p.prefix_splits + p.private_splits;
+    auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+    p.logit_stride = ((long long)max_len + 15) / 16 * 16;
+    p.part = 0;
+    p.part_lse = up(rows * splits * D * sizeof(float));
+    p.logits = p.part_lse + up(rows * splits * sizeof(float));
+    p.total = p.logits + (weights ? up(rows * p.logit_stride * sizeof(float)) : 0);
+    return p;
+}
+
+cudaError_t launch_attention(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStream_t s,
+                             int* launched) {
+    (void)sm_count;
+    if (dt == IDX_BF16)
+        return a.D == 128 ? launch_typed<__nv_bfloat16, 128>(a, s, launched)
+                          : launch_typed<__nv_bfloat16, 64>(a, s, launched);
+    return a.D == 128 ? launch_typed<__half, 128>(a, s, launched)
+                      : launch_typed<__half, 64>(a, s, launched);
+}
+
+}  // namespace idx

@@ -1,0 +1,54 @@
+// Launch interface of the shared-prefix decode attention (attention.cu).
+#pragma once
+
+#include <cstdint>
+#include <cuda_runtime.h>
+
+#include "../../include/idx.h"
+
+namespace idx {
+
+constexpr int kAttnMaxTokens = 16;   // new tokens per request
+constexpr int kAttnMaxGroup = 128;   // query heads per key head
+
+// One attention call.  Rows: query row (b, t, head) = (b * Q + t) * Hq + head.  The
+// keys of a row are cut into `splits` parts, the prefix's first; each part leaves its
+// softmax-weighted mean of V and its log2-sum-exp2 in the workspace.
+struct AttnArgs {
+    const void* q;            // [B, Q, Hq, D]
+    const void* k;            // [pages, Hkv, page_size, D]
+    const void* v;
+    const int* prefix_table;  // [ceil(prefix_len / page_size)]
+    const int* table;         // [B, table_stride]
+    const int* lens;          // [B]
+    const float* w;           // [B, Hkv, slots] or null
+    float* w_out;             // [B, Hkv, slots] or null; may be w
+    void* out;                // [B, Q, Hq, D]
+    float* lse;               // [B, Q, Hq] or null
+    // workspace
+    float* part;              // [rows, splits, D]
+    float* part_lse;          // [rows, splits], log2 units; -inf: no keys
+    float* logits;            // [B, Hkv, Q * G, logit_stride] log2 units, or null
+    long long table_stride, slots, logit_stride;
+    int B, Q, Hq, Hkv, G, D, pages, page_size, page_shift;
+    int prefix_len, max_len;
+    int prefix_splits, prefix_chunk;    // keys per prefix part (a multiple of 64)
+    int private_splits, private_chunk;  // keys per private part (a multiple of 64)
+    float scale_log2;                   // scale * log2(e)
+    int* d_status;
+};
+
+struct AttnPlan {
+    int prefix_splits, prefix_chunk, private_splits, private_chunk;
+    size_t part, part_lse, logits, total;
+    long long logit_stride;
+};
+
+AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max_len, bool weights,
+                   int sm_count);
+
+// Returns the number of kernels launched through *launched.
+cudaError_t launch_attention(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStream_t s,
+                             int* launched);
+
+}  // namespace idx
