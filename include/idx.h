@@ -109,8 +109,10 @@ typedef struct idx_options {
                              microseconds (instead of about 2 s).  A pass with more
                              than one tile then stops early with IDX_DEV_TIMEOUT in
                              *d_status, leaving no copy or MMA in flight; the call
-                             returns and its results are meaningless.  It exists to
-                             run the timeout unwind on purpose. */
+                             returns and its results are meaningless.  The prefix
+                             kernel of idx_prefix_attention does the same with its
+                             key tile 1.  It exists to run the timeout unwind on
+                             purpose. */
     void* const* stage_events; /* optional array of cudaEvent_t, recorded on `stream`
                              at stage boundaries (NULL entries are skipped).
                              idx_score_topk: [0] start, [1] after the sample and its
@@ -413,7 +415,7 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
  *   ws  idx_prefix_attention_workspace(...) bytes, 256-byte aligned; needs no
  *       clearing between calls
  * Supported: D 64 or 128; page_size 16, 32, 64 or 128; 1 <= Q <= 16; Hq a
- * multiple of Hkv with Hq / Hkv <= 128; B * Hkv <= 65535.  Device errors
+ * multiple of Hkv with Hq / Hkv <= 128; B * Hkv <= 65535; pages >= 1 with keys.  Device errors
  * (IDX_DEV_RANGE): lens[b] outside [0, max_len] is clamped; a page outside
  * [0, pages) reads as zeros, and the results of its request (of all of them,
  * for a page of the prefix) are meaningless.

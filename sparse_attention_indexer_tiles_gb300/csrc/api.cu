@@ -1062,7 +1062,7 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
     if (w && slots < max_len) return IDX_EINVAL;
     if (B == 0) return IDX_OK;
     if (!q || !out || !lens || (prefix_len > 0 && !prefix_table) || (max_len > 0 && !table) ||
-        ((prefix_len > 0 || max_len > 0) && (!k_cache || !v_cache)))
+        ((prefix_len > 0 || max_len > 0) && (!k_cache || !v_cache || pages < 1)))
         return IDX_EINVAL;
     if (!aligned(q, 16) || !aligned(out, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
         !aligned(lens, 4) || !aligned(prefix_table, 4) || !aligned(table, 4) || !aligned(w, 4) ||
@@ -1107,6 +1107,9 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
     a.private_splits = p.private_splits;
     a.private_chunk = p.private_chunk;
     a.scale_log2 = scale * 1.4426950408889634f;
+    const int stall_us = opt ? opt->test_stall_us : 0;
+    a.wait_limit = stall_us > 0 ? 2100LL * stall_us : (1LL << 32);
+    a.withhold_tile = stall_us > 0 ? 1 : -1;
     a.d_status = opt ? opt->d_status : nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int launched = 0;

@@ -87,37 +87,30 @@ template <> struct Mma<__half> {
 // eight rows at one chunk without bank conflicts).  The ring is reused for the join.
 template <int D> constexpr int part_smem() { return kPartWarps * kStages * 2 * kStep * D * 2; }
 
-// One part: 16 rows against keys [lo, hi) of one page table.  The block's warps take
+// One private part: 16 rows against a request's keys [lo, hi).  The block's warps take
 // the 16-key steps in turn, each with its own softmax state; the states are joined at
-// the end.  blockIdx.x: key head, row block and split; blockIdx.y: the request (private
-// parts); the prefix's rows are the batch's.
-template <typename T, int D, bool PREFIX>
+// the end.  blockIdx.x: key head, row block and split; blockIdx.y: the request.
+template <typename T, int D>
 __global__ void __launch_bounds__(kPartWarps * 32) attn_part_kernel(AttnArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int splits = PREFIX ? a.prefix_splits : a.private_splits;
-    const int split = blockIdx.x % splits;
-    const int hk = blockIdx.x / splits % a.Hkv, rb = blockIdx.x / splits / a.Hkv;
-    const int b = PREFIX ? 0 : blockIdx.y;
-    const int rows = (PREFIX ? a.B : 1) * a.Q * a.G;
+    const int split = blockIdx.x % a.private_splits;
+    const int hk = blockIdx.x / a.private_splits % a.Hkv;
+    const int rb = blockIdx.x / a.private_splits / a.Hkv, b = blockIdx.y;
+    const int rows = a.Q * a.G;
     const int total_splits = a.prefix_splits + a.private_splits;
-    const int slot = PREFIX ? split : a.prefix_splits + split;
+    const int slot = a.prefix_splits + split;
 
-    int n = a.prefix_len;
-    if (!PREFIX) {
-        n = a.lens[b];
-        if ((n < 0 || n > a.max_len) && tid == 0) raise_status(a.d_status, IDX_DEV_RANGE);
-        n = min(max(n, 0), a.max_len);
-    }
-    const int chunk = PREFIX ? a.prefix_chunk : a.private_chunk;
-    const int lo = split * chunk, hi = min(n, lo + chunk);
-    const int* table = PREFIX ? a.prefix_table : a.table + (long long)b * a.table_stride;
+    int n = a.lens[b];
+    if ((n < 0 || n > a.max_len) && tid == 0) raise_status(a.d_status, IDX_DEV_RANGE);
+    n = min(max(n, 0), a.max_len);
+    const int lo = split * a.private_chunk, hi = min(n, lo + a.private_chunk);
+    const int* table = a.table + (long long)b * a.table_stride;
 
-    // row i of the block: query token bt, head of the group g
+    // row i of the block: query token t, head g of the group
     auto query_row = [&](int i) {
-        const int r = rb * 16 + i;
-        const int bt = r / a.G;
-        return ((long long)(PREFIX ? bt : b * a.Q + bt)) * a.Hq + hk * a.G + (r - bt * a.G);
+        const int r = rb * 16 + i, t = r / a.G;
+        return ((long long)b * a.Q + t) * a.Hq + hk * a.G + (r - t * a.G);
     };
     if (lo >= hi) {  // no keys in this part
         for (int i = tid; i < 16 && rb * 16 + i < rows; i += kPartWarps * 32)
@@ -126,12 +119,9 @@ __global__ void __launch_bounds__(kPartWarps * 32) attn_part_kernel(AttnArgs a) 
     }
     const int r0 = rb * 16 + lane / 4, r1 = r0 + 8;  // this thread's two rows
     const bool live0 = r0 < rows, live1 = r1 < rows;
-    // keys a private row sees: all but the tokens after its own
-    int see0 = n, see1 = n;
-    if (!PREFIX) {
-        see0 = live0 ? n - (a.Q - 1 - r0 / a.G) : 0;
-        see1 = live1 ? n - (a.Q - 1 - r1 / a.G) : 0;
-    }
+    // keys a row sees: all but the tokens after its own
+    const int see0 = live0 ? n - (a.Q - 1 - r0 / a.G) : 0;
+    const int see1 = live1 ? n - (a.Q - 1 - r1 / a.G) : 0;
 
     uint32_t qf[D / 16][4];
     {
@@ -188,7 +178,7 @@ __global__ void __launch_bounds__(kPartWarps * 32) attn_part_kernel(AttnArgs a) 
         for (int j = 0; j < 4; ++j) o[i][j] = 0.f;
     float m0 = -INFINITY, m1 = -INFINITY, l0 = 0.f, l1 = 0.f;
     float* logits = nullptr;
-    if (!PREFIX && a.logits)
+    if (a.logits)
         logits = a.logits + ((long long)b * a.Hkv + hk) * (a.Q * a.G) * a.logit_stride;
 
     for (int i = 0; i < kStages - 1; ++i) {
@@ -404,25 +394,19 @@ __global__ void __launch_bounds__(kWeightSlots) attn_weights_kernel(AttnArgs a) 
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const AttnArgs& a, cudaStream_t s, int* launched) {
+cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, cudaStream_t s, int* launched) {
     const int smem = part_smem<D>();
     cudaError_t e = cudaSuccess;
     if (a.prefix_splits > 0) {
-        const long long rows = (long long)a.B * a.Q * a.G;
-        const long long blocks = (rows + 15) / 16 * a.Hkv * a.prefix_splits;
-        e = cudaFuncSetAttribute(attn_part_kernel<T, D, true>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-        if (e != cudaSuccess) return e;
-        attn_part_kernel<T, D, true><<<(unsigned)blocks, kPartWarps * 32, smem, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
+        if ((e = launch_prefix_parts(a, dt, s)) != cudaSuccess) return e;
         ++*launched;
     }
     if (a.private_splits > 0) {
         const dim3 grid((a.Q * a.G + 15) / 16 * a.Hkv * a.private_splits, a.B);
-        e = cudaFuncSetAttribute(attn_part_kernel<T, D, false>,
+        e = cudaFuncSetAttribute(attn_part_kernel<T, D>,
                                  cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
         if (e != cudaSuccess) return e;
-        attn_part_kernel<T, D, false><<<grid, kPartWarps * 32, smem, s>>>(a);
+        attn_part_kernel<T, D><<<grid, kPartWarps * 32, smem, s>>>(a);
         if ((e = cudaGetLastError()) != cudaSuccess) return e;
         ++*launched;
     }
@@ -455,7 +439,28 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
         chunk = (int)(((len + want - 1) / want + 63) / 64 * 64);
         splits = (len + chunk - 1) / chunk;
     };
-    cut(((long long)B * Q * G + 15) / 16 * Hkv, prefix_len, p.prefix_splits, p.prefix_chunk);
+    p.prefix_splits = p.prefix_chunk = 0;
+    if (prefix_len > 0) {
+        // Key tiles per part: one CTA per SM takes about 1 us per 128-key tile of a pair of
+        // row tiles (0.6 us of a single one) and 4 us besides, and every part writes D
+        // floats per row that the join reads (about 5 MB per us).
+        const int tokens = 128 / G, tiles = (prefix_len + 127) / 128;
+        const long long row_tiles = ((long long)B * Q + tokens - 1) / tokens;
+        const long long items = (row_tiles + 1) / 2 * Hkv;
+        const double per_tile = row_tiles > 1 ? 1.0 : 0.6;
+        double best = 0;
+        for (int s = 1; s <= tiles && s <= 256; ++s) {
+            const int t = (tiles + s - 1) / s;
+            const long long ctas = items * ((tiles + t - 1) / t);
+            const double us = (double)((ctas + sm_count - 1) / sm_count) * (t * per_tile + 4.0) +
+                              (double)B * Q * Hq * s * D * 8 / 5e6;
+            if (best == 0 || us < best) {
+                best = us;
+                p.prefix_chunk = t * 128;
+            }
+        }
+        p.prefix_splits = (prefix_len + p.prefix_chunk - 1) / p.prefix_chunk;
+    }
     cut((long long)(Q * G + 15) / 16 * Hkv * B, max_len, p.private_splits, p.private_chunk);
     const size_t rows = (size_t)B * Q * Hq, splits = p.prefix_splits + p.private_splits;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
@@ -471,10 +476,10 @@ cudaError_t launch_attention(const AttnArgs& a, idx_dtype dt, int sm_count, cuda
                              int* launched) {
     (void)sm_count;
     if (dt == IDX_BF16)
-        return a.D == 128 ? launch_typed<__nv_bfloat16, 128>(a, s, launched)
-                          : launch_typed<__nv_bfloat16, 64>(a, s, launched);
-    return a.D == 128 ? launch_typed<__half, 128>(a, s, launched)
-                      : launch_typed<__half, 64>(a, s, launched);
+        return a.D == 128 ? launch_typed<__nv_bfloat16, 128>(a, dt, s, launched)
+                          : launch_typed<__nv_bfloat16, 64>(a, dt, s, launched);
+    return a.D == 128 ? launch_typed<__half, 128>(a, dt, s, launched)
+                      : launch_typed<__half, 64>(a, dt, s, launched);
 }
 
 }  // namespace idx

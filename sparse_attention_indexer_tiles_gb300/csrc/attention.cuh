@@ -32,9 +32,11 @@ struct AttnArgs {
     long long table_stride, slots, logit_stride;
     int B, Q, Hq, Hkv, G, D, pages, page_size, page_shift;
     int prefix_len, max_len;
-    int prefix_splits, prefix_chunk;    // keys per prefix part (a multiple of 64)
+    int prefix_splits, prefix_chunk;    // keys per prefix part (a multiple of 128)
     int private_splits, private_chunk;  // keys per private part (a multiple of 64)
     float scale_log2;                   // scale * log2(e)
+    long long wait_limit;               // SM clocks a wait of the prefix kernel may take
+    int withhold_tile;                  // test only: the key tile that is never loaded, or -1
     int* d_status;
 };
 
@@ -46,6 +48,9 @@ struct AttnPlan {
 
 AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max_len, bool weights,
                    int sm_count);
+
+// The prefix's parts (attention_prefix.cu).
+cudaError_t launch_prefix_parts(const AttnArgs& a, idx_dtype dt, cudaStream_t s);
 
 // Returns the number of kernels launched through *launched.
 cudaError_t launch_attention(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStream_t s,

@@ -1,0 +1,503 @@
+// The shared prefix's parts of the decode attention on the 5th-generation tensor cores.
+//
+// The rows of a key head over the whole batch (B * Q * G of them) read the same prefix
+// keys, so they are the rows of two dense products per key tile,
+//     S = Q K^T  (128 rows x 128 keys, over D),     O += P V  (128 rows x D, over keys),
+// with P = 2^(S scale_log2 - m) between them.  A CTA runs two streams, each with its own
+// S and O accumulators in TMEM and its own four softmax warps (one thread per row); while
+// one stream's softmax runs, the tensor core works for the other:
+//   * two row tiles over the same keys (each K and V tile in shared memory serves both), or
+//   * for a last, odd row tile, the same rows over the even and the odd key tiles, joined
+//     through shared memory at the end.
+// Warp 8 issues the MMAs, warp 9 the TMA copies: K and V tiles of 128 keys through a ring,
+// page by page (each page's rows of a head are contiguous).  P goes back to TMEM over S, in
+// the tensors' type, and is the A operand of the second product; V is used as it lies in
+// memory (its rows are the product's K axis, so the B operand is MN-major).
+//
+// The running maximum m is renewed only when a row's maximum has grown by more than 8 (a
+// factor 256; P <= 256 then, well inside either type), so O is rarely rescaled; the sum l
+// and O stay relative to the m in use, in fp32, and the result does not depend on it.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <cudaTypedefs.h>
+
+#include <mutex>
+
+#include "attention.cuh"
+#include "common.cuh"
+
+namespace idx {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace {
+
+constexpr int kKeys = 128;                 // keys per tile
+constexpr int kHalf = 128 * 128;           // 128 rows of 64 16-bit elements, 128-byte swizzled
+constexpr int kSoftmaxWarps = 8;
+constexpr int kPrefixThreads = (kSoftmaxWarps + 2) * 32;
+constexpr float kRenew = 8.f;
+
+template <int D> struct PrefixCfg {
+    static constexpr int HALVES = D / 64;
+    static constexpr int TILE = HALVES * kHalf;      // a Q, K or V tile
+    static constexpr int NS = D == 128 ? 5 : 8;      // ring slots
+    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int OFF_BAR = OFF_KV + NS * TILE;
+    static constexpr int NBAR = 1 + 2 * NS + 7;
+    static constexpr int OFF_CTL = OFF_BAR + NBAR * 8;   // [0] TMEM base, [1] abort flag
+    static constexpr int OFF_ML = OFF_CTL + 16;          // the odd stream's m and l per row
+    static constexpr int SMEM = OFF_ML + 128 * 8 + 1024;
+};
+static_assert(PrefixCfg<128>::SMEM <= 227 * 1024 && PrefixCfg<64>::SMEM <= 227 * 1024, "");
+// the odd stream's O is joined through the ring
+static_assert(128 * 128 * 4 <= PrefixCfg<128>::NS * PrefixCfg<128>::TILE, "");
+
+IDX_DEVI float ex2(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+IDX_DEVI void tma_load_4d(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2,
+                          int c3) {
+    asm volatile(
+        "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5, %6}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(c0), "r"(c1), "r"(c2),
+        "r"(c3)
+        : "memory");
+}
+
+// D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, fp32 accumulator.
+IDX_DEVI void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
+                     uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32x32b shape, 32 columns: thread t writes lane t.
+IDX_DEVI void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
+        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
+        "%29, %30, %31, %32};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+        "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+IDX_DEVI void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Descriptor of a V tile as an MN-major B operand, 128-byte swizzled: 64 elements of D are
+// contiguous, the next 64 lie `kHalf` further (leading offset), 8 keys are 1024 bytes
+// (stride offset).
+IDX_DEVI uint64_t v_desc(uint32_t saddr) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(kHalf >> 4) << 16) |
+           ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+}
+
+template <typename T> struct Elem;
+template <> struct Elem<__nv_bfloat16> {
+    static constexpr uint32_t FMT = 1;
+    static IDX_DEVI uint32_t pack(float lo, float hi) {
+        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+};
+template <> struct Elem<__half> {
+    static constexpr uint32_t FMT = 0;
+    static IDX_DEVI uint32_t pack(float lo, float hi) {
+        const __half2 v = __floats2half2_rn(lo, hi);
+        return *reinterpret_cast<const uint32_t*>(&v);
+    }
+};
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kPrefixThreads, 1)
+attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                   const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnArgs a) {
+    using C = PrefixCfg<D>;
+    extern __shared__ __align__(1024) uint8_t smem_raw[];
+    uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+    uint64_t* qfull = reinterpret_cast<uint64_t*>(smem + C::OFF_BAR);
+    uint64_t* full = qfull + 1;
+    uint64_t* empty = full + C::NS;
+    uint64_t* sfull = empty + C::NS;  // per stream: S is there
+    uint64_t* pfull = sfull + 2;      // P is there (and S has been read)
+    uint64_t* pvdone = pfull + 2;     // O has the tile's P V
+    uint64_t* done = pvdone + 2;      // every MMA of the CTA
+    volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
+    volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    // this CTA: key head, pair of row tiles, part of the prefix
+    const int tokens = kKeys / a.G;  // query tokens per row tile (its rows: tokens * G <= 128)
+    const int ntiles = (a.B * a.Q + tokens - 1) / tokens, npairs = (ntiles + 1) / 2;
+    const int split = blockIdx.x % a.prefix_splits;
+    const int pair = blockIdx.x / a.prefix_splits % npairs;
+    const int hk = blockIdx.x / a.prefix_splits / npairs;
+    const bool solo = 2 * pair + 1 == ntiles;
+    const int lo = split * a.prefix_chunk, hi = min(a.prefix_len, lo + a.prefix_chunk);
+    const int n = (hi - lo + kKeys - 1) / kKeys;  // key tiles, at least one
+
+    if (tid == 0) {
+        mbar_init(qfull, 1);
+        for (int i = 0; i < C::NS; ++i) {
+            mbar_init(&full[i], 1);
+            mbar_init(&empty[i], 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(&sfull[i], 1);
+            mbar_init(&pfull[i], 4);
+            mbar_init(&pvdone[i], 1);
+        }
+        mbar_init(done, 1);
+        *abort_flag = 0;
+        fence_barrier_init();
+    }
+    if (warp == 8) {
+        tmem_alloc(const_cast<uint32_t*>(tslot), 512);
+        tmem_relinquish();
+    }
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = *tslot;
+    const uint32_t kv = smem_u32(smem + C::OFF_KV);
+    auto give_up = [&] {
+        *abort_flag = 1;
+        raise_status(a.d_status, IDX_DEV_TIMEOUT);
+    };
+
+    if (warp == 9) {
+        // ---------------------------------------------------- TMA producer
+        const int qbytes = tokens * a.G * 128;
+        if (lane == 0) {
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+            const int tiles = solo ? 1 : 2;
+            mbar_arrive_expect_tx(qfull, tiles * C::HALVES * qbytes);
+            for (int t = 0; t < tiles; ++t)
+                for (int h = 0; h < C::HALVES; ++h)
+                    tma_load_4d(smem_u32(smem) + t * C::TILE + h * kHalf, &tm_q, qfull, h * 64, 0,
+                                hk, (2 * pair + t) * tokens);
+        }
+        const int per = kKeys / a.page_size;  // pages per tile
+        bool bad = false;
+        int issued = 0;
+        for (int x = 0; x < 2 * n; ++x) {  // K and V tiles in turn
+            const int s = x % C::NS, use = x / C::NS;
+            const int key = lo + (x >> 1) * kKeys;
+            // a page per lane; one that does not exist reads as zeros past the last page
+            int page = a.pages;
+            if (lane < per && key + lane * a.page_size < hi) {
+                page = a.prefix_table[(key >> a.page_shift) + lane];
+                if (page < 0 || page >= a.pages) {
+                    page = a.pages;
+                    bad = true;
+                }
+            }
+            bool ok = true;
+            if (use > 0 && lane == 0)
+                ok = mbar_wait(&empty[s], (use & 1) ^ 1, abort_flag, a.wait_limit);
+            if (!__all_sync(~0u, ok)) {
+                if (lane == 0) give_up();
+                break;
+            }
+            if (x == 2 * a.withhold_tile) break;  // test only: this tile never comes
+            if (lane == 0) mbar_arrive_expect_tx(&full[s], C::TILE);
+            __syncwarp();
+            const uint32_t dst = kv + s * C::TILE;
+            if (lane < per)
+                for (int h = 0; h < C::HALVES; ++h)
+                    tma_load_4d(dst + h * kHalf + lane * a.page_size * 128, x & 1 ? &tm_v : &tm_k,
+                                &full[s], h * 64, 0, hk, page);
+            issued = x + 1;
+        }
+        if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
+        // nothing may be in flight when the CTA ends: the last use of every slot has landed
+        if (lane == 0) {
+            for (int x = max(0, issued - C::NS); x < issued; ++x)
+                mbar_wait(&full[x % C::NS], (x / C::NS) & 1, nullptr, 1ll << 28);
+            mbar_wait(qfull, 0, nullptr, 1ll << 28);
+        }
+        __syncwarp();
+    } else if (warp == 8) {
+        // ------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            const uint32_t id_s = instr_desc(Elem<T>::FMT, 128, kKeys);
+            const uint32_t id_o = instr_desc(Elem<T>::FMT, 128, D) | (1u << 16);  // B is MN-major
+            auto wait = [&](uint64_t* bar, uint32_t parity) {
+                return mbar_wait(bar, parity, abort_flag, a.wait_limit);
+            };
+            auto tile_of = [&](int s, int i) { return solo ? 2 * i + s : i; };
+            auto count = [&](int s) { return solo ? (n + 1 - s) / 2 : n; };
+            auto last_use = [&](int s) { return solo || s == 1; };
+            // S of stream s, its i-th tile
+            auto qk = [&](int s, int i) {
+                const int x = 2 * tile_of(s, i);
+                if (!wait(&full[x % C::NS], (x / C::NS) & 1)) return false;
+                tc_fence_after();
+                const uint32_t q = smem_u32(smem) + (solo ? 0 : s) * C::TILE;
+                const uint32_t k = kv + (x % C::NS) * C::TILE;
+#pragma unroll
+                for (int d = 0; d < D / 16; ++d) {
+                    const uint32_t off = (d / 4) * kHalf + (d % 4) * 32;
+                    mma_bf16(tmem + s * kKeys, smem_desc(q + off, 128), smem_desc(k + off, 128),
+                             id_s, d > 0);
+                }
+                mma_commit(&sfull[s]);
+                if (last_use(s)) mma_commit(&empty[x % C::NS]);
+                return true;
+            };
+            bool ok = wait(qfull, 0);
+            for (int s = 0; s < 2 && ok; ++s)
+                if (count(s) > 0) ok = qk(s, 0);
+            const int most = count(0);
+            for (int i = 0; i < most && ok; ++i) {
+                for (int s = 0; s < 2 && ok; ++s) {
+                    if (i >= count(s)) continue;
+                    const int x = 2 * tile_of(s, i) + 1;
+                    if (!wait(&pfull[s], i & 1) || !wait(&full[x % C::NS], (x / C::NS) & 1)) {
+                        ok = false;
+                        break;
+                    }
+                    tc_fence_after();
+                    const uint32_t v = kv + (x % C::NS) * C::TILE;
+#pragma unroll
+                    for (int k = 0; k < kKeys / 16; ++k)
+                        mma_ts(tmem + 256 + s * 128, tmem + s * kKeys + k * 8,
+                               v_desc(v + k * 2048), id_o, i > 0 || k > 0);
+                    mma_commit(&pvdone[s]);
+                    if (last_use(s)) mma_commit(&empty[x % C::NS]);
+                    if (i + 1 < count(s))
+                        // the next S overwrites this P, which the product above reads
+                        ok = wait(&pvdone[s], i & 1) && qk(s, i + 1);
+                }
+            }
+            if (!ok) give_up();
+            mma_commit(done);  // nothing may be in flight when TMEM is freed
+            mbar_wait(done, 0, nullptr, 1ll << 28);
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------- softmax, one thread per row
+        const int s = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t ts = tmem + lanes + s * kKeys, to = tmem + lanes + 256 + s * 128;
+        const int tile = 2 * pair + (solo ? 0 : s);
+        const int bt = tile * tokens + row / a.G;
+        const bool live = row < tokens * a.G && bt < a.B * a.Q;
+        const int mine = solo ? (n + 1 - s) / 2 : n;
+        float m = -INFINITY, l = 0.f;
+        bool ok = true;
+        for (int i = 0; i < mine; ++i) {
+            const int t = solo ? 2 * i + s : i;
+            ok = __all_sync(~0u, mbar_wait(&sfull[s], i & 1, abort_flag, a.wait_limit));
+            if (!ok) break;
+            tc_fence_after();
+            float z[kKeys];
+#pragma unroll
+            for (int c = 0; c < 4; ++c) tmem_ld32x32b<32>(ts + c * 32, z + c * 32);
+            tmem_ld_wait();
+            const int valid = hi - lo - t * kKeys;  // keys of this tile
+            float scale = a.scale_log2;
+            if (valid < kKeys || scale < 0.f) {  // uniform; the maximum below wants scale >= 0
+#pragma unroll
+                for (int c = 0; c < kKeys; ++c) z[c] = c < valid ? z[c] * scale : -INFINITY;
+                scale = 1.f;
+            }
+            float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+            for (int c = 0; c < kKeys; ++c)
+                x[c & 3] = fmaxf(x[c & 3], z[c]);
+            const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
+            if (i == 0) {
+                m = top == -INFINITY ? 0.f : top;
+            } else if (__any_sync(~0u, live && top > m + kRenew)) {
+                const float next = live ? fmaxf(m, top) : m;
+                const float f = ex2(m - next);
+                m = next;
+                l *= f;
+                // O is at rest: S of this tile was issued after the last P V had completed
+                tc_fence_after();
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    uint32_t r[32];
+                    tmem_ld32x32b<32>(to + c * 32, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(o[j] * f);
+                    tmem_st32(to + c * 32, r);
+                }
+            }
+            float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    const float p0 = ex2(fmaf(z[h * 64 + 2 * c], scale, -m));
+                    const float p1 = ex2(fmaf(z[h * 64 + 2 * c + 1], scale, -m));
+                    sum[(2 * c) & 3] += p0;
+                    sum[(2 * c + 1) & 3] += p1;
+                    p[c] = Elem<T>::pack(p0, p1);
+                }
+                tmem_st32(ts + h * 32, p);
+            }
+            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+            if (valid < kKeys) {
+                // V's rows past the end hold anything; their weights are 0, so they must be finite
+                const int v = 2 * t + 1;
+                ok = __all_sync(~0u, mbar_wait(&full[v % C::NS], (v / C::NS) & 1, abort_flag,
+                                               a.wait_limit));
+                if (!ok) break;
+                uint8_t* vt = smem + C::OFF_KV + (v % C::NS) * C::TILE;
+                for (int c = row; c < (kKeys - valid) * 8 * C::HALVES; c += 128) {
+                    const int h = c / ((kKeys - valid) * 8), at = c % ((kKeys - valid) * 8);
+                    *reinterpret_cast<uint4*>(vt + h * kHalf + valid * 128 + at * 16) =
+                        make_uint4(0u, 0u, 0u, 0u);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+            }
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[s]);
+        }
+        if (mine > 0 && ok)
+            ok = __all_sync(~0u, mbar_wait(&pvdone[s], (mine - 1) & 1, abort_flag, a.wait_limit));
+        if (!ok && lane == 0) give_up();
+        tc_fence_after();
+        const int total_splits = a.prefix_splits + a.private_splits;
+        float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
+        float4* join = reinterpret_cast<float4*>(smem + C::OFF_KV);  // [D / 4][128]
+        if (solo && s == 1) {
+            // hand O over to stream 0, which waits until both streams' MMAs are done
+            named_bar_sync(1, 256);
+            if (mine > 0 && ok) {
+#pragma unroll
+                for (int c = 0; c < D / 32; ++c) {
+                    float o[32];
+                    tmem_ld32x32b<32>(to + c * 32, o);
+                    tmem_ld_wait();
+#pragma unroll
+                    for (int j = 0; j < 8; ++j)
+                        join[(c * 8 + j) * 128 + row] =
+                            make_float4(o[4 * j], o[4 * j + 1], o[4 * j + 2], o[4 * j + 3]);
+                }
+            }
+            ml[row] = mine > 0 && ok ? m : -INFINITY;
+            ml[128 + row] = mine > 0 && ok ? l : 0.f;
+            named_bar_sync(1, 256);
+        } else {
+            float f0 = 1.f, f1 = 0.f;
+            float top = m;
+            if (solo) {
+                named_bar_sync(1, 256);
+                named_bar_sync(1, 256);
+                top = fmaxf(m, ml[row]);
+                f0 = ex2(m - top);
+                f1 = ex2(ml[row] - top);
+                l = l * f0 + ml[128 + row] * f1;
+            }
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            f0 *= inv;
+            f1 *= inv;
+            const long long at =
+                ((long long)bt * a.Hq + hk * a.G + row % a.G) * total_splits + split;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                float o[32];
+                tmem_ld32x32b<32>(to + c * 32, o);
+                tmem_ld_wait();
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    float4 v = make_float4(o[4 * j] * f0, o[4 * j + 1] * f0, o[4 * j + 2] * f0,
+                                           o[4 * j + 3] * f0);
+                    if (solo && f1 > 0.f) {
+                        const float4 w = join[(c * 8 + j) * 128 + row];
+                        v.x += w.x * f1;
+                        v.y += w.y * f1;
+                        v.z += w.z * f1;
+                        v.w += w.w * f1;
+                    }
+                    if (live)
+                        *reinterpret_cast<float4*>(a.part + at * D + c * 32 + j * 4) = v;
+                }
+            }
+            if (live) a.part_lse[at] = l > 0.f ? top + log2f(l) : -INFINITY;
+        }
+        tc_fence_before();
+    }
+    __syncthreads();
+    if (warp == 8) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// 4D map of 16-bit elements: box [64, rows of one page or token group ...], 128-byte swizzle.
+CUresult make_map_4d(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
+                     const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return CUDA_ERROR_NOT_SUPPORTED;
+    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
+    const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
+    const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
+    const cuuint32_t one[4] = {1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), d, st, b, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+template <typename T, int D>
+cudaError_t launch_prefix_t(const AttnArgs& a, cudaStream_t s) {
+    using C = PrefixCfg<D>;
+    CUtensorMap tq, tk, tv;
+    const int tokens = kKeys / a.G;
+    const uint64_t row = D * 2;
+    const uint64_t qd[4] = {(uint64_t)D, (uint64_t)a.G, (uint64_t)a.Hkv, (uint64_t)a.B * a.Q};
+    const uint64_t qs[3] = {row, row * a.G, row * a.Hq};
+    const uint32_t qb[4] = {64, (uint32_t)a.G, 1, (uint32_t)tokens};
+    const uint64_t kd[4] = {(uint64_t)D, (uint64_t)a.page_size, (uint64_t)a.Hkv, (uint64_t)a.pages};
+    const uint64_t ks[3] = {row, row * a.page_size, row * a.page_size * a.Hkv};
+    const uint32_t kb[4] = {64, (uint32_t)a.page_size, 1, 1};
+    if (make_map_4d(&tq, a.q, qd, qs, qb) != CUDA_SUCCESS ||
+        make_map_4d(&tk, a.k, kd, ks, kb) != CUDA_SUCCESS ||
+        make_map_4d(&tv, a.v, kd, ks, kb) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    static std::once_flag once;
+    static cudaError_t attr_err = cudaSuccess;
+    std::call_once(once, [] {
+        attr_err = cudaFuncSetAttribute(attn_prefix_kernel<T, D>,
+                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    });
+    if (attr_err != cudaSuccess) return attr_err;
+    const int ntiles = (a.B * a.Q + tokens - 1) / tokens;
+    const long long grid = (long long)a.prefix_splits * ((ntiles + 1) / 2) * a.Hkv;
+    if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
+    return launch_k(attn_prefix_kernel<T, D>, dim3((unsigned)grid), dim3(kPrefixThreads), C::SMEM,
+                    s, false, tq, tk, tv, a);
+}
+
+}  // namespace
+
+cudaError_t launch_prefix_parts(const AttnArgs& a, idx_dtype dt, cudaStream_t s) {
+    if (dt == IDX_BF16)
+        return a.D == 128 ? launch_prefix_t<__nv_bfloat16, 128>(a, s)
+                          : launch_prefix_t<__nv_bfloat16, 64>(a, s);
+    return a.D == 128 ? launch_prefix_t<__half, 128>(a, s) : launch_prefix_t<__half, 64>(a, s);
+}
+
+}  // namespace idx

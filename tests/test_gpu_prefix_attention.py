@@ -270,3 +270,16 @@ def test_refusals(idx):
         with pytest.raises(idx.IdxError) as e:
             run(**kw)
         assert e.value.code == code, (kw.keys(), e.value)
+
+
+@pytest.mark.parametrize("B", [3, 90])
+def test_a_wait_that_runs_out_ends_the_prefix_kernel(idx, B):
+    """Key tile 1 of every part of the prefix is withheld (60000 keys: several tiles a part):
+    the kernel gives up, raises the timeout bit and leaves nothing in flight; the next call
+    gives what the one before gave."""
+    s = make([20] * B, 1, 4, 1, 128, 60000, 64, BF16, seed=12)
+    want = call(idx, s)
+    stats = idx.Stats(torch.device(DEV))
+    call(idx, s, stats, options=idx.Options(test_stall_us=2000))
+    assert stats.read()["status"] & 1
+    assert all(torch.equal(x, y) for x, y in zip(call(idx, s), want))
