@@ -36,7 +36,7 @@ namespace {
 constexpr int kKeys = 128;                 // keys per tile
 constexpr int kHalf = 128 * 128;           // 128 rows of 64 16-bit elements, 128-byte swizzled
 constexpr int kSoftmaxWarps = 8;
-constexpr int kPrefixThreads = (kSoftmaxWarps + 2) * 32;
+constexpr int kPrefixThreads = (kSoftmaxWarps + 4) * 32;  // warps 10 and 11 only give registers
 constexpr float kRenew = 8.f;
 
 template <int D> struct PrefixCfg {
@@ -45,7 +45,7 @@ template <int D> struct PrefixCfg {
     static constexpr int NS = D == 128 ? 5 : 8;      // ring slots
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
-    static constexpr int NBAR = 1 + 2 * NS + 7;
+    static constexpr int NBAR = 1 + 2 * NS + 9;
     static constexpr int OFF_CTL = OFF_BAR + NBAR * 8;   // [0] TMEM base, [1] abort flag
     static constexpr int OFF_ML = OFF_CTL + 16;          // the odd stream's m and l per row
     static constexpr int SMEM = OFF_ML + 128 * 8 + 1024;
@@ -54,10 +54,50 @@ static_assert(PrefixCfg<128>::SMEM <= 227 * 1024 && PrefixCfg<64>::SMEM <= 227 *
 // the odd stream's O is joined through the ring
 static_assert(128 * 128 * 4 <= PrefixCfg<128>::NS * PrefixCfg<128>::TILE, "");
 
+// Registers: the launch gives 384 x 168; the softmax warps (a row of S each thread) take
+// 256 x 208, the others keep 128 x 80.
+IDX_DEVI void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 208;" ::: "memory"); }
+IDX_DEVI void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 80;" ::: "memory"); }
+static_assert(256 * 208 + 128 * 80 <= 384 * 168, "");
+
+// Two fp32 operations at once.
+IDX_DEVI float2 fma2(float2 a, float2 b, float2 c) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return d;
+}
+IDX_DEVI float2 add2(float2 a, float2 b) {
+    float2 d;
+    asm("{\n\t.reg .b64 x, y, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(d.x), "=f"(d.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return d;
+}
+IDX_DEVI float max3(float a, float b, float c) {
+    float d;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
+
 IDX_DEVI float ex2(float x) {
     float y;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
     return y;
+}
+
+// One lane of a converged warp.
+IDX_DEVI bool elect_one() {
+    uint32_t p;
+    asm volatile(
+        "{\n\t.reg .pred q;\n\telect.sync _|q, 0xffffffff;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(p));
+    return p != 0;
 }
 
 IDX_DEVI void tma_load_4d(uint32_t dst, const void* tmap, uint64_t* bar, int c0, int c1, int c2,
@@ -131,8 +171,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint64_t* full = qfull + 1;
     uint64_t* empty = full + C::NS;
     uint64_t* sfull = empty + C::NS;  // per stream: S is there
-    uint64_t* pfull = sfull + 2;      // P is there (and S has been read)
-    uint64_t* pvdone = pfull + 2;     // O has the tile's P V
+    uint64_t* pfull = sfull + 2;      // half of P is there (and S has been read)
+    uint64_t* pvdone = pfull + 4;     // O has the tile's P V
     uint64_t* done = pvdone + 2;      // every MMA of the CTA
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
@@ -156,7 +196,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[i], 4);
+            mbar_init(&pfull[2 * i], 4);
+            mbar_init(&pfull[2 * i + 1], 4);
             mbar_init(&pvdone[i], 1);
         }
         mbar_init(done, 1);
@@ -177,119 +218,142 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         raise_status(a.d_status, IDX_DEV_TIMEOUT);
     };
 
-    if (warp == 9) {
-        // ---------------------------------------------------- TMA producer
-        const int qbytes = tokens * a.G * 128;
-        if (lane == 0) {
-            prefetch_tmap(&tm_q);
-            prefetch_tmap(&tm_k);
-            prefetch_tmap(&tm_v);
-            const int tiles = solo ? 1 : 2;
-            mbar_arrive_expect_tx(qfull, tiles * C::HALVES * qbytes);
-            for (int t = 0; t < tiles; ++t)
-                for (int h = 0; h < C::HALVES; ++h)
-                    tma_load_4d(smem_u32(smem) + t * C::TILE + h * kHalf, &tm_q, qfull, h * 64, 0,
-                                hk, (2 * pair + t) * tokens);
-        }
-        const int per = kKeys / a.page_size;  // pages per tile
-        bool bad = false;
-        int issued = 0;
-        for (int x = 0; x < 2 * n; ++x) {  // K and V tiles in turn
-            const int s = x % C::NS, use = x / C::NS;
-            const int key = lo + (x >> 1) * kKeys;
-            // a page per lane; one that does not exist reads as zeros past the last page
-            int page = a.pages;
-            if (lane < per && key + lane * a.page_size < hi) {
-                page = a.prefix_table[(key >> a.page_shift) + lane];
-                if (page < 0 || page >= a.pages) {
-                    page = a.pages;
-                    bad = true;
+    if (warp >= 8) {
+        regs_less();
+        if (warp == 9) {
+            // ---------------------------------------------------- TMA producer
+            const int qbytes = tokens * a.G * 128;
+            if (lane == 0) {
+                prefetch_tmap(&tm_q);
+                prefetch_tmap(&tm_k);
+                prefetch_tmap(&tm_v);
+                const int tiles = solo ? 1 : 2;
+                mbar_arrive_expect_tx(qfull, tiles * C::HALVES * qbytes);
+                for (int t = 0; t < tiles; ++t)
+                    for (int h = 0; h < C::HALVES; ++h)
+                        tma_load_4d(smem_u32(smem) + t * C::TILE + h * kHalf, &tm_q, qfull, h * 64, 0,
+                                    hk, (2 * pair + t) * tokens);
+            }
+            const int per = kKeys / a.page_size;  // pages per tile
+            bool bad = false;
+            int issued = 0;
+            for (int x = 0; x < 2 * n; ++x) {  // K and V tiles in turn
+                const int s = x % C::NS, use = x / C::NS;
+                const int key = lo + (x >> 1) * kKeys;
+                // a page per lane; one that does not exist reads as zeros past the last page
+                int page = a.pages;
+                if (lane < per && key + lane * a.page_size < hi) {
+                    page = a.prefix_table[(key >> a.page_shift) + lane];
+                    if (page < 0 || page >= a.pages) {
+                        page = a.pages;
+                        bad = true;
+                    }
                 }
+                bool ok = true;
+                if (use > 0 && lane == 0)
+                    ok = mbar_wait(&empty[s], (use & 1) ^ 1, abort_flag, a.wait_limit);
+                if (!__all_sync(~0u, ok)) {
+                    if (lane == 0) give_up();
+                    break;
+                }
+                if (x == 2 * a.withhold_tile) break;  // test only: this tile never comes
+                if (lane == 0) mbar_arrive_expect_tx(&full[s], C::TILE);
+                __syncwarp();
+                const uint32_t dst = kv + s * C::TILE;
+                if (lane < per)
+                    for (int h = 0; h < C::HALVES; ++h)
+                        tma_load_4d(dst + h * kHalf + lane * a.page_size * 128, x & 1 ? &tm_v : &tm_k,
+                                    &full[s], h * 64, 0, hk, page);
+                issued = x + 1;
             }
-            bool ok = true;
-            if (use > 0 && lane == 0)
-                ok = mbar_wait(&empty[s], (use & 1) ^ 1, abort_flag, a.wait_limit);
-            if (!__all_sync(~0u, ok)) {
-                if (lane == 0) give_up();
-                break;
+            if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
+            // nothing may be in flight when the CTA ends: the last use of every slot has landed
+            if (lane == 0) {
+                for (int x = max(0, issued - C::NS); x < issued; ++x)
+                    mbar_wait(&full[x % C::NS], (x / C::NS) & 1, nullptr, 1ll << 28);
+                mbar_wait(qfull, 0, nullptr, 1ll << 28);
             }
-            if (x == 2 * a.withhold_tile) break;  // test only: this tile never comes
-            if (lane == 0) mbar_arrive_expect_tx(&full[s], C::TILE);
             __syncwarp();
-            const uint32_t dst = kv + s * C::TILE;
-            if (lane < per)
-                for (int h = 0; h < C::HALVES; ++h)
-                    tma_load_4d(dst + h * kHalf + lane * a.page_size * 128, x & 1 ? &tm_v : &tm_k,
-                                &full[s], h * 64, 0, hk, page);
-            issued = x + 1;
-        }
-        if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
-        // nothing may be in flight when the CTA ends: the last use of every slot has landed
-        if (lane == 0) {
-            for (int x = max(0, issued - C::NS); x < issued; ++x)
-                mbar_wait(&full[x % C::NS], (x / C::NS) & 1, nullptr, 1ll << 28);
-            mbar_wait(qfull, 0, nullptr, 1ll << 28);
-        }
-        __syncwarp();
-    } else if (warp == 8) {
-        // ------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        } else if (warp == 8) {
+            // -------------------------------------------------- MMA issuer
+            // The whole warp runs the control flow, so that descriptors stay in uniform
+            // registers; one elected lane issues (issued from a plain `lane == 0` branch
+            // an MMA took about 100 clocks instead of the 64 of its arithmetic).
             const uint32_t id_s = instr_desc(Elem<T>::FMT, 128, kKeys);
             const uint32_t id_o = instr_desc(Elem<T>::FMT, 128, D) | (1u << 16);  // B is MN-major
             auto wait = [&](uint64_t* bar, uint32_t parity) {
-                return mbar_wait(bar, parity, abort_flag, a.wait_limit);
+                return __all_sync(~0u, mbar_wait(bar, parity, abort_flag, a.wait_limit));
             };
             auto tile_of = [&](int s, int i) { return solo ? 2 * i + s : i; };
             auto count = [&](int s) { return solo ? (n + 1 - s) / 2 : n; };
             auto last_use = [&](int s) { return solo || s == 1; };
-            // S of stream s, its i-th tile
+            auto landed = [&](int x) { return wait(&full[x % C::NS], (x / C::NS) & 1); };
+            // S of stream s, its i-th tile (K has landed)
             auto qk = [&](int s, int i) {
                 const int x = 2 * tile_of(s, i);
-                if (!wait(&full[x % C::NS], (x / C::NS) & 1)) return false;
                 tc_fence_after();
-                const uint32_t q = smem_u32(smem) + (solo ? 0 : s) * C::TILE;
-                const uint32_t k = kv + (x % C::NS) * C::TILE;
+                const uint64_t q = smem_desc(smem_u32(smem) + (solo ? 0 : s) * C::TILE, 128);
+                const uint64_t k = smem_desc(kv + (x % C::NS) * C::TILE, 128);
+                if (elect_one()) {
 #pragma unroll
-                for (int d = 0; d < D / 16; ++d) {
-                    const uint32_t off = (d / 4) * kHalf + (d % 4) * 32;
-                    mma_bf16(tmem + s * kKeys, smem_desc(q + off, 128), smem_desc(k + off, 128),
-                             id_s, d > 0);
+                    for (int d = 0; d < D / 16; ++d) {
+                        const uint32_t off = ((d / 4) * kHalf + (d % 4) * 32) >> 4;
+                        mma_bf16(tmem + s * kKeys, q + off, k + off, id_s, d > 0);
+                    }
+                    mma_commit(&sfull[s]);
+                    if (last_use(s)) mma_commit(&empty[x % C::NS]);
                 }
-                mma_commit(&sfull[s]);
-                if (last_use(s)) mma_commit(&empty[x % C::NS]);
-                return true;
+                __syncwarp();
+            };
+            // half h of the keys of O += P V
+            auto pv = [&](int s, int i, int h) {
+                const int x = 2 * tile_of(s, i) + 1;
+                tc_fence_after();
+                const uint64_t v = v_desc(kv + (x % C::NS) * C::TILE);
+                if (elect_one()) {
+#pragma unroll
+                    for (int k = 0; k < kKeys / 32; ++k) {
+                        const int kk = h * (kKeys / 32) + k;
+                        mma_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8,
+                               v + kk * (2048 >> 4), id_o, i > 0 || kk > 0);
+                    }
+                    if (h == 1) {
+                        mma_commit(&pvdone[s]);
+                        if (last_use(s)) mma_commit(&empty[x % C::NS]);
+                    }
+                }
+                __syncwarp();
             };
             bool ok = wait(qfull, 0);
             for (int s = 0; s < 2 && ok; ++s)
-                if (count(s) > 0) ok = qk(s, 0);
+                if (count(s) > 0 && (ok = landed(2 * tile_of(s, 0)))) qk(s, 0);
             const int most = count(0);
             for (int i = 0; i < most && ok; ++i) {
                 for (int s = 0; s < 2 && ok; ++s) {
                     if (i >= count(s)) continue;
-                    const int x = 2 * tile_of(s, i) + 1;
-                    if (!wait(&pfull[s], i & 1) || !wait(&full[x % C::NS], (x / C::NS) & 1)) {
-                        ok = false;
-                        break;
-                    }
-                    tc_fence_after();
-                    const uint32_t v = kv + (x % C::NS) * C::TILE;
-#pragma unroll
-                    for (int k = 0; k < kKeys / 16; ++k)
-                        mma_ts(tmem + 256 + s * 128, tmem + s * kKeys + k * 8,
-                               v_desc(v + k * 2048), id_o, i > 0 || k > 0);
-                    mma_commit(&pvdone[s]);
-                    if (last_use(s)) mma_commit(&empty[x % C::NS]);
-                    if (i + 1 < count(s))
+                    // what has long landed is waited for first: a wait costs over 100 clocks
+                    // even then, and from P on every one of them is the tensor core's
+                    ok = landed(2 * tile_of(s, i) + 1) && wait(&pfull[2 * s], i & 1);
+                    if (!ok) break;
+                    pv(s, i, 0);
+                    if (!(ok = wait(&pfull[2 * s + 1], i & 1))) break;
+                    pv(s, i, 1);
+                    if (i + 1 < count(s)) {
                         // the next S overwrites this P, which the product above reads
-                        ok = wait(&pvdone[s], i & 1) && qk(s, i + 1);
+                        ok = landed(2 * tile_of(s, i + 1)) && wait(&pvdone[s], i & 1);
+                        if (ok) qk(s, i + 1);
+                    }
                 }
             }
-            if (!ok) give_up();
-            mma_commit(done);  // nothing may be in flight when TMEM is freed
-            mbar_wait(done, 0, nullptr, 1ll << 28);
+            if (!ok && lane == 0) give_up();
+            if (elect_one()) {
+                mma_commit(done);  // nothing may be in flight when TMEM is freed
+                mbar_wait(done, 0, nullptr, 1ll << 28);
+            }
+            __syncwarp();
         }
-        __syncwarp();
     } else {
+        regs_more();
         // --------------------------------------------- softmax, one thread per row
         const int s = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -318,8 +382,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < kKeys; ++c)
-                x[c & 3] = fmaxf(x[c & 3], z[c]);
+            for (int c = 0; c < kKeys; c += 8)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) x[j] = max3(x[j], z[c + 2 * j], z[c + 2 * j + 1]);
             const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
             if (i == 0) {
                 m = top == -INFINITY ? 0.f : top;
@@ -341,21 +406,6 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tmem_st32(to + c * 32, r);
                 }
             }
-            float sum[4] = {0.f, 0.f, 0.f, 0.f};
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    const float p0 = ex2(fmaf(z[h * 64 + 2 * c], scale, -m));
-                    const float p1 = ex2(fmaf(z[h * 64 + 2 * c + 1], scale, -m));
-                    sum[(2 * c) & 3] += p0;
-                    sum[(2 * c + 1) & 3] += p1;
-                    p[c] = Elem<T>::pack(p0, p1);
-                }
-                tmem_st32(ts + h * 32, p);
-            }
-            l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
             if (valid < kKeys) {
                 // V's rows past the end hold anything; their weights are 0, so they must be finite
                 const int v = 2 * t + 1;
@@ -370,10 +420,28 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
-            tmem_st_wait();
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&pfull[s]);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+            const float2 scale2 = make_float2(scale, scale), less_m = make_float2(-m, -m);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t p[32];
+#pragma unroll
+                for (int c = 0; c < 32; ++c) {
+                    float2 e = fma2(make_float2(z[h * 64 + 2 * c], z[h * 64 + 2 * c + 1]), scale2,
+                                    less_m);
+                    e.x = ex2(e.x);
+                    e.y = ex2(e.y);
+                    sum[c & 1] = add2(sum[c & 1], e);
+                    p[c] = Elem<T>::pack(e.x, e.y);
+                }
+                tmem_st32(ts + h * 32, p);
+                tmem_st_wait();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&pfull[2 * s + h]);  // the product may start on it
+            }
+            const float2 both = add2(sum[0], sum[1]);
+            l += both.x + both.y;
         }
         if (mine > 0 && ok)
             ok = __all_sync(~0u, mbar_wait(&pvdone[s], (mine - 1) & 1, abort_flag, a.wait_limit));
