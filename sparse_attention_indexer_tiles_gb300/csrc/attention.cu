@@ -23,7 +23,7 @@ namespace {
 
 constexpr int kPartWarps = 4;
 constexpr int kStep = 16;    // keys a warp takes at a time; pages hold at least as many
-constexpr int kStages = 4;   // steps in flight per warp
+constexpr int kStages = 2;   // steps in flight per warp
 
 IDX_DEVI float exp2_approx(float x) {
     float y;
@@ -65,7 +65,6 @@ template <> struct Mma<__nv_bfloat16> {
         const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
-    static IDX_DEVI __nv_bfloat16 one(float v) { return __float2bfloat16_rn(v); }
 };
 template <> struct Mma<__half> {
     static IDX_DEVI void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -79,7 +78,6 @@ template <> struct Mma<__half> {
         const __half2 v = __floats2half2_rn(lo, hi);
         return *reinterpret_cast<const uint32_t*>(&v);
     }
-    static IDX_DEVI __half one(float v) { return __float2half_rn(v); }
 };
 
 // Shared memory of a block: per warp a ring of kStages steps of K and V, rows of D
@@ -335,62 +333,97 @@ IDX_DEVI float join_lse(const float* part_lse, int splits, int lane) {
     return m + log2f(l);
 }
 
-constexpr int kJoinWarps = 4;
+constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
+constexpr int kSlotsPerThread = 4, kWeightSlots = kJoinThreads * kSlotsPerThread;
 
-// One warp per query row: the join of its parts.
+// The join of a query row's parts, one warp per row: lane l holds D / 32 columns.
 template <typename T, int D>
-__global__ void __launch_bounds__(kJoinWarps * 32) attn_join_kernel(AttnArgs a) {
-    const int lane = threadIdx.x & 31;
-    const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-    if (row >= (long long)a.B * a.Q * a.Hq) return;
+IDX_DEVI void join_row(const AttnArgs& a, long long row, int lane) {
+    constexpr int W = D / 32;
     const int splits = a.prefix_splits + a.private_splits;
     const float* pl = a.part_lse + row * splits;
     const float lse = join_lse(pl, splits, lane);
-    float acc[D / 32];
+    float acc[W];
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) acc[i] = 0.f;
+    for (int i = 0; i < W; ++i) acc[i] = 0.f;
     if (lse != -INFINITY) {
-        const float* part = a.part + row * splits * D;
-        for (int p = 0; p < splits; ++p) {
-            const float f = exp2_approx(pl[p] - lse);
-            if (pl[p] == -INFINITY) continue;  // nothing was written there
+        const float* part = a.part + row * splits * D + lane * W;
+        // four parts at a time, all their loads before the first use; a part without keys
+        // has written nothing and is not read
+        for (int p = 0; p < splits; p += 4) {
+            float f[4], v[4][W];
 #pragma unroll
-            for (int i = 0; i < D / 32; ++i) acc[i] += f * part[(long long)p * D + i * 32 + lane];
+            for (int k = 0; k < 4; ++k) f[k] = p + k < splits ? pl[p + k] : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < W; ++i)
+                    v[k][i] = f[k] != -INFINITY ? part[(long long)(p + k) * D + i] : 0.f;
+#pragma unroll
+            for (int k = 0; k < 4; ++k)
+#pragma unroll
+                for (int i = 0; i < W; ++i) acc[i] = fmaf(exp2_approx(f[k] - lse), v[k][i], acc[i]);
         }
     }
-    T* out = static_cast<T*>(a.out) + row * D;
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D) + lane * (W / 2);
 #pragma unroll
-    for (int i = 0; i < D / 32; ++i) out[i * 32 + lane] = Mma<T>::one(acc[i]);
+    for (int i = 0; i < W / 2; ++i) out[i] = Mma<T>::pack(acc[2 * i], acc[2 * i + 1]);
     if (a.lse && lane == 0) a.lse[row] = lse * 0.6931471805599453f;
 }
 
-constexpr int kWeightSlots = 256;
-
-// One thread per private slot: the weight its key received from the request's rows.
-// blockIdx.x: slots, blockIdx.y: request and key head.
-__global__ void __launch_bounds__(kWeightSlots) attn_weights_kernel(AttnArgs a) {
-    extern __shared__ __align__(16) float row_lse[];
-    const int b = blockIdx.y / a.Hkv, hk = blockIdx.y % a.Hkv;
+// The weight that private slots received from their request's rows: block `u` takes
+// kWeightSlots slots of a request and key head.
+IDX_DEVI void add_weights(const AttnArgs& a, int u, float* row_lse) {
+    const int per = (a.max_len + kWeightSlots - 1) / kWeightSlots;
+    const int bh = u / per, b = bh / a.Hkv, hk = bh % a.Hkv;
     const int n = min(max(a.lens[b], 0), a.max_len);
-    const int first = blockIdx.x * kWeightSlots;
+    const int first = (u % per) * kWeightSlots;
     if (first >= n) return;
     const int rows = a.Q * a.G, splits = a.prefix_splits + a.private_splits;
-    const int lane = threadIdx.x & 31;
-    for (int r = threadIdx.x / 32; r < rows; r += kWeightSlots / 32) {
+    for (int r = threadIdx.x / 32; r < rows; r += kJoinWarps) {
         const long long row = ((long long)b * a.Q + r / a.G) * a.Hq + hk * a.G + r % a.G;
-        const float l = join_lse(a.part_lse + row * splits, splits, lane);
-        if (lane == 0) row_lse[r] = l;
+        const float l = join_lse(a.part_lse + row * splits, splits, threadIdx.x & 31);
+        // a row that sees nothing has logits -inf only: any finite value gives weight 0
+        if ((threadIdx.x & 31) == 0) row_lse[r] = l == -INFINITY ? 0.f : l;
     }
     __syncthreads();
-    const int j = first + (int)threadIdx.x;
-    if (j >= n) return;
-    const long long at = (long long)blockIdx.y * a.slots + j;
-    const float* z = a.logits + (long long)blockIdx.y * rows * a.logit_stride + j;
-    // the newest tokens' slots have gathered nothing yet, whatever the array holds
-    float sum = 0.f;
-    for (int r = 0; r < rows; ++r)
-        if (row_lse[r] != -INFINITY) sum += exp2_approx(z[r * a.logit_stride] - row_lse[r]);
-    a.w_out[at] = (j < n - a.Q ? a.w[at] : 0.f) + sum;
+    const float* z = a.logits + (long long)bh * rows * a.logit_stride;
+    const float* w = a.w + (long long)bh * a.slots;
+    float* w_out = a.w_out + (long long)bh * a.slots;
+    float sum[kSlotsPerThread];
+#pragma unroll
+    for (int k = 0; k < kSlotsPerThread; ++k) {
+        // the newest tokens' slots have gathered nothing yet, whatever the array holds
+        const int j = first + k * kJoinThreads + (int)threadIdx.x;
+        sum[k] = j < n - a.Q ? w[j] : 0.f;
+    }
+#pragma unroll 4
+    for (int r = 0; r < rows; ++r) {
+        const float l = row_lse[r];
+#pragma unroll
+        for (int k = 0; k < kSlotsPerThread; ++k) {
+            const int j = first + k * kJoinThreads + (int)threadIdx.x;
+            if (j < n) sum[k] += exp2_approx(z[r * a.logit_stride + j] - l);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kSlotsPerThread; ++k) {
+        const int j = first + k * kJoinThreads + (int)threadIdx.x;
+        if (j < n) w_out[j] = sum[k];
+    }
+}
+
+// Blocks [0, join_blocks) join the parts of kJoinWarps query rows each, the others add up
+// the weights of the private slots.
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int join_blocks) {
+    __shared__ float row_lse[kAttnMaxTokens * kAttnMaxGroup];
+    if ((int)blockIdx.x < join_blocks) {
+        const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
+        if (row < (long long)a.B * a.Q * a.Hq) join_row<T, D>(a, row, threadIdx.x & 31);
+    } else {
+        add_weights(a, blockIdx.x - join_blocks, row_lse);
+    }
 }
 
 template <typename T, int D>
@@ -411,15 +444,14 @@ cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, cudaStream_t s, int* l
         ++*launched;
     }
     const long long rows = (long long)a.B * a.Q * a.Hq;
-    attn_join_kernel<T, D><<<(unsigned)((rows + kJoinWarps - 1) / kJoinWarps), kJoinWarps * 32, 0, s>>>(a);
+    const long long join_blocks = (rows + kJoinWarps - 1) / kJoinWarps;
+    const long long weight_blocks =
+        a.w_out ? (long long)a.B * a.Hkv * ((a.max_len + kWeightSlots - 1) / kWeightSlots) : 0;
+    if (join_blocks + weight_blocks > 0x7fffffffll) return cudaErrorInvalidValue;
+    attn_join_kernel<T, D><<<(unsigned)(join_blocks + weight_blocks), kJoinThreads, 0, s>>>(
+        a, (int)join_blocks);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     ++*launched;
-    if (a.w_out && a.max_len > 0) {
-        const dim3 grid((a.max_len + kWeightSlots - 1) / kWeightSlots, a.B * a.Hkv);
-        attn_weights_kernel<<<grid, kWeightSlots, a.Q * a.G * sizeof(float), s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
-        ++*launched;
-    }
     return e;
 }
 
@@ -432,8 +464,8 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
     auto cut = [&](long long items, int len, int& splits, int& chunk) {
         splits = chunk = 0;
         if (len <= 0) return;
-        // about four blocks per SM, at least 256 keys each
-        long long want = (4ll * sm_count + items - 1) / items;
+        // about eight blocks per SM, at least 256 keys each
+        long long want = (8ll * sm_count + items - 1) / items;
         const long long most = (len + 255) / 256;
         want = want < most ? want : most;
         chunk = (int)(((len + want - 1) / want + 63) / 64 * 64);

@@ -9,8 +9,8 @@
 //   * two row tiles over the same keys (each K and V tile in shared memory serves both), or
 //   * for a last, odd row tile, the same rows over the even and the odd key tiles, joined
 //     through shared memory at the end.
-// Warp 8 issues the MMAs, warp 9 the TMA copies: K and V tiles of 128 keys through a ring,
-// page by page (each page's rows of a head are contiguous).  P goes back to TMEM over S, in
+// Warps 8 and 10 issue the streams' MMAs, warp 9 the TMA copies: K and V tiles of 128 keys
+// through a ring, page by page (each page's rows of a head are contiguous).  P goes back to TMEM over S, in
 // the tensors' type, and is the A operand of the second product; V is used as it lies in
 // memory (its rows are the product's K axis, so the B operand is MN-major).
 //
@@ -36,7 +36,7 @@ namespace {
 constexpr int kKeys = 128;                 // keys per tile
 constexpr int kHalf = 128 * 128;           // 128 rows of 64 16-bit elements, 128-byte swizzled
 constexpr int kSoftmaxWarps = 8;
-constexpr int kPrefixThreads = (kSoftmaxWarps + 4) * 32;  // warps 10 and 11 only give registers
+constexpr int kPrefixThreads = (kSoftmaxWarps + 4) * 32;  // warp 11 only gives registers
 constexpr float kRenew = 8.f;
 
 template <int D> struct PrefixCfg {
@@ -45,7 +45,7 @@ template <int D> struct PrefixCfg {
     static constexpr int NS = D == 128 ? 5 : 8;      // ring slots
     static constexpr int OFF_KV = 2 * TILE;
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
-    static constexpr int NBAR = 1 + 2 * NS + 9;
+    static constexpr int NBAR = 1 + 2 * NS + 10;
     static constexpr int OFF_CTL = OFF_BAR + NBAR * 8;   // [0] TMEM base, [1] abort flag
     static constexpr int OFF_ML = OFF_CTL + 16;          // the odd stream's m and l per row
     static constexpr int SMEM = OFF_ML + 128 * 8 + 1024;
@@ -173,7 +173,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint64_t* sfull = empty + C::NS;  // per stream: S is there
     uint64_t* pfull = sfull + 2;      // half of P is there (and S has been read)
     uint64_t* pvdone = pfull + 4;     // O has the tile's P V
-    uint64_t* done = pvdone + 2;      // every MMA of the CTA
+    uint64_t* done = pvdone + 2;      // every MMA of the stream
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -188,21 +188,67 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     const int lo = split * a.prefix_chunk, hi = min(a.prefix_len, lo + a.prefix_chunk);
     const int n = (hi - lo + kKeys - 1) / kKeys;  // key tiles, at least one
 
-    if (tid == 0) {
-        mbar_init(qfull, 1);
-        for (int i = 0; i < C::NS; ++i) {
-            mbar_init(&full[i], 1);
-            mbar_init(&empty[i], 1);
+    const uint32_t kv = smem_u32(smem + C::OFF_KV);
+    // K and V tiles in turn (warp 9): a page per lane; one that does not exist reads as zeros
+    // past the last page
+    bool bad = false;
+    const int per = kKeys / a.page_size;  // pages per tile
+    auto page_of = [&](int x) {
+        const int key = lo + (x >> 1) * kKeys + lane * a.page_size;
+        int page = a.pages;
+        if (lane < per && key < hi) {
+            page = a.prefix_table[key >> a.page_shift];
+            if (page < 0 || page >= a.pages) {
+                page = a.pages;
+                bad = true;
+            }
         }
-        for (int i = 0; i < 2; ++i) {
-            mbar_init(&sfull[i], 1);
-            mbar_init(&pfull[2 * i], 4);
-            mbar_init(&pfull[2 * i + 1], 4);
-            mbar_init(&pvdone[i], 1);
+        return page;
+    };
+    auto fetch = [&](int x, int page) {
+        const int slot = x % C::NS;
+        if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::TILE);
+        __syncwarp();
+        if (lane < per)
+            for (int h = 0; h < C::HALVES; ++h)
+                tma_load_4d(kv + slot * C::TILE + h * kHalf + lane * a.page_size * 128,
+                            x & 1 ? &tm_v : &tm_k, &full[slot], h * 64, 0, hk, page);
+    };
+    const int first = a.withhold_tile >= 0 ? min(2 * n, 2 * a.withhold_tile) : 2 * n;  // tiles that come
+    if (warp == 9) {
+        int page[(C::NS + 1) / 2];  // on their way while the barriers are set up
+#pragma unroll
+        for (int i = 0; i < (C::NS + 1) / 2; ++i) page[i] = page_of(2 * i);
+        if (lane == 0) {
+            prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
+            mbar_init(qfull, 1);
+            for (int i = 0; i < C::NS; ++i) {
+                mbar_init(&full[i], 1);
+                mbar_init(&empty[i], solo ? 1 : 2);  // the streams that read a tile
+            }
+            for (int i = 0; i < 2; ++i) {
+                mbar_init(&sfull[i], 1);
+                mbar_init(&pfull[2 * i], 4);
+                mbar_init(&pfull[2 * i + 1], 4);
+                mbar_init(&pvdone[i], 1);
+                mbar_init(&done[i], 1);
+            }
+            *abort_flag = 0;
+            fence_barrier_init();
+            // the first copies do not wait for the rest of the block
+            const int tiles = solo ? 1 : 2;
+            mbar_arrive_expect_tx(qfull, tiles * C::HALVES * tokens * a.G * 128);
+            for (int t = 0; t < tiles; ++t)
+                for (int h = 0; h < C::HALVES; ++h)
+                    tma_load_4d(smem_u32(smem) + t * C::TILE + h * kHalf, &tm_q, qfull, h * 64, 0,
+                                hk, (2 * pair + t) * tokens);
         }
-        mbar_init(done, 1);
-        *abort_flag = 0;
-        fence_barrier_init();
+        __syncwarp();
+#pragma unroll
+        for (int x = 0; x < C::NS; ++x)
+            if (x < first) fetch(x, page[x / 2]);
     }
     if (warp == 8) {
         tmem_alloc(const_cast<uint32_t*>(tslot), 512);
@@ -212,7 +258,6 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     __syncthreads();
     tc_fence_after();
     const uint32_t tmem = *tslot;
-    const uint32_t kv = smem_u32(smem + C::OFF_KV);
     auto give_up = [&] {
         *abort_flag = 1;
         raise_status(a.d_status, IDX_DEV_TIMEOUT);
@@ -222,48 +267,17 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         regs_less();
         if (warp == 9) {
             // ---------------------------------------------------- TMA producer
-            const int qbytes = tokens * a.G * 128;
-            if (lane == 0) {
-                prefetch_tmap(&tm_q);
-                prefetch_tmap(&tm_k);
-                prefetch_tmap(&tm_v);
-                const int tiles = solo ? 1 : 2;
-                mbar_arrive_expect_tx(qfull, tiles * C::HALVES * qbytes);
-                for (int t = 0; t < tiles; ++t)
-                    for (int h = 0; h < C::HALVES; ++h)
-                        tma_load_4d(smem_u32(smem) + t * C::TILE + h * kHalf, &tm_q, qfull, h * 64, 0,
-                                    hk, (2 * pair + t) * tokens);
-            }
-            const int per = kKeys / a.page_size;  // pages per tile
-            bool bad = false;
-            int issued = 0;
-            for (int x = 0; x < 2 * n; ++x) {  // K and V tiles in turn
-                const int s = x % C::NS, use = x / C::NS;
-                const int key = lo + (x >> 1) * kKeys;
-                // a page per lane; one that does not exist reads as zeros past the last page
-                int page = a.pages;
-                if (lane < per && key + lane * a.page_size < hi) {
-                    page = a.prefix_table[(key >> a.page_shift) + lane];
-                    if (page < 0 || page >= a.pages) {
-                        page = a.pages;
-                        bad = true;
-                    }
-                }
+            int issued = min(C::NS, first), page = page_of(issued);
+            for (int x = issued; x < first; ++x) {
+                if (!(x & 1)) page = page_of(x);
                 bool ok = true;
-                if (use > 0 && lane == 0)
-                    ok = mbar_wait(&empty[s], (use & 1) ^ 1, abort_flag, a.wait_limit);
+                if (lane == 0)
+                    ok = mbar_wait(&empty[x % C::NS], ((x / C::NS) & 1) ^ 1, abort_flag, a.wait_limit);
                 if (!__all_sync(~0u, ok)) {
                     if (lane == 0) give_up();
                     break;
                 }
-                if (x == 2 * a.withhold_tile) break;  // test only: this tile never comes
-                if (lane == 0) mbar_arrive_expect_tx(&full[s], C::TILE);
-                __syncwarp();
-                const uint32_t dst = kv + s * C::TILE;
-                if (lane < per)
-                    for (int h = 0; h < C::HALVES; ++h)
-                        tma_load_4d(dst + h * kHalf + lane * a.page_size * 128, x & 1 ? &tm_v : &tm_k,
-                                    &full[s], h * 64, 0, hk, page);
+                fetch(x, page);
                 issued = x + 1;
             }
             if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
@@ -274,81 +288,83 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 mbar_wait(qfull, 0, nullptr, 1ll << 28);
             }
             __syncwarp();
-        } else if (warp == 8) {
-            // -------------------------------------------------- MMA issuer
+        } else if (warp != 11) {
+            // -------------------------------------------------- MMA issuers
+            // One warp per stream: while the tensor core reads its operands an mbarrier
+            // access takes about 140 clocks, and one warp that waited for both streams
+            // was the bottleneck (4200 clocks per pair of tiles against 2048 of MMAs).
             // The whole warp runs the control flow, so that descriptors stay in uniform
-            // registers; one elected lane issues (issued from a plain `lane == 0` branch
-            // an MMA took about 100 clocks instead of the 64 of its arithmetic).
+            // registers, and one elected lane issues.
+            const int s = warp == 10;
             const uint32_t id_s = instr_desc(Elem<T>::FMT, 128, kKeys);
             const uint32_t id_o = instr_desc(Elem<T>::FMT, 128, D) | (1u << 16);  // B is MN-major
+            const uint32_t t_s = tmem + s * kKeys, t_o = tmem + 256 + s * 128;
+            const int mine = solo ? (n + 1 - s) / 2 : n;
             auto wait = [&](uint64_t* bar, uint32_t parity) {
                 return __all_sync(~0u, mbar_wait(bar, parity, abort_flag, a.wait_limit));
             };
-            auto tile_of = [&](int s, int i) { return solo ? 2 * i + s : i; };
-            auto count = [&](int s) { return solo ? (n + 1 - s) / 2 : n; };
-            auto last_use = [&](int s) { return solo || s == 1; };
+            auto tile_of = [&](int i) { return solo ? 2 * i + s : i; };
             auto landed = [&](int x) { return wait(&full[x % C::NS], (x / C::NS) & 1); };
-            // S of stream s, its i-th tile (K has landed)
-            auto qk = [&](int s, int i) {
-                const int x = 2 * tile_of(s, i);
+            const uint64_t q = smem_desc(smem_u32(smem) + (solo ? 0 : s) * C::TILE, 128);
+            // S of the i-th tile (K has landed)
+            auto qk = [&](int i) {
+                const int x = 2 * tile_of(i);
                 tc_fence_after();
-                const uint64_t q = smem_desc(smem_u32(smem) + (solo ? 0 : s) * C::TILE, 128);
                 const uint64_t k = smem_desc(kv + (x % C::NS) * C::TILE, 128);
                 if (elect_one()) {
 #pragma unroll
                     for (int d = 0; d < D / 16; ++d) {
                         const uint32_t off = ((d / 4) * kHalf + (d % 4) * 32) >> 4;
-                        mma_bf16(tmem + s * kKeys, q + off, k + off, id_s, d > 0);
+                        mma_bf16(t_s, q + off, k + off, id_s, d > 0);
                     }
                     mma_commit(&sfull[s]);
-                    if (last_use(s)) mma_commit(&empty[x % C::NS]);
+                    mma_commit(&empty[x % C::NS]);
                 }
                 __syncwarp();
             };
-            // half h of the keys of O += P V
-            auto pv = [&](int s, int i, int h) {
-                const int x = 2 * tile_of(s, i) + 1;
+            // half h of the keys of O += P V (V has landed)
+            auto pv = [&](int i, int h) {
+                const int x = 2 * tile_of(i) + 1;
                 tc_fence_after();
                 const uint64_t v = v_desc(kv + (x % C::NS) * C::TILE);
                 if (elect_one()) {
 #pragma unroll
                     for (int k = 0; k < kKeys / 32; ++k) {
                         const int kk = h * (kKeys / 32) + k;
-                        mma_ts(tmem + 256 + s * 128, tmem + s * kKeys + kk * 8,
-                               v + kk * (2048 >> 4), id_o, i > 0 || kk > 0);
+                        mma_ts(t_o, t_s + kk * 8, v + kk * (2048 >> 4), id_o, i > 0 || kk > 0);
                     }
                     if (h == 1) {
                         mma_commit(&pvdone[s]);
-                        if (last_use(s)) mma_commit(&empty[x % C::NS]);
+                        mma_commit(&empty[x % C::NS]);
                     }
                 }
                 __syncwarp();
             };
-            bool ok = wait(qfull, 0);
-            for (int s = 0; s < 2 && ok; ++s)
-                if (count(s) > 0 && (ok = landed(2 * tile_of(s, 0)))) qk(s, 0);
-            const int most = count(0);
-            for (int i = 0; i < most && ok; ++i) {
-                for (int s = 0; s < 2 && ok; ++s) {
-                    if (i >= count(s)) continue;
-                    // what has long landed is waited for first: a wait costs over 100 clocks
-                    // even then, and from P on every one of them is the tensor core's
-                    ok = landed(2 * tile_of(s, i) + 1) && wait(&pfull[2 * s], i & 1);
-                    if (!ok) break;
-                    pv(s, i, 0);
-                    if (!(ok = wait(&pfull[2 * s + 1], i & 1))) break;
-                    pv(s, i, 1);
-                    if (i + 1 < count(s)) {
-                        // the next S overwrites this P, which the product above reads
-                        ok = landed(2 * tile_of(s, i + 1)) && wait(&pvdone[s], i & 1);
-                        if (ok) qk(s, i + 1);
-                    }
+            bool ok = true;
+            if (mine > 0) {
+                ok = wait(qfull, 0) && landed(2 * tile_of(0));
+                // half a period behind stream 0: one stream's softmax under the other's MMAs
+                // (started together they stay together, 15 % slower)
+                if (ok && s == 1) ok = wait(&pfull[0], 0);
+                if (ok) qk(0);
+            }
+            for (int i = 0; i < mine && ok; ++i) {
+                ok = landed(2 * tile_of(i) + 1) && (i + 1 == mine || landed(2 * tile_of(i + 1))) &&
+                     wait(&pfull[2 * s], i & 1);
+                if (!ok) break;
+                pv(i, 0);
+                if (!(ok = wait(&pfull[2 * s + 1], i & 1))) break;
+                pv(i, 1);
+                if (i + 1 < mine) {
+                    // the next S overwrites this P, which the product above reads
+                    if (!(ok = wait(&pvdone[s], i & 1))) break;
+                    qk(i + 1);
                 }
             }
             if (!ok && lane == 0) give_up();
             if (elect_one()) {
-                mma_commit(done);  // nothing may be in flight when TMEM is freed
-                mbar_wait(done, 0, nullptr, 1ll << 28);
+                mma_commit(&done[s]);  // nothing may be in flight when TMEM is freed
+                mbar_wait(&done[s], 0, nullptr, 1ll << 28);
             }
             __syncwarp();
         }
@@ -482,29 +498,48 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             const float inv = l > 0.f ? 1.f / l : 0.f;
             f0 *= inv;
             f1 *= inv;
-            const long long at =
+            // Rows leave through the stream's own Q tile (its products are done): a thread
+            // holds a row, a warp writes whole rows.  16-byte chunks are xor-ed with the row.
+            constexpr int kCols = C::TILE / (128 * 4), kChunk = kCols / 4;
+            uint8_t* stage = smem + s * C::TILE;
+            const int r0 = row & ~31;
+            const long long part =
                 ((long long)bt * a.Hq + hk * a.G + row % a.G) * total_splits + split;
+            float* const mine_at = live ? a.part + part * D : nullptr;
+            for (int c0 = 0; c0 < D; c0 += kCols) {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c) {
-                float o[32];
-                tmem_ld32x32b<32>(to + c * 32, o);
-                tmem_ld_wait();
+                for (int c = 0; c < kCols; c += 32) {
+                    float o[32];
+                    tmem_ld32x32b<32>(to + c0 + c, o);
+                    tmem_ld_wait();
 #pragma unroll
-                for (int j = 0; j < 8; ++j) {
-                    float4 v = make_float4(o[4 * j] * f0, o[4 * j + 1] * f0, o[4 * j + 2] * f0,
-                                           o[4 * j + 3] * f0);
-                    if (solo && f1 > 0.f) {
-                        const float4 w = join[(c * 8 + j) * 128 + row];
-                        v.x += w.x * f1;
-                        v.y += w.y * f1;
-                        v.z += w.z * f1;
-                        v.w += w.w * f1;
+                    for (int j = 0; j < 8; ++j) {
+                        float4 v = make_float4(o[4 * j] * f0, o[4 * j + 1] * f0, o[4 * j + 2] * f0,
+                                               o[4 * j + 3] * f0);
+                        if (solo && f1 > 0.f) {
+                            const float4 w = join[((c0 + c) / 4 + j) * 128 + row];
+                            v.x += w.x * f1;
+                            v.y += w.y * f1;
+                            v.z += w.z * f1;
+                            v.w += w.w * f1;
+                        }
+                        *reinterpret_cast<float4*>(stage + row * (kCols * 4) +
+                                                   (((c / 4 + j) ^ (row & (kChunk - 1))) * 16)) = v;
                     }
-                    if (live)
-                        *reinterpret_cast<float4*>(a.part + at * D + c * 32 + j * 4) = v;
                 }
+                __syncwarp();
+#pragma unroll
+                for (int k = 0; k < kChunk; ++k) {
+                    const int r = (k * 32 + lane) / kChunk, c = lane % kChunk;
+                    float* to_row = reinterpret_cast<float*>(
+                        __shfl_sync(~0u, reinterpret_cast<unsigned long long>(mine_at), r));
+                    const float4 v = *reinterpret_cast<const float4*>(
+                        stage + (r0 + r) * (kCols * 4) + ((c ^ (r & (kChunk - 1))) * 16));
+                    if (to_row) *reinterpret_cast<float4*>(to_row + c0 + c * 4) = v;
+                }
+                __syncwarp();
             }
-            if (live) a.part_lse[at] = l > 0.f ? top + log2f(l) : -INFINITY;
+            if (live) a.part_lse[part] = l > 0.f ? top + log2f(l) : -INFINITY;
         }
         tc_fence_before();
     }
