@@ -14,6 +14,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <mutex>
+
 #include "attention.cuh"
 #include "common.cuh"
 
@@ -91,6 +93,10 @@ template <int D> constexpr int part_smem() { return kPartWarps * kStages * 2 * k
 template <typename T, int D>
 __global__ void __launch_bounds__(kPartWarps * 32) attn_part_kernel(AttnArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
+    pdl_trigger();
+    // This grid reads nothing that the prefix's writes; one block's wait for it makes the
+    // join's wait for this grid cover both.
+    const bool last = blockIdx.x == 0 && blockIdx.y == 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int split = blockIdx.x % a.private_splits;
     const int hk = blockIdx.x / a.private_splits % a.Hkv;
@@ -113,6 +119,7 @@ __global__ void __launch_bounds__(kPartWarps * 32) attn_part_kernel(AttnArgs a) 
     if (lo >= hi) {  // no keys in this part
         for (int i = tid; i < 16 && rb * 16 + i < rows; i += kPartWarps * 32)
             a.part_lse[query_row(i) * total_splits + slot] = -INFINITY;
+        if (last) pdl_wait();
         return;
     }
     const int r0 = rb * 16 + lane / 4, r1 = r0 + 8;  // this thread's two rows
@@ -317,6 +324,7 @@ __global__ void __launch_bounds__(kPartWarps * 32) attn_part_kernel(AttnArgs a) 
             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
         if (d == 0) a.part_lse[at] = l > 0.f ? m + log2f(l) : -INFINITY;
     }
+    if (last) pdl_wait();
 }
 
 // log2-sum-exp2 of a row's parts: every lane of the warp gets it
@@ -336,10 +344,11 @@ IDX_DEVI float join_lse(const float* part_lse, int splits, int lane) {
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kSlotsPerThread = 4, kWeightSlots = kJoinThreads * kSlotsPerThread;
 
-// The join of a query row's parts, one warp per row: lane l holds D / 32 columns.
-template <typename T, int D>
-IDX_DEVI void join_row(const AttnArgs& a, long long row, int lane) {
-    constexpr int W = D / 32;
+// The join of a query row's parts by WPR warps: lane l holds D / 32 columns, the warps
+// take the parts in turn and add up through shared memory.
+template <typename T, int D, int WPR>
+IDX_DEVI void join_row(const AttnArgs& a, long long row, int lane, int warp, float* sums) {
+    constexpr int W = D / 32, kBatch = WPR == 1 ? 8 : 4;
     const int splits = a.prefix_splits + a.private_splits;
     const float* pl = a.part_lse + row * splits;
     const float lse = join_lse(pl, splits, lane);
@@ -348,22 +357,33 @@ IDX_DEVI void join_row(const AttnArgs& a, long long row, int lane) {
     for (int i = 0; i < W; ++i) acc[i] = 0.f;
     if (lse != -INFINITY) {
         const float* part = a.part + row * splits * D + lane * W;
-        // four parts at a time, all their loads before the first use; a part without keys
-        // has written nothing and is not read
-        for (int p = 0; p < splits; p += 4) {
-            float f[4], v[4][W];
+        // kBatch parts at a time, all their loads before the first use; a part without
+        // keys has written nothing and is not read
+        for (int p = warp; p < splits; p += WPR * kBatch) {
+            float f[kBatch], v[kBatch][W];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) f[k] = p + k < splits ? pl[p + k] : -INFINITY;
+            for (int k = 0; k < kBatch; ++k)
+                f[k] = p + k * WPR < splits ? pl[p + k * WPR] : -INFINITY;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kBatch; ++k)
 #pragma unroll
                 for (int i = 0; i < W; ++i)
-                    v[k][i] = f[k] != -INFINITY ? part[(long long)(p + k) * D + i] : 0.f;
+                    v[k][i] = f[k] != -INFINITY ? part[(long long)(p + k * WPR) * D + i] : 0.f;
 #pragma unroll
-            for (int k = 0; k < 4; ++k)
+            for (int k = 0; k < kBatch; ++k)
 #pragma unroll
                 for (int i = 0; i < W; ++i) acc[i] = fmaf(exp2_approx(f[k] - lse), v[k][i], acc[i]);
         }
+    }
+    if constexpr (WPR > 1) {
+#pragma unroll
+        for (int i = 0; i < W; ++i) sums[warp * D + lane * W + i] = acc[i];
+        __syncthreads();
+        if (warp != 0) return;
+#pragma unroll
+        for (int k = 1; k < WPR; ++k)
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] += sums[k * D + lane * W + i];
     }
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D) + lane * (W / 2);
 #pragma unroll
@@ -413,22 +433,25 @@ IDX_DEVI void add_weights(const AttnArgs& a, int u, float* row_lse) {
     }
 }
 
-// Blocks [0, join_blocks) join the parts of kJoinWarps query rows each, the others add up
+// Blocks [0, join_blocks) join the parts of query rows (WPR warps each), the others add up
 // the weights of the private slots.
-template <typename T, int D>
+template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int join_blocks) {
-    __shared__ float row_lse[kAttnMaxTokens * kAttnMaxGroup];
+    __shared__ float scratch[kAttnMaxTokens * kAttnMaxGroup];
+    pdl_wait();
     if ((int)blockIdx.x < join_blocks) {
-        const long long row = (long long)blockIdx.x * kJoinWarps + (threadIdx.x >> 5);
-        if (row < (long long)a.B * a.Q * a.Hq) join_row<T, D>(a, row, threadIdx.x & 31);
+        const int warp = threadIdx.x >> 5;
+        const long long row = (long long)blockIdx.x * (kJoinWarps / WPR) + warp / WPR;
+        if (row < (long long)a.B * a.Q * a.Hq)
+            join_row<T, D, WPR>(a, row, threadIdx.x & 31, warp % WPR, scratch);
     } else {
-        add_weights(a, blockIdx.x - join_blocks, row_lse);
+        add_weights(a, blockIdx.x - join_blocks, scratch);
     }
 }
 
 template <typename T, int D>
-cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, cudaStream_t s, int* launched) {
-    const int smem = part_smem<D>();
+cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStream_t s,
+                         int* launched) {
     cudaError_t e = cudaSuccess;
     if (a.prefix_splits > 0) {
         if ((e = launch_prefix_parts(a, dt, s)) != cudaSuccess) return e;
@@ -436,22 +459,32 @@ cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, cudaStream_t s, int* l
     }
     if (a.private_splits > 0) {
         const dim3 grid((a.Q * a.G + 15) / 16 * a.Hkv * a.private_splits, a.B);
-        e = cudaFuncSetAttribute(attn_part_kernel<T, D>,
-                                 cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+        static std::once_flag once;
+        static cudaError_t attr_err = cudaSuccess;
+        std::call_once(once, [] {
+            attr_err = cudaFuncSetAttribute(attn_part_kernel<T, D>,
+                                            cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                            part_smem<D>());
+        });
+        if (attr_err != cudaSuccess) return attr_err;
+        e = launch_k(attn_part_kernel<T, D>, grid, dim3(kPartWarps * 32), part_smem<D>(), s,
+                     *launched > 0, a);
         if (e != cudaSuccess) return e;
-        attn_part_kernel<T, D><<<grid, kPartWarps * 32, smem, s>>>(a);
-        if ((e = cudaGetLastError()) != cudaSuccess) return e;
         ++*launched;
     }
+    // A block per row while there are few rows with many parts (a warp alone takes its
+    // batches of parts one after the other: 512 rows x 20 parts 6.0 us, by blocks XX us).
     const long long rows = (long long)a.B * a.Q * a.Hq;
-    const long long join_blocks = (rows + kJoinWarps - 1) / kJoinWarps;
+    const bool wide = a.prefix_splits + a.private_splits > 8 && rows <= 32ll * sm_count;
+    const int per_block = wide ? 1 : kJoinWarps;
+    const long long join_blocks = (rows + per_block - 1) / per_block;
     const long long weight_blocks =
         a.w_out ? (long long)a.B * a.Hkv * ((a.max_len + kWeightSlots - 1) / kWeightSlots) : 0;
     if (join_blocks + weight_blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    attn_join_kernel<T, D><<<(unsigned)(join_blocks + weight_blocks), kJoinThreads, 0, s>>>(
-        a, (int)join_blocks);
-    if ((e = cudaGetLastError()) != cudaSuccess) return e;
-    ++*launched;
+    const auto kern = wide ? attn_join_kernel<T, D, kJoinWarps> : attn_join_kernel<T, D, 1>;
+    e = launch_k(kern, dim3((unsigned)(join_blocks + weight_blocks)), dim3(kJoinThreads), 0, s,
+                 *launched > 0, a, (int)join_blocks);
+    if (e == cudaSuccess) ++*launched;
     return e;
 }
 
@@ -506,12 +539,11 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
 
 cudaError_t launch_attention(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStream_t s,
                              int* launched) {
-    (void)sm_count;
     if (dt == IDX_BF16)
-        return a.D == 128 ? launch_typed<__nv_bfloat16, 128>(a, dt, s, launched)
-                          : launch_typed<__nv_bfloat16, 64>(a, dt, s, launched);
-    return a.D == 128 ? launch_typed<__half, 128>(a, dt, s, launched)
-                      : launch_typed<__half, 64>(a, dt, s, launched);
+        return a.D == 128 ? launch_typed<__nv_bfloat16, 128>(a, dt, sm_count, s, launched)
+                          : launch_typed<__nv_bfloat16, 64>(a, dt, sm_count, s, launched);
+    return a.D == 128 ? launch_typed<__half, 128>(a, dt, sm_count, s, launched)
+                      : launch_typed<__half, 64>(a, dt, sm_count, s, launched);
 }
 
 }  // namespace idx

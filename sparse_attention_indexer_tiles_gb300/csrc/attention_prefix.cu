@@ -177,6 +177,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    pdl_trigger();  // the private parts may take the SMs that this grid leaves idle
 
     // this CTA: key head, pair of row tiles, part of the prefix
     const int tokens = kKeys / a.G;  // query tokens per row tile (its rows: tokens * G <= 128)

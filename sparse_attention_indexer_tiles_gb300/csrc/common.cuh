@@ -60,9 +60,12 @@ IDX_DEVI void mbar_init(uint64_t* bar, uint32_t count) {
 // launch_k) is launched as the kernel before it on the stream finishes, its
 // CTAs taking SMs as that kernel's CTAs leave them: pdl_wait blocks until that
 // kernel has completed and its memory is visible (at once for a launch without
-// the attribute).  (No kernel here signals its dependents early: measured on
+// the attribute).  (No scoring kernel signals its dependents early: measured on
 // GB300, letting the next grid launch from the start of this one slowed the
 // long scoring passes it overlapped.)
+// pdl_trigger lets the next such launch begin once every CTA of this grid has
+// called it or ended.
+IDX_DEVI void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 IDX_DEVI void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 IDX_DEVI void fence_barrier_init() {
