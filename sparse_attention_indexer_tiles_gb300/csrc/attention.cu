@@ -514,15 +514,20 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
         const long long items = (row_tiles + 1) / 2 * Hkv;
         const double per_tile = row_tiles > 1 ? 1.0 : 0.6;
         double best = 0;
-        for (int s = 1; s <= tiles && s <= 256; ++s) {
-            const int t = (tiles + s - 1) / s;
-            const long long ctas = items * ((tiles + t - 1) / t);
-            const double us = (double)((ctas + sm_count - 1) / sm_count) * (t * per_tile + 4.0) +
+        auto consider = [&](long long t) {  // t tiles per part
+            t = t < 1 ? 1 : t > tiles ? tiles : t;
+            const long long s = (tiles + t - 1) / t;
+            const double us = (double)((items * s + sm_count - 1) / sm_count) * (t * per_tile + 4.0) +
                               (double)B * Q * Hq * s * D * 8 / 5e6;
             if (best == 0 || us < best) {
                 best = us;
-                p.prefix_chunk = t * 128;
+                p.prefix_chunk = (int)t * 128;
             }
+        };
+        for (int t = 1; t <= 4; ++t) consider(t);
+        for (long long waves = 1; waves <= 6; ++waves) {  // as many parts as fill whole waves
+            const long long s = waves * sm_count / items;
+            consider((tiles + (s > 0 ? s : 1) - 1) / (s > 0 ? s : 1));
         }
         p.prefix_splits = (prefix_len + p.prefix_chunk - 1) / p.prefix_chunk;
     }
