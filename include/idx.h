@@ -451,7 +451,8 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
  *   max_len  an upper bound on lens (0 = table_stride * page_size)
  *   ws  idx_cache_evict_workspace(...) bytes, 256-byte aligned
  * No two requests may share a private page.  budget >= 1, recent, sink >= 0 and
- * recent + sink <= budget (IDX_EINVAL); D 64 or 128; page_size 16, 32, 64 or 128.
+ * recent + sink <= budget (IDX_EINVAL); D 64 or 128; page_size 16, 32, 64 or 128;
+ * B * Hkv < 2^28 and pages * Hkv * page_size < 2^32 - 16 (IDX_EUNSUPPORTED).
  * Device errors (IDX_DEV_RANGE): lens[b] outside [0, max_len] is clamped; a K/V
  * row in a page outside [0, pages) is not moved.
  * ------------------------------------------------------------------------ */

@@ -1122,7 +1122,9 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
 
 size_t idx_cache_evict_workspace(int B, int Hkv, int budget, int max_len) {
     if (B <= 0 || Hkv <= 0 || budget < 1 || max_len < 0) return 0;
-    return ((size_t)B * Hkv * 2 * evict_max_moves(budget, max_len) * sizeof(int) + 255) / 256 * 256;
+    const size_t moves = evict_max_moves(budget, max_len);
+    if (moves == 0) return 0;
+    return ((size_t)B * Hkv * (2 * moves + 1) * sizeof(int) + 255) / 256 * 256;
 }
 
 idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const int* lens,
@@ -1135,7 +1137,7 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
         recent < 0 || sink < 0 || (long long)recent + sink > budget)
         return IDX_EINVAL;
     if (!is_16bit(dt) || (D != 64 && D != 128) || !page_size_ok(page_size) ||
-        (long long)B * Hkv > 0x7fffffffll)
+        (long long)B * Hkv > 0x0fffffffll || (long long)pages * Hkv * page_size > 0xfffffff0ll)
         return IDX_EUNSUPPORTED;
     if (!private_bound(max_len, table_stride, page_size) || slots < max_len) return IDX_EINVAL;
     if (B == 0) return IDX_OK;
@@ -1176,11 +1178,13 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
     a.sink = sink;
     a.max_len = max_len;
     a.max_moves = evict_max_moves(budget, max_len);
+    a.counts = a.moves + (size_t)B * Hkv * 2 * a.max_moves;
     a.d_status = opt ? opt->d_status : nullptr;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     record(opt, 0, s);
-    const cudaError_t e = launch_evict(a, sm_count(), s);
-    if (e == cudaSuccess) count_launches(1);
+    int launched = 0;
+    const cudaError_t e = launch_evict(a, sm_count(), s, &launched);
+    count_launches(launched);
     record(opt, 1, s);
     return cuda_status(e);
 }

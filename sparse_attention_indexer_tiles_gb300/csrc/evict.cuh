@@ -20,6 +20,7 @@ struct EvictArgs {
     float* w_out;          // [B, Hkv, slots]; may be w
     int* pos_out;          // [B, Hkv, slots]; may be pos
     int* moves;            // workspace [B * Hkv, 2, max_moves]: holes, then sources
+    int* counts;           // workspace [B * Hkv]: moves of each
     long long slots, table_stride;
     int B, Hkv, page_size, page_shift, pages, row_bytes;
     int budget, recent, sink, max_len, max_moves;
@@ -32,6 +33,7 @@ inline int evict_max_moves(int budget, int max_len) {
     return gone <= 0 ? 0 : (gone < budget ? gone : budget);
 }
 
-cudaError_t launch_evict(const EvictArgs& a, int sm_count, cudaStream_t s);
+// Adds the number of kernels launched to *launched.
+cudaError_t launch_evict(const EvictArgs& a, int sm_count, cudaStream_t s, int* launched);
 
 }  // namespace idx
