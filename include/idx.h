@@ -380,8 +380,8 @@ idx_status idx_score_materialise_mxfp4(const uint8_t* q, const uint8_t* q_sf, co
  *                `residual` itself, not x); weight [N]; all of x's type
  *   out [rows, N] e4m3 bytes, scale fp32
  * 1 <= N <= 32768 (IDX_EUNSUPPORTED above).  Pointers are aligned to their
- * element (IDX_EALIGN); rows on 16-byte boundaries with N % 8 == 0 take the
- * vector path.  A row with no finite norm gives no meaningful codes; other rows
+ * element (IDX_EALIGN); rows on 16-byte boundaries (out: 8) with N % 8 == 0 take
+ * the vector path, and with a group they have to.  A row with no finite norm gives no meaningful codes; other rows
  * are not affected.  No workspace.
  * ------------------------------------------------------------------------ */
 idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* residual,

@@ -1011,7 +1011,6 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
     if (!aligned(x, es) || !aligned(weight, es) || !aligned(scale, 4) ||
         (residual && !aligned(residual, es)) || (residual_out && !aligned(residual_out, es)))
         return IDX_EALIGN;
-    if (!arch_ok()) return IDX_EUNSUPPORTED;
     NormArgs a;
     std::memset(&a, 0, sizeof(a));
     a.x = x;
@@ -1028,6 +1027,8 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
     a.vec = N % 8 == 0 && x_stride * es % 16 == 0 && aligned(x, 16) && aligned(weight, 16) &&
             aligned(out, 8) && (!residual || aligned(residual, 16)) &&
             (!residual_out || aligned(residual_out, 16));
+    if (group != 0 && !a.vec) return IDX_EALIGN;
+    if (!arch_ok()) return IDX_EUNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     record(opt, 0, s);
     const cudaError_t e = launch_norm_quant(a, dt, sm_count(), s);

@@ -89,7 +89,7 @@ template <bool CLUSTER, bool STAGED, int kThreads>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int C) {
     using S = Shared<kThreads>;
     constexpr int kWarps = S::kWarps, kBins = S::kBins;
-    constexpr int kBinBits = kThreads == 128 ? 9 : kThreads == 256 ? 10 : kThreads == 512 ? 11 : 12;
+    constexpr int kBinBits = kThreads == 256 ? 10 : 11;
     static_assert(kBins == 1 << kBinBits, "");
     __shared__ S sh;
     extern __shared__ uint32_t keys[];
@@ -451,13 +451,11 @@ cudaError_t launch_evict(const EvictArgs& a, int sm_count, cudaStream_t s, int* 
     // Threads: the scans cost the same whatever the slice, so short slices take few threads.
     cudaError_t e;
     if (slice > kSliceMax)
-        e = launch_select<true, false, 1024>(a, C, 0, s);
-    else if (slice > 8192)
-        e = launch_threads<1024>(a, C, slice, s);
+        e = launch_select<true, false, 512>(a, C, 0, s);
     else if (slice > 4096)
         e = launch_threads<512>(a, C, slice, s);
     else
-        e = launch_threads<128>(a, C, slice, s);
+        e = launch_threads<256>(a, C, slice, s);
     if (e != cudaSuccess) return e;
     ++*launched;
     if (a.max_moves == 0) return e;

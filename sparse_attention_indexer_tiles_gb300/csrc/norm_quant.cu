@@ -16,6 +16,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <mutex>
+
 #include "common.cuh"
 #include "norm_quant.cuh"
 
@@ -26,197 +28,236 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 
-template <typename T> struct Vec8;  // 8 consecutive elements
-template <> struct Vec8<float> { float4 a, b; };
-template <> struct Vec8<__nv_bfloat16> { uint4 a; };
-template <> struct Vec8<__half> { uint4 a; };
-
-IDX_DEVI float to_f(float v) { return v; }
-IDX_DEVI float to_f(__nv_bfloat16 v) { return __bfloat162float(v); }
-IDX_DEVI float to_f(__half v) { return __half2float(v); }
-template <typename T> IDX_DEVI T from_f(float v);
-template <> IDX_DEVI float from_f<float>(float v) { return v; }
-template <> IDX_DEVI __nv_bfloat16 from_f<__nv_bfloat16>(float v) { return __float2bfloat16_rn(v); }
-template <> IDX_DEVI __half from_f<__half>(float v) { return __float2half_rn(v); }
-
-// n valid elements at p (fewer than 8 only on the element-wise path)
-template <typename T, bool VEC>
-IDX_DEVI void load8(const T* p, int n, float (&v)[8]) {
-    if constexpr (VEC) {
-        const Vec8<T> raw = *reinterpret_cast<const Vec8<T>*>(p);
-        const T* e = reinterpret_cast<const T*>(&raw);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = to_f(e[i]);
-    } else {
-#pragma unroll
-        for (int i = 0; i < 8; ++i) v[i] = i < n ? to_f(p[i]) : 0.f;
-    }
+// 8 consecutive columns as they lie in memory, taken as four pairs of fp32.
+template <typename T> struct alignas(16) Raw8 {  // 16-bit types
+    uint32_t u[4];
+    IDX_DEVI void clear() { u[0] = u[1] = u[2] = u[3] = 0u; }
+    IDX_DEVI float2 pair(int i) const;
+    IDX_DEVI void set(int i, float2 v);
+};
+template <> IDX_DEVI float2 Raw8<__nv_bfloat16>::pair(int i) const {
+    return make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
 }
-
-template <typename T, bool VEC>
-IDX_DEVI void store8(T* p, int n, const float (&v)[8]) {
-    if constexpr (VEC) {
-        Vec8<T> raw;
-        T* e = reinterpret_cast<T*>(&raw);
+template <> IDX_DEVI void Raw8<__nv_bfloat16>::set(int i, float2 v) {
+    const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
+    u[i] = *reinterpret_cast<const uint32_t*>(&p);
+}
+template <> IDX_DEVI float2 Raw8<__half>::pair(int i) const {
+    return __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
+}
+template <> IDX_DEVI void Raw8<__half>::set(int i, float2 v) {
+    const __half2 p = __floats2half2_rn(v.x, v.y);
+    u[i] = *reinterpret_cast<const uint32_t*>(&p);
+}
+template <> struct alignas(16) Raw8<float> {
+    float f[8];
+    IDX_DEVI void clear() {
 #pragma unroll
-        for (int i = 0; i < 8; ++i) e[i] = from_f<T>(v[i]);
-        *reinterpret_cast<Vec8<T>*>(p) = raw;
+        for (int i = 0; i < 8; ++i) f[i] = 0.f;
+    }
+    IDX_DEVI float2 pair(int i) const { return make_float2(f[2 * i], f[2 * i + 1]); }
+    IDX_DEVI void set(int i, float2 v) {
+        f[2 * i] = v.x;
+        f[2 * i + 1] = v.y;
+    }
+};
+
+// A thread's eight columns of a row of n, from the row's start: consecutive ones from c on
+// (VEC, n % 8 == 0), or every `step`-th one from c on, so that a warp's element-wise
+// accesses are consecutive whatever the row's alignment.
+template <bool VEC, typename T>
+IDX_DEVI void load8(Raw8<T>& r, const T* row, int c, int step, int n) {
+    if constexpr (VEC) {
+        if (c < n) r = *reinterpret_cast<const Raw8<T>*>(row + c);
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = from_f<T>(v[i]);
+            if (c + i * step < n) reinterpret_cast<T*>(&r)[i] = row[c + i * step];
     }
 }
-
+template <bool VEC, typename T>
+IDX_DEVI void store8(T* row, const Raw8<T>& r, int c, int step, int n) {
+    if constexpr (VEC) {
+        if (c < n) *reinterpret_cast<Raw8<T>*>(row + c) = r;
+    } else {
+#pragma unroll
+        for (int i = 0; i < 8; ++i)
+            if (c + i * step < n) row[c + i * step] = reinterpret_cast<const T*>(&r)[i];
+    }
+}
 template <bool VEC>
-IDX_DEVI void store_codes(uint8_t* p, int n, const float (&v)[8]) {
-    uint32_t w[2];
+IDX_DEVI void store_codes(uint8_t* row, const float2 (&v)[4], int c, int step, int n) {
+    uint32_t p[4];
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t lo = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i], v[4 * i + 1]),
-                                                     __NV_SATFINITE, __NV_E4M3);
-        const uint32_t hi = __nv_cvt_float2_to_fp8x2(make_float2(v[4 * i + 2], v[4 * i + 3]),
-                                                     __NV_SATFINITE, __NV_E4M3);
-        w[i] = lo | (hi << 16);
-    }
+    for (int i = 0; i < 4; ++i) p[i] = __nv_cvt_float2_to_fp8x2(v[i], __NV_SATFINITE, __NV_E4M3);
     if constexpr (VEC) {
-        *reinterpret_cast<uint2*>(p) = make_uint2(w[0], w[1]);
+        if (c < n) *reinterpret_cast<uint2*>(row + c) = make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
     } else {
 #pragma unroll
         for (int i = 0; i < 8; ++i)
-            if (i < n) p[i] = (uint8_t)(w[i >> 2] >> (8 * (i & 3)));
+            if (c + i * step < n) row[c + i * step] = (uint8_t)(p[i >> 1] >> (8 * (i & 1)));
     }
 }
 
-// TPR threads per row, VPT vectors of 8 columns per thread; a block of
-// max(TPR, 128) threads.
-template <typename T, int TPR, int VPT, bool VEC>
+// TPR threads per row, VPT vectors of 8 columns per thread, blocks of max(TPR, 128)
+// threads.  A block takes every gridDim.x-th group of rows and has the next one's x and
+// residual on their way while it works on the current one.  Columns and rows past the end
+// are zeros.  The arithmetic is on pairs of fp32: at 16-bit inputs the instructions per
+// element, not HBM, bound the first version (44 per element, 62 us at 4096 x 8192).
+template <typename T, int TPR, int VPT, bool VEC, bool RES>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormArgs a) {
     constexpr int kThreads = TPR < 128 ? 128 : TPR;
-    constexpr int kRows = kThreads / TPR;
-    const int t = (int)threadIdx.x % TPR;
-    const long long row = (long long)blockIdx.x * kRows + (int)threadIdx.x / TPR;
-    const bool live = row < a.rows;
-    float h[VPT][8], hw[VPT][8];
-    float sum = 0.f, most = 0.f;
-    const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
-    const T* res = static_cast<const T*>(a.residual) + row * a.N;
-    T* res_out = static_cast<T*>(a.residual_out) + row * a.N;
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const int c = (v * TPR + t) * 8;
-        if (live && c < a.N) {
-            load8<T, VEC>(x + c, a.N - c, h[v]);
-            if (a.residual) {
-                float r[8];
-                load8<T, VEC>(res + c, a.N - c, r);
-#pragma unroll
-                for (int i = 0; i < 8; ++i) h[v][i] += r[i];
-            }
-        } else {
-#pragma unroll
-            for (int i = 0; i < 8; ++i) h[v][i] = 0.f;
-        }
-    }
-    float gmost[VPT];
-#pragma unroll
-    for (int v = 0; v < VPT; ++v) {
-        const int c = (v * TPR + t) * 8;
-        gmost[v] = 0.f;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) hw[v][i] = 0.f;
-        if (c < a.N) {
-            load8<T, VEC>(static_cast<const T*>(a.weight) + c, a.N - c, hw[v]);
-            if (live && a.residual_out) store8<T, VEC>(res_out + c, a.N - c, h[v]);
-        }
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            sum = fmaf(h[v][i], h[v][i], sum);
-            hw[v][i] *= h[v][i];
-            gmost[v] = fmaxf(gmost[v], fabsf(hw[v][i]));
-        }
-        most = fmaxf(most, gmost[v]);
-    }
-#pragma unroll
-    for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o /= 2) {
-        sum += __shfl_xor_sync(~0u, sum, o);
-        most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
-    }
-    if constexpr (TPR > 32) {
-        __shared__ float s_sum[TPR / 32], s_most[TPR / 32];
-        if ((threadIdx.x & 31) == 0) {
-            s_sum[threadIdx.x / 32] = sum;
-            s_most[threadIdx.x / 32] = most;
-        }
-        __syncthreads();
-        sum = 0.f;
-#pragma unroll
-        for (int i = 0; i < TPR / 32; ++i) {  // the same order in every thread
-            sum += s_sum[i];
-            most = fmaxf(most, s_most[i]);
-        }
-    }
-    const float rstd = rsqrtf(sum / (float)a.N + a.eps);
-    if (a.group == 0) {
-        const float scale = fmaxf(rstd * most / kE4m3Max, kScaleFloor);
-        if (live && t == 0) a.scale[row] = scale;
-        const float f = rstd / scale;
-#pragma unroll
-        for (int v = 0; v < VPT; ++v)
-#pragma unroll
-            for (int i = 0; i < 8; ++i) hw[v][i] *= f;
-    } else {
-        const int lanes = a.group / 8;  // consecutive threads of a group: 4, 8 or 16
-        const int groups = a.N / a.group;
+    constexpr int kRows = kThreads / TPR;  // rows side by side in a block
+    constexpr int kWarps = TPR / 32;       // warps of a row, where it has several
+    const int t = (int)threadIdx.x % TPR, lane = threadIdx.x & 31;
+    const int units = (a.rows + kRows - 1) / kRows;
+    auto row_of = [&](int u) { return (long long)u * kRows + (int)threadIdx.x / TPR; };
+    auto col_of = [&](int v) { return VEC ? (v * TPR + t) * 8 : v * 8 * TPR + t; };
+    struct Row {
+        Raw8<T> x[VPT], res[RES ? VPT : 1];
+    };
+    auto fetch = [&](Row& r, int u) {
+        const long long row = row_of(u);
+        const T* x = static_cast<const T*>(a.x) + row * a.x_stride;
+        const T* res = static_cast<const T*>(a.residual) + row * a.N;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            float m = gmost[v];
-            for (int o = lanes / 2; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
-            const float scale = fmaxf(rstd * m / kE4m3Max, kScaleFloor);
-            const int c = (v * TPR + t) * 8;
-            if (live && c < a.N && t % lanes == 0) a.scale[row * groups + c / a.group] = scale;
-            const float f = rstd / scale;
-#pragma unroll
-            for (int i = 0; i < 8; ++i) hw[v][i] *= f;
+            r.x[v].clear();
+            if constexpr (RES) r.res[v].clear();
+            if (row < a.rows) {
+                load8<VEC>(r.x[v], x, col_of(v), TPR, a.N);
+                if constexpr (RES) load8<VEC>(r.res[v], res, col_of(v), TPR, a.N);
+            }
         }
-    }
+    };
+    Row next;
+    fetch(next, blockIdx.x);
+    Raw8<T> wgt[VPT];
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
-        const int c = (v * TPR + t) * 8;
-        if (live && c < a.N) store_codes<VEC>(a.out + row * a.N + c, a.N - c, hw[v]);
+        wgt[v].clear();
+        load8<VEC>(wgt[v], static_cast<const T*>(a.weight), col_of(v), TPR, a.N);
+    }
+    const float per_col = 1.f / (float)a.N;
+    const int lanes = a.group / 8;  // consecutive threads of a group: 4, 8 or 16
+    for (int u = blockIdx.x, it = 0; u < units; u += gridDim.x, ++it) {
+        const Row cur = next;
+        if (u + (int)gridDim.x < units) fetch(next, u + gridDim.x);
+        const long long row = row_of(u);
+        const bool row_live = row < a.rows;
+        float2 hw[VPT][4], sum2 = make_float2(0.f, 0.f);
+        float gmost[VPT], most = 0.f;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            Raw8<T> h_out;
+            gmost[v] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                float2 h = cur.x[v].pair(i);
+                if constexpr (RES) h = add2(h, cur.res[v].pair(i));
+                sum2 = fma2(h, h, sum2);
+                hw[v][i] = mul2(h, wgt[v].pair(i));
+                gmost[v] = fmaxf(gmost[v], fmaxf(fabsf(hw[v][i].x), fabsf(hw[v][i].y)));
+                h_out.set(i, h);
+            }
+            if (a.residual_out && row_live)
+                store8<VEC>(static_cast<T*>(a.residual_out) + row * a.N, h_out, col_of(v), TPR, a.N);
+            most = fmaxf(most, gmost[v]);
+        }
+        float sum = sum2.x + sum2.y;
+#pragma unroll
+        for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o /= 2) {
+            sum += __shfl_xor_sync(~0u, sum, o);
+            most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+        }
+        if constexpr (TPR > 32) {
+            __shared__ float2 part[2][kWarps];  // two: a block's barrier per row group is enough
+            if (lane == 0) part[it & 1][threadIdx.x / 32] = make_float2(sum, most);
+            __syncthreads();
+            constexpr int kSpan = kWarps <= 4 ? 4 : kWarps <= 8 ? 8 : kWarps <= 16 ? 16 : 32;
+            const bool there = lane % kSpan < kWarps;
+            sum = there ? part[it & 1][lane % kSpan].x : 0.f;
+            most = there ? part[it & 1][lane % kSpan].y : 0.f;
+#pragma unroll
+            for (int o = kSpan / 2; o > 0; o /= 2) {  // the same sum in every thread
+                sum += __shfl_xor_sync(~0u, sum, o);
+                most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+            }
+        }
+        const float rstd = rsqrtf(fmaf(sum, per_col, a.eps));
+        const float row_scale = fmaxf(rstd * most * (1.f / kE4m3Max), kScaleFloor);
+        if (a.group == 0 && row_live && t == 0) a.scale[row] = row_scale;
+#pragma unroll
+        for (int v = 0; v < VPT; ++v) {
+            float scale = row_scale;
+            if (VEC && a.group != 0) {
+                float m = gmost[v];
+                if (lanes > 8) m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
+                if (lanes > 4) m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
+                m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
+                m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
+                scale = fmaxf(rstd * m * (1.f / kE4m3Max), kScaleFloor);
+                if (row_live && col_of(v) < a.N && (t & (lanes - 1)) == 0)
+                    a.scale[row * (a.N / a.group) + col_of(v) / a.group] = scale;
+            }
+            const float f = __fdividef(rstd, scale);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) hw[v][i] = mul2(hw[v][i], make_float2(f, f));
+            if (row_live) store_codes<VEC>(a.out + row * a.N, hw[v], col_of(v), TPR, a.N);
+        }
     }
 }
 
-template <typename T, int TPR, int VPT>
-cudaError_t launch_shape(const NormArgs& a, cudaStream_t s) {
-    constexpr int kThreads = TPR < 128 ? 128 : TPR;
-    const int grid = (int)(((long long)a.rows * TPR + kThreads - 1) / kThreads);
-    if (a.vec)
-        norm_quant_kernel<T, TPR, VPT, true><<<grid, kThreads, 0, s>>>(a);
-    else
-        norm_quant_kernel<T, TPR, VPT, false><<<grid, kThreads, 0, s>>>(a);
+template <typename T, int TPR, int VPT, bool VEC, bool RES>
+cudaError_t launch_blocks(const NormArgs& a, int sm_count, cudaStream_t s) {
+    constexpr int kThreads = TPR < 128 ? 128 : TPR, kRows = kThreads / TPR;
+    static std::once_flag once;
+    static int resident = 1;  // blocks per SM
+    std::call_once(once, [] {
+        if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
+                &resident, norm_quant_kernel<T, TPR, VPT, VEC, RES>, kThreads, 0) != cudaSuccess ||
+            resident < 1)
+            resident = 1;
+    });
+    // as many blocks as are resident, each with the same number of row groups
+    const long long units = ((long long)a.rows + kRows - 1) / kRows;
+    const long long room = (long long)resident * sm_count;
+    const long long each = (units + room - 1) / room;
+    const long long grid = (units + each - 1) / each;
+    norm_quant_kernel<T, TPR, VPT, VEC, RES><<<(unsigned)grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
+template <typename T, int TPR, int VPT>
+cudaError_t launch_shape(const NormArgs& a, int sm_count, cudaStream_t s) {
+    if (a.vec)
+        return a.residual ? launch_blocks<T, TPR, VPT, true, true>(a, sm_count, s)
+                          : launch_blocks<T, TPR, VPT, true, false>(a, sm_count, s);
+    return a.residual ? launch_blocks<T, TPR, VPT, false, true>(a, sm_count, s)
+                      : launch_blocks<T, TPR, VPT, false, false>(a, sm_count, s);
+}
+
+// Shapes: a narrow row is a half-warp's or a warp's; a wide one's threads hold one or two
+// vectors.
 template <typename T>
-cudaError_t launch_type(const NormArgs& a, cudaStream_t s) {
-    if (a.N <= 128) return launch_shape<T, 16, 1>(a, s);
-    if (a.N <= 256) return launch_shape<T, 32, 1>(a, s);
-    if (a.N <= 1024) return launch_shape<T, 128, 1>(a, s);
-    if (a.N <= 2048) return launch_shape<T, 256, 1>(a, s);
-    if (a.N <= 4096) return launch_shape<T, 512, 1>(a, s);
-    if (a.N <= 8192) return launch_shape<T, 1024, 1>(a, s);
-    if (a.N <= 16384) return launch_shape<T, 1024, 2>(a, s);
-    return launch_shape<T, 1024, 4>(a, s);
+cudaError_t launch_type(const NormArgs& a, int sm_count, cudaStream_t s) {
+    if (a.N <= 128) return launch_shape<T, 16, 1>(a, sm_count, s);
+    if (a.N <= 256) return launch_shape<T, 32, 1>(a, sm_count, s);
+    if (a.N <= 1024) return launch_shape<T, 128, 1>(a, sm_count, s);
+    if (a.N <= 2048) return launch_shape<T, 256, 1>(a, sm_count, s);
+    if (a.N <= 4096) return launch_shape<T, 256, 2>(a, sm_count, s);
+    if (a.N <= 6144) return launch_shape<T, 384, 2>(a, sm_count, s);
+    if (a.N <= 8192) return launch_shape<T, 256, 4>(a, sm_count, s);
+    if (a.N <= 16384) return launch_shape<T, 1024, 2>(a, sm_count, s);
+    return launch_shape<T, 1024, 4>(a, sm_count, s);
 }
 
 }  // namespace
 
 cudaError_t launch_norm_quant(const NormArgs& a, idx_dtype dt, int sm_count, cudaStream_t s) {
-    (void)sm_count;
-    if (dt == IDX_BF16) return launch_type<__nv_bfloat16>(a, s);
-    if (dt == IDX_FP16) return launch_type<__half>(a, s);
-    return launch_type<float>(a, s);
+    if (dt == IDX_BF16) return launch_type<__nv_bfloat16>(a, sm_count, s);
+    if (dt == IDX_FP16) return launch_type<__half>(a, sm_count, s);
+    return launch_type<float>(a, sm_count, s);
 }
 
 }  // namespace idx

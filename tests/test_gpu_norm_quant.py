@@ -43,6 +43,25 @@ def test_widths(idx, cols, dtype, residual):
     ref.check_norm(out, scale, x, w, r, ro)
 
 
+@pytest.mark.parametrize("cols", [154, 926, 1500, 2052, 4500, 5003, 6146, 7999, 12345])
+@pytest.mark.parametrize("dtype,residual", [(BF16, True), (FP16, True), (FP32, False)])
+def test_many_rows_of_odd_widths(idx, cols, dtype, residual):
+    """More row groups than blocks: every block takes several, one ahead."""
+    rows = 3000 if cols < 3000 else 1300
+    x, w, r = inputs(rows, cols, dtype, residual, seed=cols)
+    out, scale, ro = run(idx, x, w, r)
+    ref.check_norm(out, scale, x, w, r, ro)
+
+
+@pytest.mark.parametrize("cols,group", [(128, 0), (256, 64), (1024, 32), (2048, 128), (4096, 0), (5120, 128), (6144, 0),
+                                        (8192, 128), (16384, 32)])
+def test_many_rows_in_vectors(idx, cols, group):
+    rows = 30001 if cols < 512 else 2500
+    x, w, r = inputs(rows, cols, BF16, True, seed=cols + group)
+    out, scale, ro = run(idx, x, w, r, group=group)
+    ref.check_norm(out, scale, x, w, r, ro, group=group)
+
+
 @pytest.mark.parametrize("rows", [1, 2, 9, 131, 3001])
 @pytest.mark.parametrize("cols,group", [(128, 0), (128, 128), (384, 128), (64, 64), (96, 32), (4096, 128), (7168, 64)])
 def test_rows_and_groups(idx, rows, cols, group):

@@ -34,7 +34,8 @@ def norm(lib, **kw):
     (dict(N=32769, x_stride=32769), EUNSUPPORTED), (dict(x=None), EINVAL), (dict(weight=None), EINVAL),
     (dict(out=None), EINVAL), (dict(scale=None), EINVAL), (dict(residual_out=P), EINVAL),
     (dict(x=P + 1), EALIGN), (dict(dt=FP32, x=P + 2), EALIGN), (dict(scale=P + 2), EALIGN),
-    (dict(residual=P + 1), EALIGN), (dict(rows=0, x=None), OK)])
+    (dict(residual=P + 1), EALIGN), (dict(group=32, x=P + 2), EALIGN), (dict(group=32, x_stride=129), EALIGN),
+    (dict(group=32, out=P + 4), EALIGN), (dict(rows=0, x=None), OK)])
 def test_norm_checks(lib, kw, code):
     assert norm(lib, **kw) == code
 
