@@ -1057,7 +1057,8 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
         return IDX_EINVAL;
     if (!is_16bit(dt) || (D != 64 && D != 128) || !page_size_ok(page_size) ||
         Q > kAttnMaxTokens || Hq / Hkv > kAttnMaxGroup || (long long)B * Hkv > 65535 ||
-        (long long)B * Q * Hq > 0x7fffff00ll || prefix_len > 0x3fffffff)
+        (long long)B * Q * Hq > 0x7fffff00ll || prefix_len > 0x3fffffff ||
+        (long long)pages * Hkv > 0x7fffff00ll)
         return IDX_EUNSUPPORTED;
     if (!private_bound(max_len, table_stride, page_size)) return IDX_EINVAL;
     if (w && slots < max_len) return IDX_EINVAL;

@@ -506,13 +506,13 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
     };
     p.prefix_splits = p.prefix_chunk = 0;
     if (prefix_len > 0) {
-        // Key tiles per part: one CTA per SM takes about 1 us per 128-key tile of a pair of
+        // Key tiles per part: one CTA per SM takes about 1 us per 128 keys of a pair of
         // row tiles (0.6 us of a single one) and 4 us besides, and every part writes D
         // floats per row that the join reads (about 5 MB per us).
-        const int tokens = 128 / G, tiles = (prefix_len + 127) / 128;
+        const int keys = attn_prefix_keys(D), tokens = 128 / G, tiles = (prefix_len + keys - 1) / keys;
         const long long row_tiles = ((long long)B * Q + tokens - 1) / tokens;
         const long long items = (row_tiles + 1) / 2 * Hkv;
-        const double per_tile = row_tiles > 1 ? 1.0 : 0.6;
+        const double per_tile = (row_tiles > 1 ? 1.0 : 0.6) * keys / 128;
         double best = 0;
         auto consider = [&](long long t) {  // t tiles per part
             t = t < 1 ? 1 : t > tiles ? tiles : t;
@@ -521,7 +521,7 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
                               (double)B * Q * Hq * s * D * 8 / 5e6;
             if (best == 0 || us < best) {
                 best = us;
-                p.prefix_chunk = (int)t * 128;
+                p.prefix_chunk = (int)t * keys;
             }
         };
         for (int t = 1; t <= 4; ++t) consider(t);

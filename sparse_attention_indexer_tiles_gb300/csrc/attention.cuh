@@ -11,6 +11,9 @@ namespace idx {
 constexpr int kAttnMaxTokens = 16;   // new tokens per request
 constexpr int kAttnMaxGroup = 128;   // query heads per key head
 
+// Keys per tile of the prefix kernel (see there).
+__host__ __device__ constexpr int attn_prefix_keys(int D) { return D == 128 ? 80 : 128; }
+
 // One attention call.  Rows: query row (b, t, head) = (b * Q + t) * Hq + head.  The
 // keys of a row are cut into `splits` parts, the prefix's first; each part leaves its
 // softmax-weighted mean of V and its log2-sum-exp2 in the workspace.
@@ -32,7 +35,8 @@ struct AttnArgs {
     long long table_stride, slots, logit_stride;
     int B, Q, Hq, Hkv, G, D, pages, page_size, page_shift;
     int prefix_len, max_len;
-    int prefix_splits, prefix_chunk;    // keys per prefix part (a multiple of 128)
+    int prefix_splits, prefix_chunk;    // keys per prefix part (whole key tiles)
+    int prefix_unit;                    // keys per copy (set by launch_prefix_parts)
     int private_splits, private_chunk;  // keys per private part (a multiple of 64)
     float scale_log2;                   // scale * log2(e)
     long long wait_limit;               // SM clocks a wait of the prefix kernel may take

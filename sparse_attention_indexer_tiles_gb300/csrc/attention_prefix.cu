@@ -2,17 +2,22 @@
 //
 // The rows of a key head over the whole batch (B * Q * G of them) read the same prefix
 // keys, so they are the rows of two dense products per key tile,
-//     S = Q K^T  (128 rows x 128 keys, over D),     O += P V  (128 rows x D, over keys),
+//     S = Q K^T  (128 rows x tile keys, over D),    O += P V  (128 rows x D, over keys),
 // with P = 2^(S scale_log2 - m) between them.  A CTA runs two streams, each with its own
-// S and O accumulators in TMEM and its own four softmax warps (one thread per row); while
-// one stream's softmax runs, the tensor core works for the other:
+// S, P and O in TMEM and its own four softmax warps (one thread per row):
 //   * two row tiles over the same keys (each K and V tile in shared memory serves both), or
 //   * for a last, odd row tile, the same rows over the even and the odd key tiles, joined
 //     through shared memory at the end.
-// Warps 8 and 10 issue the streams' MMAs, warp 9 the TMA copies: K and V tiles of 128 keys
-// through a ring, page by page (each page's rows of a head are contiguous).  P goes back to TMEM over S, in
-// the tensors' type, and is the A operand of the second product; V is used as it lies in
-// memory (its rows are the product's K axis, so the B operand is MN-major).
+// P is written to TMEM in the tensors' type and is the A operand of the second product; V is
+// used as it lies in memory (its rows are the product's K axis, so the B operand is
+// MN-major).  Warps 8 and 10 issue the streams' MMAs, warps 9 and 11 the TMA copies of K and
+// of V through one ring.  A copy brings whole rows of a page into groups of 8 keys, each
+// group's 64-column halves one after the other (1024 bytes each, 128-byte swizzled).
+//
+// Tile width: S and P have columns of their own, so the next S is computed while the
+// softmax works on this one, and nothing waits for a product's end before the next is
+// issued.  Beside two O of D columns, 512 columns leave 128 per stream at D = 128: 80 keys
+// (80 + 40).  Tiles of 128 keys with P over S cost a wait for P V before every Q K^T.
 //
 // The running maximum m is renewed only when a row's maximum has grown by more than 8 (a
 // factor 256; P <= 256 then, well inside either type), so O is rarely rescaled; the sum l
@@ -33,26 +38,34 @@ PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 namespace {
 
-constexpr int kKeys = 128;                 // keys per tile
-constexpr int kHalf = 128 * 128;           // 128 rows of 64 16-bit elements, 128-byte swizzled
+constexpr int kRows = 128;                 // rows per tile
+constexpr int kHalfQ = kRows * 128;        // 64 columns of a row tile, 128-byte swizzled
 constexpr int kSoftmaxWarps = 8;
 constexpr int kPrefixThreads = (kSoftmaxWarps + 4) * 32;  // warp 11 only gives registers
 constexpr float kRenew = 8.f;
 
 template <int D> struct PrefixCfg {
+    static constexpr int KEYS = attn_prefix_keys(D);         // per tile
     static constexpr int HALVES = D / 64;
-    static constexpr int TILE = HALVES * kHalf;      // a Q, K or V tile
-    static constexpr int NS = D == 128 ? 5 : 8;      // ring slots
-    static constexpr int OFF_KV = 2 * TILE;
+    static constexpr int QTILE = HALVES * kHalfQ;
+    static constexpr int GROUP = HALVES * 1024;              // 8 keys of a K or V tile
+    static constexpr int TILE = KEYS / 8 * GROUP;
+    static constexpr int NS = D == 128 ? 7 : 8;              // ring slots (>= 7: two streams
+                                                             // over tiles of their own)
+    static constexpr int OFF_KV = 2 * QTILE;
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
     static constexpr int NBAR = 1 + 2 * NS + 10;
-    static constexpr int OFF_CTL = OFF_BAR + NBAR * 8;   // [0] TMEM base, [1] abort flag
-    static constexpr int OFF_ML = OFF_CTL + 16;          // the odd stream's m and l per row
-    static constexpr int SMEM = OFF_ML + 128 * 8 + 1024;
+    static constexpr int OFF_CTL = OFF_BAR + NBAR * 8;       // [0] TMEM base, [1] abort flag,
+                                                             // [2] [3] the producers' next tiles
+    static constexpr int OFF_ML = OFF_CTL + 16;              // the odd stream's m and l
+    static constexpr int SMEM = OFF_ML + kRows * 8 + 1024;
+    // TMEM columns: S and P of a stream, then both O
+    static constexpr int COL_P = KEYS, COL_STREAM = D == 128 ? 128 : KEYS + KEYS / 2;
+    static constexpr int COL_O = 512 - 2 * D;
+    static_assert(SMEM <= 227 * 1024, "");
+    static_assert(KEYS + KEYS / 2 <= COL_STREAM && 2 * COL_STREAM <= COL_O, "");
+    static_assert(kRows * D * 4 <= NS * TILE, "the odd stream's O is joined through the ring");
 };
-static_assert(PrefixCfg<128>::SMEM <= 227 * 1024 && PrefixCfg<64>::SMEM <= 227 * 1024, "");
-// the odd stream's O is joined through the ring
-static_assert(128 * 128 * 4 <= PrefixCfg<128>::NS * PrefixCfg<128>::TILE, "");
 
 // Registers: the launch gives 384 x 168; the softmax warps (a row of S each thread) take
 // 256 x 208, the others keep 128 x 80.
@@ -90,6 +103,28 @@ IDX_DEVI void tma_load_4d(uint32_t dst, const void* tmap, uint64_t* bar, int c0,
         "r"(c3)
         : "memory");
 }
+// From the start of the first three axes.
+IDX_DEVI void tma_load_5d(uint32_t dst, const void* tmap, uint64_t* bar, int c3, int c4) {
+    asm volatile(
+        "cp.async.bulk.tensor.5d.shared::cluster.global.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %3, %3, %4, %5}], [%2];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(0), "r"(c3), "r"(c4)
+        : "memory");
+}
+
+// mbar_wait on two barriers, their tests in flight together.
+IDX_DEVI bool mbar_wait2(uint64_t* bar0, uint32_t parity0, uint64_t* bar1, uint32_t parity1,
+                         volatile int* abort, long long limit) {
+    bool ok0 = mbar_try_wait(bar0, parity0), ok1 = mbar_try_wait(bar1, parity1);
+    if (ok0 && ok1) return true;
+    const long long t0 = clock64();
+    for (;;) {
+        if (!ok0) ok0 = mbar_try_wait(bar0, parity0);
+        if (!ok1) ok1 = mbar_try_wait(bar1, parity1);
+        if (ok0 && ok1) return true;
+        if (*abort || clock64() - t0 > limit) return false;
+    }
+}
 
 // D[tmem] (+)= A[tmem] * B[smem], 16-bit inputs, fp32 accumulator.
 IDX_DEVI void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc,
@@ -102,27 +137,37 @@ IDX_DEVI void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t 
         : "memory");
 }
 
-// 32x32b shape, 32 columns: thread t writes lane t.
-IDX_DEVI void tmem_st32(uint32_t taddr, const uint32_t (&r)[32]) {
-    asm volatile(
-        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, "
-        "%11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, "
-        "%29, %30, %31, %32};" ::"r"(taddr),
-        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
-        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
-        "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
-        "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
-        "r"(r[29]), "r"(r[30]), "r"(r[31])
-        : "memory");
+// 32x32b shape, N columns (8 or 32): thread t writes lane t.
+template <int N>
+IDX_DEVI void tmem_st32x32b(uint32_t taddr, const uint32_t* r) {
+    if constexpr (N == 8) {
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"r"(
+                taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+            : "memory");
+    } else {
+        static_assert(N == 32, "8 or 32 columns");
+        asm volatile(
+            "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, "
+            "%10, %11, %12, %13, %14, %15, %16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, "
+            "%27, %28, %29, %30, %31, %32};" ::"r"(taddr),
+            "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+            "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]),
+            "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]),
+            "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]),
+            "r"(r[29]), "r"(r[30]), "r"(r[31])
+            : "memory");
+    }
 }
 IDX_DEVI void tmem_st_wait() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
-// Descriptor of a V tile as an MN-major B operand, 128-byte swizzled: 64 elements of D are
-// contiguous, the next 64 lie `kHalf` further (leading offset), 8 keys are 1024 bytes
-// (stride offset).
-IDX_DEVI uint64_t v_desc(uint32_t saddr) {
-    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(kHalf >> 4) << 16) |
-           ((uint64_t)(1024 >> 4) << 32) | (1ull << 46) | (2ull << 61);
+// Descriptors of a K tile as a K-major operand and of a V tile as an MN-major one, both
+// 128-byte swizzled: 8 keys are `group` bytes apart (stride offset); V's next 64 columns are
+// 1024 bytes further (leading offset).
+IDX_DEVI uint64_t kv_desc(uint32_t saddr, uint32_t group) {
+    return (uint64_t)((saddr >> 4) & 0x3FFFu) | ((uint64_t)(1024 >> 4) << 16) |
+           ((uint64_t)(group >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
 template <typename T> struct Elem;
@@ -152,8 +197,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     uint64_t* full = qfull + 1;
     uint64_t* empty = full + C::NS;
     uint64_t* sfull = empty + C::NS;  // per stream: S is there
-    uint64_t* pfull = sfull + 2;      // half of P is there (and S has been read)
-    uint64_t* pvdone = pfull + 4;     // O has the tile's P V
+    uint64_t* sfree = sfull + 2;      // S has been read
+    uint64_t* pfull = sfree + 2;      // P is there
+    uint64_t* pvdone = pfull + 2;     // O has the tile's P V, P has been read
     uint64_t* done = pvdone + 2;      // every MMA of the stream
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
@@ -161,24 +207,24 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     pdl_trigger();  // the private parts may take the SMs that this grid leaves idle
 
     // this CTA: key head, pair of row tiles, part of the prefix
-    const int tokens = kKeys / a.G;  // query tokens per row tile (its rows: tokens * G <= 128)
+    const int tokens = kRows / a.G;  // query tokens per row tile (its rows: tokens * G <= 128)
     const int ntiles = (a.B * a.Q + tokens - 1) / tokens, npairs = (ntiles + 1) / 2;
     const int split = blockIdx.x % a.prefix_splits;
     const int pair = blockIdx.x / a.prefix_splits % npairs;
     const int hk = blockIdx.x / a.prefix_splits / npairs;
     const bool solo = 2 * pair + 1 == ntiles;
     const int lo = split * a.prefix_chunk, hi = min(a.prefix_len, lo + a.prefix_chunk);
-    const int n = (hi - lo + kKeys - 1) / kKeys;  // key tiles, at least one
+    const int n = (hi - lo + C::KEYS - 1) / C::KEYS;  // key tiles, at least one
 
     const uint32_t kv = smem_u32(smem + C::OFF_KV);
-    // K and V tiles in turn (warp 9): a page per lane; one that does not exist reads as zeros
-    // past the last page
+    // K and V tiles in turn, `unit` keys of a page per copy; keys past the end and pages that
+    // do not exist read as zeros past the last page.  A lane looks up a copy's page.
     bool bad = false;
-    const int per = kKeys / a.page_size;  // pages per tile
+    const int unit = a.prefix_unit, copies = C::KEYS / unit;
     auto page_of = [&](int x) {
-        const int key = lo + (x >> 1) * kKeys + lane * a.page_size;
+        const int key = lo + (x >> 1) * C::KEYS + lane * unit;
         int page = a.pages;
-        if (lane < per && key < hi) {
+        if (lane < copies && x < 2 * n && key < hi) {
             page = a.prefix_table[key >> a.page_shift];
             if (page < 0 || page >= a.pages) {
                 page = a.pages;
@@ -187,20 +233,26 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
         return page;
     };
-    auto fetch = [&](int x, int page) {
+    auto fetch = [&](int x, int pages) {
         const int slot = x % C::NS;
-        if (lane == 0) mbar_arrive_expect_tx(&full[slot], C::TILE);
+        if (elect_one()) mbar_arrive_expect_tx(&full[slot], C::TILE);
         __syncwarp();
-        if (lane < per)
-            for (int h = 0; h < C::HALVES; ++h)
-                tma_load_4d(kv + slot * C::TILE + h * kHalf + lane * a.page_size * 128,
-                            x & 1 ? &tm_v : &tm_k, &full[slot], h * 64, 0, hk, page);
+        for (int u = 0; u < copies; ++u) {
+            const int page = __shfl_sync(~0u, pages, u);
+            const int key = lo + (x >> 1) * C::KEYS + u * unit;
+            if (elect_one())
+                tma_load_5d(kv + slot * C::TILE + u * unit / 8 * C::GROUP, x & 1 ? &tm_v : &tm_k,
+                            &full[slot], (key & (a.page_size - 1)) / 8,
+                            page == a.pages ? a.pages * a.Hkv : page * a.Hkv + hk);
+            __syncwarp();
+        }
     };
     const int first = a.withhold_tile >= 0 ? min(2 * n, 2 * a.withhold_tile) : 2 * n;  // tiles that come
+    constexpr int kFirstK = (C::NS + 1) / 2;
     if (warp == 9) {
-        int page[(C::NS + 1) / 2];  // on their way while the barriers are set up
+        int page[kFirstK];  // on their way while the barriers are set up
 #pragma unroll
-        for (int i = 0; i < (C::NS + 1) / 2; ++i) page[i] = page_of(2 * i);
+        for (int i = 0; i < kFirstK; ++i) page[i] = page_of(2 * i);
         if (lane == 0) {
             prefetch_tmap(&tm_q);
             prefetch_tmap(&tm_k);
@@ -212,8 +264,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             }
             for (int i = 0; i < 2; ++i) {
                 mbar_init(&sfull[i], 1);
-                mbar_init(&pfull[2 * i], 4);
-                mbar_init(&pfull[2 * i + 1], 4);
+                mbar_init(&sfree[i], 4);
+                mbar_init(&pfull[i], 4);
                 mbar_init(&pvdone[i], 1);
                 mbar_init(&done[i], 1);
             }
@@ -224,13 +276,13 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             mbar_arrive_expect_tx(qfull, tiles * C::HALVES * tokens * a.G * 128);
             for (int t = 0; t < tiles; ++t)
                 for (int h = 0; h < C::HALVES; ++h)
-                    tma_load_4d(smem_u32(smem) + t * C::TILE + h * kHalf, &tm_q, qfull, h * 64, 0,
+                    tma_load_4d(smem_u32(smem) + t * C::QTILE + h * kHalfQ, &tm_q, qfull, h * 64, 0,
                                 hk, (2 * pair + t) * tokens);
         }
         __syncwarp();
 #pragma unroll
-        for (int x = 0; x < C::NS; ++x)
-            if (x < first) fetch(x, page[x / 2]);
+        for (int i = 0; i < kFirstK; ++i)
+            if (2 * i < first) fetch(2 * i, page[i]);
     }
     if (warp == 8) {
         tmem_alloc(const_cast<uint32_t*>(tslot), 512);
@@ -247,30 +299,36 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     if (warp >= 8) {
         regs_less();
-        if (warp == 9) {
-            // ---------------------------------------------------- TMA producer
-            int issued = min(C::NS, first), page = page_of(issued);
-            for (int x = issued; x < first; ++x) {
-                if (!(x & 1)) page = page_of(x);
+        if (warp == 9 || warp == 11) {
+            // ----------------------------------------- TMA producers: K tiles, V tiles
+            int x = warp == 9 ? 2 * kFirstK : 1;
+            int page = page_of(x);
+            for (; x < first; x += 2) {
+                const int next = page_of(x + 2);  // looked up a tile ahead
                 bool ok = true;
-                if (lane == 0)
-                    ok = mbar_wait(&empty[x % C::NS], ((x / C::NS) & 1) ^ 1, abort_flag, a.wait_limit);
-                if (!__all_sync(~0u, ok)) {
+                if (x >= C::NS)
+                    ok = __all_sync(~0u, mbar_wait(&empty[x % C::NS], ((x / C::NS) & 1) ^ 1,
+                                                   abort_flag, a.wait_limit));
+                if (!ok) {
                     if (lane == 0) give_up();
                     break;
                 }
                 fetch(x, page);
-                issued = x + 1;
+                page = next;
             }
             if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
-            // nothing may be in flight when the CTA ends: the last use of every slot has landed
-            if (lane == 0) {
-                for (int x = max(0, issued - C::NS); x < issued; ++x)
-                    mbar_wait(&full[x % C::NS], (x / C::NS) & 1, nullptr, 1ll << 28);
-                mbar_wait(qfull, 0, nullptr, 1ll << 28);
-            }
+            // Nothing may be in flight when the CTA ends: the last copy into every slot has
+            // landed (tile y, when tile y + NS has not been issued; a slot's earlier copies
+            // were consumed before its next one).
+            volatile int* next = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 8);
+            if (lane == 0) next[x & 1] = min(x, first + ((x ^ first) & 1));
+            named_bar_sync(2, 64);
+            for (int y = next[x & 1] - 2; y >= 0 && y > x - 4 * C::NS; y -= 2)
+                if (y + C::NS >= next[(y + C::NS) & 1])
+                    mbar_wait(&full[y % C::NS], (y / C::NS) & 1, nullptr, 1ll << 28);
+            if (warp == 9) mbar_wait(qfull, 0, nullptr, 1ll << 28);
             __syncwarp();
-        } else if (warp != 11) {
+        } else {
             // -------------------------------------------------- MMA issuers
             // One warp per stream: while the tensor core reads its operands an mbarrier
             // access takes about 140 clocks, and one warp that waited for both streams
@@ -278,70 +336,59 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             // The whole warp runs the control flow, so that descriptors stay in uniform
             // registers, and one elected lane issues.
             const int s = warp == 10;
-            const uint32_t id_s = instr_desc(Elem<T>::FMT, 128, kKeys);
-            const uint32_t id_o = instr_desc(Elem<T>::FMT, 128, D) | (1u << 16);  // B is MN-major
-            const uint32_t t_s = tmem + s * kKeys, t_o = tmem + 256 + s * 128;
+            const uint32_t id_s = instr_desc(Elem<T>::FMT, kRows, C::KEYS);
+            const uint32_t id_o = instr_desc(Elem<T>::FMT, kRows, D) | (1u << 16);  // B is MN-major
+            const uint32_t t_s = tmem + s * C::COL_STREAM, t_p = t_s + C::COL_P;
+            const uint32_t t_o = tmem + C::COL_O + s * D;
             const int mine = solo ? (n + 1 - s) / 2 : n;
-            auto wait = [&](uint64_t* bar, uint32_t parity) {
-                return __all_sync(~0u, mbar_wait(bar, parity, abort_flag, a.wait_limit));
-            };
             auto tile_of = [&](int i) { return solo ? 2 * i + s : i; };
-            auto landed = [&](int x) { return wait(&full[x % C::NS], (x / C::NS) & 1); };
-            const uint64_t q = smem_desc(smem_u32(smem) + (solo ? 0 : s) * C::TILE, 128);
-            // S of the i-th tile (K has landed)
+            // K or V tile x has landed, and a softmax barrier's i-th phase has completed
+            auto both = [&](int x, uint64_t* bar, int i) {
+                return __all_sync(~0u, mbar_wait2(&full[x % C::NS], (x / C::NS) & 1, bar, i & 1,
+                                                  abort_flag, a.wait_limit));
+            };
+            const uint64_t q = smem_desc(smem_u32(smem) + (solo ? 0 : s) * C::QTILE, 128);
+            // S of the i-th tile (K has landed, the last S has been read)
             auto qk = [&](int i) {
                 const int x = 2 * tile_of(i);
                 tc_fence_after();
-                const uint64_t k = smem_desc(kv + (x % C::NS) * C::TILE, 128);
+                const uint64_t k = kv_desc(kv + (x % C::NS) * C::TILE, C::GROUP);
                 if (elect_one()) {
 #pragma unroll
-                    for (int d = 0; d < D / 16; ++d) {
-                        const uint32_t off = ((d / 4) * kHalf + (d % 4) * 32) >> 4;
-                        mma_bf16(t_s, q + off, k + off, id_s, d > 0);
-                    }
+                    for (int d = 0; d < D / 16; ++d)
+                        mma_bf16(t_s, q + (((d / 4) * kHalfQ + (d % 4) * 32) >> 4),
+                                 k + (((d / 4) * 1024 + (d % 4) * 32) >> 4), id_s, d > 0);
                     mma_commit(&sfull[s]);
                     mma_commit(&empty[x % C::NS]);
                 }
                 __syncwarp();
             };
-            // half h of the keys of O += P V (V has landed)
-            auto pv = [&](int i, int h) {
+            // O += P V (V has landed, P is there)
+            auto pv = [&](int i) {
                 const int x = 2 * tile_of(i) + 1;
                 tc_fence_after();
-                const uint64_t v = v_desc(kv + (x % C::NS) * C::TILE);
+                const uint64_t v = kv_desc(kv + (x % C::NS) * C::TILE, C::GROUP);
                 if (elect_one()) {
 #pragma unroll
-                    for (int k = 0; k < kKeys / 32; ++k) {
-                        const int kk = h * (kKeys / 32) + k;
-                        mma_ts(t_o, t_s + kk * 8, v + kk * (2048 >> 4), id_o, i > 0 || kk > 0);
-                    }
-                    if (h == 1) {
-                        mma_commit(&pvdone[s]);
-                        mma_commit(&empty[x % C::NS]);
-                    }
+                    for (int k = 0; k < C::KEYS / 16; ++k)
+                        mma_ts(t_o, t_p + k * 8, v + k * (2 * C::GROUP >> 4), id_o, i > 0 || k > 0);
+                    mma_commit(&pvdone[s]);
+                    mma_commit(&empty[x % C::NS]);
                 }
                 __syncwarp();
             };
             bool ok = true;
             if (mine > 0) {
-                ok = wait(qfull, 0) && landed(2 * tile_of(0));
-                // half a period behind stream 0: one stream's softmax under the other's MMAs
-                // (started together they stay together, 15 % slower)
-                if (ok && s == 1) ok = wait(&pfull[0], 0);
+                ok = both(2 * tile_of(0), qfull, 0);
                 if (ok) qk(0);
             }
             for (int i = 0; i < mine && ok; ++i) {
-                ok = landed(2 * tile_of(i) + 1) && (i + 1 == mine || landed(2 * tile_of(i + 1))) &&
-                     wait(&pfull[2 * s], i & 1);
-                if (!ok) break;
-                pv(i, 0);
-                if (!(ok = wait(&pfull[2 * s + 1], i & 1))) break;
-                pv(i, 1);
-                if (i + 1 < mine) {
-                    // the next S overwrites this P, which the product above reads
-                    if (!(ok = wait(&pvdone[s], i & 1))) break;
+                if (i + 1 < mine) {  // S of the next tile under this one's softmax
+                    if (!(ok = both(2 * tile_of(i + 1), &sfree[s], i))) break;
                     qk(i + 1);
                 }
+                if (!(ok = both(2 * tile_of(i) + 1, &pfull[s], i))) break;
+                pv(i);
             }
             if (!ok && lane == 0) give_up();
             if (elect_one()) {
@@ -355,7 +402,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         // --------------------------------------------- softmax, one thread per row
         const int s = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-        const uint32_t ts = tmem + lanes + s * kKeys, to = tmem + lanes + 256 + s * 128;
+        const uint32_t ts = tmem + lanes + s * C::COL_STREAM, to = tmem + lanes + C::COL_O + s * D;
         const int tile = 2 * pair + (solo ? 0 : s);
         const int bt = tile * tokens + row / a.G;
         const bool live = row < tokens * a.G && bt < a.B * a.Q;
@@ -367,23 +414,33 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = __all_sync(~0u, mbar_wait(&sfull[s], i & 1, abort_flag, a.wait_limit));
             if (!ok) break;
             tc_fence_after();
-            float z[kKeys];
+            float z[C::KEYS];
 #pragma unroll
-            for (int c = 0; c < 4; ++c) tmem_ld32x32b<32>(ts + c * 32, z + c * 32);
+            for (int c = 0; c < C::KEYS / 32; ++c) tmem_ld32x32b<32>(ts + c * 32, z + c * 32);
+            if constexpr (C::KEYS % 32 != 0)
+                tmem_ld32x32b<C::KEYS % 32>(ts + C::KEYS / 32 * 32, z + C::KEYS / 32 * 32);
             tmem_ld_wait();
-            const int valid = hi - lo - t * kKeys;  // keys of this tile
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&sfree[s]);  // the next S may be computed
+            const int valid = hi - lo - t * C::KEYS;  // keys of this tile
             float scale = a.scale_log2;
-            if (valid < kKeys || scale < 0.f) {  // uniform; the maximum below wants scale >= 0
+            if (valid < C::KEYS || scale < 0.f) {  // uniform; the maximum below wants scale >= 0
 #pragma unroll
-                for (int c = 0; c < kKeys; ++c) z[c] = c < valid ? z[c] * scale : -INFINITY;
+                for (int c = 0; c < C::KEYS; ++c) z[c] = c < valid ? z[c] * scale : -INFINITY;
                 scale = 1.f;
             }
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
-            for (int c = 0; c < kKeys; c += 8)
+            for (int c = 0; c < C::KEYS; c += 8)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = max3(x[j], z[c + 2 * j], z[c + 2 * j + 1]);
             const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
+            // O is at rest and P has been read once the last P V has completed
+            auto last_done = [&] {
+                return i == 0 || __all_sync(~0u, mbar_wait(&pvdone[s], (i - 1) & 1, abort_flag,
+                                                           a.wait_limit));
+            };
             if (i == 0) {
                 m = top == -INFINITY ? 0.f : top;
             } else if (__any_sync(~0u, live && top > m + kRenew)) {
@@ -391,7 +448,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 const float f = ex2(m - next);
                 m = next;
                 l *= f;
-                // O is at rest: S of this tile was issued after the last P V had completed
+                if (!(ok = last_done())) break;
                 tc_fence_after();
 #pragma unroll
                 for (int c = 0; c < D / 32; ++c) {
@@ -401,45 +458,46 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                     tmem_ld_wait();
 #pragma unroll
                     for (int j = 0; j < 32; ++j) r[j] = __float_as_uint(o[j] * f);
-                    tmem_st32(to + c * 32, r);
+                    tmem_st32x32b<32>(to + c * 32, r);
                 }
             }
-            if (valid < kKeys) {
+            if (valid < C::KEYS) {
                 // V's rows past the end hold anything; their weights are 0, so they must be finite
                 const int v = 2 * t + 1;
                 ok = __all_sync(~0u, mbar_wait(&full[v % C::NS], (v / C::NS) & 1, abort_flag,
                                                a.wait_limit));
                 if (!ok) break;
                 uint8_t* vt = smem + C::OFF_KV + (v % C::NS) * C::TILE;
-                for (int c = row; c < (kKeys - valid) * 8 * C::HALVES; c += 128) {
-                    const int h = c / ((kKeys - valid) * 8), at = c % ((kKeys - valid) * 8);
-                    *reinterpret_cast<uint4*>(vt + h * kHalf + valid * 128 + at * 16) =
-                        make_uint4(0u, 0u, 0u, 0u);
+                for (int c = row; c < (C::KEYS - valid) * 8 * C::HALVES; c += 128) {
+                    const int key = valid + c / (8 * C::HALVES), at = c % (8 * C::HALVES);
+                    *reinterpret_cast<uint4*>(vt + key / 8 * C::GROUP + at / 8 * 1024 +
+                                              key % 8 * 128 + at % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
             }
             float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
             const float2 scale2 = make_float2(scale, scale), less_m = make_float2(-m, -m);
+            uint32_t p[C::KEYS / 2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                uint32_t p[32];
-#pragma unroll
-                for (int c = 0; c < 32; ++c) {
-                    float2 e = fma2(make_float2(z[h * 64 + 2 * c], z[h * 64 + 2 * c + 1]), scale2,
-                                    less_m);
-                    e.x = ex2(e.x);
-                    e.y = ex2(e.y);
-                    sum[c & 1] = add2(sum[c & 1], e);
-                    p[c] = Elem<T>::pack(e.x, e.y);
-                }
-                tmem_st32(ts + h * 32, p);
-                tmem_st_wait();
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&pfull[2 * s + h]);  // the product may start on it
+            for (int c = 0; c < C::KEYS / 2; ++c) {
+                float2 e = fma2(make_float2(z[2 * c], z[2 * c + 1]), scale2, less_m);
+                e.x = ex2(e.x);
+                e.y = ex2(e.y);
+                sum[c & 1] = add2(sum[c & 1], e);
+                p[c] = Elem<T>::pack(e.x, e.y);
             }
             const float2 both = add2(sum[0], sum[1]);
             l += both.x + both.y;
+            if (!(ok = last_done())) break;
+            tc_fence_after();
+#pragma unroll
+            for (int c = 0; c < C::KEYS / 64; ++c) tmem_st32x32b<32>(ts + C::COL_P + c * 32, p + c * 32);
+            if constexpr (C::KEYS % 64 != 0)
+                tmem_st32x32b<C::KEYS % 64 / 2>(ts + C::COL_P + C::KEYS / 64 * 32, p + C::KEYS / 64 * 32);
+            tmem_st_wait();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&pfull[s]);
         }
         if (mine > 0 && ok)
             ok = __all_sync(~0u, mbar_wait(&pvdone[s], (mine - 1) & 1, abort_flag, a.wait_limit));
@@ -482,8 +540,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             f1 *= inv;
             // Rows leave through the stream's own Q tile (its products are done): a thread
             // holds a row, a warp writes whole rows.  16-byte chunks are xor-ed with the row.
-            constexpr int kCols = C::TILE / (128 * 4), kChunk = kCols / 4;
-            uint8_t* stage = smem + s * C::TILE;
+            constexpr int kCols = C::QTILE / (128 * 4), kChunk = kCols / 4;
+            uint8_t* stage = smem + s * C::QTILE;
             const int r0 = row & ~31;
             const long long part =
                 ((long long)bt * a.Hq + hk * a.G + row % a.G) * total_splits + split;
@@ -532,35 +590,39 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     }
 }
 
-// 4D map of 16-bit elements: box [64, rows of one page or token group ...], 128-byte swizzle.
-CUresult make_map_4d(CUtensorMap* m, const void* base, const uint64_t (&dims)[4],
-                     const uint64_t (&strides)[3], const uint32_t (&box)[4]) {
+// Map of 16-bit elements with a 128-byte inner box, swizzled at that width.
+template <int N>
+CUresult make_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[N],
+                  const cuuint64_t (&strides)[N - 1], const cuuint32_t (&box)[N]) {
     auto enc = tensor_map_encoder();
     if (!enc) return CUDA_ERROR_NOT_SUPPORTED;
-    const cuuint64_t d[4] = {dims[0], dims[1], dims[2], dims[3]};
-    const cuuint64_t st[3] = {strides[0], strides[1], strides[2]};
-    const cuuint32_t b[4] = {box[0], box[1], box[2], box[3]};
-    const cuuint32_t one[4] = {1, 1, 1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, 4, const_cast<void*>(base), d, st, b, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
+    const cuuint32_t one[5] = {1, 1, 1, 1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT16, N, const_cast<void*>(base), dims, strides, box,
+               one, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <typename T, int D>
-cudaError_t launch_prefix_t(const AttnArgs& a, cudaStream_t s) {
+cudaError_t launch_prefix_t(const AttnArgs& args, cudaStream_t s) {
     using C = PrefixCfg<D>;
+    AttnArgs a = args;
+    // keys per copy: a whole page where it divides the tile, else 16 (no page is smaller)
+    a.prefix_unit = C::KEYS % a.page_size == 0 ? a.page_size : 16;
     CUtensorMap tq, tk, tv;
-    const int tokens = kKeys / a.G;
+    const int tokens = kRows / a.G;
     const uint64_t row = D * 2;
-    const uint64_t qd[4] = {(uint64_t)D, (uint64_t)a.G, (uint64_t)a.Hkv, (uint64_t)a.B * a.Q};
-    const uint64_t qs[3] = {row, row * a.G, row * a.Hq};
-    const uint32_t qb[4] = {64, (uint32_t)a.G, 1, (uint32_t)tokens};
-    const uint64_t kd[4] = {(uint64_t)D, (uint64_t)a.page_size, (uint64_t)a.Hkv, (uint64_t)a.pages};
-    const uint64_t ks[3] = {row, row * a.page_size, row * a.page_size * a.Hkv};
-    const uint32_t kb[4] = {64, (uint32_t)a.page_size, 1, 1};
-    if (make_map_4d(&tq, a.q, qd, qs, qb) != CUDA_SUCCESS ||
-        make_map_4d(&tk, a.k, kd, ks, kb) != CUDA_SUCCESS ||
-        make_map_4d(&tv, a.v, kd, ks, kb) != CUDA_SUCCESS)
+    // q: 64 columns, the heads of a group, groups, tokens
+    const cuuint64_t qd[4] = {(uint64_t)D, (uint64_t)a.G, (uint64_t)a.Hkv, (uint64_t)a.B * a.Q};
+    const cuuint64_t qs[3] = {row, row * a.G, row * a.Hq};
+    const cuuint32_t qb[4] = {64, (uint32_t)a.G, 1, (uint32_t)tokens};
+    // K, V: 64 columns, 8 keys, the halves of a row, groups of 8 keys, pages and heads
+    const cuuint64_t kd[5] = {64, 8, (uint64_t)C::HALVES, (uint64_t)a.page_size / 8,
+                              (uint64_t)a.pages * a.Hkv};
+    const cuuint64_t ks[4] = {row, 128, row * 8, row * a.page_size};
+    const cuuint32_t kb[5] = {64, 8, (uint32_t)C::HALVES, (uint32_t)a.prefix_unit / 8, 1};
+    if (make_map<4>(&tq, a.q, qd, qs, qb) != CUDA_SUCCESS ||
+        make_map<5>(&tk, a.k, kd, ks, kb) != CUDA_SUCCESS ||
+        make_map<5>(&tv, a.v, kd, ks, kb) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
