@@ -500,9 +500,14 @@ def idx_score_topk_routed(q, k, k_scale, w, ks, ke, topk: int, *, max_len: int =
 # The serving operators are called per layer and token, so their bindings keep the host's
 # part short: one pass over the tensors, and the device switched only when it differs.
 
+# the current stream's handle without a Stream object (a microsecond less), where torch has it
+_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _raw_stream(stream, index: int) -> int:
     if stream is None:
-        return torch.cuda.current_stream(index).cuda_stream
+        return _current_handle(index)
     return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
 
 
@@ -513,7 +518,10 @@ def _serve_device(fn: str, *ts) -> int:
         if t is None:
             continue
         i = t.get_device()
-        if i != index:
+        if i == index:
+            if t.is_contiguous():
+                continue
+        else:
             if i < 0:
                 raise ValueError(f"{fn}: every tensor must live on a CUDA device")
             if index is not None:
@@ -526,12 +534,14 @@ def _serve_device(fn: str, *ts) -> int:
 
 def _serve_call(fn: str, f, index: int, args, options, stats, stream):
     """f(*args, options, stream) with the tensors' device current."""
-    o = make_options(options, stats)
+    o = None
+    if options is not None or stats is not None:
+        o = _opt_ref(make_options(options, stats))
     if torch.cuda.current_device() == index:
-        code = f(*args, _opt_ref(o), _raw_stream(stream, index))
+        code = f(*args, o, _raw_stream(stream, index))
     else:
         with torch.cuda.device(index):
-            code = f(*args, _opt_ref(o), _raw_stream(stream, index))
+            code = f(*args, o, _raw_stream(stream, index))
     if code:
         _check(fn, code)
 

@@ -105,29 +105,27 @@ __global__ void __launch_bounds__(kPartWarps * 32) attn_part_kernel(AttnArgs a) 
     const int total_splits = a.prefix_splits + a.private_splits;
     const int slot = a.prefix_splits + split;
 
-    int n = a.lens[b];
-    if ((n < 0 || n > a.max_len) && tid == 0) raise_status(a.d_status, IDX_DEV_RANGE);
-    n = min(max(n, 0), a.max_len);
-    const int lo = split * a.private_chunk, hi = min(n, lo + a.private_chunk);
+    const int lo = split * a.private_chunk;
     const int* table = a.table + (long long)b * a.table_stride;
+    // The length, the first pages and q are on their way together: the pages are looked up to
+    // max_len, which the table covers.
+    int n = a.lens[b];
+    int pages_from = 0, page_of = 0;  // 32 steps of this warp at a time, one per lane
+    const int far = min(a.max_len, lo + a.private_chunk);
+    auto look_up = [&](int i) {
+        pages_from = i;
+        const int at = lo + ((i + lane) * kPartWarps + warp) * kStep;
+        page_of = at < far ? table[at >> a.page_shift] : 0;
+    };
+    look_up(0);
 
     // row i of the block: query token t, head g of the group
     auto query_row = [&](int i) {
         const int r = rb * 16 + i, t = r / a.G;
         return ((long long)b * a.Q + t) * a.Hq + hk * a.G + (r - t * a.G);
     };
-    if (lo >= hi) {  // no keys in this part
-        for (int i = tid; i < 16 && rb * 16 + i < rows; i += kPartWarps * 32)
-            a.part_lse[query_row(i) * total_splits + slot] = -INFINITY;
-        if (last) pdl_wait();
-        return;
-    }
     const int r0 = rb * 16 + lane / 4, r1 = r0 + 8;  // this thread's two rows
     const bool live0 = r0 < rows, live1 = r1 < rows;
-    // keys a row sees: all but the tokens after its own
-    const int see0 = live0 ? n - (a.Q - 1 - r0 / a.G) : 0;
-    const int see1 = live1 ? n - (a.Q - 1 - r1 / a.G) : 0;
-
     uint32_t qf[D / 16][4];
     {
         const T* q = static_cast<const T*>(a.q);
@@ -142,19 +140,24 @@ __global__ void __launch_bounds__(kPartWarps * 32) attn_part_kernel(AttnArgs a) 
         }
     }
 
+    if ((n < 0 || n > a.max_len) && tid == 0) raise_status(a.d_status, IDX_DEV_RANGE);
+    n = min(max(n, 0), a.max_len);
+    const int hi = min(n, lo + a.private_chunk);
+    if (lo >= hi) {  // no keys in this part
+        for (int i = tid; i < 16 && rb * 16 + i < rows; i += kPartWarps * 32)
+            a.part_lse[query_row(i) * total_splits + slot] = -INFINITY;
+        if (last) pdl_wait();
+        return;
+    }
+    // keys a row sees: all but the tokens after its own
+    const int see0 = live0 ? n - (a.Q - 1 - r0 / a.G) : 0;
+    const int see1 = live1 ? n - (a.Q - 1 - r1 / a.G) : 0;
+
     constexpr int kRowBytes = D * 2, kChunks = D / 8, kTile = kStep * kRowBytes;
     const uint32_t ring = smem_u32(smem) + warp * kStages * 2 * kTile;
     const int steps = (hi - lo + kStep - 1) / kStep;
     const int mine = warp < steps ? (steps - 1 - warp) / kPartWarps + 1 : 0;
     bool bad = false;
-    // a warp's pages are looked up 32 steps at a time, one per lane
-    int pages_from = 0, page_of = 0;
-    auto look_up = [&](int i) {
-        pages_from = i;
-        const int at = lo + ((i + lane) * kPartWarps + warp) * kStep;
-        page_of = i + lane < mine ? table[at >> a.page_shift] : 0;
-    };
-    look_up(0);
     auto fetch = [&](int i) {
         if (i - pages_from >= 32) look_up(i);
         const int page = __shfl_sync(~0u, page_of, i - pages_from);
@@ -475,7 +478,7 @@ cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStre
     // A block per row while there are few rows with many parts (a warp alone takes its
     // batches of parts one after the other: 512 rows x 20 parts 6.0 us, by blocks XX us).
     const long long rows = (long long)a.B * a.Q * a.Hq;
-    const bool wide = a.prefix_splits + a.private_splits > 8 && rows <= 32ll * sm_count;
+    const bool wide = a.prefix_splits + a.private_splits > 8 && rows <= 4ll * sm_count;
     const int per_block = wide ? 1 : kJoinWarps;
     const long long join_blocks = (rows + per_block - 1) / per_block;
     const long long weight_blocks =
@@ -494,16 +497,6 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
                    int sm_count) {
     AttnPlan p;
     const int G = Hq / Hkv;
-    auto cut = [&](long long items, int len, int& splits, int& chunk) {
-        splits = chunk = 0;
-        if (len <= 0) return;
-        // about eight blocks per SM, at least 256 keys each
-        long long want = (8ll * sm_count + items - 1) / items;
-        const long long most = (len + 255) / 256;
-        want = want < most ? want : most;
-        chunk = (int)(((len + want - 1) / want + 63) / 64 * 64);
-        splits = (len + chunk - 1) / chunk;
-    };
     p.prefix_splits = p.prefix_chunk = 0;
     if (prefix_len > 0) {
         // Key tiles per part: one CTA per SM takes about 1 us per 128 keys of a pair of
@@ -531,7 +524,32 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
         }
         p.prefix_splits = (prefix_len + p.prefix_chunk - 1) / p.prefix_chunk;
     }
-    cut((long long)(Q * G + 15) / 16 * Hkv * B, max_len, p.private_splits, p.private_chunk);
+    p.private_splits = p.private_chunk = 0;
+    if (max_len > 0) {
+        // Keys per private part: a block takes about 4 us and, among the three that an SM
+        // holds, 34 ns per key (D = 128: 512 bytes at a third of the SM's share of HBM), so
+        // whole waves of long parts are cheap but a wave that is mostly empty is not; the
+        // join reads D floats per row and part.  The lengths are on the device: the mean of
+        // the times with all of them at max_len and at half of it is taken.
+        const long long items = (long long)(Q * G + 15) / 16 * Hkv * B;
+        const int steps = (max_len + 63) / 64;  // of 64 keys: four warps' 16
+        auto waves = [&](long long blocks) {
+            return (double)((blocks + 3 * sm_count - 1) / (3 * sm_count));
+        };
+        double best = 0;
+        for (int s = 1; s <= 32 && s <= steps; ++s) {
+            const int chunk = (steps + s - 1) / s;
+            const long long all = (steps + chunk - 1) / chunk, half = (steps / 2 + chunk) / chunk;
+            const double us = (waves(items * all) + waves(items * half)) / 2 *
+                                  (chunk * 64 * (D * 34e-3 / 128) + 4.0) +
+                              (double)B * Q * Hq * s * D * 8 / 5e6;
+            if (best == 0 || us < best) {
+                best = us;
+                p.private_chunk = chunk * 64;
+            }
+        }
+        p.private_splits = (max_len + p.private_chunk - 1) / p.private_chunk;
+    }
     const size_t rows = (size_t)B * Q * Hq, splits = p.prefix_splits + p.private_splits;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     p.logit_stride = ((long long)max_len + 15) / 16 * 16;
