@@ -10,10 +10,10 @@
 //
 // Selection: slots are ranked by a 32-bit key whose unsigned order is the weights'
 // order (protected slots hold the largest key).  One pass reads weights and positions,
-// leaves the keys in shared memory and finds their range; then a histogram of 2048 bins
-// over the range finds the bin that holds the rank, which is the next range.  The bits
-// of a float grow with its logarithm, so heavy-tailed weights spread over the bins, and
-// a bin is usually decided (all of it stays) after two.  Few long rows take a cluster
+// leaves the keys in shared memory and finds their range; then a histogram over the range
+// (1024 bins, for short rows 512) finds the bin that holds the rank, which is the next
+// range.  The bits of a float grow with its logarithm, so heavy-tailed weights spread over
+// the bins, and a bin is usually decided (all of it stays) after two.  Few long rows take a cluster
 // of CTAs each, every CTA with a slice of the row and the histograms summed through
 // distributed shared memory.  The moves are a second launch, so that they spread over the
 // whole GPU whichever rows they belong to.  HBM-bound: 8 bytes per slot read, 8 per kept
@@ -31,7 +31,7 @@ namespace idx {
 
 namespace {
 
-constexpr int kBinsPerThread = 4;
+constexpr int kBinsPerThread = 2;
 constexpr int kMaxCluster = 8;           // the portable limit
 constexpr int kSliceMax = 48 * 1024;     // keys a CTA keeps in shared memory
 constexpr uint32_t kProtected = 0xffffffffu;
@@ -89,7 +89,7 @@ template <bool CLUSTER, bool STAGED, int kThreads>
 __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int C) {
     using S = Shared<kThreads>;
     constexpr int kWarps = S::kWarps, kBins = S::kBins;
-    constexpr int kBinBits = kThreads == 256 ? 10 : 11;
+    constexpr int kBinBits = kThreads == 256 ? 9 : 10;
     static_assert(kBins == 1 << kBinBits, "");
     __shared__ S sh;
     extern __shared__ uint32_t keys[];
@@ -110,7 +110,6 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     const bool bad = n < 0 || n > a.max_len;
     n = min(max(n, 0), a.max_len);
     const int keep = min(n, a.budget);
-    pdl_trigger();
     if (rank == 0 && tid == 0) {
         if (h == 0) a.lens_out[b] = keep;
         if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
@@ -206,26 +205,24 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
                 if (d <= span) atomicAdd(&hist[d >> shift], 1u);
             }
             sync_all();
-            // counts from the top: thread t has the four bins below kBins - 4 t
+            // counts from the top: thread t has the two bins below kBins - 2 t
             const int low_bin = kBins - kBinsPerThread * (tid + 1);
-            uint32_t c[kBinsPerThread] = {0u, 0u, 0u, 0u};
+            uint32_t c[kBinsPerThread] = {0u, 0u};
             {
-                uint4 v[CLUSTER ? kMaxCluster : 1];
+                uint2 v[CLUSTER ? kMaxCluster : 1];
 #pragma unroll
                 for (int r = 0; r < (CLUSTER ? kMaxCluster : 1); ++r)
-                    v[r] = r < C ? *reinterpret_cast<const uint4*>(&of(r).hist[pass & 1][low_bin])
-                                 : make_uint4(0u, 0u, 0u, 0u);
+                    v[r] = r < C ? *reinterpret_cast<const uint2*>(&of(r).hist[pass & 1][low_bin])
+                                 : make_uint2(0u, 0u);
 #pragma unroll
                 for (int r = 0; r < (CLUSTER ? kMaxCluster : 1); ++r) {
-                    c[0] += v[r].w;
-                    c[1] += v[r].z;
-                    c[2] += v[r].y;
-                    c[3] += v[r].x;
+                    c[0] += v[r].y;
+                    c[1] += v[r].x;
                 }
             }
-            const uint32_t sum = c[0] + c[1] + c[2] + c[3];
+            const uint32_t sum = c[0] + c[1];
             // (the other buffer has been read by nobody since the last sync_all)
-            *reinterpret_cast<uint4*>(&sh.hist[(pass & 1) ^ 1][low_bin]) = make_uint4(0u, 0u, 0u, 0u);
+            *reinterpret_cast<uint2*>(&sh.hist[(pass & 1) ^ 1][low_bin]) = make_uint2(0u, 0u);
             const uint32_t run = (uint32_t)warp_scan((int)sum, lane);
             if (lane == 31) sh.warp_sum[warp] = run;
             __syncthreads();
@@ -265,15 +262,17 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     const int g0 = min(warp * per, mine), g1 = min(g0 + per, mine);
     {
         int cnt[4] = {0, 0, 0, 0};
-        const int stop = min(first + g1 * 32, end);
+        const int begin = first + g0 * 32, stop = min(first + g1 * 32, end);
+        auto count = [&](int from, int to, int& gt, int& eq) {
 #pragma unroll 4
-        for (int j = first + g0 * 32 + lane; j < stop; j += 32) {
-            const uint32_t k = key_of(j);
-            if (k < cut) continue;
-            const int i = (j < keep ? 0 : 1) + (k == cut ? 2 : 0);
-#pragma unroll
-            for (int c = 0; c < 4; ++c) cnt[c] += i == c;
-        }
+            for (int j = from + lane; j < to; j += 32) {
+                const uint32_t k = key_of(j);
+                gt += k > cut;
+                eq += k == cut;
+            }
+        };
+        count(begin, min(stop, keep), cnt[0], cnt[2]);
+        count(max(begin, keep), stop, cnt[1], cnt[3]);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int v = __reduce_add_sync(~0u, cnt[i]);
@@ -329,29 +328,38 @@ __global__ void __launch_bounds__(kThreads) evict_select_kernel(EvictArgs a, int
     int* dst = a.moves + (long long)bh * 2 * a.max_moves;
     int* src = dst + a.max_moves;
     const uint32_t lt = (1u << lane) - 1u;
-#pragma unroll 4
-    for (int g = g0; g < g1; ++g) {
-        const int j0 = first + g * 32, j = j0 + lane;
-        const uint32_t k = j < end ? key_of(j) : 0u;
-        bool stays = j < end && k > cut;
-        const uint32_t meq = __ballot_sync(~0u, j < end && k == cut);
-        if (meq) {
-            stays |= (meq >> lane & 1u) && eq + __popc(meq & lt) < ties;
-            eq += __popc(meq);
+    constexpr int kAhead = 4;  // groups whose keys are read and voted on together
+    for (int g = g0; g < g1; g += kAhead) {
+        uint32_t mgt[kAhead], meq[kAhead];
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int j = first + (g + u) * 32 + lane;
+            const bool in = g + u < g1 && j < end;
+            const uint32_t k = in ? key_of(j) : 0u;
+            mgt[u] = __ballot_sync(~0u, in && k > cut);
+            meq[u] = __ballot_sync(~0u, in && k == cut);
         }
-        // holes are the slots below `keep` that go, sources those from it on that stay
-        const uint32_t hit = __ballot_sync(~0u, j < keep ? !stays : stays);
-        if (!hit) continue;
-        const int low = min(max(keep - j0, 0), 32);
-        const uint32_t holes = hit & (low < 32 ? (1u << low) - 1u : ~0u), srcs = hit & ~holes;
-        if (hit >> lane & 1u) {
-            if (j < keep)
-                dst[hole + __popc(holes & lt)] = j;
-            else
-                src[from + __popc(srcs & lt)] = j;
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            if (g + u >= g1) break;
+            const int j0 = first + (g + u) * 32;
+            uint32_t stays = mgt[u];
+            if (meq[u]) {
+                const uint32_t tie = __ballot_sync(~0u, (meq[u] >> lane & 1u) &&
+                                                            eq + __popc(meq[u] & lt) < ties);
+                stays |= tie;
+                eq += __popc(meq[u]);
+            }
+            // holes are the slots below `keep` that go, sources those from it on that stay
+            // (`keep` is the budget here, so every slot below it exists)
+            const int low = min(max(keep - j0, 0), 32);
+            const uint32_t below = low < 32 ? (1u << low) - 1u : ~0u;
+            const uint32_t holes = below & ~stays, srcs = stays & ~below;
+            if (holes >> lane & 1u) dst[hole + __popc(holes & lt)] = j0 + lane;
+            if (srcs >> lane & 1u) src[from + __popc(srcs & lt)] = j0 + lane;
+            hole += __popc(holes);
+            from += __popc(srcs);
         }
-        hole += __popc(holes);
-        from += __popc(srcs);
     }
 }
 
