@@ -50,14 +50,17 @@ template <int D> struct PrefixCfg {
     static constexpr int QTILE = HALVES * kHalfQ;
     static constexpr int GROUP = HALVES * 1024;              // 8 keys of a K or V tile
     static constexpr int TILE = KEYS / 8 * GROUP;
-    static constexpr int NS = D == 128 ? 7 : 8;              // ring slots (>= 7: two streams
-                                                             // over tiles of their own)
+    // Ring slots, K and V tiles in turn.  An even number, so that a slot only ever holds K or
+    // only V and its one producer sees every phase of its barriers: with an odd number a
+    // producer could wait on a slot whose last tile but one, of the other producer's, was
+    // still wanted, and the parity of its wait would let it through.
+    static constexpr int NS = 8;
+    static_assert(NS % 2 == 0, "");
     static constexpr int OFF_KV = 2 * QTILE;
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
     static constexpr int NBAR = 1 + 2 * NS + 10;
-    static constexpr int OFF_CTL = OFF_BAR + NBAR * 8;       // [0] TMEM base, [1] abort flag,
-                                                             // [2] [3] the producers' next tiles
-    static constexpr int OFF_ML = OFF_CTL + 16;              // the odd stream's m and l
+    static constexpr int OFF_CTL = OFF_BAR + NBAR * 8;       // [0] TMEM base, [1] abort flag
+    static constexpr int OFF_ML = OFF_CTL + 8;              // the odd stream's m and l
     static constexpr int SMEM = OFF_ML + kRows * 8 + 1024;
     // TMEM columns: S and P of a stream, then both O
     static constexpr int COL_P = KEYS, COL_STREAM = D == 128 ? 128 : KEYS + KEYS / 2;
@@ -248,7 +251,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     };
     const int first = a.withhold_tile >= 0 ? min(2 * n, 2 * a.withhold_tile) : 2 * n;  // tiles that come
-    constexpr int kFirstK = (C::NS + 1) / 2;
+    constexpr int kFirstK = C::NS / 2;
     if (warp == 9) {
         int page[kFirstK];  // on their way while the barriers are set up
 #pragma unroll
@@ -317,15 +320,10 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 page = next;
             }
             if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
-            // Nothing may be in flight when the CTA ends: the last copy into every slot has
-            // landed (tile y, when tile y + NS has not been issued; a slot's earlier copies
-            // were consumed before its next one).
-            volatile int* next = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 8);
-            if (lane == 0) next[x & 1] = min(x, first + ((x ^ first) & 1));
-            named_bar_sync(2, 64);
-            for (int y = next[x & 1] - 2; y >= 0 && y > x - 4 * C::NS; y -= 2)
-                if (y + C::NS >= next[(y + C::NS) & 1])
-                    mbar_wait(&full[y % C::NS], (y / C::NS) & 1, nullptr, 1ll << 28);
+            // Nothing may be in flight when the CTA ends: the last copy into each of this
+            // warp's slots has landed.
+            for (int y = x - 2; y >= 0 && y >= x - C::NS; y -= 2)
+                if (y < first) mbar_wait(&full[y % C::NS], (y / C::NS) & 1, nullptr, 1ll << 28);
             if (warp == 9) mbar_wait(qfull, 0, nullptr, 1ll << 28);
             __syncwarp();
         } else {

@@ -109,6 +109,14 @@ def test_long_prefix(idx, dtype, D):
     check(idx, make([30, 500], 1, 8, 1, D, 20000, 64, dtype, seed=D), max_len=500)
 
 
+@pytest.mark.parametrize("B,Q,prefix", [(2, 1, 24000), (3, 3, 30011), (70, 1, 12000)])
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, FP16)])
+def test_many_tiles_per_part(idx, B, Q, prefix, D, dtype):
+    """Eight key heads leave few parts per head, so every one has many key tiles: more than
+    the ring of copies holds, for one row tile (its even and odd tiles run apart) and for two."""
+    check(idx, make([5 + Q] * B, Q, 2, 8, D, prefix, 64, dtype, seed=B, weights=False))
+
+
 def test_sharp_and_flat_logits(idx):
     """One key holds all the weight; all keys hold the same."""
     s = make([200, 90], 1, 4, 2, 128, 500, 64, BF16, seed=2, qscale=12.0)
