@@ -544,6 +544,7 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
         auto consider = [&](long long t) {  // t tiles per part
             t = t < 1 ? 1 : t > tiles ? tiles : t;
             const long long s = (tiles + t - 1) / t;
+            if (s > 65535) return;  // a grid dimension
             const double us = (double)((items * s + sm_count - 1) / sm_count) * (t * per_tile + 4.0) +
                               (double)B * Q * Hq * s * D * 8 / 5e6;
             if (best == 0 || us < best) {
@@ -552,6 +553,7 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
             }
         };
         for (int t = 1; t <= 4; ++t) consider(t);
+        consider((tiles + 1023) / 1024);
         for (long long waves = 1; waves <= 6; ++waves) {  // as many parts as fill whole waves
             const long long s = waves * sm_count / items;
             consider((tiles + (s > 0 ? s : 1) - 1) / (s > 0 ? s : 1));

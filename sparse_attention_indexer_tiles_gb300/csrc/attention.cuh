@@ -36,7 +36,8 @@ struct AttnArgs {
     int B, Q, Hq, Hkv, G, D, pages, page_size, page_shift;
     int prefix_len, max_len;
     int prefix_splits, prefix_chunk;    // keys per prefix part (whole key tiles)
-    int prefix_unit;                    // keys per copy (set by launch_prefix_parts)
+    int prefix_unit, prefix_tokens;     // keys per copy, query tokens per row tile (set by
+                                        // launch_prefix_parts)
     int private_splits, private_chunk;  // keys per private part (a multiple of 64)
     float scale_log2;                   // scale * log2(e)
     long long wait_limit;               // SM clocks a wait of the prefix kernel may take

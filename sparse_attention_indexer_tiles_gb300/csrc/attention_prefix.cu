@@ -210,12 +210,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     pdl_trigger();  // the private parts may take the SMs that this grid leaves idle
 
     // this CTA: key head, pair of row tiles, part of the prefix
-    const int tokens = kRows / a.G;  // query tokens per row tile (its rows: tokens * G <= 128)
-    const int ntiles = (a.B * a.Q + tokens - 1) / tokens, npairs = (ntiles + 1) / 2;
-    const int split = blockIdx.x % a.prefix_splits;
-    const int pair = blockIdx.x / a.prefix_splits % npairs;
-    const int hk = blockIdx.x / a.prefix_splits / npairs;
-    const bool solo = 2 * pair + 1 == ntiles;
+    const int tokens = a.prefix_tokens;  // query tokens per row tile (its rows: tokens * G <= 128)
+    const int pair = blockIdx.x, split = blockIdx.y, hk = blockIdx.z;
+    const bool solo = (2 * pair + 1) * tokens >= a.B * a.Q;
     const int lo = split * a.prefix_chunk, hi = min(a.prefix_len, lo + a.prefix_chunk);
     const int n = (hi - lo + C::KEYS - 1) / C::KEYS;  // key tiles, at least one
 
@@ -251,30 +248,26 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         }
     };
     const int first = a.withhold_tile >= 0 ? min(2 * n, 2 * a.withhold_tile) : 2 * n;  // tiles that come
-    constexpr int kFirstK = C::NS / 2;
+    int page = 0;  // of the producer's next tile, looked up ahead
+    if (warp == 9 || warp == 11) page = page_of(warp == 11);
     if (warp == 9) {
-        int page[kFirstK];  // on their way while the barriers are set up
-#pragma unroll
-        for (int i = 0; i < kFirstK; ++i) page[i] = page_of(2 * i);
         if (lane == 0) {
             prefetch_tmap(&tm_q);
             prefetch_tmap(&tm_k);
             prefetch_tmap(&tm_v);
-            mbar_init(qfull, 1);
-            for (int i = 0; i < C::NS; ++i) {
-                mbar_init(&full[i], 1);
-                mbar_init(&empty[i], solo ? 1 : 2);  // the streams that read a tile
-            }
-            for (int i = 0; i < 2; ++i) {
-                mbar_init(&sfull[i], 1);
-                mbar_init(&sfree[i], 4);
-                mbar_init(&pfull[i], 4);
-                mbar_init(&pvdone[i], 1);
-                mbar_init(&done[i], 1);
-            }
             *abort_flag = 0;
-            fence_barrier_init();
-            // the first copies do not wait for the rest of the block
+        }
+        // a barrier per lane, in their order: q; full, empty (the streams that read a tile);
+        // per stream S, S free, P (a warp each), P V, done
+        for (int i = lane; i < C::NBAR; i += 32) {
+            const int k = (i - 1 - 2 * C::NS) / 2;
+            mbar_init(qfull + i, i <= C::NS ? 1 : i <= 2 * C::NS ? (solo ? 1 : 2)
+                                                                 : k == 1 || k == 2 ? 4 : 1);
+        }
+        fence_barrier_init();
+        __syncwarp();
+        if (lane == 0) {
+            // q does not wait for the rest of the block
             const int tiles = solo ? 1 : 2;
             mbar_arrive_expect_tx(qfull, tiles * C::HALVES * tokens * a.G * 128);
             for (int t = 0; t < tiles; ++t)
@@ -283,9 +276,6 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                                 hk, (2 * pair + t) * tokens);
         }
         __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kFirstK; ++i)
-            if (2 * i < first) fetch(2 * i, page[i]);
     }
     if (warp == 8) {
         tmem_alloc(const_cast<uint32_t*>(tslot), 512);
@@ -304,8 +294,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         regs_less();
         if (warp == 9 || warp == 11) {
             // ----------------------------------------- TMA producers: K tiles, V tiles
-            int x = warp == 9 ? 2 * kFirstK : 1;
-            int page = page_of(x);
+            int x = warp == 11;
             for (; x < first; x += 2) {
                 const int next = page_of(x + 2);  // looked up a tile ahead
                 bool ok = true;
@@ -608,6 +597,7 @@ cudaError_t launch_prefix_t(const AttnArgs& args, cudaStream_t s) {
     a.prefix_unit = C::KEYS % a.page_size == 0 ? a.page_size : 16;
     CUtensorMap tq, tk, tv;
     const int tokens = kRows / a.G;
+    a.prefix_tokens = tokens;
     const uint64_t row = D * 2;
     // q: 64 columns, the heads of a group, groups, tokens
     const cuuint64_t qd[4] = {(uint64_t)D, (uint64_t)a.G, (uint64_t)a.Hkv, (uint64_t)a.B * a.Q};
@@ -630,10 +620,8 @@ cudaError_t launch_prefix_t(const AttnArgs& args, cudaStream_t s) {
     });
     if (attr_err != cudaSuccess) return attr_err;
     const int ntiles = (a.B * a.Q + tokens - 1) / tokens;
-    const long long grid = (long long)a.prefix_splits * ((ntiles + 1) / 2) * a.Hkv;
-    if (grid > 0x7fffffffll) return cudaErrorInvalidValue;
-    return launch_k(attn_prefix_kernel<T, D>, dim3((unsigned)grid), dim3(kPrefixThreads), C::SMEM,
-                    s, false, tq, tk, tv, a);
+    return launch_k(attn_prefix_kernel<T, D>, dim3((ntiles + 1) / 2, a.prefix_splits, a.Hkv),
+                    dim3(kPrefixThreads), C::SMEM, s, false, tq, tk, tv, a);
 }
 
 }  // namespace
