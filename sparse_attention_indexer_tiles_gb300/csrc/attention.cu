@@ -531,42 +531,16 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
                    int sm_count) {
     AttnPlan p;
     const int G = Hq / Hkv;
-    p.prefix_splits = p.prefix_chunk = 0;
-    if (prefix_len > 0) {
-        // Key tiles per part: one CTA per SM takes about 1 us per 128 keys of a pair of
-        // row tiles (0.6 us of a single one) and 4 us besides, and every part writes D
-        // floats per row that the join reads (about 5 MB per us).
-        const int keys = attn_prefix_keys(D), tokens = 128 / G, tiles = (prefix_len + keys - 1) / keys;
-        const long long row_tiles = ((long long)B * Q + tokens - 1) / tokens;
-        const long long items = (row_tiles + 1) / 2 * Hkv;
-        const double per_tile = (row_tiles > 1 ? 1.0 : 0.6) * keys / 128;
-        double best = 0;
-        auto consider = [&](long long t) {  // t tiles per part
-            t = t < 1 ? 1 : t > tiles ? tiles : t;
-            const long long s = (tiles + t - 1) / t;
-            if (s > 65535) return;  // a grid dimension
-            const double us = (double)((items * s + sm_count - 1) / sm_count) * (t * per_tile + 4.0) +
-                              (double)B * Q * Hq * s * D * 8 / 5e6;
-            if (best == 0 || us < best) {
-                best = us;
-                p.prefix_chunk = (int)t * keys;
-            }
-        };
-        for (int t = 1; t <= 4; ++t) consider(t);
-        consider((tiles + 1023) / 1024);
-        for (long long waves = 1; waves <= 6; ++waves) {  // as many parts as fill whole waves
-            const long long s = waves * sm_count / items;
-            consider((tiles + (s > 0 ? s : 1) - 1) / (s > 0 ? s : 1));
-        }
-        p.prefix_splits = (prefix_len + p.prefix_chunk - 1) / p.prefix_chunk;
-    }
-    p.private_splits = p.private_chunk = 0;
+    p.prefix_splits = p.prefix_chunk = p.private_splits = p.private_chunk = 0;
+    // the join reads D floats per row and part, about 5 MB per us
+    const double join_us = (double)B * Q * Hq * D * 8 / 5e6;
+
+    // Keys per private part: a block takes about 4 us and, among the three that an SM holds,
+    // 34 ns per key (D = 128: 512 bytes at a third of the SM's share of HBM), so whole waves of
+    // long parts are cheap but a wave that is mostly empty is not.  The lengths are on the
+    // device: the mean of the times with all of them at max_len and at half of it is taken.
+    double private_us = 0;
     if (max_len > 0) {
-        // Keys per private part: a block takes about 4 us and, among the three that an SM
-        // holds, 34 ns per key (D = 128: 512 bytes at a third of the SM's share of HBM), so
-        // whole waves of long parts are cheap but a wave that is mostly empty is not; the
-        // join reads D floats per row and part.  The lengths are on the device: the mean of
-        // the times with all of them at max_len and at half of it is taken.
         const long long items = (long long)(Q * G + 15) / 16 * Hkv * B;
         const int steps = (max_len + 63) / 64;  // of 64 keys: four warps' 16
         auto waves = [&](long long blocks) {
@@ -577,14 +551,52 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
             const int chunk = (steps + s - 1) / s;
             const long long all = (steps + chunk - 1) / chunk, half = (steps / 2 + chunk) / chunk;
             const double us = (waves(items * all) + waves(items * half)) / 2 *
-                                  (chunk * 64 * (D * 34e-3 / 128) + 4.0) +
-                              (double)B * Q * Hq * s * D * 8 / 5e6;
-            if (best == 0 || us < best) {
-                best = us;
+                              (chunk * 64 * (D * 34e-3 / 128) + 4.0);
+            if (best == 0 || us + s * join_us < best) {
+                best = us + s * join_us;
+                private_us = us;
                 p.private_chunk = chunk * 64;
             }
         }
         p.private_splits = (max_len + p.private_chunk - 1) / p.private_chunk;
+    }
+
+    // Key tiles per prefix part: a CTA, one per SM, takes about 1.4 us per 128 keys of a pair of
+    // row tiles (0.75 us of a single one, whose keys two streams share) and 4 us besides.  SMs
+    // without one take private parts meanwhile, so the time is the longer of a CTA's and the
+    // mean over all SMs of both kinds' work: with private parts, fewer and longer prefix parts.
+    // The estimate above is for the largest lengths and no overlap; about a third of it is what
+    // the private parts take beside the prefix.  (With no share and with it: 64 requests of
+    // 64-1024 keys behind 32768 81 and 74 us, 32 of 100-2048 behind 16384 62 and 52, 64 of
+    // 512-4096 behind 4096 120 and 104, 16 of 64-1024 behind 4096 22.1 and 20.4; the whole
+    // estimate makes the prefix parts too few: 104, 68, 105 and 24.)
+    constexpr double kShare = 0.35;
+    if (prefix_len > 0) {
+        const int keys = attn_prefix_keys(D), tokens = 128 / G, tiles = (prefix_len + keys - 1) / keys;
+        const long long row_tiles = ((long long)B * Q + tokens - 1) / tokens;
+        const long long items = (row_tiles + 1) / 2 * Hkv;
+        const double per_tile = (row_tiles > 1 ? 1.4 : 0.75) * keys / 128;
+        double best = 0;
+        auto consider = [&](long long t) {  // t tiles per part
+            t = t < 1 ? 1 : t > tiles ? tiles : t;
+            const long long s = (tiles + t - 1) / t, ctas = items * s;
+            if (s > 65535) return;  // a grid dimension
+            const double one = t * per_tile + 4.0;
+            const double dense = (double)((ctas + sm_count - 1) / sm_count) * one;
+            const double mean = (ctas * one) / sm_count + private_us * kShare;
+            const double us = (dense > mean ? dense : mean) + s * join_us;
+            if (best == 0 || us < best) {
+                best = us;
+                p.prefix_chunk = (int)t * keys;
+            }
+        };
+        for (int t = 1; t <= 4; ++t) consider(t);
+        consider((tiles + 1023) / 1024);
+        for (int eighths = 2; eighths <= 48; ++eighths) {  // as many parts as fill so much of a wave
+            const long long s = eighths * sm_count / (8 * items);
+            consider((tiles + (s > 0 ? s : 1) - 1) / (s > 0 ? s : 1));
+        }
+        p.prefix_splits = (prefix_len + p.prefix_chunk - 1) / p.prefix_chunk;
     }
     const size_t rows = (size_t)B * Q * Hq, splits = p.prefix_splits + p.private_splits;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
