@@ -34,9 +34,21 @@ IDX_DEVI float exp2_approx(float x) {
 }
 
 // 16-byte asynchronous copy; bytes = 0 writes zeros and reads nothing
-IDX_DEVI void cp_async16_zfill(uint32_t dst, const void* src, uint32_t bytes) {
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes)
+IDX_DEVI void cp_async16_zfill(uint32_t dst, const void* src, uint32_t bytes, uint64_t policy) {
+    asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
+                 "l"(src), "r"(bytes), "l"(policy)
                  : "memory");
+}
+// L2 policies: data that is not read again leaves first; the default.
+IDX_DEVI uint64_t l2_evict_first() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_first.b64 %0, 1.0;" : "=l"(p));
+    return p;
+}
+IDX_DEVI uint64_t l2_evict_normal() {
+    uint64_t p;
+    asm volatile("createpolicy.fractional.L2::evict_normal.b64 %0, 1.0;" : "=l"(p));
+    return p;
 }
 IDX_DEVI void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
 template <int N> IDX_DEVI void cp_async_wait() {
@@ -178,6 +190,9 @@ __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_ke
     const int steps = (hi - lo + kStep - 1) / kStep;
     const int mine = warp < steps ? (steps - 1 - warp) / kPartWarps + 1 : 0;
     bool bad = false;
+    // K and V that one block reads pass through L2 without pushing out the logits and parts
+    // that the join reads back
+    const uint64_t policy = rows <= kRows ? l2_evict_first() : l2_evict_normal();
     // tile u: K of step u / 2, or V of it
     auto fetch = [&](int u) {
         const int i = u >> 1;
@@ -195,7 +210,7 @@ __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_ke
             const int c = j * 32 + lane, rr = c / kChunks, cc = c % kChunks;
             cp_async16_zfill(dst + rr * kRowBytes + ((cc ^ (rr & 7)) * 16),
                              src + rr * kRowBytes + cc * 16,
-                             ok && key + rr < hi ? 16u : 0u);  // zeros past the end
+                             ok && key + rr < hi ? 16u : 0u, policy);  // zeros past the end
         }
     };
 
