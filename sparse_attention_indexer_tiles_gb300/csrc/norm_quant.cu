@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
         if (a.group == 0 && row_live && t == 0) a.scale[row] = row_scale;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
-            float scale = row_scale;
+            float scale = row_scale, top = most;
             if (VEC && a.group != 0) {
                 float m = gmost[v];
                 if (lanes > 8) m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
@@ -197,10 +197,13 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
                 m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
                 m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
                 scale = fmaxf(rstd * m * (1.f / kE4m3Max), kScaleFloor);
+                top = m;
                 if (row_live && col_of(v) < a.N && (t & (lanes - 1)) == 0)
                     a.scale[row * (a.N / a.group) + col_of(v) / a.group] = scale;
             }
-            const float f = __fdividef(rstd, scale);
+            // y / scale = h weight (rstd / scale), and rstd cancels unless the scale is its floor:
+            // 448 / max|h weight| has one rounding where rstd / scale has four
+            const float f = scale > kScaleFloor ? __fdiv_rn(kE4m3Max, top) : rstd / kScaleFloor;
 #pragma unroll
             for (int i = 0; i < 4; ++i) hw[v][i] = mul2(hw[v][i], make_float2(f, f));
             if (row_live) store_codes<VEC>(a.out + row * a.N, hw[v], col_of(v), TPR, a.N);
