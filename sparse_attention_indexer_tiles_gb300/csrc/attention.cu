@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "attention.cuh"
@@ -558,15 +559,14 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
     if (max_len > 0) {
         const long long items = (long long)(Q * G + 15) / 16 * Hkv * B;
         const int steps = (max_len + 63) / 64;  // of 64 keys: four warps' 16
-        auto waves = [&](long long blocks) {
-            return (double)((blocks + 3 * sm_count - 1) / (3 * sm_count));
-        };
+        const double per_wave = 1.0 / (3 * sm_count);
         double best = 0;
-        for (int s = 1; s <= 32 && s <= steps; ++s) {
+        for (int s = 1; s <= 32 && s <= steps; s += s < 8 ? 1 : s / 4) {
             const int chunk = (steps + s - 1) / s;
-            const long long all = (steps + chunk - 1) / chunk, half = (steps / 2 + chunk) / chunk;
-            const double us = (waves(items * all) + waves(items * half)) / 2 *
-                              (chunk * 64 * (D * 34e-3 / 128) + 4.0);
+            const int all = (steps + chunk - 1) / chunk, half = (steps / 2 + chunk) / chunk;
+            const double us =
+                (std::ceil(items * all * per_wave) + std::ceil(items * half * per_wave)) / 2 *
+                (chunk * 64 * (D * 34e-3 / 128) + 4.0);
             if (best == 0 || us + s * join_us < best) {
                 best = us + s * join_us;
                 private_us = us;
@@ -592,13 +592,13 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
         const long long items = (row_tiles + 1) / 2 * Hkv;
         const double per_tile = (row_tiles > 1 ? 1.4 : 0.75) * keys / 128;
         double best = 0;
-        auto consider = [&](long long t) {  // t tiles per part
+        const double per_sm = 1.0 / sm_count;
+        auto consider = [&](int t) {  // t tiles per part
             t = t < 1 ? 1 : t > tiles ? tiles : t;
-            const long long s = (tiles + t - 1) / t, ctas = items * s;
+            const int s = (tiles + t - 1) / t;
             if (s > 65535) return;  // a grid dimension
-            const double one = t * per_tile + 4.0;
-            const double dense = (double)((ctas + sm_count - 1) / sm_count) * one;
-            const double mean = (ctas * one) / sm_count + private_us * kShare;
+            const double one = t * per_tile + 4.0, waves = (double)items * s * per_sm;
+            const double dense = std::ceil(waves) * one, mean = waves * one + private_us * kShare;
             const double us = (dense > mean ? dense : mean) + s * join_us;
             if (best == 0 || us < best) {
                 best = us;
@@ -607,9 +607,9 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
         };
         for (int t = 1; t <= 4; ++t) consider(t);
         consider((tiles + 1023) / 1024);
-        for (int eighths = 2; eighths <= 48; ++eighths) {  // as many parts as fill so much of a wave
-            const long long s = eighths * sm_count / (8 * items);
-            consider((tiles + (s > 0 ? s : 1) - 1) / (s > 0 ? s : 1));
+        for (int eighths = 2; eighths <= 48; eighths += eighths < 8 ? 1 : 8) {  // of a wave's CTAs
+            const int n = (int)(eighths * sm_count / (8 * items));
+            consider(n > 1 ? (tiles + n - 1) / n : tiles);
         }
         p.prefix_splits = (prefix_len + p.prefix_chunk - 1) / p.prefix_chunk;
     }
