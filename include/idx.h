@@ -412,7 +412,8 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
  *            for j < lens[b]; the newest Q slots start from 0 whatever w holds.
  *            Slots from lens[b] on are not written.
  *   out [B, Q, Hq, D] of q's type;  lse [B, Q, Hq] fp32 or NULL
- *   ws  idx_prefix_attention_workspace(...) bytes, 256-byte aligned; needs no
+ *   ws  idx_prefix_attention_workspace(...) bytes for the same max_len (the
+ *       table's width where the call says 0), 256-byte aligned; needs no
  *       clearing between calls
  * Supported: D 64 or 128; page_size 16, 32, 64 or 128; 1 <= Q <= 16; Hq a
  * multiple of Hkv with Hq / Hkv <= 128; B * Hkv <= 65535; pages >= 1 with keys.  Device errors
@@ -449,7 +450,8 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
  *         then only the filled holes are)
  *   lens_out [B] int32 = min(lens[b], budget); not lens itself
  *   max_len  an upper bound on lens (0 = table_stride * page_size)
- *   ws  idx_cache_evict_workspace(...) bytes, 256-byte aligned
+ *   ws  idx_cache_evict_workspace(...) bytes for the same max_len (the table's
+ *       width where the call says 0), 256-byte aligned
  * No two requests may share a private page.  budget >= 1, recent, sink >= 0 and
  * recent + sink <= budget (IDX_EINVAL); D 64 or 128; page_size 16, 32, 64 or 128;
  * B * Hkv < 2^28 and pages * Hkv * page_size < 2^32 - 16 (IDX_EUNSUPPORTED).

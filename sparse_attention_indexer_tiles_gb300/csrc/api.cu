@@ -1108,6 +1108,7 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
     a.prefix_chunk = p.prefix_chunk;
     a.private_splits = p.private_splits;
     a.private_chunk = p.private_chunk;
+    a.private_dense = p.private_dense;
     a.scale_log2 = scale * 1.4426950408889634f;
     const int stall_us = opt ? opt->test_stall_us : 0;
     a.wait_limit = stall_us > 0 ? 2100LL * stall_us : (1LL << 32);

@@ -113,7 +113,7 @@ template <int D> constexpr int part_smem() { return kPartWarps * kRing * kStep *
 // the long axis half of it was empty, at 163 registers and 12 warps per SM: the call of 64
 // requests with 64-1024 keys behind a 32768-key prefix took 84 us instead of 80).
 // The block's warps take the 16-key steps in turn, each with its own softmax state; the
-// states are joined at the end.  blockIdx.x: key head, row block and split; blockIdx.y: the
+// states are joined at the end.  blockIdx.x: row block, split and key head; blockIdx.y: the
 // request.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_kernel(AttnArgs a) {
@@ -123,11 +123,12 @@ __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_ke
     // join's wait for this grid cover both.
     const bool last = blockIdx.x == 0 && blockIdx.y == 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int split = blockIdx.x % a.private_splits;
-    const int hk = blockIdx.x / a.private_splits % a.Hkv;
-    const int rb = blockIdx.x / a.private_splits / a.Hkv, b = blockIdx.y;
     constexpr int kRows = 8 * NT;
     const int rows = a.Q * a.G;
+    // row blocks next to each other: they read the same keys, from L2 but for the first
+    const int row_blocks = (rows + kRows - 1) / kRows;
+    const int rb = blockIdx.x % row_blocks, split = blockIdx.x / row_blocks % a.private_splits;
+    const int hk = blockIdx.x / row_blocks / a.private_splits, b = blockIdx.y;
     const int total_splits = a.prefix_splits + a.private_splits;
     const int slot = a.prefix_splits + split;
 
@@ -520,8 +521,9 @@ cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStre
         ++*launched;
     }
     if (a.private_splits > 0) {
-        e = a.Q * a.G <= 8 ? launch_private<T, D, 1>(a, *launched > 0, s)
-                           : launch_private<T, D, 2>(a, *launched > 0, s);
+        e = a.private_dense  ? launch_private_dense(a, dt, *launched > 0, s)
+            : a.Q * a.G <= 8 ? launch_private<T, D, 1>(a, *launched > 0, s)
+                             : launch_private<T, D, 2>(a, *launched > 0, s);
         if (e != cudaSuccess) return e;
         ++*launched;
     }
@@ -555,23 +557,39 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
     // 34 ns per key (D = 128: 512 bytes at a third of the SM's share of HBM), so whole waves of
     // long parts are cheap but a wave that is mostly empty is not.  The lengths are on the
     // device: the mean of the times with all of them at max_len and at half of it is taken.
+    //
+    // More than 16 rows read a key several times over that way, at about its HBM time each; the
+    // dense path of the prefix kernel reads it once, for about 8 us per CTA, one per SM.  The
+    // cheaper is taken (16 requests of 4 tokens, 8 heads, 100-1000 keys: 24.7 and dense 18.4 us;
+    // 16 of 7 tokens, 16 heads, 1024-8192 keys 150 and 52; 8 of 4 tokens, 16 heads, 100-500 keys
+    // 14.3 and 18.0).  Beside logits, which the dense path writes a row per thread, it gains only
+    // at D = 128 (16 of 7 tokens with weights: D 128 224 and 164 us, D 64 157 and 183).
     double private_us = 0;
+    p.private_dense = false;
     if (max_len > 0) {
-        const long long items = (long long)(Q * G + 15) / 16 * Hkv * B;
-        const int steps = (max_len + 63) / 64;  // of 64 keys: four warps' 16
-        const double per_wave = 1.0 / (3 * sm_count);
         double best = 0;
-        for (int s = 1; s <= 32 && s <= steps; s += s < 8 ? 1 : s / 4) {
-            const int chunk = (steps + s - 1) / s;
-            const int all = (steps + chunk - 1) / chunk, half = (steps / 2 + chunk) / chunk;
+        auto consider = [&](bool dense, double items, int unit, int units, int s, double per_unit,
+                            double base) {  // s parts of `units` units of keys
+            const int t = (units + s - 1) / s, all = (units + t - 1) / t, half = (units / 2 + t) / t;
             const double us =
-                (std::ceil(items * all * per_wave) + std::ceil(items * half * per_wave)) / 2 *
-                (chunk * 64 * (D * 34e-3 / 128) + 4.0);
+                (std::ceil(items * all) + std::ceil(items * half)) / 2 * (t * per_unit + base);
             if (best == 0 || us + s * join_us < best) {
                 best = us + s * join_us;
                 private_us = us;
-                p.private_chunk = chunk * 64;
+                p.private_chunk = t * unit;
+                p.private_dense = dense;
             }
+        };
+        const int row_blocks = (Q * G + 15) / 16, steps = (max_len + 63) / 64;  // 64: four warps' 16
+        for (int s = 1; s <= 32 && s <= steps; s += s < 8 ? 1 : s / 4)
+            consider(false, (double)row_blocks * Hkv * B / (3 * sm_count), 64, steps, s,
+                     64 * (D * 34e-3 / 128), 4.0);
+        if (row_blocks > 1 && !(weights && D == 64)) {
+            const int keys = attn_prefix_keys(D), tiles = (max_len + keys - 1) / keys;
+            const int row_tiles = (Q + 128 / G - 1) / (128 / G);
+            for (int s = 1; s <= 32 && s <= tiles; s += s < 8 ? 1 : s / 4)
+                consider(true, (double)B * Hkv * ((row_tiles + 1) / 2) / sm_count, keys, tiles, s,
+                         keys * D * 4 / 45e3, 8.0);
         }
         p.private_splits = (max_len + p.private_chunk - 1) / p.private_chunk;
     }

@@ -39,6 +39,8 @@ struct AttnArgs {
     int prefix_unit, prefix_tokens;     // keys per copy, query tokens per row tile (set by
                                         // launch_prefix_parts)
     int private_splits, private_chunk;  // keys per private part (a multiple of 64)
+    bool private_dense;                 // private parts on the tensor cores' dense path (their
+                                        // chunk: whole key tiles)
     float scale_log2;                   // scale * log2(e)
     long long wait_limit;               // SM clocks a wait of the prefix kernel may take
     int withhold_tile;                  // test only: the key tile that is never loaded, or -1
@@ -47,6 +49,7 @@ struct AttnArgs {
 
 struct AttnPlan {
     int prefix_splits, prefix_chunk, private_splits, private_chunk;
+    bool private_dense;
     size_t part, part_lse, logits, total;
     long long logit_stride;
 };
@@ -54,8 +57,10 @@ struct AttnPlan {
 AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max_len, bool weights,
                    int sm_count);
 
-// The prefix's parts (attention_prefix.cu).
+// The prefix's parts, and the private ones of requests with many rows (attention_prefix.cu).
+// `overlap`: the launch may start beside the one before it.
 cudaError_t launch_prefix_parts(const AttnArgs& a, idx_dtype dt, cudaStream_t s);
+cudaError_t launch_private_dense(const AttnArgs& a, idx_dtype dt, bool overlap, cudaStream_t s);
 
 // Returns the number of kernels launched through *launched.
 cudaError_t launch_attention(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStream_t s,

@@ -19,6 +19,10 @@
 // issued.  Beside two O of D columns, 512 columns leave 128 per stream at D = 128: 80 keys
 // (80 + 40).  Tiles of 128 keys with P over S cost a wait for P V before every Q K^T.
 //
+// The private parts of requests with many rows per key head (several new tokens) are taken the
+// same way, with a request's own rows, pages and length (PRIVATE): they also mask the tokens
+// after a row's own and leave the logits that the weights are made from.
+//
 // The running maximum m is renewed only when a row's maximum has grown by more than 8 (a
 // factor 256; P <= 256 then, well inside either type), so O is rarely rescaled; the sum l
 // and O stay relative to the m in use, in fp32, and the result does not depend on it.
@@ -189,7 +193,7 @@ template <> struct Elem<__half> {
     }
 };
 
-template <typename T, int D>
+template <typename T, int D, bool PRIVATE>
 __global__ void __launch_bounds__(kPrefixThreads, 1)
 attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ AttnArgs a) {
@@ -211,9 +215,33 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 
     // this CTA: key head, pair of row tiles, part of the prefix
     const int tokens = a.prefix_tokens;  // query tokens per row tile (its rows: tokens * G <= 128)
-    const int pair = blockIdx.x, split = blockIdx.y, hk = blockIdx.z;
-    const bool solo = (2 * pair + 1) * tokens >= a.B * a.Q;
-    const int lo = split * a.prefix_chunk, hi = min(a.prefix_len, lo + a.prefix_chunk);
+    const int pair = blockIdx.x, split = blockIdx.y;
+    const int hk = PRIVATE ? blockIdx.z % a.Hkv : blockIdx.z, b = PRIVATE ? blockIdx.z / a.Hkv : 0;
+    const int all_tokens = PRIVATE ? a.Q : a.B * a.Q, token0 = b * a.Q;  // whose rows these are
+    const bool solo = (2 * pair + 1) * tokens >= all_tokens;
+    const int total_splits = a.prefix_splits + a.private_splits;
+    const int slot = PRIVATE ? a.prefix_splits + split : split;
+    const int* const table = PRIVATE ? a.table + b * a.table_stride : a.prefix_table;
+    int len = a.prefix_len;
+    if constexpr (PRIVATE) {
+        len = a.lens[b];
+        if ((len < 0 || len > a.max_len) && tid == 0) raise_status(a.d_status, IDX_DEV_RANGE);
+        len = min(max(len, 0), a.max_len);
+    }
+    const int chunk = PRIVATE ? a.private_chunk : a.prefix_chunk;
+    const int lo = split * chunk, hi = min(len, lo + chunk);
+    // (one CTA's wait for the prefix's grid makes the join's wait for this one cover both)
+    const bool last = PRIVATE && blockIdx.x == 0 && blockIdx.y == 0 && blockIdx.z == 0;
+    if (PRIVATE && lo >= hi) {  // no keys in this part
+        for (int i = tid; i < 2 * tokens * a.G; i += kPrefixThreads) {
+            const int t = 2 * pair * tokens + i / a.G;
+            if (t < all_tokens)
+                a.part_lse[((long long)(token0 + t) * a.Hq + hk * a.G + i % a.G) * total_splits + slot] =
+                    -INFINITY;
+        }
+        if (last) pdl_wait();
+        return;
+    }
     const int n = (hi - lo + C::KEYS - 1) / C::KEYS;  // key tiles, at least one
 
     const uint32_t kv = smem_u32(smem + C::OFF_KV);
@@ -225,7 +253,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const int key = lo + (x >> 1) * C::KEYS + lane * unit;
         int page = a.pages;
         if (lane < copies && x < 2 * n && key < hi) {
-            page = a.prefix_table[key >> a.page_shift];
+            page = table[key >> a.page_shift];
             if (page < 0 || page >= a.pages) {
                 page = a.pages;
                 bad = true;
@@ -273,7 +301,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int t = 0; t < tiles; ++t)
                 for (int h = 0; h < C::HALVES; ++h)
                     tma_load_4d(smem_u32(smem) + t * C::QTILE + h * kHalfQ, &tm_q, qfull, h * 64, 0,
-                                hk, (2 * pair + t) * tokens);
+                                hk, token0 + (2 * pair + t) * tokens);
         }
         __syncwarp();
     }
@@ -391,8 +419,15 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t ts = tmem + lanes + s * C::COL_STREAM, to = tmem + lanes + C::COL_O + s * D;
         const int tile = 2 * pair + (solo ? 0 : s);
-        const int bt = tile * tokens + row / a.G;
-        const bool live = row < tokens * a.G && bt < a.B * a.Q;
+        const int bt = tile * tokens + row / a.G;  // token of the row, from token0 on
+        const bool live = row < tokens * a.G && bt < all_tokens;
+        // a private row does not see the tokens after its own
+        const int see = PRIVATE ? min(hi, len - (a.Q - 1 - bt)) : hi;
+        const int see_all = PRIVATE ? min(hi, len - (a.Q - 1)) : hi;  // what every row sees
+        float* logits = nullptr;
+        if (PRIVATE && a.logits && live)
+            logits = a.logits + (((long long)b * a.Hkv + hk) * (a.Q * a.G) +
+                                 tile * tokens * a.G + row) * a.logit_stride + lo;
         const int mine = solo ? (n + 1 - s) / 2 : n;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
@@ -412,10 +447,19 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             if (lane == 0) mbar_arrive(&sfree[s]);  // the next S may be computed
             const int valid = hi - lo - t * C::KEYS;  // keys of this tile
             float scale = a.scale_log2;
-            if (valid < C::KEYS || scale < 0.f) {  // uniform; the maximum below wants scale >= 0
+            // uniform; the maximum below wants scale >= 0
+            if (see_all - lo - t * C::KEYS < C::KEYS || scale < 0.f || (PRIVATE && a.logits)) {
+                const int mine_valid = see - lo - t * C::KEYS;
 #pragma unroll
-                for (int c = 0; c < C::KEYS; ++c) z[c] = c < valid ? z[c] * scale : -INFINITY;
+                for (int c = 0; c < C::KEYS; ++c) z[c] = c < mine_valid ? z[c] * scale : -INFINITY;
                 scale = 1.f;
+                if (PRIVATE && logits) {
+#pragma unroll
+                    for (int c = 0; c < C::KEYS; c += 4)
+                        if (c < valid)
+                            *reinterpret_cast<float4*>(logits + t * C::KEYS + c) =
+                                make_float4(z[c], z[c + 1], z[c + 2], z[c + 3]);
+                }
             }
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
@@ -490,7 +534,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             ok = __all_sync(~0u, mbar_wait(&pvdone[s], (mine - 1) & 1, abort_flag, a.wait_limit));
         if (!ok && lane == 0) give_up();
         tc_fence_after();
-        const int total_splits = a.prefix_splits + a.private_splits;
+        if (l == 0.f) m = -INFINITY;  // nothing seen: no part in a join
         float* ml = reinterpret_cast<float*>(smem + C::OFF_ML);
         float4* join = reinterpret_cast<float4*>(smem + C::OFF_KV);  // [D / 4][128]
         if (solo && s == 1) {
@@ -518,8 +562,9 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 named_bar_sync(1, 256);
                 named_bar_sync(1, 256);
                 top = fmaxf(m, ml[row]);
-                f0 = ex2(m - top);
-                f1 = ex2(ml[row] - top);
+                const float base = top == -INFINITY ? 0.f : top;
+                f0 = ex2(m - base);
+                f1 = ex2(ml[row] - base);
                 l = l * f0 + ml[128 + row] * f1;
             }
             const float inv = l > 0.f ? 1.f / l : 0.f;
@@ -531,7 +576,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             uint8_t* stage = smem + s * C::QTILE;
             const int r0 = row & ~31;
             const long long part =
-                ((long long)bt * a.Hq + hk * a.G + row % a.G) * total_splits + split;
+                ((long long)(token0 + bt) * a.Hq + hk * a.G + row % a.G) * total_splits + slot;
             float* const mine_at = live ? a.part + part * D : nullptr;
             for (int c0 = 0; c0 < D; c0 += kCols) {
 #pragma unroll
@@ -575,6 +620,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
         tc_fence_after();
         tmem_dealloc(tmem, 512);
     }
+    if (last) pdl_wait();
 }
 
 // Map of 16-bit elements with a 128-byte inner box, swizzled at that width.
@@ -589,8 +635,8 @@ CUresult make_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[N],
                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
-template <typename T, int D>
-cudaError_t launch_prefix_t(const AttnArgs& args, cudaStream_t s) {
+template <typename T, int D, bool PRIVATE>
+cudaError_t launch_t(const AttnArgs& args, bool overlap, cudaStream_t s) {
     using C = PrefixCfg<D>;
     AttnArgs a = args;
     // keys per copy: a whole page where it divides the tile, else 16 (no page is smaller)
@@ -615,22 +661,34 @@ cudaError_t launch_prefix_t(const AttnArgs& args, cudaStream_t s) {
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(attn_prefix_kernel<T, D>,
+        attr_err = cudaFuncSetAttribute(attn_prefix_kernel<T, D, PRIVATE>,
                                         cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     });
     if (attr_err != cudaSuccess) return attr_err;
-    const int ntiles = (a.B * a.Q + tokens - 1) / tokens;
-    return launch_k(attn_prefix_kernel<T, D>, dim3((ntiles + 1) / 2, a.prefix_splits, a.Hkv),
-                    dim3(kPrefixThreads), C::SMEM, s, false, tq, tk, tv, a);
+    const int ntiles = ((PRIVATE ? a.Q : a.B * a.Q) + tokens - 1) / tokens;
+    return launch_k(attn_prefix_kernel<T, D, PRIVATE>,
+                    dim3((ntiles + 1) / 2, PRIVATE ? a.private_splits : a.prefix_splits,
+                         PRIVATE ? a.B * a.Hkv : a.Hkv),
+                    dim3(kPrefixThreads), C::SMEM, s, overlap, tq, tk, tv, a);
+}
+
+template <bool PRIVATE>
+cudaError_t launch_dense(const AttnArgs& a, idx_dtype dt, bool overlap, cudaStream_t s) {
+    if (dt == IDX_BF16)
+        return a.D == 128 ? launch_t<__nv_bfloat16, 128, PRIVATE>(a, overlap, s)
+                          : launch_t<__nv_bfloat16, 64, PRIVATE>(a, overlap, s);
+    return a.D == 128 ? launch_t<__half, 128, PRIVATE>(a, overlap, s)
+                      : launch_t<__half, 64, PRIVATE>(a, overlap, s);
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_parts(const AttnArgs& a, idx_dtype dt, cudaStream_t s) {
-    if (dt == IDX_BF16)
-        return a.D == 128 ? launch_prefix_t<__nv_bfloat16, 128>(a, s)
-                          : launch_prefix_t<__nv_bfloat16, 64>(a, s);
-    return a.D == 128 ? launch_prefix_t<__half, 128>(a, s) : launch_prefix_t<__half, 64>(a, s);
+    return launch_dense<false>(a, dt, false, s);
+}
+
+cudaError_t launch_private_dense(const AttnArgs& a, idx_dtype dt, bool overlap, cudaStream_t s) {
+    return launch_dense<true>(a, dt, overlap, s);
 }
 
 }  // namespace idx

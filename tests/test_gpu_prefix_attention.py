@@ -90,6 +90,32 @@ def test_several_tokens(idx, Q, G):
     check(idx, make([Q + 40, Q, 2, 0, 100], Q, G, 2, 64, 33, 32, FP16, seed=Q * G))
 
 
+@pytest.mark.parametrize("lens", [[400], [81, 79, 80, 400, 0, 3, 161], [129, 127, 128, 256, 1, 640]])
+@pytest.mark.parametrize("Q,G,Hkv", [(16, 8, 1), (16, 16, 2), (7, 16, 1), (5, 7, 2), (16, 2, 1), (3, 40, 1), (2, 128, 1)])
+@pytest.mark.parametrize("D,dtype,page,prefix", [(128, BF16, 16, 0), (64, FP16, 64, 50), (128, FP16, 128, 200)])
+def test_many_rows_per_key_head(idx, lens, Q, G, Hkv, D, dtype, page, prefix):
+    """Private parts on the dense path: row tiles of one request, its last tokens' masks, lengths
+    around the key tiles and below the number of new tokens."""
+    check(idx, make(lens, Q, G, Hkv, D, prefix, page, dtype, seed=Q * G + len(lens)))
+
+
+@pytest.mark.parametrize("B,Q,G,Hkv", [(24, 16, 8, 4), (30, 16, 16, 2), (30, 7, 16, 4), (40, 5, 7, 8), (20, 3, 40, 4)])
+@pytest.mark.parametrize("D,dtype,weights", [(128, BF16, True), (64, FP16, False), (64, BF16, False)])
+def test_many_requests_of_many_rows(idx, B, Q, G, Hkv, D, dtype, weights):
+    """Batches for which the dense path is the cheaper at either head size, their lengths around
+    its key tiles and down to nothing."""
+    lens = [0, 1, 3, Q - 1, Q, 15, 16, 79, 80, 81, 127, 128, 129, 159, 160, 161, 240, 300, 511, 512, 513, 640, 699]
+    check(idx, make([700] + (2 * lens)[:B - 1], Q, G, Hkv, D, 40, 64, dtype, seed=B + Q, weights=weights))
+
+
+@pytest.mark.parametrize("D,dtype", [(128, BF16), (64, FP16)])
+def test_many_rows_over_long_private_parts(idx, D, dtype):
+    """Several parts and many tiles per part, for an odd and an even number of row tiles."""
+    check(idx, make([5000, 777, 2600], 4, 16, 2, D, 100, 64, dtype, seed=1))
+    check(idx, make([3000, 1], 16, 16, 1, D, 0, 32, dtype, seed=2, weights=False))
+    check(idx, make([20000], 4, 8, 8, D, 64, 64, dtype, seed=3), scale=-0.05)
+
+
 def test_several_tokens_without_a_prefix_leave_rows_empty(idx):
     got = check(idx, make([2, 5, 0], 5, 2, 1, 64, 0, 16, BF16, seed=1))
     assert (got[1][0, :3] == -math.inf).all() and (got[0][2] == 0).all()
