@@ -1024,10 +1024,15 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
     a.N = N;
     a.group = group;
     a.eps = eps;
-    a.vec = N % 8 == 0 && x_stride * es % 16 == 0 && aligned(x, 16) && aligned(weight, 16) &&
-            aligned(out, 8) && (!residual || aligned(residual, 16)) &&
-            (!residual_out || aligned(residual_out, 16));
-    if (group != 0 && !a.vec) return IDX_EALIGN;
+    // can rows be accessed `unit` columns at a time?
+    auto fits = [&](int unit) {
+        const size_t b = std::min<size_t>(unit * es, 16);
+        return N % unit == 0 && x_stride % unit == 0 && aligned(x, b) && aligned(weight, b) &&
+               aligned(out, unit) && (!residual || aligned(residual, b)) &&
+               (!residual_out || aligned(residual_out, b));
+    };
+    a.unit = fits(8) ? 8 : fits(2) ? 2 : 1;
+    if (group != 0 && a.unit != 8) return IDX_EALIGN;
     if (!arch_ok()) return IDX_EUNSUPPORTED;
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     record(opt, 0, s);

@@ -62,40 +62,48 @@ template <> struct alignas(16) Raw8<float> {
     }
 };
 
-// A thread's eight columns of a row of n, from the row's start: consecutive ones from c on
-// (VEC, n % 8 == 0), or every `step`-th one from c on, so that a warp's element-wise
-// accesses are consecutive whatever the row's alignment.
-template <bool VEC, typename T>
-IDX_DEVI void load8(Raw8<T>& r, const T* row, int c, int step, int n) {
-    if constexpr (VEC) {
-        if (c < n) r = *reinterpret_cast<const Raw8<T>*>(row + c);
-    } else {
+// A thread's eight columns of a row, in accesses of U columns: eight consecutive ones (U = 8),
+// or every `step`-th pair or single column from the c-th on, so that a warp's accesses are
+// consecutive when rows are not on 16-byte boundaries.  `have` of its accesses are inside the
+// row.
+template <typename T, int U> struct Unit;  // U columns as they are loaded
+template <> struct Unit<float, 2> { using type = float2; };
+template <> struct Unit<__nv_bfloat16, 2> { using type = uint32_t; };
+template <> struct Unit<__half, 2> { using type = uint32_t; };
+template <typename T> struct Unit<T, 8> { using type = Raw8<T>; };
+template <typename T> struct Unit<T, 1> { using type = T; };
+
+template <int U, typename T>
+IDX_DEVI void load8(Raw8<T>& r, const T* row, int c, int step, int have) {
+    using V = typename Unit<T, U>::type;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i * step < n) reinterpret_cast<T*>(&r)[i] = row[c + i * step];
-    }
+    for (int i = 0; i < 8 / U; ++i)
+        if (i < have)
+            reinterpret_cast<V*>(&r)[i] = *reinterpret_cast<const V*>(row + (c + i * step) * U);
 }
-template <bool VEC, typename T>
-IDX_DEVI void store8(T* row, const Raw8<T>& r, int c, int step, int n) {
-    if constexpr (VEC) {
-        if (c < n) *reinterpret_cast<Raw8<T>*>(row + c) = r;
-    } else {
+template <int U, typename T>
+IDX_DEVI void store8(T* row, const Raw8<T>& r, int c, int step, int have) {
+    using V = typename Unit<T, U>::type;
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i * step < n) row[c + i * step] = reinterpret_cast<const T*>(&r)[i];
-    }
+    for (int i = 0; i < 8 / U; ++i)
+        if (i < have)
+            *reinterpret_cast<V*>(row + (c + i * step) * U) = reinterpret_cast<const V*>(&r)[i];
 }
-template <bool VEC>
-IDX_DEVI void store_codes(uint8_t* row, const float2 (&v)[4], int c, int step, int n) {
+template <int U>
+IDX_DEVI void store_codes(uint8_t* row, const float2 (&v)[4], int c, int step, int have) {
     uint32_t p[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) p[i] = __nv_cvt_float2_to_fp8x2(v[i], __NV_SATFINITE, __NV_E4M3);
-    if constexpr (VEC) {
-        if (c < n) *reinterpret_cast<uint2*>(row + c) = make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
-    } else {
 #pragma unroll
-        for (int i = 0; i < 8; ++i)
-            if (c + i * step < n) row[c + i * step] = (uint8_t)(p[i >> 1] >> (8 * (i & 1)));
+    for (int i = 0; i < 8 / U; ++i) {
+        if (i >= have) break;
+        uint8_t* at = row + (c + i * step) * U;
+        if constexpr (U == 8)
+            *reinterpret_cast<uint2*>(at) = make_uint2(p[0] | (p[1] << 16), p[2] | (p[3] << 16));
+        else if constexpr (U == 2)
+            *reinterpret_cast<uint16_t*>(at) = (uint16_t)p[i];
+        else
+            *at = (uint8_t)(p[i >> 1] >> (8 * (i & 1)));
     }
 }
 
@@ -104,7 +112,7 @@ IDX_DEVI void store_codes(uint8_t* row, const float2 (&v)[4], int c, int step, i
 // residual on their way while it works on the current one.  Columns and rows past the end
 // are zeros.  The arithmetic is on pairs of fp32: at 16-bit inputs the instructions per
 // element, not HBM, bound the first version (44 per element, 62 us at 4096 x 8192).
-template <typename T, int TPR, int VPT, bool VEC, bool RES>
+template <typename T, int TPR, int VPT, int U, bool RES>
 __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormArgs a) {
     constexpr int kThreads = TPR < 128 ? 128 : TPR;
     constexpr int kRows = kThreads / TPR;  // rows side by side in a block
@@ -112,7 +120,14 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
     const int t = (int)threadIdx.x % TPR, lane = threadIdx.x & 31;
     const int units = (a.rows + kRows - 1) / kRows;
     auto row_of = [&](int u) { return (long long)u * kRows + (int)threadIdx.x / TPR; };
-    auto col_of = [&](int v) { return VEC ? (v * TPR + t) * 8 : v * 8 * TPR + t; };
+    // vector v's first access, in units of U columns, and how many of its 8 / U are in the row
+    auto unit_of = [&](int v) { return v * (8 / U) * TPR + t; };
+    int have[VPT];
+#pragma unroll
+    for (int v = 0; v < VPT; ++v) {
+        const int left = a.N / U - unit_of(v);
+        have[v] = left <= 0 ? 0 : min(8 / U, (left + TPR - 1) / TPR);
+    }
     struct Row {
         Raw8<T> x[VPT], res[RES ? VPT : 1];
     };
@@ -125,8 +140,8 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
             r.x[v].clear();
             if constexpr (RES) r.res[v].clear();
             if (row < a.rows) {
-                load8<VEC>(r.x[v], x, col_of(v), TPR, a.N);
-                if constexpr (RES) load8<VEC>(r.res[v], res, col_of(v), TPR, a.N);
+                load8<U>(r.x[v], x, unit_of(v), TPR, have[v]);
+                if constexpr (RES) load8<U>(r.res[v], res, unit_of(v), TPR, have[v]);
             }
         }
     };
@@ -136,7 +151,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
 #pragma unroll
     for (int v = 0; v < VPT; ++v) {
         wgt[v].clear();
-        load8<VEC>(wgt[v], static_cast<const T*>(a.weight), col_of(v), TPR, a.N);
+        load8<U>(wgt[v], static_cast<const T*>(a.weight), unit_of(v), TPR, have[v]);
     }
     const float per_col = 1.f / (float)a.N;
     const int lanes = a.group / 8;  // consecutive threads of a group: 4, 8 or 16
@@ -161,7 +176,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
                 h_out.set(i, h);
             }
             if (a.residual_out && row_live)
-                store8<VEC>(static_cast<T*>(a.residual_out) + row * a.N, h_out, col_of(v), TPR, a.N);
+                store8<U>(static_cast<T*>(a.residual_out) + row * a.N, h_out, unit_of(v), TPR, have[v]);
             most = fmaxf(most, gmost[v]);
         }
         float sum = sum2.x + sum2.y;
@@ -190,7 +205,7 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             float scale = row_scale, top = most;
-            if (VEC && a.group != 0) {
+            if (U == 8 && a.group != 0) {
                 float m = gmost[v];
                 if (lanes > 8) m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
                 if (lanes > 4) m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
@@ -198,27 +213,27 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
                 m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
                 scale = fmaxf(rstd * m * (1.f / kE4m3Max), kScaleFloor);
                 top = m;
-                if (row_live && col_of(v) < a.N && (t & (lanes - 1)) == 0)
-                    a.scale[row * (a.N / a.group) + col_of(v) / a.group] = scale;
+                if (row_live && have[v] > 0 && (t & (lanes - 1)) == 0)
+                    a.scale[row * (a.N / a.group) + unit_of(v) * 8 / a.group] = scale;
             }
             // y / scale = h weight (rstd / scale), and rstd cancels unless the scale is its floor:
             // 448 / max|h weight| has one rounding where rstd / scale has four
             const float f = scale > kScaleFloor ? __fdiv_rn(kE4m3Max, top) : rstd / kScaleFloor;
 #pragma unroll
             for (int i = 0; i < 4; ++i) hw[v][i] = mul2(hw[v][i], make_float2(f, f));
-            if (row_live) store_codes<VEC>(a.out + row * a.N, hw[v], col_of(v), TPR, a.N);
+            if (row_live) store_codes<U>(a.out + row * a.N, hw[v], unit_of(v), TPR, have[v]);
         }
     }
 }
 
-template <typename T, int TPR, int VPT, bool VEC, bool RES>
+template <typename T, int TPR, int VPT, int U, bool RES>
 cudaError_t launch_blocks(const NormArgs& a, int sm_count, cudaStream_t s) {
     constexpr int kThreads = TPR < 128 ? 128 : TPR, kRows = kThreads / TPR;
     static std::once_flag once;
     static int resident = 1;  // blocks per SM
     std::call_once(once, [] {
         if (cudaOccupancyMaxActiveBlocksPerMultiprocessor(
-                &resident, norm_quant_kernel<T, TPR, VPT, VEC, RES>, kThreads, 0) != cudaSuccess ||
+                &resident, norm_quant_kernel<T, TPR, VPT, U, RES>, kThreads, 0) != cudaSuccess ||
             resident < 1)
             resident = 1;
     });
@@ -227,31 +242,38 @@ cudaError_t launch_blocks(const NormArgs& a, int sm_count, cudaStream_t s) {
     const long long room = (long long)resident * sm_count;
     const long long each = (units + room - 1) / room;
     const long long grid = (units + each - 1) / each;
-    norm_quant_kernel<T, TPR, VPT, VEC, RES><<<(unsigned)grid, kThreads, 0, s>>>(a);
+    norm_quant_kernel<T, TPR, VPT, U, RES><<<(unsigned)grid, kThreads, 0, s>>>(a);
     return cudaGetLastError();
 }
 
 template <typename T, int TPR, int VPT>
 cudaError_t launch_shape(const NormArgs& a, int sm_count, cudaStream_t s) {
-    if (a.vec)
-        return a.residual ? launch_blocks<T, TPR, VPT, true, true>(a, sm_count, s)
-                          : launch_blocks<T, TPR, VPT, true, false>(a, sm_count, s);
-    return a.residual ? launch_blocks<T, TPR, VPT, false, true>(a, sm_count, s)
-                      : launch_blocks<T, TPR, VPT, false, false>(a, sm_count, s);
+    if (a.unit == 8)
+        return a.residual ? launch_blocks<T, TPR, VPT, 8, true>(a, sm_count, s)
+                          : launch_blocks<T, TPR, VPT, 8, false>(a, sm_count, s);
+    if (a.unit == 2)
+        return a.residual ? launch_blocks<T, TPR, VPT, 2, true>(a, sm_count, s)
+                          : launch_blocks<T, TPR, VPT, 2, false>(a, sm_count, s);
+    return a.residual ? launch_blocks<T, TPR, VPT, 1, true>(a, sm_count, s)
+                      : launch_blocks<T, TPR, VPT, 1, false>(a, sm_count, s);
 }
 
-// Shapes: a narrow row is a half-warp's or a warp's; a wide one's threads hold one or two
-// vectors.
+// Shapes: a narrow row is a half-warp's or a warp's (65536 x 256 bf16 by half-warps of two
+// vectors a thread 11.1 us, by warps of one 13.4; 30000 x 512 by warps 11.0, by 128 threads
+// 23.5).  A wide one's threads hold as many vectors as measured fastest (bf16 with residual:
+// 8192 x 4096 with one 41.4 us, two 37.3, four 38.6; 777 x 5000 fp16 with one 7.5, two 5.3,
+// three 5.7; 4096 x 8192 with one 44.4, two 43.4, four 37.9).
 template <typename T>
 cudaError_t launch_type(const NormArgs& a, int sm_count, cudaStream_t s) {
     if (a.N <= 128) return launch_shape<T, 16, 1>(a, sm_count, s);
-    if (a.N <= 256) return launch_shape<T, 32, 1>(a, sm_count, s);
+    if (a.N <= 256) return launch_shape<T, 16, 2>(a, sm_count, s);
+    if (a.N <= 512) return launch_shape<T, 32, 2>(a, sm_count, s);
     if (a.N <= 1024) return launch_shape<T, 128, 1>(a, sm_count, s);
     if (a.N <= 2048) return launch_shape<T, 256, 1>(a, sm_count, s);
     if (a.N <= 4096) return launch_shape<T, 256, 2>(a, sm_count, s);
     if (a.N <= 6144) return launch_shape<T, 384, 2>(a, sm_count, s);
     if (a.N <= 8192) return launch_shape<T, 256, 4>(a, sm_count, s);
-    if (a.N <= 16384) return launch_shape<T, 1024, 2>(a, sm_count, s);
+    if (a.N <= 16384) return launch_shape<T, 512, 4>(a, sm_count, s);
     return launch_shape<T, 1024, 4>(a, sm_count, s);
 }
 

@@ -20,7 +20,9 @@ struct NormArgs {
     long long x_stride;
     int rows, N, group;
     float eps;
-    bool vec;              // every row starts on a 16-byte boundary and N % 8 == 0
+    int unit;              // columns per access: 8 when every row starts on a 16-byte boundary
+                           // (its codes on an 8-byte one) and N % 8 == 0; 2 when every row starts
+                           // on a pair of elements and N is even; else 1
 };
 
 cudaError_t launch_norm_quant(const NormArgs& a, idx_dtype dt, int sm_count, cudaStream_t s);
