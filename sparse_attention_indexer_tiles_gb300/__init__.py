@@ -20,6 +20,8 @@ Entry points (same names as the C ABI in ``include/idx.h``):
 from __future__ import annotations
 
 import ctypes
+import importlib.machinery
+import importlib.util
 import os
 
 import torch
@@ -41,9 +43,7 @@ LIB_PATH = os.path.join(_HERE, "_build", "libidx.so")
 
 IDX_BF16, IDX_FP8_E4M3, IDX_MXFP4 = 1, 2, 3
 DTYPES = {torch.bfloat16: IDX_BF16, torch.float8_e4m3fn: IDX_FP8_E4M3}
-IDX_FP16, IDX_FP32 = 4, 5
-# the serving operators' types (the indexer's own are DTYPES)
-SERVE_DTYPES = {torch.bfloat16: IDX_BF16, torch.float16: IDX_FP16, torch.float32: IDX_FP32}
+IDX_FP16, IDX_FP32 = 4, 5  # the serving operators' further types
 STAT_FIELDS = ("emit_all_rows", "overflow_rows", "short_rows", "fallback_rows", "max_count",
                "split_rows", "tie_rescan_rows", "reserved")
 
@@ -497,70 +497,39 @@ def idx_score_topk_routed(q, k, k_scale, w, ks, ke, topk: int, *, max_len: int =
         return out
 
 
-# The serving operators are called per layer and token, so their bindings keep the host's
-# part short: one pass over the tensors, and the device switched only when it differs.
-
-# the current stream's handle without a Stream object (a microsecond less), where torch has it
-_current_handle = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
-    lambda index: torch.cuda.current_stream(index).cuda_stream)
+# The serving operators are called per layer and token, so the checks of their tensors and the
+# calls themselves are a small C++ module (csrc/serve_binding.cpp); what is left here is the
+# allocation of the outputs that the caller did not bring.
+_serve_module = None
 
 
-def _raw_stream(stream, index: int) -> int:
-    if stream is None:
-        return _current_handle(index)
-    return stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+def _serve():
+    """The binding module, on the functions of the loaded libidx."""
+    global _serve_module
+    if _serve_module is None:
+        lib = load()
+        p = os.path.join(_HERE, "_build", "_serve.so")
+        if not os.path.exists(p):
+            raise ImportError(f"_serve.so not found at {p}; run "
+                              "`python -c 'import __graft_entry__ as g; g.build()'` first")
+        loader = importlib.machinery.ExtensionFileLoader("_serve", p)
+        module = importlib.util.module_from_spec(importlib.util.spec_from_loader("_serve", loader))
+        loader.exec_module(module)
+        module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.idx_add_rmsnorm_quant, lib.idx_prefix_attention, lib.idx_cache_evict)))
+        _serve_module = module
+    return _serve_module
 
 
-def _serve_device(fn: str, *ts) -> int:
-    """The index of the one CUDA device that every tensor (all contiguous) lives on."""
-    index = None
-    for t in ts:
-        if t is None:
-            continue
-        i = t.get_device()
-        if i == index:
-            if t.is_contiguous():
-                continue
-        else:
-            if i < 0:
-                raise ValueError(f"{fn}: every tensor must live on a CUDA device")
-            if index is not None:
-                raise ValueError(f"{fn}: tensors on different devices (cuda:{index} and cuda:{i})")
-            index = i
-        if not t.is_contiguous():
-            raise ValueError(f"{fn}: tensors must be contiguous")
-    return index
-
-
-def _serve_call(fn: str, f, index: int, args, options, stats, stream):
-    """f(*args, options, stream) with the tensors' device current."""
+def _serve_call(fn: str, f, args, options, stats, stream):
     o = None
     if options is not None or stats is not None:
-        o = _opt_ref(make_options(options, stats))
-    if torch.cuda.current_device() == index:
-        code = f(*args, o, _raw_stream(stream, index))
-    else:
-        with torch.cuda.device(index):
-            code = f(*args, o, _raw_stream(stream, index))
+        o = make_options(options, stats)
+    if isinstance(stream, torch.cuda.Stream):
+        stream = stream.cuda_stream
+    code = f(*args, None if o is None else ctypes.addressof(o), stream)
     if code:
         _check(fn, code)
-
-
-def _serve_dtype(fn: str, *ts):
-    """The one element type of the tensors, as the C ABI names it."""
-    dtype = ts[0].dtype
-    for t in ts:
-        if t is not None and t.dtype is not dtype:
-            raise ValueError(f"{fn}: {t.dtype} and {dtype} tensors where one type is needed")
-    if dtype not in SERVE_DTYPES:
-        raise ValueError(f"{fn}: unsupported type {dtype}")
-    return SERVE_DTYPES[dtype]
-
-
-def _expect(fn: str, name: str, t, dtype, shape):
-    if t is not None and (t.dtype is not dtype or t.shape != shape):
-        raise ValueError(f"{fn}: {name} must be {dtype} {tuple(shape)}, got {t.dtype} "
-                         f"{tuple(t.shape)}")
 
 
 def idx_add_rmsnorm_quant(x, weight, *, residual=None, residual_out=None, eps: float = 1e-6,
@@ -570,31 +539,17 @@ def idx_add_rmsnorm_quant(x, weight, *, residual=None, residual_out=None, eps: f
     [rows] or, with group 32, 64 or 128, [rows, N // group]).  x may be a column
     slice of a wider tensor.  residual_out receives x + residual in x's type."""
     fn = "idx_add_rmsnorm_quant"
-    if x.dim() != 2 or (x.shape[1] > 1 and x.stride(1) != 1):
-        raise ValueError(f"{fn}: x must be [rows, N] with adjacent columns")
-    rows, N = x.shape
-    x_stride = x.stride(0) if rows > 1 else max(N, x.stride(0))
-    index = _serve_device(fn, weight, residual, residual_out, out, scale)
-    if x.get_device() != index:
-        raise ValueError(f"{fn}: x is not on cuda:{index}, the other tensors' device")
-    dt = _serve_dtype(fn, x, weight, residual, residual_out)
-    _expect(fn, "weight", weight, x.dtype, (N,))
-    _expect(fn, "residual", residual, x.dtype, (rows, N))
-    _expect(fn, "residual_out", residual_out, x.dtype, (rows, N))
-    if group < 0 or (group and N % group):
-        raise ValueError(f"{fn}: {N} columns are not whole groups of {group}")
-    scales = (rows, N // group) if group else (rows,)
-    if out is None:
-        out = torch.empty(rows, N, dtype=torch.float8_e4m3fn, device=x.device)
-    else:
-        _expect(fn, "out", out, torch.float8_e4m3fn, (rows, N))
-    if scale is None:
-        scale = torch.empty(scales, dtype=torch.float32, device=x.device)
-    else:
-        _expect(fn, "scale", scale, torch.float32, scales)
-    _serve_call(fn, load().idx_add_rmsnorm_quant, index, (
-        x.data_ptr(), x_stride, _ptr(residual), weight.data_ptr(), rows, N, eps, group, dt,
-        _ptr(residual_out), out.data_ptr(), scale.data_ptr()), options, stats, stream)
+    if out is None or scale is None:
+        if x.dim() != 2:
+            raise ValueError(f"{fn}: x must be [rows, N] with adjacent columns")
+        rows, N = x.shape
+        if out is None:
+            out = torch.empty(rows, N, dtype=torch.float8_e4m3fn, device=x.device)
+        if scale is None:
+            scale = torch.empty((rows, N // group) if group > 0 else (rows,), dtype=torch.float32,
+                                device=x.device)
+    _serve_call(fn, _serve().add_rmsnorm_quant, (
+        x, weight, residual, residual_out, eps, group, out, scale), options, stats, stream)
     return out, scale
 
 
@@ -613,53 +568,26 @@ def idx_prefix_attention(q, k_cache, v_cache, table, lens, *, prefix_table=None,
     [pages, Hkv, page_size, D]: (out, lse [B, Q, Hq]), and weights_out when weights
     [B, Hkv, slots] (what each private slot has gathered) is given."""
     fn = "idx_prefix_attention"
-    index = _serve_device(fn, q, k_cache, v_cache, table, lens, prefix_table, weights,
-                          weights_out, out, lse, ws)
-    dt = _serve_dtype(fn, q, k_cache, v_cache)
-    cache = k_cache.shape
-    if q.dim() != 4 or len(cache) != 4 or cache != v_cache.shape or table.dim() != 2:
-        raise ValueError(f"{fn}: q [B, Q, Hq, D], caches [pages, Hkv, page_size, D], table [B, P]")
-    B, Q, Hq, D = q.shape
-    pages, Hkv, page_size, cache_d = cache
-    if cache_d != D:
-        raise ValueError(f"{fn}: q has {D} dimensions, the caches {cache_d}")
-    width = table.shape[1]
-    _expect(fn, "table", table, torch.int32, (B, width))
-    _expect(fn, "lens", lens, torch.int32, (B,))
-    if prefix_len > 0 and (prefix_table is None or prefix_table.dtype is not torch.int32 or
-                           prefix_table.numel() * page_size < prefix_len):
-        raise ValueError(f"{fn}: prefix_table must be int32 and cover prefix_len")
-    slots = 0
-    if weights is not None:
-        if weights.dim() != 3 or weights.dtype is not torch.float32 or \
-                weights.shape[:2] != (B, Hkv):
-            raise ValueError(f"{fn}: weights must be float32 [B, Hkv, slots]")
-        slots = weights.shape[2]
-        if weights_out is None:
-            weights_out = torch.zeros_like(weights)
-        else:
-            _expect(fn, "weights_out", weights_out, torch.float32, (B, Hkv, slots))
-    elif weights_out is not None:
-        raise ValueError(f"{fn}: weights_out without weights")
-    if out is None:
-        out = torch.empty_like(q)
-    else:
-        _expect(fn, "out", out, q.dtype, q.shape)
-    if lse is None:
-        lse = torch.empty(B, Q, Hq, dtype=torch.float32, device=q.device)
-    else:
-        _expect(fn, "lse", lse, torch.float32, (B, Q, Hq))
-    if ws is None:
-        need = idx_prefix_attention_workspace(
-            B, Q, Hq, Hkv, D, prefix_len, max_len or width * page_size,
-            weights is not None) if Hq % Hkv == 0 else 0
-        ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
-    _serve_call(fn, load().idx_prefix_attention, index, (
-        q.data_ptr(), k_cache.data_ptr(), v_cache.data_ptr(), _ptr(prefix_table),
-        table.data_ptr(), lens.data_ptr(), _ptr(weights), B, Q, Hq, Hkv, D, pages, page_size,
-        prefix_len, width, max_len, slots, D ** -0.5 if scale is None else scale, dt,
-        out.data_ptr(), lse.data_ptr(), _ptr(weights_out), ws.data_ptr(), ws.nbytes),
-        options, stats, stream)
+    if out is None or lse is None or ws is None:
+        if q.dim() != 4 or k_cache.dim() != 4 or table.dim() != 2:
+            raise ValueError(f"{fn}: q [B, Q, Hq, D], caches [pages, Hkv, page_size, D], "
+                             "table [B, P]")
+        B, Q, Hq, D = q.shape
+        if out is None:
+            out = torch.empty_like(q)
+        if lse is None:
+            lse = torch.empty(B, Q, Hq, dtype=torch.float32, device=q.device)
+        if ws is None:
+            Hkv, page_size = k_cache.shape[1:3]
+            need = idx_prefix_attention_workspace(
+                B, Q, Hq, Hkv, D, prefix_len, max_len or table.shape[1] * page_size,
+                weights is not None) if Hkv and Hq % Hkv == 0 else 0
+            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    if weights is not None and weights_out is None:
+        weights_out = torch.zeros_like(weights)
+    _serve_call(fn, _serve().prefix_attention, (
+        q, k_cache, v_cache, table, lens, prefix_table, prefix_len, max_len, scale, weights,
+        weights_out, out, lse, ws), options, stats, stream)
     return (out, lse) if weights is None else (out, lse, weights_out)
 
 
@@ -676,41 +604,20 @@ def idx_cache_evict(k_cache, v_cache, table, lens, weights, positions, next_pos,
     that move do so in place.  Returns (lens_out, weights_out, positions_out);
     weights_out and positions_out may be the inputs themselves."""
     fn = "idx_cache_evict"
-    index = _serve_device(fn, k_cache, v_cache, table, lens, weights, positions, next_pos,
-                          lens_out, weights_out, positions_out, ws)
-    dt = _serve_dtype(fn, k_cache, v_cache)
-    cache = k_cache.shape
-    if len(cache) != 4 or cache != v_cache.shape or table.dim() != 2 or weights.dim() != 3:
-        raise ValueError(f"{fn}: caches [pages, Hkv, page_size, D], table [B, P], weights "
-                         "[B, Hkv, slots]")
-    pages, Hkv, page_size, D = cache
-    B, width = table.shape
-    shape = (B, Hkv, weights.shape[2])
-    _expect(fn, "table", table, torch.int32, (B, width))
-    _expect(fn, "lens", lens, torch.int32, (B,))
-    _expect(fn, "next_pos", next_pos, torch.int32, (B,))
-    _expect(fn, "weights", weights, torch.float32, shape)
-    _expect(fn, "positions", positions, torch.int32, shape)
     if lens_out is None:
         lens_out = torch.empty_like(lens)
-    else:
-        _expect(fn, "lens_out", lens_out, torch.int32, (B,))
     if weights_out is None:
         weights_out = torch.zeros_like(weights)
-    else:
-        _expect(fn, "weights_out", weights_out, torch.float32, shape)
     if positions_out is None:
         positions_out = torch.full_like(positions, -1)
-    else:
-        _expect(fn, "positions_out", positions_out, torch.int32, shape)
     if ws is None:
-        ws = torch.empty(max(256, idx_cache_evict_workspace(B, Hkv, budget,
-                                                            max_len or width * page_size)),
-                         dtype=torch.uint8, device=lens.device)
-    _serve_call(fn, load().idx_cache_evict, index, (
-        k_cache.data_ptr(), v_cache.data_ptr(), table.data_ptr(), lens.data_ptr(),
-        weights.data_ptr(), positions.data_ptr(), next_pos.data_ptr(), B, Hkv, D, pages,
-        page_size, width, max_len, shape[2], budget, recent, sink, dt, lens_out.data_ptr(),
-        weights_out.data_ptr(), positions_out.data_ptr(), ws.data_ptr(), ws.nbytes),
-        options, stats, stream)
+        if k_cache.dim() != 4 or table.dim() != 2:
+            raise ValueError(f"{fn}: caches [pages, Hkv, page_size, D], table [B, P], weights "
+                             "[B, Hkv, slots]")
+        need = idx_cache_evict_workspace(table.shape[0], k_cache.shape[1], budget,
+                                         max_len or table.shape[1] * k_cache.shape[2])
+        ws = torch.empty(max(256, need), dtype=torch.uint8, device=lens.device)
+    _serve_call(fn, _serve().cache_evict, (
+        k_cache, v_cache, table, lens, weights, positions, next_pos, budget, recent, sink, max_len,
+        lens_out, weights_out, positions_out, ws), options, stats, stream)
     return lens_out, weights_out, positions_out
