@@ -118,6 +118,7 @@ template <int D> constexpr int part_smem() { return kPartWarps * kRing * kStep *
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_kernel(AttnArgs a) {
     extern __shared__ __align__(128) uint8_t smem[];
+    if (a.prefix_splits == 0) pdl_wait();  // the call's first launch
     pdl_trigger();
     // This grid reads nothing that the prefix's writes; one block's wait for it makes the
     // join's wait for this grid cover both.
@@ -487,7 +488,7 @@ IDX_DEVI void add_weights(const AttnArgs& a, int u, float* row_lse) {
 template <typename T, int D, int WPR>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int join_blocks) {
     __shared__ float scratch[kAttnMaxTokens * kAttnMaxGroup];
-    pdl_wait();
+    pdl_wait();  // (no pdl_trigger: the next call's prefix grid came in its way, 74 -> 81 us)
     if ((int)blockIdx.x < join_blocks) {
         const int warp = threadIdx.x >> 5;
         const long long row = (long long)blockIdx.x * (kJoinWarps / WPR) + warp / WPR;
@@ -499,7 +500,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
 }
 
 template <typename T, int D, int NT>
-cudaError_t launch_private(const AttnArgs& a, bool overlap, cudaStream_t s) {
+cudaError_t launch_private(const AttnArgs& a, cudaStream_t s) {
     static std::once_flag once;
     static cudaError_t attr_err = cudaSuccess;
     std::call_once(once, [] {
@@ -509,7 +510,7 @@ cudaError_t launch_private(const AttnArgs& a, bool overlap, cudaStream_t s) {
     if (attr_err != cudaSuccess) return attr_err;
     const dim3 grid((a.Q * a.G + 8 * NT - 1) / (8 * NT) * a.Hkv * a.private_splits, a.B);
     return launch_k(attn_part_kernel<T, D, NT>, grid, dim3(kPartWarps * 32), part_smem<D>(), s,
-                    overlap, a);
+                    true, a);
 }
 
 template <typename T, int D>
@@ -521,9 +522,9 @@ cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStre
         ++*launched;
     }
     if (a.private_splits > 0) {
-        e = a.private_dense  ? launch_private_dense(a, dt, *launched > 0, s)
-            : a.Q * a.G <= 8 ? launch_private<T, D, 1>(a, *launched > 0, s)
-                             : launch_private<T, D, 2>(a, *launched > 0, s);
+        e = a.private_dense  ? launch_private_dense(a, dt, s)
+            : a.Q * a.G <= 8 ? launch_private<T, D, 1>(a, s)
+                             : launch_private<T, D, 2>(a, s);
         if (e != cudaSuccess) return e;
         ++*launched;
     }
@@ -538,7 +539,7 @@ cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStre
     if (join_blocks + weight_blocks > 0x7fffffffll) return cudaErrorInvalidValue;
     const auto kern = wide ? attn_join_kernel<T, D, kJoinWarps> : attn_join_kernel<T, D, 1>;
     e = launch_k(kern, dim3((unsigned)(join_blocks + weight_blocks)), dim3(kJoinThreads), 0, s,
-                 *launched > 0, a, (int)join_blocks);
+                 true, a, (int)join_blocks);
     if (e == cudaSuccess) ++*launched;
     return e;
 }

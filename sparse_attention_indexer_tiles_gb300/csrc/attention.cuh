@@ -58,9 +58,8 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
                    int sm_count);
 
 // The prefix's parts, and the private ones of requests with many rows (attention_prefix.cu).
-// `overlap`: the launch may start beside the one before it.
 cudaError_t launch_prefix_parts(const AttnArgs& a, idx_dtype dt, cudaStream_t s);
-cudaError_t launch_private_dense(const AttnArgs& a, idx_dtype dt, bool overlap, cudaStream_t s);
+cudaError_t launch_private_dense(const AttnArgs& a, idx_dtype dt, cudaStream_t s);
 
 // Returns the number of kernels launched through *launched.
 cudaError_t launch_attention(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStream_t s,

@@ -211,6 +211,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    if (!PRIVATE || a.prefix_splits == 0) pdl_wait();  // the call's first launch
     pdl_trigger();  // the private parts may take the SMs that this grid leaves idle
 
     // this CTA: key head, pair of row tiles, part of the prefix
@@ -636,7 +637,7 @@ CUresult make_map(CUtensorMap* m, const void* base, const cuuint64_t (&dims)[N],
 }
 
 template <typename T, int D, bool PRIVATE>
-cudaError_t launch_t(const AttnArgs& args, bool overlap, cudaStream_t s) {
+cudaError_t launch_t(const AttnArgs& args, cudaStream_t s) {
     using C = PrefixCfg<D>;
     AttnArgs a = args;
     // keys per copy: a whole page where it divides the tile, else 16 (no page is smaller)
@@ -669,26 +670,26 @@ cudaError_t launch_t(const AttnArgs& args, bool overlap, cudaStream_t s) {
     return launch_k(attn_prefix_kernel<T, D, PRIVATE>,
                     dim3((ntiles + 1) / 2, PRIVATE ? a.private_splits : a.prefix_splits,
                          PRIVATE ? a.B * a.Hkv : a.Hkv),
-                    dim3(kPrefixThreads), C::SMEM, s, overlap, tq, tk, tv, a);
+                    dim3(kPrefixThreads), C::SMEM, s, true, tq, tk, tv, a);
 }
 
 template <bool PRIVATE>
-cudaError_t launch_dense(const AttnArgs& a, idx_dtype dt, bool overlap, cudaStream_t s) {
+cudaError_t launch_dense(const AttnArgs& a, idx_dtype dt, cudaStream_t s) {
     if (dt == IDX_BF16)
-        return a.D == 128 ? launch_t<__nv_bfloat16, 128, PRIVATE>(a, overlap, s)
-                          : launch_t<__nv_bfloat16, 64, PRIVATE>(a, overlap, s);
-    return a.D == 128 ? launch_t<__half, 128, PRIVATE>(a, overlap, s)
-                      : launch_t<__half, 64, PRIVATE>(a, overlap, s);
+        return a.D == 128 ? launch_t<__nv_bfloat16, 128, PRIVATE>(a, s)
+                          : launch_t<__nv_bfloat16, 64, PRIVATE>(a, s);
+    return a.D == 128 ? launch_t<__half, 128, PRIVATE>(a, s)
+                      : launch_t<__half, 64, PRIVATE>(a, s);
 }
 
 }  // namespace
 
 cudaError_t launch_prefix_parts(const AttnArgs& a, idx_dtype dt, cudaStream_t s) {
-    return launch_dense<false>(a, dt, false, s);
+    return launch_dense<false>(a, dt, s);
 }
 
-cudaError_t launch_private_dense(const AttnArgs& a, idx_dtype dt, bool overlap, cudaStream_t s) {
-    return launch_dense<true>(a, dt, overlap, s);
+cudaError_t launch_private_dense(const AttnArgs& a, idx_dtype dt, cudaStream_t s) {
+    return launch_dense<true>(a, dt, s);
 }
 
 }  // namespace idx
