@@ -202,6 +202,45 @@ def _stream(stream) -> int:
     return int(stream)
 
 
+class _Launch:
+    """The context in which a call on `device` makes what the caller did not bring.  When the call
+    was given a stream, that stream is current in it: fills are ordered with the kernels, and the
+    memory of what the call drops on return (its workspace) is not handed out again before they
+    have ended.  `result` marks a tensor that is returned as used on the caller's stream too."""
+
+    __slots__ = ("context", "caller")
+
+    def __init__(self, stream, device):
+        self.caller = self.context = None
+        if stream is None:
+            return
+        if device.type != "cuda":
+            raise ValueError("idx: every tensor must live on a CUDA device")
+        if not isinstance(stream, torch.cuda.Stream):
+            # 0 and 1 are handles of the default stream, which torch keeps as one of its own
+            stream = torch.cuda.default_stream(device) if int(stream) in (0, 1) else \
+                torch.cuda.ExternalStream(int(stream), device=device)
+        if stream.device != device:
+            raise ValueError(f"idx: a stream of {stream.device} for tensors on {device}")
+        caller = torch.cuda.current_stream(device)
+        if caller.cuda_stream != stream.cuda_stream:
+            self.caller, self.context = caller, torch.cuda.stream(stream)
+
+    def __enter__(self):
+        if self.context is not None:
+            self.context.__enter__()
+        return self
+
+    def __exit__(self, *exc):
+        if self.context is not None:
+            self.context.__exit__(*exc)
+
+    def result(self, t):
+        if self.caller is not None:
+            t.record_stream(self.caller)
+        return t
+
+
 def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
@@ -543,11 +582,12 @@ def idx_add_rmsnorm_quant(x, weight, *, residual=None, residual_out=None, eps: f
         if x.dim() != 2:
             raise ValueError(f"{fn}: x must be [rows, N] with adjacent columns")
         rows, N = x.shape
-        if out is None:
-            out = torch.empty(rows, N, dtype=torch.float8_e4m3fn, device=x.device)
-        if scale is None:
-            scale = torch.empty((rows, N // group) if group > 0 else (rows,), dtype=torch.float32,
-                                device=x.device)
+        with _Launch(stream, x.device) as on:
+            if out is None:
+                out = on.result(torch.empty(rows, N, dtype=torch.float8_e4m3fn, device=x.device))
+            if scale is None:
+                scale = on.result(torch.empty((rows, N // group) if group > 0 else (rows,),
+                                              dtype=torch.float32, device=x.device))
     _serve_call(fn, _serve().add_rmsnorm_quant, (
         x, weight, residual, residual_out, eps, group, out, scale), options, stats, stream)
     return out, scale
@@ -573,18 +613,20 @@ def idx_prefix_attention(q, k_cache, v_cache, table, lens, *, prefix_table=None,
             raise ValueError(f"{fn}: q [B, Q, Hq, D], caches [pages, Hkv, page_size, D], "
                              "table [B, P]")
         B, Q, Hq, D = q.shape
-        if out is None:
-            out = torch.empty_like(q)
-        if lse is None:
-            lse = torch.empty(B, Q, Hq, dtype=torch.float32, device=q.device)
-        if ws is None:
-            Hkv, page_size = k_cache.shape[1:3]
-            need = idx_prefix_attention_workspace(
-                B, Q, Hq, Hkv, D, prefix_len, max_len or table.shape[1] * page_size,
-                weights is not None) if Hkv and Hq % Hkv == 0 else 0
-            ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+        with _Launch(stream, q.device) as on:
+            if out is None:
+                out = on.result(torch.empty_like(q))
+            if lse is None:
+                lse = on.result(torch.empty(B, Q, Hq, dtype=torch.float32, device=q.device))
+            if ws is None:
+                Hkv, page_size = k_cache.shape[1:3]
+                need = idx_prefix_attention_workspace(
+                    B, Q, Hq, Hkv, D, prefix_len, max_len or table.shape[1] * page_size,
+                    weights is not None) if Hkv and Hq % Hkv == 0 else 0
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
     if weights is not None and weights_out is None:
-        weights_out = torch.zeros_like(weights)
+        with _Launch(stream, q.device) as on:
+            weights_out = on.result(torch.zeros_like(weights))
     _serve_call(fn, _serve().prefix_attention, (
         q, k_cache, v_cache, table, lens, prefix_table, prefix_len, max_len, scale, weights,
         weights_out, out, lse, ws), options, stats, stream)
@@ -604,19 +646,21 @@ def idx_cache_evict(k_cache, v_cache, table, lens, weights, positions, next_pos,
     that move do so in place.  Returns (lens_out, weights_out, positions_out);
     weights_out and positions_out may be the inputs themselves."""
     fn = "idx_cache_evict"
-    if lens_out is None:
-        lens_out = torch.empty_like(lens)
-    if weights_out is None:
-        weights_out = torch.zeros_like(weights)
-    if positions_out is None:
-        positions_out = torch.full_like(positions, -1)
-    if ws is None:
+    if lens_out is None or weights_out is None or positions_out is None or ws is None:
         if k_cache.dim() != 4 or table.dim() != 2:
             raise ValueError(f"{fn}: caches [pages, Hkv, page_size, D], table [B, P], weights "
                              "[B, Hkv, slots]")
-        need = idx_cache_evict_workspace(table.shape[0], k_cache.shape[1], budget,
-                                         max_len or table.shape[1] * k_cache.shape[2])
-        ws = torch.empty(max(256, need), dtype=torch.uint8, device=lens.device)
+        with _Launch(stream, lens.device) as on:
+            if lens_out is None:
+                lens_out = on.result(torch.empty_like(lens))
+            if weights_out is None:
+                weights_out = on.result(torch.zeros_like(weights))
+            if positions_out is None:
+                positions_out = on.result(torch.full_like(positions, -1))
+            if ws is None:
+                need = idx_cache_evict_workspace(table.shape[0], k_cache.shape[1], budget,
+                                                 max_len or table.shape[1] * k_cache.shape[2])
+                ws = torch.empty(max(256, need), dtype=torch.uint8, device=lens.device)
     _serve_call(fn, _serve().cache_evict, (
         k_cache, v_cache, table, lens, weights, positions, next_pos, budget, recent, sink, max_len,
         lens_out, weights_out, positions_out, ws), options, stats, stream)
