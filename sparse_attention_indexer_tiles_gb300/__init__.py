@@ -220,7 +220,7 @@ class _Launch:
             # 0 and 1 are handles of the default stream, which torch keeps as one of its own
             stream = torch.cuda.default_stream(device) if int(stream) in (0, 1) else \
                 torch.cuda.ExternalStream(int(stream), device=device)
-        if stream.device != device:
+        if device.index is not None and stream.device != device:
             raise ValueError(f"idx: a stream of {stream.device} for tensors on {device}")
         caller = torch.cuda.current_stream(device)
         if caller.cuda_stream != stream.cuda_stream:
@@ -288,14 +288,14 @@ def idx_score_topk(q, k, k_scale, w, ks, ke, topk: int, *, max_len: int = 0, out
                    options=None, stats: Stats | None = None, stream=None):
     """Exact top-k indices [rows, topk] int32 (ascending, -1 padded)."""
     dev = _dev(q, k, k_scale, w, ks, ke, out, ws)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _Launch(stream, dev) as on:
         rows, H, D = q.shape
         keys = k.shape[0]
         dt = DTYPES[q.dtype]
         o = make_options(options, stats)
         need = idx_score_topk_workspace(rows, keys, max_len, H, D, topk, dt, o)
         if out is None:
-            out = torch.empty(rows, topk, dtype=torch.int32, device=q.device)
+            out = on.result(torch.empty(rows, topk, dtype=torch.int32, device=q.device))
         if ws is None:
             ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
         _check("idx_score_topk", load().idx_score_topk(
@@ -326,7 +326,7 @@ def idx_score_topk_host(q, k, k_scale, w, ks, ke, topk: int, *, max_len: int = 0
         if device is None else torch.device(device)
     if not dev.type == "cuda":
         raise ValueError("idx_score_topk_host: the workspace lives on a CUDA device")
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _Launch(stream, dev):
         rows, H, D = q.shape
         keys = k.shape[0]
         dt = DTYPES[q.dtype]
@@ -351,14 +351,14 @@ def idx_topk_from_scores(scores, ks, ke, topk: int, *, out=None, ws=None, option
                          stats: Stats | None = None, stream=None):
     """Exact top-k of fp32 scores [rows, row_stride]; ks may be None."""
     dev = _dev(scores, ks, ke, out, ws)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _Launch(stream, dev) as on:
         if scores.dtype != torch.float32:
             raise ValueError("idx_topk_from_scores: scores must be float32")
         rows, stride = scores.shape
         o = make_options(options, stats)
         need = int(load().idx_topk_workspace(rows, stride, topk, _opt_ref(o)))
         if out is None:
-            out = torch.empty(rows, topk, dtype=torch.int32, device=scores.device)
+            out = on.result(torch.empty(rows, topk, dtype=torch.int32, device=scores.device))
         if ws is None and need:
             ws = torch.empty(need, dtype=torch.uint8, device=scores.device)
         nbytes = 0 if ws is None else ws.numel() * ws.element_size()
@@ -372,12 +372,12 @@ def idx_score_materialise(q, k, k_scale, w, ks, ke, *, out=None, row_stride: int
                           options=None, stats: Stats | None = None, stream=None):
     """fp32 scores [rows, row_stride]; row r's key j at column j - ks[r]."""
     dev = _dev(q, k, k_scale, w, ks, ke, out)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _Launch(stream, dev) as on:
         rows, H, D = q.shape
         keys = k.shape[0]
         if out is None:
             stride = row_stride or keys
-            out = torch.empty(rows, stride, dtype=torch.float32, device=q.device)
+            out = on.result(torch.empty(rows, stride, dtype=torch.float32, device=q.device))
         stride = out.shape[1]
         o = make_options(options, stats)
         _check("idx_score_materialise", load().idx_score_materialise(
@@ -405,11 +405,12 @@ def idx_mxfp4_to_e4m3(x, sf, *, out=None, options=None, stats: Stats | None = No
     """MXFP4 rows x [n, D/2] + sf [n, D/32] -> e4m3 [n, D] (exact within the
     e4m3 range, else IDX_DEV_RANGE)."""
     dev = _dev(x, sf, out)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _Launch(stream, dev) as on:
         n, half = x.shape[0], x.shape[-1]
         D = 2 * half
         if out is None:
-            out = torch.empty(*x.shape[:-1], D, dtype=torch.float8_e4m3fn, device=x.device)
+            out = on.result(torch.empty(*x.shape[:-1], D, dtype=torch.float8_e4m3fn,
+                                        device=x.device))
         o = make_options(options, stats)
         _check("idx_mxfp4_to_e4m3", load().idx_mxfp4_to_e4m3(
             _ptr(x), _ptr(sf), x.numel() // half, D, _ptr(out), _opt_ref(o), _stream(stream)))
@@ -421,14 +422,14 @@ def idx_score_topk_mxfp4(q, q_sf, k, k_sf, k_scale, w, ks, ke, topk: int, *, max
                          stream=None):
     """idx_score_topk on MXFP4 q/k (with their e8m0 block scales)."""
     dev = _dev(q, q_sf, k, k_sf, k_scale, w, ks, ke, out, ws)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _Launch(stream, dev) as on:
         rows, H, D = _mx_shapes(q, q_sf, k, k_sf)
         keys = k.shape[0]
         o = make_options(options, stats)
         need = int(load().idx_score_topk_mxfp4_workspace(rows, keys, max_len, H, D, topk,
                                                          _opt_ref(o)))
         if out is None:
-            out = torch.empty(rows, topk, dtype=torch.int32, device=q.device)
+            out = on.result(torch.empty(rows, topk, dtype=torch.int32, device=q.device))
         if ws is None:
             ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
         _check("idx_score_topk_mxfp4", load().idx_score_topk_mxfp4(
@@ -443,11 +444,12 @@ def idx_score_materialise_mxfp4(q, q_sf, k, k_sf, k_scale, w, ks, ke, *, out=Non
                                 stats: Stats | None = None, stream=None):
     """idx_score_materialise on MXFP4 q/k (with their e8m0 block scales)."""
     dev = _dev(q, q_sf, k, k_sf, k_scale, w, ks, ke, out, ws)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _Launch(stream, dev) as on:
         rows, H, D = _mx_shapes(q, q_sf, k, k_sf)
         keys = k.shape[0]
         if out is None:
-            out = torch.empty(rows, row_stride or keys, dtype=torch.float32, device=q.device)
+            out = on.result(torch.empty(rows, row_stride or keys, dtype=torch.float32,
+                                        device=q.device))
         need = int(load().idx_score_materialise_mxfp4_workspace(rows, keys, H, D))
         if ws is None:
             ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
@@ -464,7 +466,7 @@ def idx_score_topk_noalloc(q, k, k_scale, w, ks, ke, topk: int, *, max_len: int 
     """idx_score_topk on the library's built-in scratch array (no workspace,
     no allocation by the library; out is allocated here when not given)."""
     dev = _dev(q, k, k_scale, w, ks, ke, out)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _Launch(stream, dev) as on:
         lib = load()
         fn = lib.idx_score_topk_noalloc
         P, I, LL = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
@@ -472,7 +474,7 @@ def idx_score_topk_noalloc(q, k, k_scale, w, ks, ke, topk: int, *, max_len: int 
         fn.restype = I
         rows, H, D = q.shape
         if out is None:
-            out = torch.empty(rows, topk, dtype=torch.int32, device=q.device)
+            out = on.result(torch.empty(rows, topk, dtype=torch.int32, device=q.device))
         o = make_options(options, stats)
         _check("idx_score_topk_noalloc", fn(
             _ptr(q), _ptr(k), _ptr(k_scale), _ptr(w), _ptr(ks), _ptr(ke), rows, k.shape[0], max_len,
@@ -518,7 +520,7 @@ def idx_score_topk_routed(q, k, k_scale, w, ks, ke, topk: int, *, max_len: int =
     """idx_score_topk by the faster path for the longest row (fused, or the
     logits then their top-k); the same indices either way."""
     dev = _dev(q, k, k_scale, w, ks, ke, out, ws)
-    with torch.cuda.device(dev):
+    with torch.cuda.device(dev), _Launch(stream, dev) as on:
         rows, H, D = q.shape
         keys = k.shape[0]
         dt = DTYPES[q.dtype]
@@ -526,7 +528,7 @@ def idx_score_topk_routed(q, k, k_scale, w, ks, ke, topk: int, *, max_len: int =
         need = int(load().idx_score_topk_routed_workspace(rows, keys, max_len, H, D, topk, dt,
                                                           _opt_ref(o)))
         if out is None:
-            out = torch.empty(rows, topk, dtype=torch.int32, device=q.device)
+            out = on.result(torch.empty(rows, topk, dtype=torch.int32, device=q.device))
         if ws is None:
             ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
         _check("idx_score_topk_routed", load().idx_score_topk_routed(

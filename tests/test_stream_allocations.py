@@ -115,3 +115,53 @@ def test_a_stream_of_another_device(monkeypatch, name):
     with pytest.raises(ValueError, match="stream of cuda:1"):
         serving(w, stream=FakeStream(42, torch.device("cuda", 1)))[name]()
     assert not w.made and not w.launches
+
+
+class FakeLibrary:
+    """Every size query answers 4096, every call 0 (with its stream, the last argument, kept)."""
+
+    def __init__(self, world):
+        self.world = world
+
+    def __getattr__(self, name):
+        if name.endswith("_workspace"):
+            f = lambda *a: 4096  # noqa: E731
+        else:
+            f = lambda *a: self.world.launches.append(a) or 0  # noqa: E731
+        return f
+
+
+def scoring(w, **kw):
+    def t(dtype, *shape):
+        x = w.t(*shape)
+        x.dtype = dtype
+        return x
+
+    q, k = t(torch.bfloat16, 4, 8, 64), t(torch.bfloat16, 100, 64)
+    rest = [w.t(100), w.t(4, 8), w.t(4), w.t(4)]
+    x, sf, kx, ksf = (t(torch.uint8, *s) for s in ((4, 8, 32), (4, 8, 2), (100, 32), (100, 2)))
+    codes = (x, sf, kx, ksf)
+    return {
+        "topk": (lambda: pkg.idx_score_topk(q, k, *rest, 16, **kw), 1, 1),
+        "from_scores": (lambda: pkg.idx_topk_from_scores(w.t(4, 100), None, rest[3], 16, **kw), 1, 1),
+        "materialise": (lambda: pkg.idx_score_materialise(q, k, *rest, **kw), 1, 0),
+        "expand": (lambda: pkg.idx_mxfp4_to_e4m3(x, sf, **kw), 1, 0),
+        "topk_mxfp4": (lambda: pkg.idx_score_topk_mxfp4(*codes, *rest, 16, **kw), 1, 1),
+        "materialise_mxfp4": (lambda: pkg.idx_score_materialise_mxfp4(*codes, *rest, **kw), 1, 1),
+        "noalloc": (lambda: pkg.idx_score_topk_noalloc(q, k, *rest, 16, **kw), 1, 0),
+        "routed": (lambda: pkg.idx_score_topk_routed(q, k, *rest, 16, **kw), 1, 1)}
+
+
+@pytest.mark.parametrize("stream", [None, FakeStream(7), FakeStream(42), 42, 0])
+@pytest.mark.parametrize("name", ["topk", "from_scores", "materialise", "expand", "topk_mxfp4", "materialise_mxfp4",
+                                  "noalloc", "routed"])
+def test_the_scoring_calls(monkeypatch, name, stream):
+    w = World(monkeypatch)
+    monkeypatch.setattr(pkg, "load", lambda: FakeLibrary(w))
+    call, results, workspaces = scoring(w, stream=stream)[name]
+    got = call()
+    handle = {None: 7, 42: 42, 0: 0}[stream] if not isinstance(stream, FakeStream) else stream.cuda_stream
+    assert [t.made_on for t in w.made] == [handle] * (results + workspaces)
+    assert w.launches[-1][-1] == handle
+    assert got.used_on == ([7] if handle != 7 else [])
+    assert sum(t.used_on == [] for t in w.made) == workspaces + (results if handle == 7 else 0)
