@@ -416,7 +416,8 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
  *       table's width where the call says 0), 256-byte aligned; needs no
  *       clearing between calls
  * Supported: D 64 or 128; page_size 16, 32, 64 or 128; 1 <= Q <= 16; Hq a
- * multiple of Hkv with Hq / Hkv <= 128; B * Hkv <= 65535; pages >= 1 with keys.  Device errors
+ * multiple of Hkv with Hq / Hkv <= 128; B * Hkv <= 65535; prefix_len, max_len < 2^30; pages >= 1
+ * with keys.  The workspace query gives 0 for sizes that the call refuses.  Device errors
  * (IDX_DEV_RANGE): lens[b] outside [0, max_len] is clamped; a page outside
  * [0, pages) reads as zeros, and the results of its request (of all of them,
  * for a page of the prefix) are meaningless.

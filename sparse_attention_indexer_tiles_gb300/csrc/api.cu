@@ -984,14 +984,24 @@ int page_shift(int p) { return p == 16 ? 4 : p == 32 ? 5 : p == 64 ? 6 : 7; }
 
 bool is_16bit(idx_dtype dt) { return dt == IDX_BF16 || dt == IDX_FP16; }
 
+constexpr int kMaxPrivate = 0x3fffffff;  // private slots per request
+
 // max_len 0 is the table's whole width; false when the bound does not fit it.
 bool private_bound(int& max_len, long long table_stride, int page_size) {
     const long long width = table_stride * page_size;
     if (max_len == 0) {
-        if (width > 0x3fffffffll) return false;
+        if (width > kMaxPrivate) return false;
         max_len = (int)width;
     }
-    return max_len <= width && max_len <= 0x3fffffff;
+    return max_len <= width && max_len <= kMaxPrivate;
+}
+
+// The sizes that an attention call takes and that attn_plan is made for; the arguments are not
+// negative, and Hq is a multiple of Hkv.
+bool attn_supported(int B, int Q, int Hq, int Hkv, int D, int prefix_len) {
+    return (D == 64 || D == 128) && Q <= kAttnMaxTokens && Hq / Hkv <= kAttnMaxGroup &&
+           (long long)B * Hkv <= 65535 && (long long)B * Q * Hq <= 0x7fffff00ll &&
+           prefix_len <= 0x3fffffff;
 }
 
 }  // namespace
@@ -1044,8 +1054,8 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
 
 size_t idx_prefix_attention_workspace(int B, int Q, int Hq, int Hkv, int D, int prefix_len,
                                       int max_len, int weights) {
-    if (B <= 0 || Q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || D < 1 || prefix_len < 0 ||
-        max_len < 0)
+    if (B <= 0 || Q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || prefix_len < 0 || max_len < 0 ||
+        !attn_supported(B, Q, Hq, Hkv, D, prefix_len) || max_len > kMaxPrivate)
         return 0;
     return attn_plan(B, Q, Hq, Hkv, D, prefix_len, max_len, weights != 0, sm_count()).total;
 }
@@ -1060,10 +1070,8 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
     if (B < 0 || Q < 1 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || pages < 0 || prefix_len < 0 ||
         table_stride < 0 || max_len < 0 || !std::isfinite(scale) || !w != !w_out)
         return IDX_EINVAL;
-    if (!is_16bit(dt) || (D != 64 && D != 128) || !page_size_ok(page_size) ||
-        Q > kAttnMaxTokens || Hq / Hkv > kAttnMaxGroup || (long long)B * Hkv > 65535 ||
-        (long long)B * Q * Hq > 0x7fffff00ll || prefix_len > 0x3fffffff ||
-        (long long)pages * Hkv > 0x7fffff00ll)
+    if (!is_16bit(dt) || !page_size_ok(page_size) ||
+        !attn_supported(B, Q, Hq, Hkv, D, prefix_len) || (long long)pages * Hkv > 0x7fffff00ll)
         return IDX_EUNSUPPORTED;
     if (!private_bound(max_len, table_stride, page_size)) return IDX_EINVAL;
     if (w && slots < max_len) return IDX_EINVAL;
