@@ -399,7 +399,8 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
  * tokens in order, and a token does not see those after it.  With key head
  * head / (Hq / Hkv), z_j = scale * q . k_j:
  *     out = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse = log sum_j exp(z_j)
- * A row that sees nothing gets out 0 and lse -inf.
+ * A row that sees nothing gets out 0 and lse -inf; one that sees a NaN logit or one of +inf
+ * gets NaN, and so do the weights of its request and key head.
  *
  *   q   [B, Q, Hq, D];  k_cache, v_cache [pages, Hkv, page_size, D]; bf16 or fp16
  *   prefix_table [ceil(prefix_len / page_size)] int32: the prefix's pages in order

@@ -368,21 +368,29 @@ __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_ke
             acc.z += f * x.z;
             acc.w += f * x.w;
         }
-        const float inv = sum > 0.f ? 1.f / sum : 0.f;
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays one
         const long long at = query_row(r) * total_splits + slot;
         *reinterpret_cast<float4*>(a.part + at * D + d) =
             make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
-        if (d == 0) a.part_lse[at] = sum > 0.f ? top + log2f(sum) : -INFINITY;
+        if (d == 0) a.part_lse[at] = sum == 0.f ? -INFINITY : top + log2f(sum);
     }
     if (last) pdl_wait();
 }
 
-// log2-sum-exp2 of a row's parts: every lane of the warp gets it
+// The larger of two, NaN when either is (fmaxf gives the other).
+IDX_DEVI float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+
+// log2-sum-exp2 of a row's parts: every lane of the warp gets it; NaN when a part's is, so that
+// a NaN or infinite logit is not lost
 IDX_DEVI float join_lse(const float* part_lse, int splits, int lane) {
     float m = -INFINITY;
-    for (int i = lane; i < splits; i += 32) m = fmaxf(m, part_lse[i]);
+    for (int i = lane; i < splits; i += 32) m = max_nan(m, part_lse[i]);
 #pragma unroll
-    for (int o = 16; o > 0; o /= 2) m = fmaxf(m, __shfl_xor_sync(~0u, m, o));
+    for (int o = 16; o > 0; o /= 2) m = max_nan(m, __shfl_xor_sync(~0u, m, o));
     if (m == -INFINITY) return m;
     float l = 0.f;
     for (int i = lane; i < splits; i += 32) l += exp2_approx(part_lse[i] - m);

@@ -568,7 +568,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 f1 = ex2(ml[row] - base);
                 l = l * f0 + ml[128 + row] * f1;
             }
-            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays one
             f0 *= inv;
             f1 *= inv;
             // Rows leave through the stream's own Q tile (its products are done): a thread
@@ -612,7 +612,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 }
                 __syncwarp();
             }
-            if (live) a.part_lse[part] = l > 0.f ? top + log2f(l) : -INFINITY;
+            if (live) a.part_lse[part] = l == 0.f ? -INFINITY : top + log2f(l);
         }
         tc_fence_before();
     }
