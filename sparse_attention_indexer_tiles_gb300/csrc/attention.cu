@@ -402,6 +402,47 @@ IDX_DEVI float join_lse(const float* part_lse, int splits, int lane) {
 constexpr int kJoinThreads = 256, kJoinWarps = kJoinThreads / 32;
 constexpr int kSlotsPerThread = 4, kWeightSlots = kJoinThreads * kSlotsPerThread;
 
+// A row that does not see its request's last keys weighs them with 0, and 0 times a V that is not
+// finite is NaN.  This is the row's sum over its parts again (`lane`'s columns of it), those that
+// reach past what it sees taken key by key up to there: called for such rows when their result is
+// not finite, so rarely that its speed does not count.
+template <typename T, int D>
+__device__ __noinline__ void sum_visible(const AttnArgs& a, long long row, float lse, int lane,
+                                         float* sum) {
+    constexpr int W = D / 32;
+    const int splits = a.prefix_splits + a.private_splits;
+    const int head = (int)(row % a.Hq), hk = head / a.G;
+    const int t = (int)(row / a.Hq % a.Q), b = (int)(row / a.Hq / a.Q);
+    const int n = min(max(a.lens[b], 0), a.max_len), see = n - (a.Q - 1 - t);
+    const int* table = a.table + (long long)b * a.table_stride;
+    const T* q = static_cast<const T*>(a.q) + row * D + lane * W;
+    for (int i = 0; i < W; ++i) sum[i] = 0.f;
+    for (int p = 0; p < splits; ++p) {
+        const float f = a.part_lse[row * splits + p];
+        if (f == -INFINITY) continue;
+        const int lo = (p - a.prefix_splits) * a.private_chunk;  // of a private part
+        if (p < a.prefix_splits || min(n, lo + a.private_chunk) <= see) {
+            const float w = exp2_approx(f - lse);
+            for (int i = 0; i < W; ++i)
+                sum[i] = fmaf(w, a.part[(row * splits + p) * D + lane * W + i], sum[i]);
+            continue;
+        }
+        for (int j = lo; j < see; ++j) {
+            const int page = table[j >> a.page_shift];
+            if (page < 0 || page >= a.pages) continue;  // V reads as zeros
+            const long long at = (((long long)page * a.Hkv + hk) * a.page_size +
+                                  (j & (a.page_size - 1))) * D + lane * W;
+            float z = 0.f;
+            for (int i = 0; i < W; ++i)
+                z = fmaf((float)q[i], (float)static_cast<const T*>(a.k)[at + i], z);
+            for (int o = 16; o > 0; o /= 2) z += __shfl_xor_sync(~0u, z, o);
+            const float w = exp2_approx(z * a.scale_log2 - lse);
+            for (int i = 0; i < W; ++i)
+                sum[i] = fmaf(w, (float)static_cast<const T*>(a.v)[at + i], sum[i]);
+        }
+    }
+}
+
 // The join of a query row's parts by WPR warps: lane l holds D / 32 columns, the warps
 // take the parts in turn and add up through shared memory.
 template <typename T, int D, int WPR>
@@ -442,6 +483,17 @@ IDX_DEVI void join_row(const AttnArgs& a, long long row, int lane, int warp, flo
         for (int k = 1; k < WPR; ++k)
 #pragma unroll
             for (int i = 0; i < W; ++i) acc[i] += sums[k * D + lane * W + i];
+    }
+    if (a.Q > 1 && row / a.Hq % a.Q < a.Q - 1) {  // not the newest token: there are later keys
+        bool odd = false;
+#pragma unroll
+        for (int i = 0; i < W; ++i) odd |= !isfinite(acc[i]);
+        if (__any_sync(~0u, odd) && isfinite(lse)) {
+            float sum[W];
+            sum_visible<T, D>(a, row, lse, lane, sum);
+#pragma unroll
+            for (int i = 0; i < W; ++i) acc[i] = sum[i];
+        }
     }
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D) + lane * (W / 2);
 #pragma unroll

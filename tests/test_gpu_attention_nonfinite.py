@@ -5,6 +5,7 @@ import math
 import pytest
 import torch
 
+import _serve_ref as ref
 from test_gpu_prefix_attention import BF16, FP16, call, idx, make  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -62,3 +63,25 @@ def test_a_prefix_key_that_is_not_finite(idx, shape, cache, value):  # noqa: F81
         assert not torch.isfinite(got[1][:, :, (Hkv - 1) * G:]).any()
     for x, y in zip(got, clean):
         assert torch.equal(x[:, :, :(Hkv - 1) * G], y[:, :, :(Hkv - 1) * G])
+
+
+@pytest.mark.parametrize("shape", [s for s in SHAPES if s[1] > 1])
+@pytest.mark.parametrize("value", [math.nan, math.inf])
+@pytest.mark.parametrize("back", [1, 2])
+def test_a_later_tokens_value_that_is_not_finite(idx, shape, value, back):  # noqa: F811
+    """V of one of the newest tokens: the tokens before it do not see it."""
+    lens, Q, G, Hkv, D, dtype, prefix = shape
+    s = make(lens, Q, G, Hkv, D, prefix, 32, dtype, seed=7, weights=D == 128)
+    for b in range(0, len(lens), 2):
+        put(s, "v", b, lens[b] - back, 0, value)
+    got = call(idx, s)
+    want = ref.attention(s["q"], s["k"], s["v"], s["table"], s["lens"], s["prefix_table"], prefix, None, s["w"])
+    blind = Q - back  # tokens before the one with the value
+    cut = lambda t: t[:, :blind]  # noqa: E731
+    assert torch.isfinite(want[0][:, :blind]).all()
+    ref.check_attention([cut(got[0]), cut(got[1])], [*map(cut, want[:4]), None], dtype, prefix + max(lens), D)
+    assert not torch.isfinite(got[0][0::2, blind:, :G]).any()
+    assert torch.isfinite(got[0][1::2]).all() and torch.isfinite(got[1]).all()
+    if s["w"] is not None:
+        for b, n in enumerate(lens):
+            assert torch.isfinite(got[2][b, :, :n]).all()
