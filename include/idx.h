@@ -381,8 +381,10 @@ idx_status idx_score_materialise_mxfp4(const uint8_t* q, const uint8_t* q_sf, co
  *   out [rows, N] e4m3 bytes, scale fp32
  * 1 <= N <= 32768 (IDX_EUNSUPPORTED above).  Pointers are aligned to their
  * element (IDX_EALIGN); rows on 16-byte boundaries (out: 8) with N % 8 == 0 take
- * the vector path, and with a group they have to.  A row with no finite norm gives no meaningful codes; other rows
- * are not affected.  No workspace.
+ * the vector path, and with a group they have to.  Scales and codes are NaN where the
+ * fp32 sum of the row's squares is not finite (a NaN or infinite h, or |h| from about
+ * 2^63 on), where mean(h^2) + eps is below 2^-126 (a row of zeros with eps 0), and where a
+ * NaN weight enters; other rows are not affected.  No workspace.
  * ------------------------------------------------------------------------ */
 idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* residual,
                                  const void* weight, int rows, int N, float eps, int group,

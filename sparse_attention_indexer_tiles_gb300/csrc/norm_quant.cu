@@ -16,6 +16,8 @@
 #include <cuda_fp16.h>
 #include <cuda_fp8.h>
 
+#include <cfloat>
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -27,6 +29,18 @@ namespace {
 
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
+
+// The larger of two, NaN when either is (fmaxf gives the other); the largest magnitude likewise.
+IDX_DEVI float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+IDX_DEVI float max_abs_nan(float a, float b, float c) {
+    float d;
+    asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+    return d;
+}
 
 // 8 consecutive columns as they lie in memory, taken as four pairs of fp32.
 template <typename T> struct alignas(16) Raw8 {  // 16-bit types
@@ -112,8 +126,11 @@ IDX_DEVI void store_codes(uint8_t* row, const float2 (&v)[4], int c, int step, i
 // residual on their way while it works on the current one.  Columns and rows past the end
 // are zeros.  The arithmetic is on pairs of fp32: at 16-bit inputs the instructions per
 // element, not HBM, bound the first version (44 per element, 62 us at 4096 x 8192).
+// (16-bit rows of 128 threads: ten blocks per SM; at nine, which the compiler's own choice of
+// registers allows, 3001 x 926 takes 5.5 us instead of 5.1.)
 template <typename T, int TPR, int VPT, int U, bool RES>
-__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormArgs a) {
+__global__ void __launch_bounds__(TPR < 128 ? 128 : TPR, TPR == 128 && sizeof(T) == 2 ? 10 : 0)
+norm_quant_kernel(NormArgs a) {
     constexpr int kThreads = TPR < 128 ? 128 : TPR;
     constexpr int kRows = kThreads / TPR;  // rows side by side in a block
     constexpr int kWarps = TPR / 32;       // warps of a row, where it has several
@@ -175,18 +192,18 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
                 if constexpr (RES) h = add2(h, cur.res[v].pair(i));
                 sum2 = fma2(h, h, sum2);
                 hw[v][i] = mul2(h, wgt[v].pair(i));
-                gmost[v] = fmaxf(gmost[v], fmaxf(fabsf(hw[v][i].x), fabsf(hw[v][i].y)));
+                gmost[v] = max_abs_nan(gmost[v], hw[v][i].x, hw[v][i].y);
                 h_out.set(i, h);
             }
             if (a.residual_out && row_live)
                 store8<U>(static_cast<T*>(a.residual_out) + row * a.N, h_out, unit_of(v), TPR, have[v]);
-            most = fmaxf(most, gmost[v]);
+            most = max_nan(most, gmost[v]);
         }
         float sum = sum2.x + sum2.y;
 #pragma unroll
         for (int o = (TPR < 32 ? TPR : 32) / 2; o > 0; o /= 2) {
             sum += __shfl_xor_sync(~0u, sum, o);
-            most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+            most = max_nan(most, __shfl_xor_sync(~0u, most, o));
         }
         if constexpr (TPR > 32) {
             __shared__ float2 part[2][kWarps];  // two: a block's barrier per row group is enough
@@ -199,29 +216,43 @@ __global__ void __launch_bounds__(TPR < 128 ? 128 : TPR) norm_quant_kernel(NormA
 #pragma unroll
             for (int o = kSpan / 2; o > 0; o /= 2) {  // the same sum in every thread
                 sum += __shfl_xor_sync(~0u, sum, o);
-                most = fmaxf(most, __shfl_xor_sync(~0u, most, o));
+                most = max_nan(most, __shfl_xor_sync(~0u, most, o));
             }
         }
-        const float rstd = rsqrtf(fmaf(sum, per_col, a.eps));
-        const float row_scale = fmaxf(rstd * most * (1.f / kE4m3Max), kScaleFloor);
+        // Where the squares leave fp32 (|h| from about 2^63 on; without eps, all |h| below 2^-63) there
+        // is no rstd: NaN, so that the row cannot pass for one.  An infinite mean times 0 is NaN.
+        const float mean = fmaf(sum, per_col, a.eps);
+        float rstd = rsqrtf(fmaf(mean, 0.f, mean));
+        if (mean < 0x1p-56f) {  // 448 / max|h weight| could be infinite below: h times 2^64
+#pragma unroll
+            for (int v = 0; v < VPT; ++v) {
+#pragma unroll
+                for (int i = 0; i < 4; ++i) hw[v][i] = mul2(hw[v][i], make_float2(0x1p64f, 0x1p64f));
+                gmost[v] *= 0x1p64f;
+            }
+            most *= 0x1p64f;
+            rstd = mean >= FLT_MIN ? rstd * 0x1p-64f : NAN;
+        }
+        const float row_scale = max_nan(rstd * most * (1.f / kE4m3Max), kScaleFloor);
         if (a.group == 0 && row_live && t == 0) a.scale[row] = row_scale;
 #pragma unroll
         for (int v = 0; v < VPT; ++v) {
             float scale = row_scale, top = most;
             if (U == 8 && a.group != 0) {
                 float m = gmost[v];
-                if (lanes > 8) m = fmaxf(m, __shfl_xor_sync(~0u, m, 8));
-                if (lanes > 4) m = fmaxf(m, __shfl_xor_sync(~0u, m, 4));
-                m = fmaxf(m, __shfl_xor_sync(~0u, m, 2));
-                m = fmaxf(m, __shfl_xor_sync(~0u, m, 1));
-                scale = fmaxf(rstd * m * (1.f / kE4m3Max), kScaleFloor);
+                if (lanes > 8) m = max_nan(m, __shfl_xor_sync(~0u, m, 8));
+                if (lanes > 4) m = max_nan(m, __shfl_xor_sync(~0u, m, 4));
+                m = max_nan(m, __shfl_xor_sync(~0u, m, 2));
+                m = max_nan(m, __shfl_xor_sync(~0u, m, 1));
+                scale = max_nan(rstd * m * (1.f / kE4m3Max), kScaleFloor);
                 top = m;
                 if (row_live && have[v] > 0 && (t & (lanes - 1)) == 0)
                     a.scale[row * (a.N / a.group) + unit_of(v) * 8 / a.group] = scale;
             }
             // y / scale = h weight (rstd / scale), and rstd cancels unless the scale is its floor:
             // 448 / max|h weight| has one rounding where rstd / scale has four
-            const float f = scale > kScaleFloor ? __fdiv_rn(kE4m3Max, top) : rstd / kScaleFloor;
+            const float f = scale > kScaleFloor ? __fdiv_rn(kE4m3Max, top)
+                                                : fmaf(top, 0.f, rstd) / kScaleFloor;  // NaN of either stays
 #pragma unroll
             for (int i = 0; i < 4; ++i) hw[v][i] = mul2(hw[v][i], make_float2(f, f));
             if (row_live) store_codes<U>(a.out + row * a.N, hw[v], unit_of(v), TPR, have[v]);
