@@ -440,8 +440,8 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
  * (request, key head), by the weights idx_prefix_attention gathers.
  *
  * Slots are ranked protected first (position < sink, or position >=
- * next_pos[b] - recent), then by weight, ties to the lower slot; the first
- * `budget` stay.  Kept slots below `budget` do not move; the i-th hole among
+ * next_pos[b] - recent), then by weight (a NaN counts as -inf), ties to the lower
+ * slot; the first `budget` stay.  Kept slots below `budget` do not move; the i-th hole among
  * them (ascending) takes the K and V rows, weight and position of the i-th kept
  * slot from `budget` on (ascending).  The heads of a request may keep different
  * tokens.  A request of at most `budget` slots keeps everything.

@@ -20,6 +20,7 @@
 // slot written, and the moved rows.
 #include <cooperative_groups.h>
 
+#include <cmath>
 #include <mutex>
 
 #include "common.cuh"
@@ -36,10 +37,10 @@ constexpr int kMaxCluster = 8;           // the portable limit
 constexpr int kSliceMax = 48 * 1024;     // keys a CTA keeps in shared memory
 constexpr uint32_t kProtected = 0xffffffffu;
 
-// Rank key of a slot: an unprotected weight stays below kProtected.
+// Rank key of a slot.  A NaN weight of either sign counts as -inf (fmaxf gives the other operand), so
+// unprotected keys end at that of infinity, below kProtected.
 IDX_DEVI uint32_t slot_key(float w, int pos, int sink, int recent_from) {
-    const uint32_t k = fkey(w);
-    return (pos < sink || pos >= recent_from) ? kProtected : (k == kProtected ? k - 1u : k);
+    return (pos < sink || pos >= recent_from) ? kProtected : fkey(fmaxf(w, -INFINITY));
 }
 
 // Row of slot j in the caches; 0xffffffff when its page is not one.
