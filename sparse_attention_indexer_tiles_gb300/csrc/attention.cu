@@ -445,7 +445,7 @@ __device__ __noinline__ void sum_visible(const AttnArgs& a, long long row, float
 
 // The join of a query row's parts by WPR warps: lane l holds D / 32 columns, the warps
 // take the parts in turn and add up through shared memory.
-template <typename T, int D, int WPR>
+template <typename T, int D, int WPR, bool SEVERAL>
 IDX_DEVI void join_row(const AttnArgs& a, long long row, int lane, int warp, float* sums) {
     constexpr int W = D / 32, kBatch = WPR == 1 ? 8 : 4;
     const int splits = a.prefix_splits + a.private_splits;
@@ -484,7 +484,7 @@ IDX_DEVI void join_row(const AttnArgs& a, long long row, int lane, int warp, flo
 #pragma unroll
             for (int i = 0; i < W; ++i) acc[i] += sums[k * D + lane * W + i];
     }
-    if (a.Q > 1 && row / a.Hq % a.Q < a.Q - 1) {  // not the newest token: there are later keys
+    if (SEVERAL && row / a.Hq % a.Q < a.Q - 1) {  // not the newest token: there are later keys
         bool odd = false;
 #pragma unroll
         for (int i = 0; i < W; ++i) odd |= !isfinite(acc[i]);
@@ -544,8 +544,9 @@ IDX_DEVI void add_weights(const AttnArgs& a, int u, float* row_lse) {
 }
 
 // Blocks [0, join_blocks) join the parts of query rows (WPR warps each), the others add up
-// the weights of the private slots.
-template <typename T, int D, int WPR>
+// the weights of the private slots.  SEVERAL: calls of several tokens; with the call of sum_visible in
+// it the kernel is slower (16 requests of one token 18.1 and 19.0 us), so the others go without.
+template <typename T, int D, int WPR, bool SEVERAL>
 __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int join_blocks) {
     __shared__ float scratch[kAttnMaxTokens * kAttnMaxGroup];
     pdl_wait();  // (no pdl_trigger: the next call's prefix grid came in its way, 74 -> 81 us)
@@ -553,7 +554,7 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
         const int warp = threadIdx.x >> 5;
         const long long row = (long long)blockIdx.x * (kJoinWarps / WPR) + warp / WPR;
         if (row < (long long)a.B * a.Q * a.Hq)
-            join_row<T, D, WPR>(a, row, threadIdx.x & 31, warp % WPR, scratch);
+            join_row<T, D, WPR, SEVERAL>(a, row, threadIdx.x & 31, warp % WPR, scratch);
     } else {
         add_weights(a, blockIdx.x - join_blocks, scratch);
     }
@@ -597,7 +598,10 @@ cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStre
     const long long weight_blocks =
         a.w_out ? (long long)a.B * a.Hkv * ((a.max_len + kWeightSlots - 1) / kWeightSlots) : 0;
     if (join_blocks + weight_blocks > 0x7fffffffll) return cudaErrorInvalidValue;
-    const auto kern = wide ? attn_join_kernel<T, D, kJoinWarps> : attn_join_kernel<T, D, 1>;
+    const auto kern = a.Q > 1 ? (wide ? attn_join_kernel<T, D, kJoinWarps, true>
+                                      : attn_join_kernel<T, D, 1, true>)
+                              : (wide ? attn_join_kernel<T, D, kJoinWarps, false>
+                                      : attn_join_kernel<T, D, 1, false>);
     e = launch_k(kern, dim3((unsigned)(join_blocks + weight_blocks)), dim3(kJoinThreads), 0, s,
                  true, a, (int)join_blocks);
     if (e == cudaSuccess) ++*launched;
