@@ -417,7 +417,8 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
  *   out [B, Q, Hq, D] of q's type;  lse [B, Q, Hq] fp32 or NULL
  *   ws  idx_prefix_attention_workspace(...) bytes for the same max_len (the
  *       table's width where the call says 0), 256-byte aligned; needs no
- *       clearing between calls
+ *       clearing between calls.  The size does not shrink when B, Q, Hq, D,
+ *       prefix_len, max_len or weights grows: one for the largest serves all.
  * Supported: D 64 or 128; page_size 16, 32, 64 or 128; 1 <= Q <= 16; Hq a
  * multiple of Hkv with Hq / Hkv <= 128; B * Hkv <= 65535; prefix_len, max_len < 2^30; pages >= 1
  * with keys.  The workspace query gives 0 for sizes that the call refuses.  Device errors
@@ -455,7 +456,8 @@ idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* 
  *   lens_out [B] int32 = min(lens[b], budget); not lens itself
  *   max_len  an upper bound on lens (0 = table_stride * page_size)
  *   ws  idx_cache_evict_workspace(...) bytes for the same max_len (the table's
- *       width where the call says 0), 256-byte aligned
+ *       width where the call says 0), 256-byte aligned; the size grows with B, Hkv
+ *       and max_len, but not with budget
  * No two requests may share a private page.  budget >= 1, recent, sink >= 0 and
  * recent + sink <= budget (IDX_EINVAL); D 64 or 128; page_size 16, 32, 64 or 128;
  * B * Hkv < 2^28 and pages * Hkv * page_size < 2^32 - 16 (IDX_EUNSUPPORTED).

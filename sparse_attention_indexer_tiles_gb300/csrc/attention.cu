@@ -14,6 +14,7 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <algorithm>
 #include <cmath>
 #include <mutex>
 
@@ -610,6 +611,16 @@ cudaError_t launch_typed(const AttnArgs& a, idx_dtype dt, int sm_count, cudaStre
 
 }  // namespace
 
+// Row parts (a row's results of one part: D + 1 floats of workspace) that the plan may take of the
+// prefix or of the private keys, when up to `splits` parts would be possible: all of them, but no more
+// than kRowParts unless every row has one.  The plan chooses within this and the workspace is sized by
+// it, so that the size grows with the rows and the lengths, as the choice itself does not.  65536 (34
+// MB at D = 128) leaves all but one in a thousand of the plans of 1-64 requests as they would be.
+constexpr size_t kRowParts = 65536;
+static size_t most_row_parts(size_t rows, size_t splits) {
+    return splits == 0 ? 0 : std::max(rows, std::min(rows * splits, kRowParts));
+}
+
 AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max_len, bool weights,
                    int sm_count) {
     AttnPlan p;
@@ -617,6 +628,8 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
     p.prefix_splits = p.prefix_chunk = p.private_splits = p.private_chunk = 0;
     // the join reads D floats per row and part, about 5 MB per us
     const double join_us = (double)B * Q * Hq * D * 8 / 5e6;
+    const size_t rows = (size_t)B * Q * Hq;
+    size_t row_parts = 0;
 
     // Keys per private part: a block takes about 4 us and, among the three that an SM holds,
     // 34 ns per key (D = 128: 512 bytes at a third of the SM's share of HBM), so whole waves of
@@ -632,10 +645,15 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
     double private_us = 0;
     p.private_dense = false;
     if (max_len > 0) {
+        constexpr int kMostSplits = 32;
+        const int steps = (max_len + 63) / 64;  // 64: four warps' 16
+        const size_t most = most_row_parts(rows, std::min(kMostSplits, steps));
+        row_parts += most;
         double best = 0;
         auto consider = [&](bool dense, double items, int unit, int units, int s, double per_unit,
                             double base) {  // s parts of `units` units of keys
             const int t = (units + s - 1) / s, all = (units + t - 1) / t, half = (units / 2 + t) / t;
+            if (all * rows > most) return;
             const double us =
                 (std::ceil(items * all) + std::ceil(items * half)) / 2 * (t * per_unit + base);
             if (best == 0 || us + s * join_us < best) {
@@ -645,14 +663,14 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
                 p.private_dense = dense;
             }
         };
-        const int row_blocks = (Q * G + 15) / 16, steps = (max_len + 63) / 64;  // 64: four warps' 16
-        for (int s = 1; s <= 32 && s <= steps; s += s < 8 ? 1 : s / 4)
+        const int row_blocks = (Q * G + 15) / 16;
+        for (int s = 1; s <= kMostSplits && s <= steps; s += s < 8 ? 1 : s / 4)
             consider(false, (double)row_blocks * Hkv * B / (3 * sm_count), 64, steps, s,
                      64 * (D * 34e-3 / 128), 4.0);
         if (row_blocks > 1 && !(weights && D == 64)) {
             const int keys = attn_prefix_keys(D), tiles = (max_len + keys - 1) / keys;
             const int row_tiles = (Q + 128 / G - 1) / (128 / G);
-            for (int s = 1; s <= 32 && s <= tiles; s += s < 8 ? 1 : s / 4)
+            for (int s = 1; s <= kMostSplits && s <= tiles; s += s < 8 ? 1 : s / 4)
                 consider(true, (double)B * Hkv * ((row_tiles + 1) / 2) / sm_count, keys, tiles, s,
                          keys * D * 4 / 45e3, 8.0);
         }
@@ -674,12 +692,15 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
         const long long row_tiles = ((long long)B * Q + tokens - 1) / tokens;
         const long long items = (row_tiles + 1) / 2 * Hkv;
         const double per_tile = (row_tiles > 1 ? 1.4 : 0.75) * keys / 128;
+        const int most_splits = std::min(tiles, 4 * sm_count);  // (a grid dimension, too)
+        const size_t most = most_row_parts(rows, most_splits);
+        row_parts += most;
         double best = 0;
         const double per_sm = 1.0 / sm_count;
         auto consider = [&](int t) {  // t tiles per part
             t = t < 1 ? 1 : t > tiles ? tiles : t;
             const int s = (tiles + t - 1) / t;
-            if (s > 65535) return;  // a grid dimension
+            if (s > most_splits || s * rows > most) return;
             const double one = t * per_tile + 4.0, waves = (double)items * s * per_sm;
             const double dense = std::ceil(waves) * one, mean = waves * one + private_us * kShare;
             const double us = (dense > mean ? dense : mean) + s * join_us;
@@ -694,14 +715,14 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
             const int n = (int)(eighths * sm_count / (8 * items));
             consider(n > 1 ? (tiles + n - 1) / n : tiles);
         }
+        if (best == 0) consider(tiles);
         p.prefix_splits = (prefix_len + p.prefix_chunk - 1) / p.prefix_chunk;
     }
-    const size_t rows = (size_t)B * Q * Hq, splits = p.prefix_splits + p.private_splits;
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     p.logit_stride = ((long long)max_len + 15) / 16 * 16;
     p.part = 0;
-    p.part_lse = up(rows * splits * D * sizeof(float));
-    p.logits = p.part_lse + up(rows * splits * sizeof(float));
+    p.part_lse = up(row_parts * D * sizeof(float));
+    p.logits = p.part_lse + up(row_parts * sizeof(float));
     p.total = p.logits + (weights ? up(rows * p.logit_stride * sizeof(float)) : 0);
     return p;
 }
