@@ -1,5 +1,5 @@
-"""idx_add_rmsnorm_quant on one row of a wider tensor: its pitch leads to no other row, so it does not
-matter to the row's alignment."""
+"""idx_add_rmsnorm_quant on slices of wider tensors: one row, whose pitch leads to no other row and does
+not matter to its alignment, and fp32 rows, which are on 16-byte boundaries at a pitch of four columns."""
 import pytest
 import torch
 
@@ -25,3 +25,14 @@ def test_a_row_of_an_odd_pitch(idx, dtype, cols, wide, group, rows):  # noqa: F8
     out, scale = idx.idx_add_rmsnorm_quant(d, w.to(DEV), group=group)
     torch.cuda.synchronize()
     ref.check_norm(out.cpu(), scale.cpu(), x[:, :cols], w, group=group)
+
+
+@pytest.mark.parametrize("cols,wide,start", [(128, 132, 0), (128, 300, 4), (256, 268, 12), (4096, 4100, 4)])
+@pytest.mark.parametrize("group", [0, 64])
+def test_fp32_rows_on_16_byte_boundaries(idx, cols, wide, start, group):  # noqa: F811
+    """Four fp32 columns are 16 bytes: a pitch or a start of an odd multiple of four is enough."""
+    x, _, _ = inputs(9, wide, FP32, False, seed=wide)
+    _, w, _ = inputs(1, cols, FP32, False, seed=cols)
+    out, scale = idx.idx_add_rmsnorm_quant(x.to(DEV)[:, start:start + cols], w.to(DEV), group=group)
+    torch.cuda.synchronize()
+    ref.check_norm(out.cpu(), scale.cpu(), x[:, start:start + cols], w, group=group)
