@@ -19,7 +19,7 @@
 #include <mutex>
 
 #include "attention.cuh"
-#include "common.cuh"
+#include "serve.cuh"
 
 namespace idx {
 

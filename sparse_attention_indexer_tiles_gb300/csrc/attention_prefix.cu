@@ -34,7 +34,7 @@
 #include <mutex>
 
 #include "attention.cuh"
-#include "common.cuh"
+#include "serve.cuh"
 
 namespace idx {
 

@@ -37,37 +37,6 @@ IDX_DEVI float key_floor_float(uint32_t L) {
     return __uint_as_float((L & 0x80000000u) ? (L & 0x7fffffffu) : ~L);
 }
 
-// ------------------------------------------------------------ packed fp32
-
-// Two fp32 operations at once.
-IDX_DEVI float2 fma2(float2 a, float2 b, float2 c) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
-        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
-    return d;
-}
-IDX_DEVI float2 add2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, w;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-IDX_DEVI float2 mul2(float2 a, float2 b) {
-    float2 d;
-    asm("{\n\t.reg .b64 x, y, w;\n\t"
-        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
-        "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
-        : "=f"(d.x), "=f"(d.y)
-        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
-    return d;
-}
-
 // --------------------------------------------------------------- smem/ptx
 
 IDX_DEVI uint32_t smem_u32(const void* p) {
@@ -91,12 +60,9 @@ IDX_DEVI void mbar_init(uint64_t* bar, uint32_t count) {
 // launch_k) is launched as the kernel before it on the stream finishes, its
 // CTAs taking SMs as that kernel's CTAs leave them: pdl_wait blocks until that
 // kernel has completed and its memory is visible (at once for a launch without
-// the attribute).  (No scoring kernel signals its dependents early: measured on
+// the attribute).  (No kernel here signals its dependents early: measured on
 // GB300, letting the next grid launch from the start of this one slowed the
 // long scoring passes it overlapped.)
-// pdl_trigger lets the next such launch begin once every CTA of this grid has
-// called it or ended.
-IDX_DEVI void pdl_trigger() { asm volatile("griddepcontrol.launch_dependents;" ::: "memory"); }
 IDX_DEVI void pdl_wait() { asm volatile("griddepcontrol.wait;" ::: "memory"); }
 
 IDX_DEVI void fence_barrier_init() {

@@ -20,8 +20,8 @@
 #include <cmath>
 #include <mutex>
 
-#include "common.cuh"
 #include "norm_quant.cuh"
+#include "serve.cuh"
 
 namespace idx {
 
