@@ -1038,8 +1038,8 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
     auto fits = [&](int unit) {
         const size_t b = std::min<size_t>(unit * es, 16);
         return N % unit == 0 && (rows == 1 || x_stride % (long long)(b / es) == 0) &&
-               aligned(x, b) && aligned(weight, b) && aligned(out, unit) && (!residual || aligned(residual, b)) &&
-               (!residual_out || aligned(residual_out, b));
+               aligned(x, b) && aligned(weight, b) && aligned(out, unit) &&
+               (!residual || aligned(residual, b)) && (!residual_out || aligned(residual_out, b));
     };
     a.unit = fits(8) ? 8 : fits(2) ? 2 : 1;
     if (group != 0 && a.unit != 8) return IDX_EALIGN;

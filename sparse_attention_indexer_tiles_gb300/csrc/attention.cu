@@ -29,12 +29,6 @@ constexpr int kPartWarps = 4;
 constexpr int kStep = 16;    // keys a warp takes at a time; pages hold at least as many
 constexpr int kRing = 3;     // copies of 16 rows, of K and of V in turn, per warp
 
-IDX_DEVI float exp2_approx(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // 16-byte asynchronous copy; bytes = 0 writes zeros and reads nothing
 IDX_DEVI void cp_async16_zfill(uint32_t dst, const void* src, uint32_t bytes, uint64_t policy) {
     asm volatile("cp.async.cg.shared.global.L2::cache_hint [%0], [%1], 16, %2, %3;" ::"r"(dst),
@@ -84,10 +78,6 @@ template <> struct Mma<__nv_bfloat16> {
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
     }
-    static IDX_DEVI uint32_t pack(float lo, float hi) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
 };
 template <> struct Mma<__half> {
     static IDX_DEVI void run(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
@@ -96,10 +86,6 @@ template <> struct Mma<__half> {
             "{%8, %9}, {%0, %1, %2, %3};"
             : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
             : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-    }
-    static IDX_DEVI uint32_t pack(float lo, float hi) {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
     }
 };
 
@@ -305,8 +291,8 @@ __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_ke
             l[t][0] += s[t][0] + s[t][2];
             l[t][1] += s[t][1] + s[t][3];
             // as the second operand of the second product: pairs of keys of a row
-            p[t][0] = transpose8(Mma<T>::pack(s[t][0], s[t][1]));
-            p[t][1] = transpose8(Mma<T>::pack(s[t][2], s[t][3]));
+            p[t][0] = transpose8(pack2<T>(s[t][0], s[t][1]));
+            p[t][1] = transpose8(pack2<T>(s[t][2], s[t][3]));
         }
         cp_async_wait<2>();
         __syncwarp();
@@ -376,13 +362,6 @@ __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_ke
         if (d == 0) a.part_lse[at] = sum == 0.f ? -INFINITY : top + log2f(sum);
     }
     if (last) pdl_wait();
-}
-
-// The larger of two, NaN when either is (fmaxf gives the other).
-IDX_DEVI float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
 }
 
 // log2-sum-exp2 of a row's parts: every lane of the warp gets it; NaN when a part's is, so that
@@ -498,7 +477,7 @@ IDX_DEVI void join_row(const AttnArgs& a, long long row, int lane, int warp, flo
     }
     uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D) + lane * (W / 2);
 #pragma unroll
-    for (int i = 0; i < W / 2; ++i) out[i] = Mma<T>::pack(acc[2 * i], acc[2 * i + 1]);
+    for (int i = 0; i < W / 2; ++i) out[i] = pack2<T>(acc[2 * i], acc[2 * i + 1]);
     if (a.lse && lane == 0) a.lse[row] = lse * 0.6931471805599453f;
 }
 

@@ -86,12 +86,6 @@ IDX_DEVI float max3(float a, float b, float c) {
     return d;
 }
 
-IDX_DEVI float ex2(float x) {
-    float y;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
-    return y;
-}
-
 // One lane of a converged warp.
 IDX_DEVI bool elect_one() {
     uint32_t p;
@@ -180,17 +174,9 @@ IDX_DEVI uint64_t kv_desc(uint32_t saddr, uint32_t group) {
 template <typename T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
     static constexpr uint32_t FMT = 1;
-    static IDX_DEVI uint32_t pack(float lo, float hi) {
-        const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
 };
 template <> struct Elem<__half> {
     static constexpr uint32_t FMT = 0;
-    static IDX_DEVI uint32_t pack(float lo, float hi) {
-        const __half2 v = __floats2half2_rn(lo, hi);
-        return *reinterpret_cast<const uint32_t*>(&v);
-    }
 };
 
 template <typename T, int D, bool PRIVATE>
@@ -477,7 +463,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 m = top == -INFINITY ? 0.f : top;
             } else if (__any_sync(~0u, live && top > m + kRenew)) {
                 const float next = live ? fmaxf(m, top) : m;
-                const float f = ex2(m - next);
+                const float f = exp2_approx(m - next);
                 m = next;
                 l *= f;
                 if (!(ok = last_done())) break;
@@ -513,10 +499,10 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
 #pragma unroll
             for (int c = 0; c < C::KEYS / 2; ++c) {
                 float2 e = fma2(make_float2(z[2 * c], z[2 * c + 1]), scale2, less_m);
-                e.x = ex2(e.x);
-                e.y = ex2(e.y);
+                e.x = exp2_approx(e.x);
+                e.y = exp2_approx(e.y);
                 sum[c & 1] = add2(sum[c & 1], e);
-                p[c] = Elem<T>::pack(e.x, e.y);
+                p[c] = pack2<T>(e.x, e.y);
             }
             const float2 both = add2(sum[0], sum[1]);
             l += both.x + both.y;
@@ -564,8 +550,8 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
                 named_bar_sync(1, 256);
                 top = fmaxf(m, ml[row]);
                 const float base = top == -INFINITY ? 0.f : top;
-                f0 = ex2(m - base);
-                f1 = ex2(ml[row] - base);
+                f0 = exp2_approx(m - base);
+                f1 = exp2_approx(ml[row] - base);
                 l = l * f0 + ml[128 + row] * f1;
             }
             const float inv = l == 0.f ? 0.f : 1.f / l;  // NaN stays one

@@ -30,12 +30,7 @@ namespace {
 constexpr float kE4m3Max = 448.f;
 constexpr float kScaleFloor = 7.888609052210118e-31f;  // 2^-100
 
-// The larger of two, NaN when either is (fmaxf gives the other); the largest magnitude likewise.
-IDX_DEVI float max_nan(float a, float b) {
-    float d;
-    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
-    return d;
-}
+// The largest magnitude, NaN when one is.
 IDX_DEVI float max_abs_nan(float a, float b, float c) {
     float d;
     asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
@@ -53,15 +48,13 @@ template <> IDX_DEVI float2 Raw8<__nv_bfloat16>::pair(int i) const {
     return make_float2(__uint_as_float(u[i] << 16), __uint_as_float(u[i] & 0xffff0000u));
 }
 template <> IDX_DEVI void Raw8<__nv_bfloat16>::set(int i, float2 v) {
-    const __nv_bfloat162 p = __floats2bfloat162_rn(v.x, v.y);
-    u[i] = *reinterpret_cast<const uint32_t*>(&p);
+    u[i] = pack2<__nv_bfloat16>(v.x, v.y);
 }
 template <> IDX_DEVI float2 Raw8<__half>::pair(int i) const {
     return __half22float2(*reinterpret_cast<const __half2*>(&u[i]));
 }
 template <> IDX_DEVI void Raw8<__half>::set(int i, float2 v) {
-    const __half2 p = __floats2half2_rn(v.x, v.y);
-    u[i] = *reinterpret_cast<const uint32_t*>(&p);
+    u[i] = pack2<__half>(v.x, v.y);
 }
 template <> struct alignas(16) Raw8<float> {
     float f[8];

@@ -2,6 +2,8 @@
 // common.cuh.
 #pragma once
 
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "common.cuh"
@@ -37,6 +39,31 @@ IDX_DEVI float2 mul2(float2 a, float2 b) {
         : "=f"(d.x), "=f"(d.y)
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return d;
+}
+
+// ------------------------------------------------------------------ scalars
+
+// 2^x to about 2 units in the last place; results below 2^-126 are 0.
+IDX_DEVI float exp2_approx(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+// The larger of two, NaN when either is (fmaxf gives the other).
+IDX_DEVI float max_nan(float a, float b) {
+    float d;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(d) : "f"(a), "f"(b));
+    return d;
+}
+// Two values in a 16-bit type, rounded to nearest.
+template <typename T> IDX_DEVI uint32_t pack2(float lo, float hi);
+template <> IDX_DEVI uint32_t pack2<__nv_bfloat16>(float lo, float hi) {
+    const __nv_bfloat162 v = __floats2bfloat162_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+template <> IDX_DEVI uint32_t pack2<__half>(float lo, float hi) {
+    const __half2 v = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&v);
 }
 
 // ---------------------------------------------- programmatic dependent launch
