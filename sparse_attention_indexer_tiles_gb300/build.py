@@ -34,7 +34,8 @@ def sources():
 
 
 def _deps():
-    return sources() + [BINDING] + glob.glob(os.path.join(CSRC, "*.cuh")) + glob.glob(os.path.join(INCLUDE, "*.h"))
+    headers = [os.path.join(CSRC, "*.cuh"), os.path.join(CSRC, "*.h"), os.path.join(INCLUDE, "*.h")]
+    return sources() + [BINDING] + [f for h in headers for f in glob.glob(h)]
 
 
 def up_to_date() -> bool:

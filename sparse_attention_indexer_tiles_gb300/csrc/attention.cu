@@ -16,7 +16,6 @@
 
 #include <algorithm>
 #include <cmath>
-#include <mutex>
 
 #include "attention.cuh"
 #include "serve.cuh"
@@ -542,13 +541,9 @@ __global__ void __launch_bounds__(kJoinThreads) attn_join_kernel(AttnArgs a, int
 
 template <typename T, int D, int NT>
 cudaError_t launch_private(const AttnArgs& a, cudaStream_t s) {
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(attn_part_kernel<T, D, NT>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, part_smem<D>());
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static PerDevice ready;
+    const cudaError_t e = allow_smem(ready, attn_part_kernel<T, D, NT>, part_smem<D>());
+    if (e != cudaSuccess) return e;
     const dim3 grid((a.Q * a.G + 8 * NT - 1) / (8 * NT) * a.Hkv * a.private_splits, a.B);
     return launch_k(attn_part_kernel<T, D, NT>, grid, dim3(kPartWarps * 32), part_smem<D>(), s,
                     true, a);

@@ -31,8 +31,6 @@
 
 #include <cudaTypedefs.h>
 
-#include <mutex>
-
 #include "attention.cuh"
 #include "serve.cuh"
 
@@ -645,13 +643,9 @@ cudaError_t launch_t(const AttnArgs& args, cudaStream_t s) {
         make_map<5>(&tk, a.k, kd, ks, kb) != CUDA_SUCCESS ||
         make_map<5>(&tv, a.v, kd, ks, kb) != CUDA_SUCCESS)
         return cudaErrorInvalidValue;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [] {
-        attr_err = cudaFuncSetAttribute(attn_prefix_kernel<T, D, PRIVATE>,
-                                        cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static PerDevice ready;
+    const cudaError_t e = allow_smem(ready, attn_prefix_kernel<T, D, PRIVATE>, C::SMEM);
+    if (e != cudaSuccess) return e;
     const int ntiles = ((PRIVATE ? a.Q : a.B * a.Q) + tokens - 1) / tokens;
     return launch_k(attn_prefix_kernel<T, D, PRIVATE>,
                     dim3((ntiles + 1) / 2, PRIVATE ? a.private_splits : a.prefix_splits,

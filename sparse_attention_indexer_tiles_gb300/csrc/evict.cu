@@ -21,10 +21,9 @@
 #include <cooperative_groups.h>
 
 #include <cmath>
-#include <mutex>
 
-#include "common.cuh"
 #include "evict.cuh"
+#include "serve.cuh"
 
 namespace cg = cooperative_groups;
 
@@ -417,13 +416,9 @@ __global__ void __launch_bounds__(kMoveThreads) evict_move_kernel(EvictArgs a) {
 template <bool CLUSTER, bool STAGED, int kThreads>
 cudaError_t launch_select(const EvictArgs& a, int C, size_t smem, cudaStream_t s) {
     const auto kern = evict_select_kernel<CLUSTER, STAGED, kThreads>;
-    static std::once_flag once;
-    static cudaError_t attr_err = cudaSuccess;
-    std::call_once(once, [&] {
-        attr_err = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                        kSliceMax * sizeof(uint32_t));
-    });
-    if (attr_err != cudaSuccess) return attr_err;
+    static PerDevice ready;
+    const cudaError_t e = allow_smem(ready, kern, kSliceMax * sizeof(uint32_t));
+    if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(a.B * a.Hkv * C));
     cfg.blockDim = dim3(kThreads);

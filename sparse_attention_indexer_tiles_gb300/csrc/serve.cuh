@@ -1,4 +1,4 @@
-// Device helpers of the serving operators' kernels (attention*.cu, norm_quant.cu), beside
+// Device helpers of the serving operators' kernels (attention*.cu, evict.cu, norm_quant.cu), beside
 // common.cuh.
 #pragma once
 
@@ -7,8 +7,21 @@
 #include <cuda_runtime.h>
 
 #include "common.cuh"
+#include "per_device.h"
 
 namespace idx {
+
+// ---------------------------------------------------------------- launches
+
+// Lets `kern` have `bytes` of dynamic shared memory on the current device.
+template <typename K> cudaError_t allow_smem(PerDevice& done, K kern, size_t bytes) {
+    int device = -1;
+    const cudaError_t e = cudaGetDevice(&device);
+    if (e != cudaSuccess) return e;
+    return (cudaError_t)done.run(device, [&] {
+        return (int)cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)bytes);
+    });
+}
 
 // ------------------------------------------------------------ packed fp32
 
