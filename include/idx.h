@@ -109,9 +109,10 @@ typedef struct idx_options {
                              microseconds (instead of about 2 s).  A pass with more
                              than one tile then stops early with IDX_DEV_TIMEOUT in
                              *d_status, leaving no copy or MMA in flight; the call
-                             returns and its results are meaningless.  The prefix
-                             kernel of idx_prefix_attention does the same with its
-                             key tile 1.  It exists to run the timeout unwind on
+                             returns and its results are meaningless.  The parts of
+                             idx_prefix_attention on the tensor cores' dense path (the
+                             prefix's, and private ones that take it) do the same with
+                             their key tile 1.  It exists to run the timeout unwind on
                              purpose. */
     void* const* stage_events; /* optional array of cudaEvent_t, recorded on `stream`
                              at stage boundaries (NULL entries are skipped).
@@ -428,6 +429,11 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
  * ------------------------------------------------------------------------ */
 size_t idx_prefix_attention_workspace(int B, int Q, int Hq, int Hkv, int D, int prefix_len,
                                       int max_len, int weights);
+/* The parts that such a call is cut into on the current device: plan[0] parts of the prefix of plan[1]
+ * keys each, plan[2] private parts of plan[3] keys, plan[4] 1 when the private parts take the tensor
+ * cores' dense path.  Nothing is launched. */
+idx_status idx_prefix_attention_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max_len,
+                                     int weights, int* plan);
 idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* v_cache,
                                 const int* prefix_table, const int* table, const int* lens,
                                 const float* w, int B, int Q, int Hq, int Hkv, int D, int pages,

@@ -34,8 +34,8 @@ __all__ = [
     "idx_score_topk_noalloc", "idx_page_table_transform", "idx_route_fused",
     "idx_score_topk_routed", "idx_score_topk_routed_workspace", "idx_mxfp4_to_e4m3",
     "idx_score_topk_mxfp4", "idx_score_materialise_mxfp4", "idx_add_rmsnorm_quant",
-    "idx_prefix_attention", "idx_prefix_attention_workspace", "idx_cache_evict",
-    "idx_cache_evict_workspace",
+    "idx_prefix_attention", "idx_prefix_attention_workspace", "idx_prefix_attention_plan",
+    "idx_cache_evict", "idx_cache_evict_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -142,6 +142,8 @@ def load(path: str | None = None):
     lib.idx_add_rmsnorm_quant.restype = I
     lib.idx_prefix_attention_workspace.argtypes = [I] * 8
     lib.idx_prefix_attention_workspace.restype = SZ
+    lib.idx_prefix_attention_plan.argtypes = [I] * 8 + [P]
+    lib.idx_prefix_attention_plan.restype = I
     lib.idx_prefix_attention.argtypes = [P] * 7 + [I] * 8 + [LL, I, LL, F, I, P, P, P, P, SZ, P, P]
     lib.idx_prefix_attention.restype = I
     lib.idx_cache_evict_workspace.argtypes = [I] * 4
@@ -599,6 +601,17 @@ def idx_prefix_attention_workspace(B: int, Q: int, Hq: int, Hkv: int, D: int, pr
                                    max_len: int, weights: bool) -> int:
     return int(load().idx_prefix_attention_workspace(B, Q, Hq, Hkv, D, prefix_len, max_len,
                                                      int(bool(weights))))
+
+
+def idx_prefix_attention_plan(B: int, Q: int, Hq: int, Hkv: int, D: int, prefix_len: int,
+                              max_len: int, weights: bool) -> dict:
+    """The parts that such a call is cut into: prefix_parts of prefix_keys keys each, private_parts
+    of private_keys, and whether the private ones take the tensor cores' dense path."""
+    plan = (ctypes.c_int * 5)()
+    _check("idx_prefix_attention_plan", load().idx_prefix_attention_plan(
+        B, Q, Hq, Hkv, D, prefix_len, max_len, int(bool(weights)), plan))
+    return dict(prefix_parts=plan[0], prefix_keys=plan[1], private_parts=plan[2],
+                private_keys=plan[3], private_dense=bool(plan[4]))
 
 
 def idx_prefix_attention(q, k_cache, v_cache, table, lens, *, prefix_table=None,

@@ -1004,6 +1004,12 @@ bool attn_supported(int B, int Q, int Hq, int Hkv, int D, int prefix_len) {
            prefix_len <= 0x3fffffff;
 }
 
+// The same for arguments that nothing has been asked of yet.
+bool attn_sizes_ok(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max_len) {
+    return Q >= 1 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && prefix_len >= 0 && max_len >= 0 &&
+           max_len <= kMaxPrivate && attn_supported(B, Q, Hq, Hkv, D, prefix_len);
+}
+
 }  // namespace
 
 idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* residual,
@@ -1054,10 +1060,22 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
 
 size_t idx_prefix_attention_workspace(int B, int Q, int Hq, int Hkv, int D, int prefix_len,
                                       int max_len, int weights) {
-    if (B <= 0 || Q < 1 || Hkv < 1 || Hq < Hkv || Hq % Hkv != 0 || prefix_len < 0 || max_len < 0 ||
-        !attn_supported(B, Q, Hq, Hkv, D, prefix_len) || max_len > kMaxPrivate)
-        return 0;
+    if (B <= 0 || !attn_sizes_ok(B, Q, Hq, Hkv, D, prefix_len, max_len)) return 0;
     return attn_plan(B, Q, Hq, Hkv, D, prefix_len, max_len, weights != 0, sm_count()).total;
+}
+
+idx_status idx_prefix_attention_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len,
+                                     int max_len, int weights, int* plan) {
+    if (B <= 0 || !plan) return IDX_EINVAL;
+    if (!attn_sizes_ok(B, Q, Hq, Hkv, D, prefix_len, max_len)) return IDX_EUNSUPPORTED;
+    const AttnPlan p =
+        attn_plan(B, Q, Hq, Hkv, D, prefix_len, max_len, weights != 0, sm_count());
+    plan[0] = p.prefix_splits;
+    plan[1] = p.prefix_chunk;
+    plan[2] = p.private_splits;
+    plan[3] = p.private_chunk;
+    plan[4] = p.private_dense;
+    return IDX_OK;
 }
 
 idx_status idx_prefix_attention(const void* q, const void* k_cache, const void* v_cache,

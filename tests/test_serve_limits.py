@@ -54,3 +54,18 @@ def test_the_call_refuses_what_the_query_refuses():
             P, P, P, P, P, P, P if weights else None, B, Q, Hq, Hkv, D, 10, 64, prefix, 1 << 25, most, INT_MAX, 0.1, 1,
             P, None, P if weights else None, P, 1 << 60, None, None)
         assert code in (1, 4), (B, Q, Hq, Hkv, D, prefix, most)
+
+
+def test_the_plan():
+    import ctypes
+    from sparse_attention_indexer_tiles_gb300 import IdxError, idx_prefix_attention_plan, load
+    p = idx_prefix_attention_plan(8, 1, 64, 8, 128, 32768, 1024, True)
+    assert p["prefix_parts"] * p["prefix_keys"] >= 32768 and p["private_parts"] * p["private_keys"] >= 1024
+    assert (p["prefix_parts"] - 1) * p["prefix_keys"] < 32768 and not p["private_dense"]
+    assert idx_prefix_attention_plan(8, 16, 16, 1, 64, 0, 4000, False)["private_dense"]
+    for sizes in REFUSED:
+        with pytest.raises(IdxError) as e:
+            idx_prefix_attention_plan(*sizes)
+        assert e.value.code == 4
+    assert load().idx_prefix_attention_plan(1, 1, 8, 2, 128, 0, 64, 0, None) == 1
+    assert load().idx_prefix_attention_plan(0, 1, 8, 2, 128, 0, 64, 0, (ctypes.c_int * 5)()) == 1
