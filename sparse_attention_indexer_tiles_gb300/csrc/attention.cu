@@ -10,12 +10,14 @@
 //     o = sum_p 2^(l_p - L) o_p,   L = log2 sum_p 2^(l_p).
 // All exponentials are base 2 on z * log2(e); sums, maxima and o are fp32, and the
 // weights enter the second product in the tensors' own type (a relative rounding of
-// half a step per weight, as V itself carries).
+// half a step per weight, as V itself carries; in fp16 they are taken times a power of
+// two, since its numbers below 2^-14 have fewer bits).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 #include "attention.cuh"
 #include "serve.cuh"
@@ -111,6 +113,8 @@ __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_ke
     const bool last = blockIdx.x == 0 && blockIdx.y == 0;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     constexpr int kRows = 8 * NT;
+    // fp16 weights are taken times 2^15, so that they have all their bits down to 2^-29 of the largest
+    constexpr float kLift = std::is_same<T, __half>::value ? 15.f : 0.f;
     const int rows = a.Q * a.G;
     // row blocks next to each other: they read the same keys, from L2 but for the first
     const int row_blocks = (rows + kRows - 1) / kRows;
@@ -281,8 +285,8 @@ __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_ke
                 }
             }
             // rows that have seen no key yet keep m = -inf: their weights are 0
-            const float b0 = m[t][0] == -INFINITY ? 0.f : m[t][0];
-            const float b1 = m[t][1] == -INFINITY ? 0.f : m[t][1];
+            const float b0 = m[t][0] == -INFINITY ? 0.f : m[t][0] - kLift;
+            const float b1 = m[t][1] == -INFINITY ? 0.f : m[t][1] - kLift;
             s[t][0] = exp2_approx(s[t][0] - b0);
             s[t][1] = exp2_approx(s[t][1] - b1);
             s[t][2] = exp2_approx(s[t][2] - b0);
@@ -329,7 +333,7 @@ __global__ void __launch_bounds__(kPartWarps * 32, NT == 1 ? 4 : 3) attn_part_ke
                 so[r * kPitch + d * 16 + lane / 4 + 8] = o[t][d][j + 2];
             }
             if (lane < 4) {
-                sm[r] = m[t][j];
+                sm[r] = m[t][j] - kLift;
                 sl[r] = l[t][j];
             }
         }

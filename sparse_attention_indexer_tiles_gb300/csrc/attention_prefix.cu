@@ -24,7 +24,7 @@
 // after a row's own and leave the logits that the weights are made from.
 //
 // The running maximum m is renewed only when a row's maximum has grown by more than 8 (a
-// factor 256; P <= 256 then, well inside either type), so O is rarely rescaled; the sum l
+// factor 256; P <= 256 then in bf16, 2^15 in fp16), so O is rarely rescaled; the sum l
 // and O stay relative to the m in use, in fp32, and the result does not depend on it.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -169,12 +169,17 @@ IDX_DEVI uint64_t kv_desc(uint32_t saddr, uint32_t group) {
            ((uint64_t)(group >> 4) << 32) | (1ull << 46) | (2ull << 61);
 }
 
+// FMT: the instruction descriptor's; LIFT: m stays this far below the row's maximum.  P is then up to
+// 2^(LIFT + kRenew) = 2^15, inside fp16, whose numbers below 2^-14 have fewer bits than the others:
+// weights down to 2^-21 of the largest have all of them.
 template <typename T> struct Elem;
 template <> struct Elem<__nv_bfloat16> {
     static constexpr uint32_t FMT = 1;
+    static constexpr float LIFT = 0.f;
 };
 template <> struct Elem<__half> {
     static constexpr uint32_t FMT = 0;
+    static constexpr float LIFT = 7.f;
 };
 
 template <typename T, int D, bool PRIVATE>
@@ -451,7 +456,7 @@ attn_prefix_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_consta
             for (int c = 0; c < C::KEYS; c += 8)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = max3(x[j], z[c + 2 * j], z[c + 2 * j + 1]);
-            const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale;
+            const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale - Elem<T>::LIFT;
             // O is at rest and P has been read once the last P V has completed
             auto last_done = [&] {
                 return i == 0 || __all_sync(~0u, mbar_wait(&pvdone[s], (i - 1) & 1, abort_flag,
