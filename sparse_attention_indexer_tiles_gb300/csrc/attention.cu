@@ -609,17 +609,19 @@ AttnPlan attn_plan(int B, int Q, int Hq, int Hkv, int D, int prefix_len, int max
     const size_t rows = (size_t)B * Q * Hq;
     size_t row_parts = 0;
 
-    // Keys per private part: a block takes about 4 us and, among the three that an SM holds,
-    // 34 ns per key (D = 128: 512 bytes at a third of the SM's share of HBM), so whole waves of
-    // long parts are cheap but a wave that is mostly empty is not.  The lengths are on the
-    // device: the mean of the times with all of them at max_len and at half of it is taken.
+    // Keys per private part: a block takes about 4 us and, among three on an SM, 34 ns per key
+    // (D = 128: 512 bytes at a third of the SM's share of HBM), so whole waves of long parts are
+    // cheap but a wave that is mostly empty is not.  (The kernel of up to 8 rows has four blocks on
+    // an SM; the figures are from when it had three as well, and it is counted so.)  The lengths are on
+    // the device: the mean of the times with all of them at max_len and at half of it is taken.
     //
     // More than 16 rows read a key several times over that way, at about its HBM time each; the
     // dense path of the prefix kernel reads it once, for about 8 us per CTA, one per SM.  The
     // cheaper is taken (16 requests of 4 tokens, 8 heads, 100-1000 keys: 24.7 and dense 18.4 us;
     // 16 of 7 tokens, 16 heads, 1024-8192 keys 150 and 52; 8 of 4 tokens, 16 heads, 100-500 keys
     // 14.3 and 18.0).  Beside logits, which the dense path writes a row per thread, it gains only
-    // at D = 128 (16 of 7 tokens with weights: D 128 224 and 164 us, D 64 157 and 183).
+    // at D = 128 (16 of 7 tokens with weights, the one shape that was compared: D 128 224 and 164 us,
+    // D 64 157 and 183).
     double private_us = 0;
     p.private_dense = false;
     if (max_len > 0) {

@@ -43,7 +43,7 @@ namespace {
 constexpr int kRows = 128;                 // rows per tile
 constexpr int kHalfQ = kRows * 128;        // 64 columns of a row tile, 128-byte swizzled
 constexpr int kSoftmaxWarps = 8;
-constexpr int kPrefixThreads = (kSoftmaxWarps + 4) * 32;  // warp 11 only gives registers
+constexpr int kPrefixThreads = (kSoftmaxWarps + 4) * 32;  // and two issuers, two producers
 constexpr float kRenew = 8.f;
 
 template <int D> struct PrefixCfg {

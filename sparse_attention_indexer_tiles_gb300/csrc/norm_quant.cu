@@ -243,7 +243,9 @@ norm_quant_kernel(NormArgs a) {
                     a.scale[row * (a.N / a.group) + unit_of(v) * 8 / a.group] = scale;
             }
             // y / scale = h weight (rstd / scale), and rstd cancels unless the scale is its floor:
-            // 448 / max|h weight| has one rounding where rstd / scale has four
+            // 448 / max|h weight| has one rounding where rstd / scale has four.  (Where |h weight| is
+            // 3/4, 3/8, .. of the largest, the quotient is halfway between two codes, and these
+            // roundings decide, as the one of the scale would in y / scale.)
             const float f = scale > kScaleFloor ? __fdiv_rn(kE4m3Max, top)
                                                 : fmaf(top, 0.f, rstd) / kScaleFloor;  // NaN of either stays
 #pragma unroll
@@ -289,7 +291,10 @@ cudaError_t launch_shape(const NormArgs& a, int sm_count, cudaStream_t s) {
 // vectors a thread 11.1 us, by warps of one 13.4; 30000 x 512 by warps 11.0, by 128 threads
 // 23.5).  A wide one's threads hold as many vectors as measured fastest (bf16 with residual:
 // 8192 x 4096 with one 41.4 us, two 37.3, four 38.6; 777 x 5000 fp16 with one 7.5, two 5.3,
-// three 5.7; 4096 x 8192 with one 44.4, two 43.4, four 37.9).
+// three 5.7; 4096 x 8192 with one 44.4, two 43.4, four 37.9).  The last two rows and fp32 have the
+// 16-bit rows' shapes and were not compared with others.  With residual, and of what HBM alone would
+// take: 2048 x 16384 bf16 41 of 35 us, 8192 x 4096 fp32 69 of 64; where a thread's rows do not fit
+// its registers much more: 2048 x 16384 fp32 93 of 64, 1000 x 32768 bf16 75 of 34, fp32 350 of 63.
 template <typename T>
 cudaError_t launch_type(const NormArgs& a, int sm_count, cudaStream_t s) {
     if (a.N <= 128) return launch_shape<T, 16, 1>(a, sm_count, s);
