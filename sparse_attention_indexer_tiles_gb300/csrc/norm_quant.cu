@@ -131,7 +131,7 @@ norm_quant_kernel(NormArgs a) {
     // -> 6.1); letting the next launch begin early as well cost the latter 0.5.
     pdl_wait();
     const int t = (int)threadIdx.x % TPR, lane = threadIdx.x & 31;
-    const int units = (a.rows + kRows - 1) / kRows;
+    const int units = (a.rows - 1) / kRows + 1;
     auto row_of = [&](int u) { return (long long)u * kRows + (int)threadIdx.x / TPR; };
     // vector v's first access, in units of U columns, and how many of its 8 / U are in the row
     auto unit_of = [&](int v) { return v * (8 / U) * TPR + t; };
