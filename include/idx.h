@@ -60,6 +60,7 @@ typedef enum {
 #define IDX_DEV_TIMEOUT 0x1   /* a bounded wait inside a kernel gave up */
 #define IDX_DEV_RANGE   0x2   /* a row's [ks, ke) is not inside [0, keys] or exceeds max_len */
 #define IDX_DEV_STATE   0x4   /* the exact fallback ran out of its refinement levels */
+#define IDX_DEV_PAGES   0x8   /* idx_cache_resize: the free pages did not suffice for every row */
 
 /* IDX_MXFP4 (the OCP MX format): e2m1 elements packed two per byte (element 2i in
  * the low nibble) with one e8m0 scale per 32 consecutive elements along D; only
@@ -481,6 +482,132 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
                            int max_len, long long slots, int budget, int recent, int sink,
                            idx_dtype dt, int* lens_out, float* w_out, int* positions_out,
                            void* ws, size_t ws_bytes, const idx_options* opt, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged K/V cache in 4 bits: the append that writes it and the attention that
+ * reads it.  K and V are MXFP4 (see idx_mxfp4_to_e4m3 for the format):
+ *   k_codes, v_codes [pages, Hkv, page_size, D / 2] bytes, 16-byte aligned
+ *   k_sf, v_sf       [pages, Hkv, page_size, D / 32] bytes, 16-byte aligned
+ *   table [B, table_stride] int32: each request's pages; lens [B] int32: its slots
+ *         in the cache, the call's new tokens among them (the last ones)
+ *   q_start [B + 1] int32: tokens q_start[b] .. q_start[b + 1] - 1 of the call's T
+ *         are request b's new ones, in order; NULL: T / B each (T % B == 0).
+ * Token i of request b's n new ones has position lens[b] - n + i.
+ * Supported: D 64 or 128; page_size 16, 32, 64 or 128; B <= 65535;
+ * pages * Hkv * page_size < 2^31 - 256 (IDX_EUNSUPPORTED).
+ *
+ * idx_cache_append_mxfp4 - writes the new tokens' keys and values at their
+ * positions.  Per block of 32 elements: e = floor(log2 max|x|) - 2, at least -127
+ * (0 for a block of zeros), scale byte e + 127, and the e2m1 code nearest to
+ * x / 2^e, ties to even, saturated at 6: exact in every bit.  A block with an
+ * element that is not finite gets the NaN scale 255 and zero codes.
+ *   k, v  [T, Hkv, D] bf16 or fp16, tokens k_stride, v_stride elements apart (at least
+ *         Hkv * D, so both may be slices of one projection); rows on 16-byte boundaries
+ *         are read with wide loads, others element by element
+ * A token whose page is negative is not kept.  Tokens outside every request are not
+ * read.  No two requests may share the page of a new token.  Device errors
+ * (IDX_DEV_RANGE): a position outside [0, table_stride * page_size) or a page from
+ * `pages` on: the token is not written.  No workspace.
+ *
+ * idx_window_attention_mxfp4 - attention of every request's new tokens (one for a decode
+ * step, a chunk of a prompt, a few drafted ones) over its cache, causal, with a sliding
+ * window and first tokens that stay visible.  The token at position p sees slots j <= p
+ * with j < sink or j > p - window (all j <= p when window is 0, and sink does not count).
+ * With key head head / (Hq / Hkv), z_j = scale * q . k_j over those slots:
+ *     out = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse = log sum_j exp(z_j).
+ * A row that sees nothing gets out 0 and lse -inf.  A row that sees a slot with a NaN scale
+ * (255, in K or V) or a logit that is NaN or +inf gets NaN, and no other row does.  Weights below 2^-31
+ * of a row's largest count as 0.  Values 2^120 and more below the largest in their 32 columns, of a slot that
+ * a row of the same request sees, lose bits.
+ *   q    [T, Hq, D] bf16 or fp16, tokens q_stride elements apart, rows on 16-byte boundaries
+ *   max_q   an upper bound on a request's new tokens (0 = T)
+ *   max_len an upper bound on lens (0 = table_stride * page_size)
+ *   out  [T, Hq, D] of q's type, contiguous; lse [T, Hq] fp32 or NULL.  Rows of tokens outside
+ *        every request are not written.
+ *   ws   idx_window_attention_mxfp4_workspace(...) bytes for the same arguments (max_q and
+ *        max_len as the call counts them), 256-byte aligned; needs no clearing between calls.
+ *        The size does not shrink when an argument grows (a window of 0 is the largest).
+ * Slots that no row of a request sees are not read, and their pages need not exist (table
+ * entries of any value).  Further limits: Hq a multiple of Hkv with Hq / Hkv <= 128; T * Hq <
+ * 2^31 - 256; max_len, window, sink < 2^30.  Device errors (IDX_DEV_RANGE): lens[b] outside [0,
+ * max_len] is clamped, a request whose q_start is not in order or that has more than max_q
+ * tokens is cut or skipped; a page outside [0, pages) that a row sees: the request's results are
+ * meaningless.
+ * ------------------------------------------------------------------------ */
+idx_status idx_cache_append_mxfp4(const void* k, long long k_stride, const void* v,
+                                  long long v_stride, uint8_t* k_codes, uint8_t* k_sf,
+                                  uint8_t* v_codes, uint8_t* v_sf, const int* table,
+                                  const int* lens, const int* q_start, int B, int T, int Hkv,
+                                  int D, int pages, int page_size, long long table_stride,
+                                  idx_dtype dt, const idx_options* opt, void* stream);
+size_t idx_window_attention_mxfp4_workspace(int B, int T, int max_q, int Hq, int Hkv, int D,
+                                            int max_len, int window, int sink);
+idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const uint8_t* k_codes,
+                                      const uint8_t* k_sf, const uint8_t* v_codes,
+                                      const uint8_t* v_sf, const int* table, const int* lens,
+                                      const int* q_start, int B, int T, int max_q, int Hq, int Hkv,
+                                      int D, int pages, int page_size, long long table_stride,
+                                      int max_len, int window, int sink, float scale, idx_dtype dt,
+                                      void* out, float* lse, void* ws, size_t ws_bytes,
+                                      const idx_options* opt, void* stream);
+
+/* ------------------------------------------------------------------------
+ * The pages of a cache (of any element type): which rows of a page table hold
+ * them.  refs[p] is the number of table entries, over all rows and within their
+ * lengths, that name page p; a page is free when it is 0 (or less).
+ *   table [B, table_stride], lens [B] (in slots), refs [pages] int32
+ *   refs_out, table_out, lens_out: the same after the call; each may be its input.  Of a row of
+ *         table_out the first ceil(lens_out / page_size) entries are written (in place: those
+ *         that change).
+ *   caches [n_caches] HOST array of device arrays whose pages move or are copied, page_bytes
+ *         [n_caches] bytes of a page in each (HOST): K and V, codes and scales, the indexer's
+ *         keys ...  Bases 16-byte aligned and page_bytes a multiple of 16 (IDX_EALIGN);
+ *         n_caches <= 8.
+ * page_size 16, 32, 64 or 128; table_stride * page_size < 2^31; B <= 2^24.  Results do not depend on
+ * the order in which threads run.  Device errors (IDX_DEV_RANGE): a length outside [0, table_stride
+ * * page_size] counts as 0 in a fork and leaves its row as it is otherwise; a table entry outside [0, pages)
+ * within a row's length is kept and not counted.
+ *
+ * idx_cache_fork - row i takes over the pages and the length of row parent[i] as they were
+ * before the call and gives its own back; all rows at once (the next step of a beam search).
+ * parent[i] = i leaves the row, -1 ends it (length 0).  Nothing is copied: rows share pages
+ * until one of them grows (idx_cache_resize).  Other parents outside [0, B): IDX_DEV_RANGE, the
+ * row is left.  ws: idx_cache_fork_workspace(...) bytes, 256-byte aligned, when table_out is
+ * table or lens_out is lens; NULL and 0 otherwise.
+ *
+ * idx_cache_resize - row i goes from lens[i] to new_lens[i] slots.  First the rows that shrink
+ * give back the pages that they no longer need.  Then the rows that grow take free pages, the
+ * lowest free page first, in the order of rows and within a row of its slots.  A row that grows
+ * into a partly filled last page which other entries name too (refs above 1 once the rows have
+ * shrunk) takes a page for a copy of it first and gives the shared one back; every such row
+ * copies, also when all that hold the page grow (it is free from the next call on).  From the
+ * first row on for which the free pages do not suffice, rows that want pages keep their pages
+ * and length, and IDX_DEV_PAGES is raised; lens_out tells.  A new length outside [0, table_stride
+ * * page_size]: IDX_DEV_RANGE, the row is left.
+ * ws: idx_cache_resize_workspace(...) bytes, 256-byte aligned.
+ *
+ * idx_cache_compact - moves the live pages to the front: with `live` pages whose count is above
+ * 0, the i-th free page below `live` takes the contents and count of the i-th live page from there on,
+ * and the tables follow.  live [1] int32 is written.  Counts of all other pages become 0.
+ * ws: idx_cache_compact_workspace(...) bytes, 256-byte aligned.
+ * ------------------------------------------------------------------------ */
+size_t idx_cache_fork_workspace(int B, long long table_stride);
+idx_status idx_cache_fork(const int* refs, const int* table, const int* lens, const int* parent,
+                          int B, int pages, int page_size, long long table_stride, int* refs_out,
+                          int* table_out, int* lens_out, void* ws, size_t ws_bytes,
+                          const idx_options* opt, void* stream);
+size_t idx_cache_resize_workspace(int B, int pages, long long table_stride);
+idx_status idx_cache_resize(void* const* caches, const long long* page_bytes, int n_caches,
+                            const int* refs, const int* table, const int* lens,
+                            const int* new_lens, int B, int pages, int page_size,
+                            long long table_stride, int* refs_out, int* table_out, int* lens_out,
+                            void* ws, size_t ws_bytes, const idx_options* opt, void* stream);
+size_t idx_cache_compact_workspace(int B, int pages);
+idx_status idx_cache_compact(void* const* caches, const long long* page_bytes, int n_caches,
+                             const int* refs, const int* table, const int* lens, int B, int pages,
+                             int page_size, long long table_stride, int* refs_out, int* table_out,
+                             int* live, void* ws, size_t ws_bytes, const idx_options* opt,
+                             void* stream);
 
 /* Static text for a status code. */
 const char* idx_status_string(idx_status s);

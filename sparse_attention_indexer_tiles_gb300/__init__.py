@@ -16,6 +16,11 @@ Entry points (same names as the C ABI in ``include/idx.h``):
   idx_add_rmsnorm_quant     residual add + RMS norm to e4m3 rows with scales (k and k_scale)
   idx_prefix_attention      decode attention over a shared prefix and private paged caches
   idx_cache_evict           keep a budget of cached slots by accumulated attention weight
+  idx_cache_append_mxfp4    new keys and values into a paged cache in 4 bits
+  idx_window_attention_mxfp4
+                            attention over that cache: decode steps and prompts, window, sinks
+  idx_cache_fork, idx_cache_resize, idx_cache_compact
+                            which row of a page table holds which page of a cache
 """
 from __future__ import annotations
 
@@ -35,7 +40,10 @@ __all__ = [
     "idx_score_topk_routed", "idx_score_topk_routed_workspace", "idx_mxfp4_to_e4m3",
     "idx_score_topk_mxfp4", "idx_score_materialise_mxfp4", "idx_add_rmsnorm_quant",
     "idx_prefix_attention", "idx_prefix_attention_workspace", "idx_prefix_attention_plan",
-    "idx_cache_evict", "idx_cache_evict_workspace",
+    "idx_cache_evict", "idx_cache_evict_workspace", "idx_cache_append_mxfp4",
+    "idx_window_attention_mxfp4", "idx_window_attention_mxfp4_workspace", "idx_cache_fork",
+    "idx_cache_fork_workspace", "idx_cache_resize", "idx_cache_resize_workspace",
+    "idx_cache_compact", "idx_cache_compact_workspace",
 ]
 
 _HERE = os.path.dirname(os.path.abspath(__file__))
@@ -150,6 +158,24 @@ def load(path: str | None = None):
     lib.idx_cache_evict_workspace.restype = SZ
     lib.idx_cache_evict.argtypes = [P] * 7 + [I] * 5 + [LL, I, LL, I, I, I, I, P, P, P, P, SZ, P, P]
     lib.idx_cache_evict.restype = I
+    lib.idx_cache_append_mxfp4.argtypes = [P, LL, P, LL] + [P] * 7 + [I] * 6 + [LL, I, P, P]
+    lib.idx_cache_append_mxfp4.restype = I
+    lib.idx_window_attention_mxfp4_workspace.argtypes = [I] * 9
+    lib.idx_window_attention_mxfp4_workspace.restype = SZ
+    lib.idx_window_attention_mxfp4.argtypes = [P, LL] + [P] * 7 + [I] * 8 + [LL, I, I, I, F, I, P, P, P, SZ, P, P]
+    lib.idx_window_attention_mxfp4.restype = I
+    lib.idx_cache_fork_workspace.argtypes = [I, LL]
+    lib.idx_cache_fork_workspace.restype = SZ
+    lib.idx_cache_fork.argtypes = [P] * 4 + [I] * 3 + [LL, P, P, P, P, SZ, P, P]
+    lib.idx_cache_fork.restype = I
+    lib.idx_cache_resize_workspace.argtypes = [I, I, LL]
+    lib.idx_cache_resize_workspace.restype = SZ
+    lib.idx_cache_resize.argtypes = [P, P, I] + [P] * 4 + [I] * 3 + [LL, P, P, P, P, SZ, P, P]
+    lib.idx_cache_resize.restype = I
+    lib.idx_cache_compact_workspace.argtypes = [I, I]
+    lib.idx_cache_compact_workspace.restype = SZ
+    lib.idx_cache_compact.argtypes = [P, P, I] + [P] * 3 + [I] * 3 + [LL, P, P, P, P, SZ, P, P]
+    lib.idx_cache_compact.restype = I
     lib.idx_status_string.argtypes = [I]
     lib.idx_status_string.restype = ctypes.c_char_p
     lib.idx_version.argtypes = []
@@ -560,6 +586,9 @@ def _serve():
         loader.exec_module(module)
         module.bind(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
             lib.idx_add_rmsnorm_quant, lib.idx_prefix_attention, lib.idx_cache_evict)))
+        module.bind_cache(*(ctypes.cast(f, ctypes.c_void_p).value for f in (
+            lib.idx_cache_append_mxfp4, lib.idx_window_attention_mxfp4, lib.idx_cache_fork,
+            lib.idx_cache_resize, lib.idx_cache_compact)))
         _serve_module = module
     return _serve_module
 
@@ -680,3 +709,132 @@ def idx_cache_evict(k_cache, v_cache, table, lens, weights, positions, next_pos,
         k_cache, v_cache, table, lens, weights, positions, next_pos, budget, recent, sink, max_len,
         lens_out, weights_out, positions_out, ws), options, stats, stream)
     return lens_out, weights_out, positions_out
+
+
+def idx_cache_append_mxfp4(k, v, k_codes, k_sf, v_codes, v_sf, table, lens, *, q_start=None,
+                           options=None, stats: Stats | None = None, stream=None) -> None:
+    """Write the new tokens' k, v [T, Hkv, D] (slices of a wider projection may be given) into a
+    paged MXFP4 cache: codes [pages, Hkv, page_size, D // 2] and scales [..., D // 32] uint8.
+    lens [B] counts the new tokens; q_start [B + 1] says which are whose (None: T / B each)."""
+    _serve_call("idx_cache_append_mxfp4", _serve().cache_append_mxfp4, (
+        k, v, k_codes, k_sf, v_codes, v_sf, table, lens, q_start), options, stats, stream)
+
+
+def idx_window_attention_mxfp4_workspace(B: int, T: int, max_q: int, Hq: int, Hkv: int, D: int,
+                                         max_len: int, window: int, sink: int) -> int:
+    return int(load().idx_window_attention_mxfp4_workspace(B, T, max_q, Hq, Hkv, D, max_len,
+                                                           window, sink))
+
+
+def idx_window_attention_mxfp4(q, k_codes, k_sf, v_codes, v_sf, table, lens, *, q_start=None,
+                               max_q: int = 0, max_len: int = 0, window: int = 0, sink: int = 0,
+                               scale: float | None = None, out=None, lse=None, ws=None,
+                               options=None, stats: Stats | None = None, stream=None):
+    """Causal attention of the new tokens' q [T, Hq, D] over each request's slots of a paged MXFP4
+    cache: (out [T, Hq, D], lse [T, Hq]).  With a window, a token sees the `window` newest slots
+    up to its own and the first `sink` ones.  max_q bounds a request's new tokens, max_len its
+    slots.  An out that is allocated here is 0 for tokens outside every request."""
+    fn = "idx_window_attention_mxfp4"
+    if out is None or lse is None or ws is None:
+        if q.dim() != 3 or k_codes.dim() != 4 or table.dim() != 2:
+            raise ValueError(f"{fn}: q [T, Hq, D], codes [pages, Hkv, page_size, D // 2], "
+                             "table [B, P]")
+        T, Hq, D = q.shape
+        make = torch.empty if q_start is None else torch.zeros
+        with _Launch(stream, q.device) as on:
+            if out is None:
+                out = on.result(make(T, Hq, D, dtype=q.dtype, device=q.device))
+            if lse is None:
+                lse = on.result(make(T, Hq, dtype=torch.float32, device=q.device))
+            if ws is None:
+                need = idx_window_attention_mxfp4_workspace(
+                    table.shape[0], T, max_q, Hq, k_codes.shape[1], D,
+                    max_len or min(table.shape[1] * k_codes.shape[2], 0x7fffffff), window, sink)
+                ws = torch.empty(max(need, 256), dtype=torch.uint8, device=q.device)
+    _serve_call(fn, _serve().window_attention_mxfp4, (
+        q, k_codes, k_sf, v_codes, v_sf, table, lens, q_start, max_q, max_len, window, sink, scale,
+        out, lse, ws), options, stats, stream)
+    return out, lse
+
+
+def idx_cache_fork_workspace(B: int, width: int) -> int:
+    return int(load().idx_cache_fork_workspace(B, width))
+
+
+def idx_cache_fork(refs, table, lens, parent, *, page_size: int, refs_out=None, table_out=None,
+                   lens_out=None, ws=None, options=None, stats: Stats | None = None, stream=None):
+    """Row i of the page table takes over the pages and the length of row parent[i] (i: stays, -1:
+    ends), all rows at once; refs [pages] counts the entries that name a page.  Returns
+    (refs_out, table_out, lens_out), each of which may be its input (then with a workspace)."""
+    fn = "idx_cache_fork"
+    with _Launch(stream, refs.device) as on:
+        refs_out, table_out, lens_out = _page_results(on, fn, refs, refs_out, table, table_out,
+                                                      lens, lens_out)
+        if ws is None and (table_out is table or lens_out is lens
+                           or table_out.data_ptr() == table.data_ptr()
+                           or lens_out.data_ptr() == lens.data_ptr()):
+            ws = torch.empty(max(256, idx_cache_fork_workspace(*table.shape)), dtype=torch.uint8,
+                             device=refs.device)
+    _serve_call(fn, _serve().cache_fork, (
+        refs, table, lens, parent, page_size, refs_out, table_out, lens_out, ws), options, stats,
+        stream)
+    return refs_out, table_out, lens_out
+
+
+def _page_results(on, fn, refs, refs_out, table, table_out, lens, lens_out):
+    """What a call on pages writes, where the caller did not bring it."""
+    if refs.dim() != 1 or table.dim() != 2:
+        raise ValueError(f"{fn}: refs [pages], table [B, P]")
+    if refs_out is None:
+        refs_out = on.result(torch.empty_like(refs))
+    if table_out is None:
+        table_out = on.result(torch.full_like(table, -1))
+    if lens_out is None:
+        lens_out = on.result(torch.empty_like(lens))
+    return refs_out, table_out, lens_out
+
+
+def idx_cache_resize_workspace(B: int, pages: int, width: int) -> int:
+    return int(load().idx_cache_resize_workspace(B, pages, width))
+
+
+def idx_cache_resize(caches, refs, table, lens, new_lens, *, page_size: int, refs_out=None,
+                     table_out=None, lens_out=None, ws=None, options=None,
+                     stats: Stats | None = None, stream=None):
+    """Rows of the page table go from lens to new_lens slots: they give pages back and take free
+    ones (refs 0, lowest first), and a row that grows into a page which others hold too takes a
+    copy of it in every one of `caches` ([pages, ...] tensors).  Returns (refs_out, table_out,
+    lens_out), each of which may be its input; lens_out tells where the pages did not suffice."""
+    fn = "idx_cache_resize"
+    with _Launch(stream, refs.device) as on:
+        refs_out, table_out, lens_out = _page_results(on, fn, refs, refs_out, table, table_out,
+                                                      lens, lens_out)
+        if ws is None:
+            need = idx_cache_resize_workspace(table.shape[0], refs.shape[0], table.shape[1])
+            ws = torch.empty(max(256, need), dtype=torch.uint8, device=refs.device)
+    _serve_call(fn, _serve().cache_resize, (
+        caches, refs, table, lens, new_lens, page_size, refs_out, table_out, lens_out, ws), options,
+        stats, stream)
+    return refs_out, table_out, lens_out
+
+
+def idx_cache_compact_workspace(B: int, pages: int) -> int:
+    return int(load().idx_cache_compact_workspace(B, pages))
+
+
+def idx_cache_compact(caches, refs, table, lens, *, page_size: int, refs_out=None, table_out=None,
+                      live=None, ws=None, options=None, stats: Stats | None = None, stream=None):
+    """Move the live pages (refs above 0) of `caches` ([pages, ...] tensors) to the front, in
+    place; returns (refs_out, table_out, live [1]), the first two may be their inputs."""
+    fn = "idx_cache_compact"
+    with _Launch(stream, refs.device) as on:
+        refs_out, table_out, _ = _page_results(on, fn, refs, refs_out, table, table_out, lens, lens)
+        if live is None:
+            live = on.result(torch.empty(1, dtype=torch.int32, device=refs.device))
+        if ws is None:
+            need = idx_cache_compact_workspace(table.shape[0], refs.shape[0])
+            ws = torch.empty(max(256, need), dtype=torch.uint8, device=refs.device)
+    _serve_call(fn, _serve().cache_compact, (
+        caches, refs, table, lens, page_size, refs_out, table_out, live, ws), options, stats,
+        stream)
+    return refs_out, table_out, live

@@ -12,6 +12,8 @@
 #include <cudaTypedefs.h>
 
 #include "attention.cuh"
+#include "cache_append.cuh"
+#include "cache_pages.cuh"
 #include "evict.cuh"
 #include "mxfp4.cuh"
 #include "norm_quant.cuh"
@@ -19,6 +21,7 @@
 #include "plan.cuh"
 #include "score.cuh"
 #include "topk.cuh"
+#include "window.cuh"
 
 namespace idx {
 
@@ -1221,6 +1224,284 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
     count_launches(launched);
     record(opt, 1, s);
     return cuda_status(e);
+}
+
+// ------------------------------------------------- the cache in 4 bits
+
+namespace {
+
+// Sizes that the append and the attention share; the arguments are not negative.
+bool mxfp4_cache_supported(int B, int Hkv, int D, int pages, int page_size) {
+    return (D == 64 || D == 128) && page_size_ok(page_size) && B <= 65535 && Hkv <= 65535 &&
+           (long long)pages * Hkv <= 0x7fffff00ll / page_size;
+}
+
+bool window_sizes_ok(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window, int sink) {
+    return B >= 1 && T >= 0 && max_q >= 0 && Hkv >= 1 && Hq >= Hkv && Hq % Hkv == 0 && max_len >= 0 &&
+           max_len <= kMaxPrivate && window >= 0 && window <= kMaxPrivate && sink >= 0 && sink <= kMaxPrivate &&
+           (D == 64 || D == 128) && B <= 65535 && Hkv <= 65535 && Hq / Hkv <= kWindowMaxGroup &&
+           (long long)T * Hq <= 0x7fffff00ll;
+}
+
+// The bound on a request's new tokens as the call counts it.
+int window_most_tokens(int T, int max_q) { return max_q == 0 || max_q > T ? T : max_q; }
+
+}  // namespace
+
+idx_status idx_cache_append_mxfp4(const void* k, long long k_stride, const void* v, long long v_stride,
+                                  uint8_t* k_codes, uint8_t* k_sf, uint8_t* v_codes, uint8_t* v_sf,
+                                  const int* table, const int* lens, const int* q_start, int B, int T, int Hkv,
+                                  int D, int pages, int page_size, long long table_stride, idx_dtype dt,
+                                  const idx_options* opt, void* stream) {
+    if (B < 0 || T < 0 || Hkv < 1 || D < 1 || pages < 0 || table_stride < 0) return IDX_EINVAL;
+    if (!is_16bit(dt) || !mxfp4_cache_supported(B, Hkv, D, pages, page_size) || table_stride > 0x7fffffffll)
+        return IDX_EUNSUPPORTED;
+    if (k_stride < (long long)Hkv * D || v_stride < (long long)Hkv * D) return IDX_EINVAL;
+    if (B == 0 || T == 0) return IDX_OK;
+    if (!q_start && T % B != 0) return IDX_EINVAL;
+    if (!k || !v || !k_codes || !k_sf || !v_codes || !v_sf || !table || !lens) return IDX_EINVAL;
+    if (!aligned(k, 2) || !aligned(v, 2) || !aligned(k_codes, 16) || !aligned(k_sf, 16) || !aligned(v_codes, 16) ||
+        !aligned(v_sf, 16) || !aligned(table, 4) || !aligned(lens, 4) || !aligned(q_start, 4))
+        return IDX_EALIGN;
+    if (!arch_ok()) return IDX_EUNSUPPORTED;
+    AppendArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.k = k;
+    a.v = v;
+    a.k_codes = k_codes;
+    a.k_sf = k_sf;
+    a.v_codes = v_codes;
+    a.v_sf = v_sf;
+    a.table = table;
+    a.lens = lens;
+    a.q_start = q_start;
+    a.table_stride = table_stride;
+    a.k_stride = k_stride;
+    a.v_stride = v_stride;
+    a.B = B;
+    a.T = T;
+    a.Hkv = Hkv;
+    a.D = D;
+    a.pages = pages;
+    a.page_size = page_size;
+    a.page_shift = page_shift(page_size);
+    a.d_status = opt ? opt->d_status : nullptr;
+    const bool wide = aligned(k, 16) && aligned(v, 16) && (T == 1 || (k_stride % 8 == 0 && v_stride % 8 == 0));
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    record(opt, 0, s);
+    const cudaError_t e = launch_append(a, dt, wide, s);
+    if (e == cudaSuccess) count_launches(1);
+    record(opt, 1, s);
+    return cuda_status(e);
+}
+
+size_t idx_window_attention_mxfp4_workspace(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window,
+                                            int sink) {
+    if (!window_sizes_ok(B, T, max_q, Hq, Hkv, D, max_len, window, sink)) return 0;
+    return window_plan(B, T, window_most_tokens(T, max_q), Hq, Hkv, D, max_len, window, sink, sm_count()).total;
+}
+
+idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const uint8_t* k_codes, const uint8_t* k_sf,
+                                      const uint8_t* v_codes, const uint8_t* v_sf, const int* table, const int* lens,
+                                      const int* q_start, int B, int T, int max_q, int Hq, int Hkv, int D, int pages,
+                                      int page_size, long long table_stride, int max_len, int window, int sink,
+                                      float scale, idx_dtype dt, void* out, float* lse, void* ws, size_t ws_bytes,
+                                      const idx_options* opt, void* stream) {
+    if (B < 0 || T < 0 || max_q < 0 || Hq < 1 || Hkv < 1 || Hq % Hkv != 0 || D < 1 || pages < 0 || table_stride < 0 ||
+        max_len < 0 || window < 0 || sink < 0 || !std::isfinite(scale))
+        return IDX_EINVAL;
+    if (!is_16bit(dt) || !mxfp4_cache_supported(B, Hkv, D, pages, page_size) || table_stride > 0x7fffffffll)
+        return IDX_EUNSUPPORTED;
+    if (!private_bound(max_len, table_stride, page_size)) return IDX_EINVAL;
+    if (B == 0 || T == 0) return IDX_OK;
+    if (!window_sizes_ok(B, T, max_q, Hq, Hkv, D, max_len, window, sink)) return IDX_EUNSUPPORTED;
+    if (q_stride < (long long)Hq * D) return IDX_EINVAL;
+    max_q = window_most_tokens(T, max_q);
+    if (!q_start && (T % B != 0 || max_q < T / B)) return IDX_EINVAL;
+    if (!q || !out || !lens || (max_len > 0 && (!table || !k_codes || !k_sf || !v_codes || !v_sf || pages < 1)))
+        return IDX_EINVAL;
+    if (!aligned(q, 16) || (T > 1 && q_stride % 8 != 0) || !aligned(out, 16) || !aligned(k_codes, 16) ||
+        !aligned(k_sf, 16) || !aligned(v_codes, 16) || !aligned(v_sf, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
+        !aligned(q_start, 4) || !aligned(lse, 4))
+        return IDX_EALIGN;
+    const WindowPlan p = window_plan(B, T, max_q, Hq, Hkv, D, max_len, window, sink, sm_count());
+    if ((long long)p.splits * p.row_tiles * Hkv > 0x7fffffffll) return IDX_EUNSUPPORTED;
+    if (p.total > 0 && (!ws || ws_bytes < p.total)) return IDX_EWORKSPACE;
+    if (!aligned(ws, 256)) return IDX_EALIGN;
+    if (!arch_ok()) return IDX_EUNSUPPORTED;
+    WindowArgs a;
+    std::memset(&a, 0, sizeof(a));
+    a.q = q;
+    a.k_codes = k_codes;
+    a.k_sf = k_sf;
+    a.v_codes = v_codes;
+    a.v_sf = v_sf;
+    a.table = table;
+    a.lens = lens;
+    a.q_start = q_start;
+    a.out = out;
+    a.lse = lse;
+    a.part = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.part);
+    a.part_lse = reinterpret_cast<float*>(static_cast<uint8_t*>(ws) + p.part_lse);
+    a.table_stride = table_stride;
+    a.q_stride = q_stride;
+    a.B = B;
+    a.T = T;
+    a.Hq = Hq;
+    a.Hkv = Hkv;
+    a.G = Hq / Hkv;
+    a.D = D;
+    a.pages = pages;
+    a.page_size = page_size;
+    a.page_shift = page_shift(page_size);
+    a.max_q = max_q;
+    a.max_len = max_len;
+    a.window = window;
+    a.sink = window > 0 ? sink : 0;
+    a.row_tiles = p.row_tiles;
+    a.splits = p.splits;
+    a.chunk = p.chunk;
+    a.scale_log2 = scale * 1.4426950408889634f;
+    const int stall_us = opt ? opt->test_stall_us : 0;
+    a.wait_limit = stall_us > 0 ? 2100LL * stall_us : (1LL << 32);
+    a.withhold_step = stall_us > 0 ? 1 : -1;
+    a.d_status = opt ? opt->d_status : nullptr;
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launched = 0;
+    record(opt, 0, s);
+    const cudaError_t e = launch_window(a, p, dt, sm_count(), s, &launched);
+    count_launches(launched);
+    record(opt, 1, s);
+    return cuda_status(e);
+}
+
+// ------------------------------------------------- pages of a cache
+
+namespace {
+
+size_t ints_bytes(size_t n) { return (n * sizeof(int) + 255) / 256 * 256; }
+
+bool pages_sizes_ok(int B, int pages, long long table_stride) {
+    return B >= 0 && B <= 1 << 24 && pages >= 0 && table_stride >= 0 && table_stride <= 0x7fffffffll;
+}
+
+// The arguments that the calls share.
+idx_status pages_args(PagesArgs& a, void* const* caches, const long long* page_bytes, int n_caches, const int* refs,
+                      const int* table, const int* lens, int B, int pages, int page_size, long long table_stride,
+                      int* refs_out, int* table_out, const idx_options* opt) {
+    if (B < 0 || pages < 0 || table_stride < 0 || n_caches < 0) return IDX_EINVAL;
+    if (!page_size_ok(page_size) || !pages_sizes_ok(B, pages, table_stride) ||
+        table_stride > 0x7fffffffll / page_size || n_caches > kMaxCaches)
+        return IDX_EUNSUPPORTED;
+    if (n_caches > 0 && (!caches || !page_bytes)) return IDX_EINVAL;
+    if ((pages > 0 && (!refs || !refs_out)) || (B > 0 && (!lens || (table_stride > 0 && (!table || !table_out)))))
+        return IDX_EINVAL;
+    std::memset(&a, 0, sizeof(a));
+    for (int i = 0; i < n_caches; ++i) {
+        if (pages > 0 && (!caches[i] || page_bytes[i] < 1)) return IDX_EINVAL;
+        if (!aligned(caches[i], 16) || page_bytes[i] % 16 != 0) return IDX_EALIGN;
+        a.caches.p[i] = static_cast<uint8_t*>(caches[i]);
+        a.caches.bytes[i] = page_bytes[i];
+    }
+    if (!aligned(refs, 4) || !aligned(refs_out, 4) || !aligned(table, 4) || !aligned(table_out, 4) || !aligned(lens, 4))
+        return IDX_EALIGN;
+    a.caches.n = n_caches;
+    a.refs = refs;
+    a.table = table;
+    a.lens = lens;
+    a.refs_out = refs_out;
+    a.table_out = table_out;
+    a.table_stride = table_stride;
+    a.B = B;
+    a.pages = pages;
+    a.page_size = page_size;
+    a.page_shift = page_shift(page_size);
+    a.d_status = opt ? opt->d_status : nullptr;
+    return IDX_OK;
+}
+
+idx_status pages_launch(cudaError_t (*launch)(const PagesArgs&, int, cudaStream_t, int*), const PagesArgs& a,
+                        const idx_options* opt, void* stream) {
+    cudaStream_t s = static_cast<cudaStream_t>(stream);
+    int launched = 0;
+    record(opt, 0, s);
+    const cudaError_t e = launch(a, sm_count(), s, &launched);
+    count_launches(launched);
+    record(opt, 1, s);
+    return cuda_status(e);
+}
+
+}  // namespace
+
+size_t idx_cache_fork_workspace(int B, long long table_stride) {
+    return B < 1 || !pages_sizes_ok(B, 0, table_stride) ? 0 : ints_bytes(fork_workspace_ints(B, table_stride));
+}
+
+idx_status idx_cache_fork(const int* refs, const int* table, const int* lens, const int* parent, int B, int pages,
+                          int page_size, long long table_stride, int* refs_out, int* table_out, int* lens_out, void* ws,
+                          size_t ws_bytes, const idx_options* opt, void* stream) {
+    PagesArgs a;
+    const idx_status st = pages_args(a, nullptr, nullptr, 0, refs, table, lens, B, pages, page_size, table_stride,
+                                     refs_out, table_out, opt);
+    if (st != IDX_OK) return st;
+    if (B > 0 && (!parent || !lens_out)) return IDX_EINVAL;
+    if (!aligned(parent, 4) || !aligned(lens_out, 4)) return IDX_EALIGN;
+    if (B == 0 && (pages == 0 || refs == refs_out)) return IDX_OK;
+    a.arg = parent;
+    a.lens_out = lens_out;
+    if (B > 0 && (table_out == table || lens_out == lens)) {
+        if (!ws || ws_bytes < idx_cache_fork_workspace(B, table_stride)) return IDX_EWORKSPACE;
+        if (!aligned(ws, 256)) return IDX_EALIGN;
+        a.ws = static_cast<int*>(ws);
+    }
+    if (!arch_ok()) return IDX_EUNSUPPORTED;
+    return pages_launch(launch_fork, a, opt, stream);
+}
+
+size_t idx_cache_resize_workspace(int B, int pages, long long table_stride) {
+    return !pages_sizes_ok(B, pages, table_stride) ? 0 : ints_bytes(resize_workspace_ints(B, pages, table_stride));
+}
+
+idx_status idx_cache_resize(void* const* caches, const long long* page_bytes, int n_caches, const int* refs,
+                            const int* table, const int* lens, const int* new_lens, int B, int pages, int page_size,
+                            long long table_stride, int* refs_out, int* table_out, int* lens_out, void* ws,
+                            size_t ws_bytes, const idx_options* opt, void* stream) {
+    PagesArgs a;
+    const idx_status st = pages_args(a, caches, page_bytes, n_caches, refs, table, lens, B, pages, page_size,
+                                     table_stride, refs_out, table_out, opt);
+    if (st != IDX_OK) return st;
+    if (B > 0 && (!new_lens || !lens_out)) return IDX_EINVAL;
+    if (!aligned(new_lens, 4) || !aligned(lens_out, 4)) return IDX_EALIGN;
+    if (!ws || ws_bytes < idx_cache_resize_workspace(B, pages, table_stride)) return IDX_EWORKSPACE;
+    if (!aligned(ws, 256)) return IDX_EALIGN;
+    if (B == 0 && (pages == 0 || refs == refs_out)) return IDX_OK;
+    a.arg = new_lens;
+    a.lens_out = lens_out;
+    a.ws = static_cast<int*>(ws);
+    if (!arch_ok()) return IDX_EUNSUPPORTED;
+    return pages_launch(launch_resize, a, opt, stream);
+}
+
+size_t idx_cache_compact_workspace(int B, int pages) {
+    return !pages_sizes_ok(B, pages, 0) ? 0 : ints_bytes(compact_workspace_ints(B, pages));
+}
+
+idx_status idx_cache_compact(void* const* caches, const long long* page_bytes, int n_caches, const int* refs,
+                             const int* table, const int* lens, int B, int pages, int page_size, long long table_stride,
+                             int* refs_out, int* table_out, int* live, void* ws, size_t ws_bytes,
+                             const idx_options* opt, void* stream) {
+    PagesArgs a;
+    const idx_status st = pages_args(a, caches, page_bytes, n_caches, refs, table, lens, B, pages, page_size,
+                                     table_stride, refs_out, table_out, opt);
+    if (st != IDX_OK) return st;
+    if (!live) return IDX_EINVAL;
+    if (!aligned(live, 4)) return IDX_EALIGN;
+    if (!ws || ws_bytes < idx_cache_compact_workspace(B, pages)) return IDX_EWORKSPACE;
+    if (!aligned(ws, 256)) return IDX_EALIGN;
+    a.live = live;
+    a.ws = static_cast<int*>(ws);
+    if (!arch_ok()) return IDX_EUNSUPPORTED;
+    return pages_launch(launch_compact, a, opt, stream);
 }
 
 }  // extern "C"

@@ -1,0 +1,782 @@
+// Attention over a paged MXFP4 cache, with a sliding window and first tokens that stay visible.
+//
+// Row (token at position p, head) sees the keys j <= p with j < sink or j > p - window (all of
+// them when window is 0), z_j = scale * q . k_j:
+//     o = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse = log sum_j exp(z_j).
+// k and v are e2m1 codes c times a power of two per 32 elements, so with K's block b of a key
+//     q . k_j = sum_b 2^(e_jb) sum_{d in b} q_d c_jd,
+// and the codes are the operand of the matrix instructions as fp16, which holds them exactly.
+// The powers of K's blocks multiply the fp32 sums.  V's multiply its codes in fp16, relative to a
+// running power 2^E per block of columns; sums against V stay in units of 2^E.
+//
+// bf16 queries are made fp16 by a power of two per row (the largest element just below 2^15): an
+// element below 2^-32 of the row's largest loses bits, 2^-40 of that one at most.  The weights
+// enter the second product as fp16 times 2^7; the running maximum is renewed when a row grows
+// past it by 2^8.  Weights below 2^-21 of a row's largest have fewer bits than fp16, those below
+// 2^-31 count as 0.  Maxima, sums and o are fp32, exponentials base 2 on z * log2(e).
+//
+// HBM-bound in theory (68 bytes per key row of 128); in practice the instructions that expand the
+// codes come close.  A block's warps each take 32 keys at a time through a ring of their own, which
+// TMA fills (rows swizzled, so that the warp's reads of 4-byte words meet no bank conflicts).  The
+// products are taken transposed, S^T = K Q^T and O^T += V^T P^T: keys and D are the long axes of the
+// matrix instructions, the rows (8 or 16) the short one.
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include <cudaTypedefs.h>
+
+#include "serve.cuh"
+#include "window.cuh"
+
+namespace idx {
+
+PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
+
+namespace {
+
+constexpr int kWarps = 4;
+constexpr int kStages = 3;
+constexpr float kLift = 7.f;    // weights are taken times 2^kLift
+constexpr float kRenew = 8.f;   // growth of a row's maximum that renews it; 2^(kLift + kRenew) fits fp16
+// Fields of an fp16 power of two 2^(field - 15) that V's codes take: 28 for a block at E, so that
+// 6 * 2^13 is the largest value; blocks below 2^-26 of it are taken in another pass over the step.
+constexpr int kTopField = 28, kBand = 26;
+constexpr int kMargin = 3;      // E is set this far above what asked for it
+
+template <int D> struct Ring {
+    static constexpr int ROW = D / 2;                        // bytes of codes
+    static constexpr int CODES = kWindowStep * ROW;
+    static constexpr int SF = kWindowStep * (D / 32);
+    static constexpr int OFF_V = CODES, OFF_KSF = 2 * CODES, OFF_VSF = 2 * CODES + SF;
+    static constexpr int STAGE = (2 * CODES + 2 * SF + 511) / 512 * 512;
+    static constexpr int BYTES = 2 * CODES + 2 * SF;         // that land per stage
+    static constexpr int OFF_BAR = kWarps * kStages * STAGE;
+    static constexpr int SMEM = OFF_BAR + kWarps * kStages * 8 + 1024;  // with room to align
+};
+
+// Eight e2m1 codes as fp16, pairs in order.
+IDX_DEVI void expand8(uint32_t w, uint32_t (&h)[4]) {
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t"
+        "mov.b32 {a, b, c, d}, %4;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %0, a;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %2, c;\n\t"
+        "cvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+        : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3])
+        : "r"(w));
+}
+IDX_DEVI uint32_t hmul2(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("mul.rn.f16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+// The bits of a where mask is set, those of b elsewhere.
+IDX_DEVI uint32_t pick(uint32_t mask, uint32_t a, uint32_t b) { return (a & mask) | (b & ~mask); }
+
+IDX_DEVI void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// Transposes an 8x8 matrix of 16-bit elements held across the warp.
+IDX_DEVI uint32_t transpose8(uint32_t v) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+    return r;
+}
+template <int N> IDX_DEVI void lds(uint32_t addr, uint32_t (&w)[N]) {
+    if constexpr (N == 1) {
+        asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
+    } else {
+        static_assert(N == 2, "one or two words");
+        asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    }
+}
+IDX_DEVI void tma_rows(uint32_t dst, const void* tmap, uint64_t* bar, int row) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
+        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(0), "r"(row)
+        : "memory");
+}
+IDX_DEVI void bulk_rows(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
+    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
+                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
+                 : "memory");
+}
+// 2^n for any n that a scale can need, as two factors.
+IDX_DEVI float times_pow2(float x, int n) {
+    const int a = n / 2, b = n - a;
+    return x * __int_as_float((a + 127) << 23) * __int_as_float((b + 127) << 23);
+}
+
+// The tokens of a request in this call and the keys that a tile of its rows sees.
+struct Span {
+    int first, count;  // tokens
+    int len;           // cached slots, the new tokens' among them
+};
+IDX_DEVI Span span_of(const WindowArgs& a, int b, bool report) {
+    Span s;
+    int end;
+    if (a.q_start) {
+        s.first = a.q_start[b];
+        end = a.q_start[b + 1];
+    } else {
+        const int per = a.T / a.B;
+        s.first = b * per;
+        end = s.first + per;
+    }
+    s.len = a.lens[b];
+    const bool bad = s.first < 0 || end < s.first || end > a.T || end - s.first > a.max_q || s.len < 0 || s.len > a.max_len;
+    if (bad && report) raise_status(a.d_status, IDX_DEV_RANGE);
+    if (s.first < 0 || end < s.first || end > a.T) {
+        s.first = 0;
+        s.count = 0;
+    } else {
+        s.count = min(end - s.first, a.max_q);
+    }
+    s.len = min(max(s.len, 0), a.max_len);
+    return s;
+}
+
+// A block: 8 NT rows of a request and key head against one split of the keys that they see.  Warps
+// take the split's steps in turn, each with its own softmax state, joined at the end.
+// blockIdx.x: split, row tile, key head; blockIdx.y: request.
+template <typename T, int D, int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
+window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
+              const __grid_constant__ WindowArgs a) {
+    using R = Ring<D>;
+    constexpr int BLOCKS = D / 32;      // of K's and V's scales in a row
+    constexpr int VW = D / 64;          // words of a V row that a lane takes
+    constexpr int TILES = D / 16;       // of O^T: 16 columns of D each
+    constexpr int kRows = 8 * NT;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* smem = smem_raw + (smem0 - smem_u32(smem_raw));
+    pdl_wait();
+    pdl_trigger();
+
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, t = lane & 3;
+    const int split = blockIdx.x % a.splits, tile = blockIdx.x / a.splits % a.row_tiles;
+    const int hk = blockIdx.x / a.splits / a.row_tiles, b = blockIdx.y;
+    const Span sp = span_of(a, b, tid == 0 && blockIdx.x == 0);
+    const int rows = sp.count * a.G, row0 = tile * kRows;
+    if (row0 >= rows) return;
+    // row i of the tile: token, head of the group
+    auto query_row = [&](int i) {
+        const int r = row0 + i, token = r / a.G;
+        return (long long)(sp.first + token) * a.Hq + hk * a.G + (r - token * a.G);
+    };
+    const int pos0 = sp.len - sp.count;  // position of the request's first new token
+    const int low = pos0 + row0 / a.G, high = pos0 + (min(row0 + kRows, rows) - 1) / a.G;
+    const int hi = max(0, min(sp.len, high + 1));
+    // the oldest key inside the first row's window, and how the steps lie: the sinks' and from the window's
+    const int wlo = a.window > 0 ? max(0, low - a.window + 1) : 0;
+    const int sink = min(a.sink, hi);
+    int sink_steps = (sink + kWindowStep - 1) / kWindowStep, from = wlo / kWindowStep;
+    if (from <= sink_steps) sink_steps = from = 0;  // no gap
+    const int total = sink_steps + max(0, (hi + kWindowStep - 1) / kWindowStep - from);
+    const int first = split * a.chunk, end = min(total, first + a.chunk);
+    const int mine = first + warp < end ? (end - 1 - first - warp) / kWarps + 1 : 0;
+    if (first >= end) {
+        for (int i = tid; i < kRows && row0 + i < rows; i += kWarps * 32) {
+            if (a.splits > 1) a.part_lse[query_row(i) * a.splits + split] = -INFINITY;
+        }
+        if (a.splits > 1) return;
+    }
+    auto base_of = [&](int i) {  // first key of the warp's i-th step
+        const int v = first + i * kWarps + warp;
+        return kWindowStep * (v < sink_steps ? v : v - sink_steps + from);
+    };
+
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::OFF_BAR) + warp * kStages;
+    const uint32_t ring = smem0 + warp * kStages * R::STAGE;
+    if (lane < kStages) mbar_init(full + lane, 1);
+    fence_barrier_init();
+    __syncwarp();
+
+    // Pages of the warp's next steps, one 16-key half per lane: 16 steps at a time.  A half that no
+    // row sees is not looked up (its page may be gone): page 0 is read for it, and masked.
+    const int* table = a.table + b * a.table_stride;
+    bool bad = false;
+    int pages_from = 0, page_of = 0;
+    auto look_up = [&](int i) {
+        pages_from = i;
+        const int s = i + (lane >> 1);
+        page_of = 0;
+        if (s < mine) {
+            const int key = base_of(s) + (lane & 1) * 16;
+            if (key < hi && (key < sink || key + 16 > wlo)) {
+                page_of = table[key >> a.page_shift];
+                if (page_of < 0 || page_of >= a.pages) {
+                    page_of = 0;
+                    bad = true;
+                }
+            }
+        }
+    };
+    const bool whole = a.page_size >= kWindowStep;  // a step lies in one page
+    auto fetch = [&](int i) {
+        if (i - pages_from >= 16 || i == 0) look_up(i);
+        const int base = base_of(i);
+        const int p0 = __shfl_sync(~0u, page_of, 2 * (i - pages_from));
+        const int p1 = __shfl_sync(~0u, page_of, 2 * (i - pages_from) + 1);
+        // (a page that only its second half is seen of)
+        const int pages[2] = {whole ? max(p0, p1) : p0, p1};
+        if (lane == 0 && i != a.withhold_step) {
+            uint64_t* bar = full + i % kStages;
+            const uint32_t dst = ring + i % kStages * R::STAGE;
+            const int unit = whole ? kWindowStep : 16;
+            mbar_arrive_expect_tx(bar, R::BYTES);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                if (h == 1 && whole) break;
+                const int row = (pages[h] * a.Hkv + hk) * a.page_size + ((base + 16 * h) & (a.page_size - 1));
+                tma_rows(dst + h * 16 * R::ROW, &tm_k, bar, row);
+                tma_rows(dst + R::OFF_V + h * 16 * R::ROW, &tm_v, bar, row);
+                bulk_rows(dst + R::OFF_KSF + h * 16 * BLOCKS, a.k_sf + (long long)row * BLOCKS, unit * BLOCKS, bar);
+                bulk_rows(dst + R::OFF_VSF + h * 16 * BLOCKS, a.v_sf + (long long)row * BLOCKS, unit * BLOCKS, bar);
+            }
+        }
+        __syncwarp();
+    };
+#pragma unroll
+    for (int i = 0; i < kStages; ++i)
+        if (i < mine) fetch(i);
+
+    // q as the products' second operand: row g of each eight; block b's two steps of 16 columns take
+    // columns 8 t .. 8 t + 7 of it (in the order of a word of codes)
+    uint32_t qf[NT][BLOCKS][4];
+    float zscale[NT][2];   // of this thread's columns of S^T: rows 2 t and 2 t + 1
+    int see[NT][2], wl[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+        const int i = n * 8 + g;
+        const bool live = row0 + i < rows;
+        const long long row = live ? query_row(i) : 0;
+        const T* q = static_cast<const T*>(a.q) + row / a.Hq * a.q_stride + row % a.Hq * D + t * 8;
+        uint4 raw[BLOCKS];
+#pragma unroll
+        for (int k = 0; k < BLOCKS; ++k)
+            raw[k] = live ? *reinterpret_cast<const uint4*>(q + k * 32) : make_uint4(0u, 0u, 0u, 0u);
+        float factor = 1.f;
+        if constexpr (std::is_same<T, __half>::value) {
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k) {
+                qf[n][k][0] = raw[k].x;
+                qf[n][k][1] = raw[k].y;
+                qf[n][k][2] = raw[k].z;
+                qf[n][k][3] = raw[k].w;
+            }
+        } else {
+            uint32_t top = 0;  // the largest magnitude's bits
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k) {
+                const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) top = max(top, max(w[j] << 16 & 0x7fff0000u, w[j] & 0x7fff0000u));
+            }
+            top = max(top, __shfl_xor_sync(~0u, top, 1));
+            top = max(top, __shfl_xor_sync(~0u, top, 2));
+            // 2^up brings it to [2^14, 2^15); rows of tiny numbers (below 2^-100) keep their distance
+            const int ex = (int)(top >> 23);
+            const int up = top == 0 ? 0 : min(127 + 14 - ex, 114);
+            const float f = __int_as_float((up + 127) << 23);
+            // a row that is not finite has no results
+            factor = ex == 255 ? NAN : __int_as_float((127 - up) << 23);
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k) {
+                const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    qf[n][k][j] = pack2<__half>(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+            const int r = row0 + n * 8 + 2 * t + j;
+            // K's powers are taken 1.5 times what they are (see there)
+            zscale[n][j] = __shfl_sync(~0u, factor, (2 * t + j) * 4) * (a.scale_log2 * (2.f / 3.f));
+            const int p = pos0 + r / a.G;
+            see[n][j] = r < rows ? min(p + 1, sp.len) : 0;
+            wl[n][j] = a.window > 0 ? p - a.window + 1 : 0;
+        }
+    }
+    const int all_see = low + 1, all_from = a.window > 0 ? high - a.window + 1 : 0;  // of every row
+
+    // This lane's key of row g of the products, and its keys of V: kv0, + kvd, + 8, + 8 + kvd.  The first
+    // product's transpose hands over the weights of keys key_of(2 t), key_of(2 t + 1).
+    constexpr int kvd = D == 128 ? 2 : 4;
+    const int kg = D == 128 ? (g & 4) | (g & 1) << 1 | (g >> 1 & 1) : (g >> 1) | (g & 1) << 2;
+    const int kv0 = D == 128 ? (t & 1) | (t & 2) << 1 : t;
+    const int vblock = g / (8 / BLOCKS);  // of this lane's columns of V
+    auto k_at = [&](int key, int block) {
+        return key * R::ROW + 16 * (D == 128 ? block ^ (key >> 1 & 3) : block ^ (key >> 2 & 1)) + 4 * t;
+    };
+    auto v_at = [&](int key) {
+        return D == 128 ? key * 64 + 16 * ((g >> 1) ^ (key >> 1 & 3)) + 8 * (g & 1)
+                        : key * 32 + 16 * ((g >> 2) ^ (key >> 2 & 1)) + 4 * (g & 3);
+    };
+
+    float o[NT][TILES][4], m[NT][2], l[NT][2];
+#pragma unroll
+    for (int n = 0; n < NT; ++n) {
+#pragma unroll
+        for (int i = 0; i < TILES; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) o[n][i][j] = 0.f;
+        m[n][0] = m[n][1] = -INFINITY;
+        l[n][0] = l[n][1] = 0.f;
+    }
+    int E = 0;  // o's unit is 2^E (biased as the scales) over 2^13
+    bool ok = true;
+    int i = 0;
+    for (; i < mine; ++i) {
+        ok = __all_sync(~0u, mbar_wait(full + i % kStages, i / kStages & 1, nullptr, a.wait_limit));
+        if (!ok) break;
+        const uint32_t at = ring + i % kStages * R::STAGE;
+        const int base = base_of(i);
+        const bool plain = base + kWindowStep <= all_see && (base >= all_from || base + kWindowStep <= a.sink);
+
+        // ---- S^T of the two halves of 16 keys
+        float s[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            uint32_t sf[2];  // of keys kg and kg + 8
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                if constexpr (BLOCKS == 4) {
+                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sf[k]) : "r"(at + R::OFF_KSF + (h * 16 + kg + 8 * k) * 4));
+                } else {
+                    uint16_t x;
+                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + R::OFF_KSF + (h * 16 + kg + 8 * k) * 2));
+                    sf[k] = x;
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < BLOCKS; ++k) {
+                uint32_t w[2][1], x0[4], x1[4];
+                lds<1>(at + h * 16 * R::ROW + k_at(kg, k), w[0]);
+                lds<1>(at + h * 16 * R::ROW + k_at(kg, k) + 8 * R::ROW, w[1]);
+                expand8(w[0][0], x0);
+                expand8(w[1][0], x1);
+                // 1.5 * 2^(sf - 127): the fraction bit makes a scale of 255 a NaN (0 becomes 2^-127)
+                float f[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    f[j] = __uint_as_float(((k < 3 ? sf[j] << (23 - 8 * k) : sf[j] >> 1) & 0x7f800000u) | 0x00400000u);
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    float c[4] = {0.f, 0.f, 0.f, 0.f};
+                    mma_f16(c, x0[0], x1[0], x0[1], x1[1], qf[n][k][0], qf[n][k][1]);
+                    mma_f16(c, x0[2], x1[2], x0[3], x1[3], qf[n][k][2], qf[n][k][3]);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) s[h][n][j] = k == 0 ? c[j] * f[j >> 1] : fmaf(c[j], f[j >> 1], s[h][n][j]);
+                }
+            }
+        }
+
+        // ---- V's scales: pairs of this lane's keys, and whether E and its band hold them
+        uint32_t vs[2][2];  // [half][keys kv0, kv0 + kvd; then both + 8]
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                uint32_t x[2];
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+                    asm volatile("ld.shared.u8 %0, [%1];"
+                                 : "=r"(x[j])
+                                 : "r"(at + R::OFF_VSF + (h * 16 + kv0 + 8 * k + kvd * j) * BLOCKS + vblock));
+                vs[h][k] = x[0] | x[1] << 16;
+            }
+        uint32_t pending = 0xffu;  // bit 4 h + 2 k + j: a key that a row sees and whose V is still to be added
+        if (!plain) {
+            pending = 0;
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int key = base + (j >> 2) * 16 + (j >> 1 & 1) * 8 + (j & 1) * kvd + kv0;
+                if (key < hi && (key < sink || key >= wlo)) pending |= 1u << j;
+            }
+        }
+        const uint32_t most = __vmaxu2(__vmaxu2(vs[0][0], vs[0][1]), __vmaxu2(vs[1][0], vs[1][1]));
+        const uint32_t least = __vminu2(__vminu2(vs[0][0], vs[0][1]), __vminu2(vs[1][0], vs[1][1]));
+        const bool slow = __any_sync(~0u, !plain || (int)max(most & 0xffffu, most >> 16) > E ||
+                                              (int)min(least & 0xffffu, least >> 16) < E - kBand);
+
+        // ---- softmax
+        uint32_t p[2][NT][2];
+#pragma unroll
+        for (int n = 0; n < NT; ++n) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[h][n][j] *= zscale[n][j & 1];
+            if (slow) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const int in = h * 16 + kg + (j >> 1) * 8, key = base + in;
+                        // a V scale of 255 counts as a NaN logit of the rows that see it
+                        uint32_t x = 0;
+#pragma unroll
+                        for (int k = 0; k < BLOCKS; ++k) {
+                            uint32_t y;
+                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(y) : "r"(at + R::OFF_VSF + in * BLOCKS + k));
+                            x = max(x, y);
+                        }
+                        if (x == 255u) s[h][n][j] = NAN;
+                        if (!(key < see[n][j & 1] && (key < a.sink || key >= wl[n][j & 1]))) s[h][n][j] = -INFINITY;
+                    }
+            }
+            float x0 = fmaxf(fmaxf(s[0][n][0], s[0][n][2]), fmaxf(s[1][n][0], s[1][n][2]));
+            float x1 = fmaxf(fmaxf(s[0][n][1], s[0][n][3]), fmaxf(s[1][n][1], s[1][n][3]));
+            if (__any_sync(~0u, x0 > m[n][0] + kRenew || x1 > m[n][1] + kRenew)) {
+#pragma unroll
+                for (int d = 4; d < 32; d *= 2) {
+                    x0 = fmaxf(x0, __shfl_xor_sync(~0u, x0, d));
+                    x1 = fmaxf(x1, __shfl_xor_sync(~0u, x1, d));
+                }
+                const float n0 = fmaxf(m[n][0], x0), n1 = fmaxf(m[n][1], x1);
+                const float f0 = n0 == -INFINITY ? 1.f : exp2_approx(m[n][0] - n0);
+                const float f1 = n1 == -INFINITY ? 1.f : exp2_approx(m[n][1] - n1);
+                m[n][0] = n0;
+                m[n][1] = n1;
+                l[n][0] *= f0;
+                l[n][1] *= f1;
+#pragma unroll
+                for (int d = 0; d < TILES; ++d) {
+                    o[n][d][0] *= f0;
+                    o[n][d][1] *= f1;
+                    o[n][d][2] *= f0;
+                    o[n][d][3] *= f1;
+                }
+            }
+            // rows that have seen no key yet keep m = -inf: their weights are 0
+            const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kLift;
+            const float b1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kLift;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                s[h][n][0] = exp2_approx(s[h][n][0] - b0);
+                s[h][n][1] = exp2_approx(s[h][n][1] - b1);
+                s[h][n][2] = exp2_approx(s[h][n][2] - b0);
+                s[h][n][3] = exp2_approx(s[h][n][3] - b1);
+                l[n][0] += s[h][n][0] + s[h][n][2];
+                l[n][1] += s[h][n][1] + s[h][n][3];
+                p[h][n][0] = transpose8(pack2<__half>(s[h][n][0], s[h][n][1]));
+                p[h][n][1] = transpose8(pack2<__half>(s[h][n][2], s[h][n][3]));
+            }
+        }
+
+        // ---- O^T += V^T P^T, V's codes times 2^(field - 15) of each pair of keys; in steps that are not plain
+        // the sums come in units of their own, `unit` of o's
+        auto add_v = [&](const uint32_t (&sc)[2][2], auto direct, float unit) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[4][VW];  // keys kv0, kv0 + kvd, and both + 8
+#pragma unroll
+                for (int k = 0; k < 4; ++k)
+                    lds<VW>(at + R::OFF_V + h * 16 * R::ROW + v_at(kv0 + (k & 1) * kvd + (k >> 1) * 8), w[k]);
+#pragma unroll
+                for (int v = 0; v < VW; ++v) {
+                    // nibbles of two keys side by side: even and odd columns
+                    uint32_t x[2][2][4];
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const uint32_t lo = w[2 * k][v], up = w[2 * k + 1][v];
+                        expand8(pick(0x0f0f0f0fu, lo, up << 4), x[k][0]);
+                        expand8(pick(0x0f0f0f0fu, lo >> 4, up), x[k][1]);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            x[k][0][j] = hmul2(x[k][0][j], sc[h][k]);
+                            x[k][1][j] = hmul2(x[k][1][j], sc[h][k]);
+                        }
+                    }
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            float(&to)[4] = o[n][v * 4 + j];
+                            if constexpr (decltype(direct)::value) {
+                                mma_f16(to, x[0][0][j], x[0][1][j], x[1][0][j], x[1][1][j], p[h][n][0], p[h][n][1]);
+                            } else {
+                                float c[4] = {0.f, 0.f, 0.f, 0.f};
+                                mma_f16(c, x[0][0][j], x[0][1][j], x[1][0][j], x[1][1][j], p[h][n][0], p[h][n][1]);
+#pragma unroll
+                                for (int y = 0; y < 4; ++y) to[y] = fmaf(c[y], unit, to[y]);
+                            }
+                        }
+                }
+            }
+        };
+        uint32_t sc[2][2];
+        if (!slow) {
+            const uint32_t c = (uint32_t)(kTopField - E) * 0x10001u;
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) sc[h][k] = (vs[h][k] + c) << 10;
+            add_v(sc, std::true_type{}, 1.f);
+        } else {
+            do {
+                // the largest scale still to be taken, of the block's four lanes
+                int top = 0;
+#pragma unroll
+                for (int j = 0; j < 8; ++j) {
+                    const int x = (int)(vs[j >> 2][j >> 1 & 1] >> (16 * (j & 1)) & 0xffu);
+                    if (x == 255) pending &= ~(1u << j);  // its rows are NaN already
+                    if (pending >> j & 1) top = max(top, x);
+                }
+                top = max(top, __shfl_xor_sync(~0u, top, 1));
+                top = max(top, __shfl_xor_sync(~0u, top, 2));
+                if (top > E) {
+                    const int to = min(top + kMargin, 254);
+                    const float f = times_pow2(1.f, max(E - to, -250));
+#pragma unroll
+                    for (int n = 0; n < NT; ++n)
+#pragma unroll
+                        for (int d = 0; d < TILES; ++d)
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) o[n][d][j] *= f;
+                    E = to;
+                }
+                const int Eb = top < E - kBand / 2 ? top : E;  // this pass's unit
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        uint32_t both = 0;
+#pragma unroll
+                        for (int j = 0; j < 2; ++j) {
+                            const int bit = 4 * h + 2 * k + j, x = (int)(vs[h][k] >> (16 * j) & 0xffu);
+                            const bool in = pending >> bit & 1 && x >= Eb - kBand;
+                            if (in) both |= (uint32_t)(x - Eb + kTopField) << (10 + 16 * j);
+                            if (in) pending &= ~(1u << bit);
+                        }
+                        sc[h][k] = both;
+                    }
+                add_v(sc, std::false_type{}, times_pow2(1.f, max(Eb - E, -250)));
+            } while (__any_sync(~0u, pending != 0));
+        }
+        __syncwarp();  // the stage has been read
+        if (i + kStages < mine) fetch(i + kStages);
+    }
+    if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
+    if (!ok) {
+        if (lane == 0) raise_status(a.d_status, IDX_DEV_TIMEOUT);
+        // nothing may be in flight when the block ends
+        for (const int sent = min(mine, i + kStages); i < sent; ++i)
+            if (i != a.withhold_step) mbar_wait(full + i % kStages, i / kStages & 1, nullptr, 1ll << 28);
+    }
+
+    // ---- join the warps' states through shared memory
+    __syncthreads();
+    constexpr int kPitch = D + 4;
+    float* so = reinterpret_cast<float*>(smem);       // [warps][rows][kPitch]
+    float* sm = so + kWarps * kRows * kPitch;         // [warps][rows] maxima, then sums
+    float* sl = sm + kWarps * kRows;
+    static_assert(kWarps * kRows * (kPitch + 2) * 4 <= R::OFF_BAR, "");
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int d = 4; d < 32; d *= 2) l[n][j] += __shfl_xor_sync(~0u, l[n][j], d);
+            const int r = warp * kRows + n * 8 + 2 * t + j;
+            // (means, not sums: the largest values of V times the weights' lift would leave fp32)
+            const float inv = l[n][j] == 0.f ? 0.f : 1.f / l[n][j];
+#pragma unroll
+            for (int d = 0; d < TILES; ++d) {
+                // codes * 2^(sf - E + 13) summed, times 2^(E - 127 - 13)
+                so[r * kPitch + g * (2 * TILES) + 2 * d] = times_pow2(o[n][d][j] * inv, E - 140);
+                so[r * kPitch + g * (2 * TILES) + 2 * d + 1] = times_pow2(o[n][d][j + 2] * inv, E - 140);
+            }
+            if (g == 0) {
+                sm[r] = m[n][j] - kLift;
+                sl[r] = l[n][j];
+            }
+        }
+    __syncthreads();
+    for (int x = tid; x < kRows * (D / 4); x += kWarps * 32) {
+        const int r = x / (D / 4), d = x % (D / 4) * 4;
+        if (row0 + r >= rows) break;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm[w * kRows + r]);
+        const float from_top = top == -INFINITY ? 0.f : top;
+        float share[kWarps], sum = 0.f;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) sum += share[w] = exp2_approx(sm[w * kRows + r] - from_top) * sl[w * kRows + r];
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays one
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            const float f = share[w] * inv;
+            const float4 v = *reinterpret_cast<const float4*>(so + (w * kRows + r) * kPitch + d);
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+        }
+        const float lse = sum == 0.f ? -INFINITY : top + log2f(sum);
+        const long long row = query_row(r);
+        if (a.splits > 1) {
+            const long long to = row * a.splits + split;
+            *reinterpret_cast<float4*>(a.part + to * D + d) = acc;
+            if (d == 0) a.part_lse[to] = lse;
+        } else {
+            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + d) =
+                make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
+            if (d == 0 && a.lse) a.lse[row] = lse * 0.6931471805599453f;
+        }
+    }
+}
+
+// Joins a row's splits: a warp per row, lane l holds D / 32 columns.
+constexpr int kJoinThreads = 128;
+
+template <typename T, int D>
+__global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_constant__ WindowArgs a) {
+    constexpr int W = D / 32, kBatch = 8;
+    pdl_wait();
+    const int lane = threadIdx.x & 31;
+    const long long row = (long long)blockIdx.x * (kJoinThreads / 32) + threadIdx.x / 32;
+    // tokens behind the last request's are not touched
+    const long long from = a.q_start ? a.q_start[0] : 0, to = a.q_start ? a.q_start[a.B] : a.T;
+    if (row >= min(to, (long long)a.T) * a.Hq || row < from * a.Hq) return;
+    const float* pl = a.part_lse + row * a.splits;
+    float m = -INFINITY;
+    for (int i = lane; i < a.splits; i += 32) m = max_nan(m, pl[i]);
+#pragma unroll
+    for (int d = 16; d > 0; d /= 2) m = max_nan(m, __shfl_xor_sync(~0u, m, d));
+    float acc[W], lse = -INFINITY;
+#pragma unroll
+    for (int i = 0; i < W; ++i) acc[i] = 0.f;
+    if (m != -INFINITY) {
+        float l = 0.f;
+        for (int i = lane; i < a.splits; i += 32) l += exp2_approx(pl[i] - m);
+#pragma unroll
+        for (int d = 16; d > 0; d /= 2) l += __shfl_xor_sync(~0u, l, d);
+        lse = m + log2f(l);
+        const float* part = a.part + row * a.splits * D + lane * W;
+        // kBatch parts at a time, their loads before the first use; one without keys is not read
+        for (int p = 0; p < a.splits; p += kBatch) {
+            float f[kBatch], v[kBatch][W];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) f[k] = p + k < a.splits ? pl[p + k] : -INFINITY;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int i = 0; i < W; ++i) v[k][i] = f[k] != -INFINITY ? part[(long long)(p + k) * D + i] : 0.f;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k)
+#pragma unroll
+                for (int i = 0; i < W; ++i) acc[i] = fmaf(exp2_approx(f[k] - lse), v[k][i], acc[i]);
+        }
+    }
+    uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<T*>(a.out) + row * D) + lane * (W / 2);
+#pragma unroll
+    for (int i = 0; i < W / 2; ++i) out[i] = pack2<T>(acc[2 * i], acc[2 * i + 1]);
+    if (a.lse && lane == 0) a.lse[row] = lse * 0.6931471805599453f;
+}
+
+// Map of rows of codes (D / 2 bytes), `unit` rows per copy, their 16-byte chunks swizzled.
+CUresult code_map(CUtensorMap* m, const uint8_t* base, int D, long long rows, int unit) {
+    auto enc = tensor_map_encoder();
+    if (!enc) return CUDA_ERROR_NOT_SUPPORTED;
+    const cuuint64_t dims[2] = {(cuuint64_t)D / 2, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)D / 2};
+    const cuuint32_t box[2] = {(cuuint32_t)D / 2, (cuuint32_t)unit}, one[2] = {1, 1};
+    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, one,
+               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
+               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+}
+
+template <typename T, int D, int NT> cudaError_t launch_rows(const WindowArgs& a, cudaStream_t s) {
+    const int unit = a.page_size >= kWindowStep ? kWindowStep : 16;
+    const long long rows = (long long)a.pages * a.Hkv * a.page_size;
+    CUtensorMap k, v;
+    if (code_map(&k, a.k_codes, D, rows, unit) != CUDA_SUCCESS || code_map(&v, a.v_codes, D, rows, unit) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
+    static PerDevice ready;
+    const cudaError_t e = allow_smem(ready, window_kernel<T, D, NT>, Ring<D>::SMEM);
+    if (e != cudaSuccess) return e;
+    return launch_k(window_kernel<T, D, NT>, dim3((unsigned)(a.splits * a.row_tiles * a.Hkv), (unsigned)a.B),
+                    dim3(kWarps * 32), Ring<D>::SMEM, s, true, k, v, a);
+}
+
+template <typename T, int D>
+cudaError_t launch_typed(const WindowArgs& a, const WindowPlan& p, cudaStream_t s, int* launched) {
+    cudaError_t e = p.tile_rows == 8 ? launch_rows<T, D, 1>(a, s) : launch_rows<T, D, 2>(a, s);
+    if (e != cudaSuccess) return e;
+    ++*launched;
+    if (a.splits == 1) return e;
+    const long long rows = (long long)a.T * a.Hq, per = kJoinThreads / 32;
+    e = launch_k(window_join_kernel<T, D>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), 0, s, true, a);
+    if (e == cudaSuccess) ++*launched;
+    return e;
+}
+
+}  // namespace
+
+// Row splits (a row's results of one split: D + 1 floats of workspace) that a plan may take: 34 MB at D =
+// 128.  The plan chooses within this and the workspace is sized by it, so that the size grows with the
+// rows and the lengths, as the choice itself does not.
+constexpr size_t kRowSplits = 65536;
+constexpr int kMostSplits = 64;
+
+WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window, int sink,
+                       int sm_count) {
+    WindowPlan p;
+    const int G = Hq / Hkv;
+    const long long most_rows = (long long)max_q * G;
+    p.tile_rows = most_rows <= 8 ? 8 : 16;
+    p.row_tiles = (int)((most_rows + p.tile_rows - 1) / p.tile_rows);
+    // steps of the tile that sees the most
+    const long long tokens = std::min<long long>(max_q, (p.tile_rows + G - 1) / G + 1);
+    long long keys = max_len;
+    if (window > 0) keys = std::min<long long>(max_len, (long long)window + tokens + sink + 4 * kWindowStep);
+    const int steps = (int)std::max<long long>(1, (keys + kWindowStep - 1) / kWindowStep);
+    const double items = (double)B * Hkv * p.row_tiles / (4.0 * sm_count);
+    // A block takes about 4 us and 18 ns per step of 32 keys and warp among four on an SM; whole waves of
+    // long splits are cheap, one that is mostly empty is not.  Lengths are on the device: the mean of the
+    // times with all of them at max_len and at half of it is taken.
+    const double join_us = (double)T * Hq * D * 8 / 5e6;
+    const int units = (steps + kWarps - 1) / kWarps;  // a step for every warp
+    const size_t rows = (size_t)T * Hq, most = std::min<size_t>(rows * std::min(kMostSplits, units), kRowSplits);
+    double best = 0;
+    p.splits = 1;
+    p.chunk = units * kWarps;
+    for (int s = 1; s <= kMostSplits && s <= units; s += s < 8 ? 1 : s / 4) {
+        const int t = (units + s - 1) / s, all = (units + t - 1) / t, half = (units / 2 + t) / t;
+        if (all > 1 && all * rows > most) break;
+        const double us = (std::ceil(items * all) + std::ceil(items * half)) / 2 * (t * 0.35 + 3.0) +
+                          (all > 1 ? all * join_us + 2.0 : 0.0);
+        if (best == 0 || us < best) {
+            best = us;
+            p.splits = all;
+            p.chunk = t * kWarps;
+        }
+    }
+    auto up = [](size_t b) { return (b + 255) / 256 * 256; };
+    const size_t parts = units > 1 ? most : 0;
+    p.part = 0;
+    p.part_lse = up(parts * D * sizeof(float));
+    p.total = p.part_lse + up(parts * sizeof(float));
+    return p;
+}
+
+cudaError_t launch_window(const WindowArgs& a, const WindowPlan& p, idx_dtype dt, int, cudaStream_t s, int* launched) {
+    if (dt == IDX_BF16)
+        return a.D == 128 ? launch_typed<__nv_bfloat16, 128>(a, p, s, launched)
+                          : launch_typed<__nv_bfloat16, 64>(a, p, s, launched);
+    return a.D == 128 ? launch_typed<__half, 128>(a, p, s, launched) : launch_typed<__half, 64>(a, p, s, launched);
+}
+
+}  // namespace idx

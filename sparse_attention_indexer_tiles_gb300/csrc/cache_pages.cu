@@ -1,0 +1,534 @@
+// Pages of a cache: rows of a page table that take over one another's pages (fork), give pages back and
+// take free ones (resize), and a pool whose live pages move together (compact).
+//
+// refs[p] counts the table entries that hold page p; a page is free when it is 0 (or less).  Free pages
+// are taken lowest first and rows are served in their order, so that the result of a call does not
+// depend on how its threads run: what is added up atomically are whole numbers, and pages are ranked by
+// counting them.  A fork only counts; the copy of a page that several rows hold and that one of them is
+// about to write to is made by the resize that lets it grow.
+//
+// resize and compact are two launches: one cluster of CTAs ranks rows and pages (its barriers are far
+// cheaper than launches, and the counts of a million pages are 4 MB), then the whole GPU copies pages
+// and writes the tables.
+#include <cooperative_groups.h>
+
+#include <algorithm>
+
+#include "cache_pages.cuh"
+#include "serve.cuh"
+
+namespace cg = cooperative_groups;
+
+namespace idx {
+
+namespace {
+
+constexpr int kThreads = 1024, kWarps = kThreads / 32;
+constexpr int kCopyThreads = 256;
+constexpr int kCluster = 8;                 // the portable limit
+constexpr int kUnit = kCopyThreads * 16 * 4;  // bytes of a page that a block copies at a time
+
+IDX_DEVI int warp_sum(int v) { return __reduce_add_sync(~0u, v); }
+// Inclusive sum over the lanes of a warp.
+IDX_DEVI int warp_scan(int v, int lane) {
+#pragma unroll
+    for (int o = 1; o < 32; o *= 2) {
+        const int u = __shfl_up_sync(~0u, v, o);
+        if (lane >= o) v += u;
+    }
+    return v;
+}
+
+// A row's length, 0 when it is outside [0, table_stride * page_size].
+IDX_DEVI bool len_ok(const PagesArgs& a, int n) { return n >= 0 && n <= a.table_stride << a.page_shift; }
+IDX_DEVI int pages_of(const PagesArgs& a, int n) { return (int)(((long long)n + a.page_size - 1) >> a.page_shift); }
+IDX_DEVI bool page_ok(const PagesArgs& a, int p) { return p >= 0 && p < a.pages; }
+
+// ---------------------------------------------------------------------- fork
+
+// The workspace of a call in place: the rows' lengths, then their pages, as they were.
+IDX_DEVI int* staged_lens(const PagesArgs& a) { return a.ws; }
+IDX_DEVI int* staged_table(const PagesArgs& a) { return a.ws + (a.B + 3) / 4 * 4; }
+
+// The counts, and in place what the rows hold before any is written.
+__global__ void __launch_bounds__(256) fork_stage_kernel(const __grid_constant__ PagesArgs a) {
+    pdl_wait();
+    const long long step = (long long)gridDim.x * 256, at = (long long)blockIdx.x * 256 + threadIdx.x;
+    if (a.refs_out != a.refs)
+        for (long long i = at; i < a.pages; i += step) a.refs_out[i] = a.refs[i];
+    if (a.ws) {
+        const int lane = threadIdx.x & 31;
+        for (long long i = at >> 5; i < a.B; i += step >> 5) {
+            const int n = a.lens[i];
+            if (lane == 0) staged_lens(a)[i] = n;
+            const int used = len_ok(a, n) ? pages_of(a, n) : 0;
+            for (int j = lane; j < used; j += 32)
+                staged_table(a)[i * a.table_stride + j] = a.table[i * a.table_stride + j];
+        }
+    }
+}
+
+// A block per row: counts off the row's own pages, counts on its parent's, and takes them over.
+__global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ PagesArgs a) {
+    pdl_wait();
+    const int i = blockIdx.x;
+    const int* const lens = a.ws ? staged_lens(a) : a.lens;
+    const int* const table = a.ws ? staged_table(a) : a.table;
+    int parent = a.arg[i], n0 = lens[i];
+    bool bad = !len_ok(a, n0);
+    if (bad) n0 = 0;
+    if (parent < -1 || parent >= a.B) {
+        bad = true;
+        parent = i;
+    }
+    int n1 = parent < 0 ? 0 : lens[parent];
+    if (!len_ok(a, n1)) n1 = 0;
+    const int own = pages_of(a, n0), use = pages_of(a, n1);
+    const int* const mine = table + i * a.table_stride;
+    const int* const from = table + max(parent, 0) * a.table_stride;
+    int* const out = a.table_out + i * a.table_stride;
+    for (int j = threadIdx.x; j < max(own, use); j += 256) {
+        const int p0 = j < own ? mine[j] : -1, p1 = j < use ? from[j] : -1;
+        bad |= (j < own && !page_ok(a, p0)) || (j < use && !page_ok(a, p1));
+        if (p0 != p1) {
+            if (page_ok(a, p0)) atomicSub(a.refs_out + p0, 1);
+            if (page_ok(a, p1)) atomicAdd(a.refs_out + p1, 1);
+        }
+        if (j < use) out[j] = p1;
+    }
+    if (threadIdx.x == 0) a.lens_out[i] = n1;
+    if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
+}
+
+// --------------------------------------------------------- ranking by a cluster
+
+// What a CTA has counted of its pages, of two kinds.
+struct Counts {
+    int before[kWarps][2];  // in the warps before one
+    int total[2];
+};
+
+// The CTAs of a ranking: kCluster of them, or one.
+template <bool CLUSTER> struct Team {
+    static constexpr int CTAS = CLUSTER ? kCluster : 1;
+    int rank;
+    IDX_DEVI Team() : rank(0) {
+        if constexpr (CLUSTER) rank = (int)cg::this_cluster().block_rank();
+    }
+    // Everything written before is visible after (to loads past L1).
+    IDX_DEVI void sync() const {
+        __threadfence();
+        if constexpr (CLUSTER)
+            cg::this_cluster().sync();
+        else
+            __syncthreads();
+    }
+    template <typename S> IDX_DEVI const S& of(S& mine, int r) const {
+        if constexpr (CLUSTER) return *cg::this_cluster().map_shared_rank(&mine, r);
+        return mine;
+    }
+};
+
+// Pages [first, end) of a warp: contiguous ranges in the order of CTAs and warps, whole groups of 32.
+struct Range {
+    int first, end;
+};
+template <bool CLUSTER> IDX_DEVI Range warp_pages(const Team<CLUSTER>& team, int pages, int warp) {
+    const long long groups = ((long long)pages + 31) / 32, of = Team<CLUSTER>::CTAS * kWarps;
+    const long long per = (groups + of - 1) / of * 32, first = (team.rank * kWarps + warp) * per;
+    return {(int)min(first, (long long)pages), (int)min(first + per, (long long)pages)};
+}
+
+// Counts the pages of the CTA for which f gives bit 0, and bit 1; published by the next team.sync().
+template <typename F> IDX_DEVI void count_pages(Counts& sh, Range r, int warp, int lane, F f) {
+    int c0 = 0, c1 = 0;
+#pragma unroll 8
+    for (int p = r.first + lane; p < r.end; p += 32) {
+        const int x = f(p);
+        c0 += x & 1;
+        c1 += x >> 1;
+    }
+    c0 = warp_sum(c0);
+    c1 = warp_sum(c1);
+    if (lane == 0) {
+        sh.before[warp][0] = c0;
+        sh.before[warp][1] = c1;
+    }
+    __syncthreads();
+    if (warp == 0) {
+        const int s0 = sh.before[lane][0], s1 = sh.before[lane][1];
+        const int i0 = warp_scan(s0, lane), i1 = warp_scan(s1, lane);
+        sh.before[lane][0] = i0 - s0;
+        sh.before[lane][1] = i1 - s1;
+        if (lane == 31) {
+            sh.total[0] = i0;
+            sh.total[1] = i1;
+        }
+    }
+}
+// What the CTAs before this one counted, and all of them.
+template <bool CLUSTER> IDX_DEVI void totals(const Team<CLUSTER>& team, Counts& sh, int (&before)[2], int (&all)[2]) {
+    before[0] = before[1] = all[0] = all[1] = 0;
+#pragma unroll
+    for (int r = 0; r < Team<CLUSTER>::CTAS; ++r)
+#pragma unroll
+        for (int k = 0; k < 2; ++k) {
+            const int n = team.of(sh, r).total[k];
+            if (r < team.rank) before[k] += n;
+            all[k] += n;
+        }
+}
+
+// -------------------------------------------------------------------- resize
+
+// Workspace: a record per row, the rows that copy a page (their number first), and the pages that rows
+// take, by rank.
+struct Row {
+    int old_len, new_len;  // new_len as served
+    int rank;              // of its first page
+    int from;              // the page that it copies, or -1
+};
+IDX_DEVI Row* row_records(const PagesArgs& a) { return reinterpret_cast<Row*>(a.ws); }
+IDX_DEVI int* copy_rows(const PagesArgs& a) { return a.ws + 4ll * a.B; }
+IDX_DEVI int* taken_pages(const PagesArgs& a) { return a.ws + 5ll * a.B + 1; }
+
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kThreads) resize_rank_kernel(const __grid_constant__ PagesArgs a) {
+    __shared__ Counts sh;
+    __shared__ int served, copies;  // CTA 0's: pages that rows take, rows that copy
+    const Team<CLUSTER> team;
+    constexpr int kAll = Team<CLUSTER>::CTAS * kThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, at = team.rank * kThreads + tid;
+    if (tid == 0) served = copies = 0;
+    pdl_wait();
+    pdl_trigger();
+    const Range r = warp_pages(team, a.pages, warp);
+    if (a.refs_out != a.refs) {
+#pragma unroll 8
+        for (int p = r.first + lane; p < r.end; p += 32) a.refs_out[p] = a.refs[p];
+        team.sync();
+    }
+    // rows that shrink give pages back
+    bool bad = false;
+    for (int i = at >> 5; i < a.B; i += kAll / 32) {
+        const int n0 = a.lens[i], n1 = a.arg[i];
+        if (!len_ok(a, n0) || !len_ok(a, n1) || n1 >= n0) continue;
+        for (int j = pages_of(a, n1) + lane; j < pages_of(a, n0); j += 32) {
+            const int p = a.table[i * a.table_stride + j];
+            if (page_ok(a, p))
+                atomicSub(a.refs_out + p, 1);
+            else
+                bad = true;
+        }
+    }
+    team.sync();
+    // what rows that grow copy, and which pages are free
+    Row* const rows = row_records(a);
+    for (int i = at; i < a.B; i += kAll) {
+        Row row = {a.lens[i], a.arg[i], 0, -1};
+        if (!len_ok(a, row.old_len) || !len_ok(a, row.new_len)) {
+            bad = true;
+            row.new_len = row.old_len;  // left as it is
+        } else if (row.new_len > row.old_len && (row.old_len & (a.page_size - 1))) {
+            const int p = a.table[i * a.table_stride + (row.old_len >> a.page_shift)];
+            if (!page_ok(a, p))
+                bad = true;
+            else if (__ldcg(a.refs_out + p) > 1)
+                row.from = p;
+        }
+        rows[i] = row;
+    }
+    if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
+    count_pages(sh, r, warp, lane, [&](int p) { return __ldcg(a.refs_out + p) <= 0 ? 1 : 0; });
+    team.sync();
+    int before[2], all[2];
+    totals(team, sh, before, all);
+    if (team.rank == 0) {
+        // rows in their order, until the free pages do not suffice for one
+        __shared__ long long part[kWarps];
+        __shared__ int part_copies[kWarps];
+        long long taken = 0;  // by the rows before these, served or not
+        int copied = 0;
+        for (int i0 = 0; i0 < a.B; i0 += kThreads) {
+            const int i = i0 + tid;
+            Row row = {0, 0, 0, -1};
+            if (i < a.B) {
+                const int4 x = __ldcg(reinterpret_cast<const int4*>(rows + i));
+                row = {x.x, x.y, x.z, x.w};
+            }
+            const bool copy = row.from >= 0;
+            const int want =
+                row.new_len > row.old_len ? pages_of(a, row.new_len) - pages_of(a, row.old_len) + copy : 0;
+            long long upto = want;
+#pragma unroll
+            for (int o = 1; o < 32; o *= 2) {
+                const long long u = __shfl_up_sync(~0u, upto, o);
+                if (lane >= o) upto += u;
+            }
+            const unsigned copying = __ballot_sync(~0u, copy);
+            int nth = copied + __popc(copying & ((1u << lane) - 1));
+            if (lane == 31) {
+                part[warp] = upto;
+                part_copies[warp] = __popc(copying);
+            }
+            __syncthreads();
+            upto += taken;
+            for (int w = 0; w < kWarps; ++w) {
+                if (w < warp) {
+                    upto += part[w];
+                    nth += part_copies[w];
+                }
+                taken += part[w];
+                copied += part_copies[w];
+            }
+            // (what is served of the rows that want pages comes before all that is not)
+            const bool ok = want == 0 || upto <= all[0];
+            if (i < a.B) {
+                if (!ok) {
+                    row.new_len = row.old_len;
+                    row.from = -1;
+                    raise_status(a.d_status, IDX_DEV_PAGES);
+                } else if (want > 0) {
+                    row.rank = (int)(upto - want);
+                    if (copy) {
+                        copy_rows(a)[nth + 1] = i;
+                        atomicMax(&copies, nth + 1);
+                    }
+                    atomicMax(&served, (int)upto);
+                }
+                rows[i] = row;
+                a.lens_out[i] = row.new_len;
+            }
+            __syncthreads();
+        }
+        if (tid == 0) copy_rows(a)[0] = copies;
+    }
+    team.sync();
+    // the free pages by rank, as many as rows take
+    const int most = team.of(served, 0);
+    int rank = before[0] + sh.before[warp][0];
+    for (int p0 = r.first; p0 < r.end && rank < most; p0 += 32) {
+        const int p = p0 + lane;
+        const bool is_free = p < r.end && __ldcg(a.refs_out + p) <= 0;
+        const unsigned m = __ballot_sync(~0u, is_free);
+        const int k = rank + __popc(m & ((1u << lane) - 1));
+        if (is_free && k < most) {
+            taken_pages(a)[k] = p;
+            a.refs_out[p] = 1;
+        }
+        rank += __popc(m);
+    }
+    if constexpr (CLUSTER) team.sync();  // no CTA leaves while another reads its counts
+}
+
+// Copies pages pair(k) = (from, to) for k < n, a unit of one of them per block at a time.
+template <typename F> IDX_DEVI void copy_pages(const PageArrays& c, int n, F pair) {
+    long long units = 0;  // of one pair
+    for (int x = 0; x < c.n; ++x) units += (c.bytes[x] + kUnit - 1) / kUnit;
+    for (long long u = blockIdx.x; u < n * units; u += gridDim.x) {
+        const int k = (int)(u / units);
+        long long at = u - k * units;
+        int x = 0;
+        for (; x < c.n - 1; ++x) {
+            const long long of = (c.bytes[x] + kUnit - 1) / kUnit;
+            if (at < of) break;
+            at -= of;
+        }
+        const int2 p = pair(k);
+        const long long bytes = c.bytes[x], first = at * kUnit + threadIdx.x * 16;
+        const uint8_t* from = c.p[x] + p.x * bytes;
+        uint8_t* to = c.p[x] + p.y * bytes;
+        uint4 v[kUnit / (kCopyThreads * 16)];
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (first + j * (kCopyThreads * 16) < bytes)
+                v[j] = *reinterpret_cast<const uint4*>(from + first + j * (kCopyThreads * 16));
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+            if (first + j * (kCopyThreads * 16) < bytes)
+                *reinterpret_cast<uint4*>(to + first + j * (kCopyThreads * 16)) = v[j];
+    }
+}
+
+__global__ void __launch_bounds__(kCopyThreads) resize_move_kernel(const __grid_constant__ PagesArgs a) {
+    pdl_wait();
+    const Row* const rows = row_records(a);
+    const int* const taken = taken_pages(a);
+    const int lane = threadIdx.x & 31;
+    const long long step = (long long)gridDim.x * (kCopyThreads / 32);
+    for (long long i = ((long long)blockIdx.x * kCopyThreads + threadIdx.x) >> 5; i < a.B; i += step) {
+        const Row row = rows[i];
+        if (!len_ok(a, row.old_len)) continue;
+        const int* in = a.table + i * a.table_stride;
+        int* out = a.table_out + i * a.table_stride;
+        const int had = pages_of(a, row.old_len), has = pages_of(a, row.new_len);
+        const bool copy = row.from >= 0 && row.new_len > row.old_len;
+        const int kept = min(had - copy, has);
+        if (out != in)
+            for (int j = lane; j < kept; j += 32) out[j] = in[j];
+        for (int j = kept + lane; j < has; j += 32) out[j] = taken[row.rank + j - kept];
+        if (copy && lane == 0) atomicSub(a.refs_out + row.from, 1);
+    }
+    const int* const list = copy_rows(a);
+    copy_pages(a.caches, list[0], [&](int k) {
+        const Row row = rows[list[k + 1]];
+        return make_int2(row.from, taken[row.rank]);
+    });
+}
+
+// ------------------------------------------------------------------- compact
+
+// Workspace: the number of moves and of live pages; the pages to fill and the pages that move, by rank;
+// where a page from the live count on goes.
+IDX_DEVI int* holes_of(const PagesArgs& a) { return a.ws + 4; }
+IDX_DEVI int* movers_of(const PagesArgs& a) { return a.ws + 4 + (a.pages / 2 + 1); }
+IDX_DEVI int* moved_to(const PagesArgs& a) { return a.ws + 4 + 2ll * (a.pages / 2 + 1); }
+
+template <bool CLUSTER>
+__global__ void __launch_bounds__(kThreads) compact_rank_kernel(const __grid_constant__ PagesArgs a) {
+    __shared__ Counts sh[2];
+    const Team<CLUSTER> team;
+    constexpr int kAll = Team<CLUSTER>::CTAS * kThreads;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, at = team.rank * kThreads + tid;
+    pdl_wait();
+    pdl_trigger();
+    const Range r = warp_pages(team, a.pages, warp);
+    int before[2], all[2];
+    count_pages(sh[0], r, warp, lane, [&](int p) { return a.refs[p] > 0 ? 1 : 0; });
+    team.sync();
+    totals(team, sh[0], before, all);
+    const int live = all[0];
+    count_pages(sh[1], r, warp, lane, [&](int p) {
+        const bool used = a.refs[p] > 0;
+        return p < live ? !used : 2 * used;
+    });
+    team.sync();
+    totals(team, sh[1], before, all);
+    const int moves = all[0];  // as many holes below the live count as live pages from it on
+    int nth[2] = {before[0] + sh[1].before[warp][0], before[1] + sh[1].before[warp][1]};
+    for (int p0 = r.first; p0 < r.end; p0 += 32) {
+        const int p = p0 + lane, n = p < r.end ? a.refs[p] : 0;
+        const bool hole = p < r.end && p < live && n <= 0, mover = p >= live && n > 0;
+        const unsigned holes = __ballot_sync(~0u, hole), movers = __ballot_sync(~0u, mover), under = (1u << lane) - 1;
+        if (hole) holes_of(a)[nth[0] + __popc(holes & under)] = p;
+        if (mover) movers_of(a)[nth[1] + __popc(movers & under)] = p;
+        if (p < r.end && !hole && !mover) {
+            if (p >= live) {
+                moved_to(a)[p] = p;
+                a.refs_out[p] = 0;
+            } else if (a.refs_out != a.refs) {
+                a.refs_out[p] = n;
+            }
+        }
+        nth[0] += __popc(holes);
+        nth[1] += __popc(movers);
+    }
+    team.sync();
+    for (int k = at; k < moves; k += kAll) {
+        const int to = __ldcg(holes_of(a) + k), from = __ldcg(movers_of(a) + k);
+        moved_to(a)[from] = to;
+        const int n = a.refs[from];
+        a.refs_out[to] = n;
+        a.refs_out[from] = 0;
+    }
+    if (at == 0) {
+        a.ws[0] = moves;
+        a.ws[1] = live;
+        *a.live = live;
+    }
+    if constexpr (CLUSTER) team.sync();  // no CTA leaves while another reads its counts
+}
+
+__global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const __grid_constant__ PagesArgs a) {
+    pdl_wait();
+    const int moves = a.ws[0], live = a.ws[1];
+    const int lane = threadIdx.x & 31;
+    const long long step = (long long)gridDim.x * (kCopyThreads / 32);
+    bool bad = false;
+    for (long long i = ((long long)blockIdx.x * kCopyThreads + threadIdx.x) >> 5; i < a.B; i += step) {
+        const int n = a.lens[i];
+        if (!len_ok(a, n)) {
+            bad = true;
+            continue;
+        }
+        const int* in = a.table + i * a.table_stride;
+        int* out = a.table_out + i * a.table_stride;
+        for (int j = lane; j < pages_of(a, n); j += 32) {
+            const int p = in[j];
+            if (!page_ok(a, p)) bad = true;
+            const int to = page_ok(a, p) && p >= live ? moved_to(a)[p] : p;
+            if (out != in || to != p) out[j] = to;
+        }
+    }
+    if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
+    copy_pages(a.caches, moves, [&](int k) { return make_int2(movers_of(a)[k], holes_of(a)[k]); });
+}
+
+// A ranking kernel: a cluster when its pages or rows are many (see kClusterFrom), one CTA otherwise.
+constexpr int kClusterFrom = 16384;
+
+cudaError_t launch_rank(void (*one)(PagesArgs), void (*many)(PagesArgs), const PagesArgs& a, cudaStream_t s) {
+    const bool cluster = a.pages >= kClusterFrom || a.B * 16ll >= kClusterFrom;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(cluster ? kCluster : 1);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = kCluster;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = cluster ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, cluster ? many : one, a);
+}
+
+// Blocks of a moving kernel: what is to be copied is known on the device only; a few waves.
+unsigned move_blocks(int sm_count) { return (unsigned)sm_count * 8; }
+
+}  // namespace
+
+size_t fork_workspace_ints(int B, long long table_stride) {
+    return (size_t)(B + 3) / 4 * 4 + (size_t)B * (size_t)table_stride;
+}
+size_t resize_workspace_ints(int B, int pages, long long table_stride) {
+    return 5 * (size_t)B + 1 + (size_t)std::min<long long>(pages, (long long)B * (table_stride + 1));
+}
+size_t compact_workspace_ints(int, int pages) { return 4 + 2 * (size_t)(pages / 2 + 1) + (size_t)pages; }
+
+cudaError_t launch_fork(const PagesArgs& a, int sm_count, cudaStream_t s, int* launched) {
+    cudaError_t e = cudaSuccess;
+    if (a.ws || a.refs_out != a.refs) {
+        const long long work = std::max<long long>(a.pages, a.ws ? a.B * 32ll : 0);
+        const long long blocks = std::min<long long>((work + 255) / 256, sm_count * 8ll);
+        e = launch_k(fork_stage_kernel, dim3((unsigned)std::max<long long>(blocks, 1)), dim3(256), 0, s, true, a);
+        if (e != cudaSuccess) return e;
+        ++*launched;
+    }
+    if (a.B == 0) return e;
+    e = launch_k(fork_kernel, dim3((unsigned)a.B), dim3(256), 0, s, true, a);
+    if (e == cudaSuccess) ++*launched;
+    return e;
+}
+
+cudaError_t launch_resize(const PagesArgs& a, int sm_count, cudaStream_t s, int* launched) {
+    cudaError_t e = launch_rank(resize_rank_kernel<false>, resize_rank_kernel<true>, a, s);
+    if (e != cudaSuccess) return e;
+    ++*launched;
+    e = launch_k(resize_move_kernel, dim3(move_blocks(sm_count)), dim3(kCopyThreads), 0, s, true, a);
+    if (e == cudaSuccess) ++*launched;
+    return e;
+}
+
+cudaError_t launch_compact(const PagesArgs& a, int sm_count, cudaStream_t s, int* launched) {
+    cudaError_t e = launch_rank(compact_rank_kernel<false>, compact_rank_kernel<true>, a, s);
+    if (e != cudaSuccess) return e;
+    ++*launched;
+    e = launch_k(compact_move_kernel, dim3(move_blocks(sm_count)), dim3(kCopyThreads), 0, s, true, a);
+    if (e == cudaSuccess) ++*launched;
+    return e;
+}
+
+}  // namespace idx
