@@ -1325,7 +1325,7 @@ idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const u
         !aligned(q_start, 4) || !aligned(lse, 4))
         return IDX_EALIGN;
     const WindowPlan p = window_plan(B, T, max_q, Hq, Hkv, D, max_len, window, sink, sm_count());
-    if ((long long)p.splits * p.row_tiles * Hkv > 0x7fffffffll) return IDX_EUNSUPPORTED;
+    if ((double)p.splits * p.row_tiles * Hkv * (p.dense ? B : 1) > 0x7fffffff) return IDX_EUNSUPPORTED;
     if (p.total > 0 && (!ws || ws_bytes < p.total)) return IDX_EWORKSPACE;
     if (!aligned(ws, 256)) return IDX_EALIGN;
     if (!arch_ok()) return IDX_EUNSUPPORTED;

@@ -30,7 +30,7 @@
 #include <cudaTypedefs.h>
 
 #include "serve.cuh"
-#include "window.cuh"
+#include "window_span.cuh"
 
 namespace idx {
 
@@ -113,35 +113,6 @@ IDX_DEVI void bulk_rows(uint32_t dst, const void* src, uint32_t bytes, uint64_t*
 IDX_DEVI float times_pow2(float x, int n) {
     const int a = n / 2, b = n - a;
     return x * __int_as_float((a + 127) << 23) * __int_as_float((b + 127) << 23);
-}
-
-// The tokens of a request in this call and the keys that a tile of its rows sees.
-struct Span {
-    int first, count;  // tokens
-    int len;           // cached slots, the new tokens' among them
-};
-IDX_DEVI Span span_of(const WindowArgs& a, int b, bool report) {
-    Span s;
-    int end;
-    if (a.q_start) {
-        s.first = a.q_start[b];
-        end = a.q_start[b + 1];
-    } else {
-        const int per = a.T / a.B;
-        s.first = b * per;
-        end = s.first + per;
-    }
-    s.len = a.lens[b];
-    const bool bad = s.first < 0 || end < s.first || end > a.T || end - s.first > a.max_q || s.len < 0 || s.len > a.max_len;
-    if (bad && report) raise_status(a.d_status, IDX_DEV_RANGE);
-    if (s.first < 0 || end < s.first || end > a.T) {
-        s.first = 0;
-        s.count = 0;
-    } else {
-        s.count = min(end - s.first, a.max_q);
-    }
-    s.len = min(max(s.len, 0), a.max_len);
-    return s;
 }
 
 // A block: 8 NT rows of a request and key head against one split of the keys that they see.  Warps
@@ -713,7 +684,8 @@ template <typename T, int D, int NT> cudaError_t launch_rows(const WindowArgs& a
 
 template <typename T, int D>
 cudaError_t launch_typed(const WindowArgs& a, const WindowPlan& p, cudaStream_t s, int* launched) {
-    cudaError_t e = p.tile_rows == 8 ? launch_rows<T, D, 1>(a, s) : launch_rows<T, D, 2>(a, s);
+    cudaError_t e = p.dense          ? launch_window_dense(a, std::is_same<T, __half>::value ? IDX_FP16 : IDX_BF16, s)
+                    : p.tile_rows == 8 ? launch_rows<T, D, 1>(a, s) : launch_rows<T, D, 2>(a, s);
     if (e != cudaSuccess) return e;
     ++*launched;
     if (a.splits == 1) return e;
@@ -735,40 +707,71 @@ WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_
                        int sm_count) {
     WindowPlan p;
     const int G = Hq / Hkv;
-    const long long most_rows = (long long)max_q * G;
-    p.tile_rows = most_rows <= 8 ? 8 : 16;
-    p.row_tiles = (int)((most_rows + p.tile_rows - 1) / p.tile_rows);
-    // steps of the tile that sees the most
-    const long long tokens = std::min<long long>(max_q, (p.tile_rows + G - 1) / G + 1);
-    long long keys = max_len;
-    if (window > 0) keys = std::min<long long>(max_len, (long long)window + tokens + sink + 4 * kWindowStep);
-    const int steps = (int)std::max<long long>(1, (keys + kWindowStep - 1) / kWindowStep);
-    const double items = (double)B * Hkv * p.row_tiles / (4.0 * sm_count);
-    // A block takes about 4 us and 18 ns per step of 32 keys and warp among four on an SM; whole waves of
-    // long splits are cheap, one that is mostly empty is not.  Lengths are on the device: the mean of the
-    // times with all of them at max_len and at half of it is taken.
-    const double join_us = (double)T * Hq * D * 8 / 5e6;
-    const int units = (steps + kWarps - 1) / kWarps;  // a step for every warp
-    const size_t rows = (size_t)T * Hq, most = std::min<size_t>(rows * std::min(kMostSplits, units), kRowSplits);
+    const size_t rows = (size_t)T * Hq;
+    const long long most_rows = (long long)max_q * G;  // of a request and key head
+    // keys that a tile of `tokens` tokens sees at most
+    auto keys_of = [&](long long tokens) {
+        return window == 0 ? (long long)max_len : std::min<long long>(max_len, (long long)window + sink + tokens);
+    };
+    // row tiles over the batch: of requests with max_q tokens, but no more than the call's tokens fill
+    auto tiles_over = [&](long long per_request, double rows_per_tile) {
+        return Hkv * std::min((double)B * per_request, (double)T * G / rows_per_tile + B);
+    };
+    const int dense_keys = window_dense_keys(D);
+    const long long far = keys_of(max_q);
+    const size_t most = far <= dense_keys
+                            ? 0
+                            : std::min<size_t>(rows * std::min<long long>(kMostSplits, (far + dense_keys - 1) / dense_keys),
+                                               kRowSplits);
+    const double join_us = (double)rows * D * 8 / 5e6;
     double best = 0;
-    p.splits = 1;
-    p.chunk = units * kWarps;
-    for (int s = 1; s <= kMostSplits && s <= units; s += s < 8 ? 1 : s / 4) {
-        const int t = (units + s - 1) / s, all = (units + t - 1) / t, half = (units / 2 + t) / t;
-        if (all > 1 && all * rows > most) break;
-        const double us = (std::ceil(items * all) + std::ceil(items * half)) / 2 * (t * 0.35 + 3.0) +
-                          (all > 1 ? all * join_us + 2.0 : 0.0);
-        if (best == 0 || us < best) {
-            best = us;
-            p.splits = all;
-            p.chunk = t * kWarps;
-        }
+    // `count` tiles whose keys are `units` units, in s splits; time(t, blocks): that of blocks of t units each
+    auto consider = [&](bool dense, int tile_rows, long long row_tiles, double count, long long units, int unit, int s,
+                        auto time) {
+        const long long t = (units + s - 1) / s, all = (units + t - 1) / t, half = (units / 2 + t) / t;
+        if (all > 1 && all * rows > most) return;
+        // lengths are on the device: the mean of the times with all of them at max_len and at half of it
+        const double us = (time(t, count * all) + time(t, count * half)) / 2 + (all > 1 ? all * join_us + 2.5 : 0.0);
+        if (best != 0 && us >= best) return;
+        best = us;
+        p.dense = dense;
+        p.tile_rows = tile_rows;
+        p.row_tiles = (int)row_tiles;
+        p.splits = (int)all;
+        p.chunk = (int)t * unit;
+    };
+    auto more = [](int s) { return s + (s < 8 ? 1 : s / 4); };
+    {
+        // Tiles of 8 or 16 rows: `slots` blocks on an SM together take 128 keys of each of them in `unit_us` times
+        // their number, or in the 0.4 us that one takes by itself; 3 us to start and end.
+        const int tile_rows = most_rows <= 8 ? 8 : 16, slots = tile_rows == 8 ? 4 : 3;
+        const double unit_us = (tile_rows == 8 ? 0.69 : 1.14) * D / 128;
+        const long long tiles = (most_rows + tile_rows - 1) / tile_rows, tokens = (tile_rows + G - 1) / G + 1;
+        const long long units = std::max<long long>(1, (keys_of(tokens) + 3 * kWindowStep + 127) / 128);
+        for (int s = 1; s <= kMostSplits && s <= units; s = more(s))
+            consider(false, tile_rows, tiles, tiles_over(tiles, tile_rows), units, kWarps, s,
+                     [&](long long t, double blocks) {
+                         const double on_sm = std::ceil(blocks / sm_count), full = std::floor(on_sm / slots);
+                         const double rest = on_sm - full * slots;
+                         return full * (t * slots * unit_us + 3.0) +
+                                (rest > 0 ? t * std::max(0.4, rest * unit_us) + 3.0 : 0.0);
+                     });
+    }
+    {
+        // Dense: a CTA per SM takes a key tile for 256 rows in about 1 us, for 128 (two streams in turn) in 0.6.
+        const int tokens = 128 / G;
+        const long long pairs = ((max_q + tokens - 1) / tokens + 1) / 2;
+        const long long units = std::max<long long>(1, (keys_of(2 * tokens) + 2 * dense_keys - 1) / dense_keys);
+        const double tile_us = max_q > tokens ? 1.0 : 0.6;
+        if (most_rows > 16)
+            for (int s = 1; s <= kMostSplits && s <= units; s = more(s))
+                consider(true, 128, pairs, tiles_over(pairs, 2.0 * tokens * G), units, 1, s,
+                         [&](long long t, double blocks) { return std::ceil(blocks / sm_count) * (t * tile_us + 9.0); });
     }
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
-    const size_t parts = units > 1 ? most : 0;
     p.part = 0;
-    p.part_lse = up(parts * D * sizeof(float));
-    p.total = p.part_lse + up(parts * sizeof(float));
+    p.part_lse = up(most * D * sizeof(float));
+    p.total = p.part_lse + up(most * sizeof(float));
     return p;
 }
 

@@ -31,21 +31,26 @@ struct WindowArgs {
     long long table_stride, q_stride;
     int B, T, Hq, Hkv, G, D, pages, page_size, page_shift;
     int max_q, max_len, window, sink;
-    int row_tiles;           // per request and key head
-    int splits, chunk;       // steps of kWindowStep keys per split
+    int row_tiles;           // per request and key head (dense: pairs of them)
+    int splits, chunk;       // steps of kWindowStep keys per split (dense: key tiles)
     float scale_log2;        // scale * log2(e)
     long long wait_limit;    // SM clocks that a wait may take
-    int withhold_step;       // test only: a warp's step that is never loaded, or -1
+    int withhold_step;       // test only: a warp's step (dense: the key tile) that is never loaded, or -1
     int* d_status;
 };
 
 struct WindowPlan {
+    bool dense;              // on the tensor cores' dense path (attention_window_dense.cu)
     int tile_rows, row_tiles, splits, chunk;
     size_t part, part_lse, total;
 };
 
 WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window, int sink,
                        int sm_count);
+
+// The dense path: keys per tile, and the launch.
+int window_dense_keys(int D);
+cudaError_t launch_window_dense(const WindowArgs& a, idx_dtype dt, cudaStream_t s);
 
 // Adds the number of kernels launched to *launched.
 cudaError_t launch_window(const WindowArgs& a, const WindowPlan& p, idx_dtype dt, int sm_count, cudaStream_t s,
