@@ -27,14 +27,10 @@
 #include <cmath>
 #include <type_traits>
 
-#include <cudaTypedefs.h>
-
 #include "serve.cuh"
 #include "window_span.cuh"
 
 namespace idx {
-
-PFN_cuTensorMapEncodeTiled_v12000 tensor_map_encoder();
 
 namespace {
 
@@ -97,17 +93,6 @@ template <int N> IDX_DEVI void lds(uint32_t addr, uint32_t (&w)[N]) {
         static_assert(N == 2, "one or two words");
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
     }
-}
-IDX_DEVI void tma_rows(uint32_t dst, const void* tmap, uint64_t* bar, int row) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%3, %4}], [%2];"
-        ::"r"(dst), "l"(reinterpret_cast<uint64_t>(tmap)), "r"(smem_u32(bar)), "r"(0), "r"(row)
-        : "memory");
-}
-IDX_DEVI void bulk_rows(uint32_t dst, const void* src, uint32_t bytes, uint64_t* bar) {
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(dst),
-                 "l"(reinterpret_cast<uint64_t>(src)), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
 }
 // 2^n for any n that a scale can need, as two factors.
 IDX_DEVI float times_pow2(float x, int n) {
@@ -656,17 +641,6 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
 #pragma unroll
     for (int i = 0; i < W / 2; ++i) out[i] = pack2<T>(acc[2 * i], acc[2 * i + 1]);
     if (a.lse && lane == 0) a.lse[row] = lse * 0.6931471805599453f;
-}
-
-// Map of rows of codes (D / 2 bytes), `unit` rows per copy, their 16-byte chunks swizzled.
-CUresult code_map(CUtensorMap* m, const uint8_t* base, int D, long long rows, int unit) {
-    auto enc = tensor_map_encoder();
-    if (!enc) return CUDA_ERROR_NOT_SUPPORTED;
-    const cuuint64_t dims[2] = {(cuuint64_t)D / 2, (cuuint64_t)rows}, strides[1] = {(cuuint64_t)D / 2};
-    const cuuint32_t box[2] = {(cuuint32_t)D / 2, (cuuint32_t)unit}, one[2] = {1, 1};
-    return enc(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(base), dims, strides, box, one,
-               CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_32B,
-               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
 }
 
 template <typename T, int D, int NT> cudaError_t launch_rows(const WindowArgs& a, cudaStream_t s) {

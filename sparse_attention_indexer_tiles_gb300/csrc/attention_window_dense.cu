@@ -4,16 +4,16 @@
 // The rows of a request and key head (its new tokens times the heads of the group) read the same keys: per key
 // tile S = Q K^T (128 rows x tile keys, over D) and O += P V, as the shared prefix's parts are taken
 // (attention_prefix.cu: two streams of 128 rows with S, P and O in TMEM columns of their own, a softmax thread per
-// row, an issuing warp per stream, K and V tiles in turn through one ring).  What differs is how tiles come: four
-// warps load codes and scales, a tile ahead in registers, and write the values that they stand for, in q's type, where
-// the matrix instructions read them (rows of 64 columns, 128-byte swizzled).  The values are the codes times powers of two, so
+// row, an issuing warp per stream, K and V tiles in turn through one ring).  What differs is how tiles come: TMA
+// brings codes and scales to a small ring of their own, and four warps write the values that they stand for, in q's
+// type, where the matrix instructions read them (rows of 64 columns, 128-byte swizzled).  (Codes that these warps
+// loaded into registers a tile ahead were late: 4096 tokens behind one another 381 us.)  The values are the codes times powers of two, so
 // bf16 holds them exactly; fp16 does from 2^-24 to 2^15 (below, they count as 0).  A value that q's type
 // cannot hold (scales above 2^125, in fp16 above 2^13) counts as a NaN scale.  K of a slot with a NaN scale becomes NaN and its V
 // 0, so that exactly the rows that see it are NaN.
 //
 // A tile that no row of the two streams sees is not taken; the tiles of the first tokens come before those of the
 // window.  Bounded by the tensor core and the softmax's instructions.
-#include "attention.cuh"
 #include "dense.cuh"
 #include "window_span.cuh"
 
@@ -26,35 +26,48 @@ constexpr int kHalfQ = kRows * 128;        // 64 columns of a row tile, 128-byte
 constexpr int kThreads = 16 * 32;          // 8 softmax warps, 2 issuers (of 4), 4 that expand codes
 constexpr int kExpandWarp = 12;            // the first of them: two for K, two for V
 
+// Keys per tile: what TMEM holds at D = 128, what a softmax thread's registers hold at D = 64.
+__host__ __device__ constexpr int dense_keys(int D) { return D == 128 ? 80 : 96; }
+
 template <int D> struct DenseCfg {
-    static constexpr int KEYS = attn_prefix_keys(D);         // per tile
+    static constexpr int KEYS = dense_keys(D);               // per tile
     static constexpr int HALVES = D / 64;
     static constexpr int BLOCKS = D / 32;                    // of a row's scales
     static constexpr int QTILE = HALVES * kHalfQ;
     static constexpr int GROUP = HALVES * 1024;              // 8 keys of a K or V tile
     static constexpr int TILE = KEYS / 8 * GROUP;
-    static constexpr int NS = 8;                             // ring slots, an even number: K or V only
+    static constexpr int NS = 6;                             // ring slots, an even number: K or V only
+    // codes and scales as they lie in the cache: a ring of tiles of their own
+    static constexpr int ROW = D / 2;
+    static constexpr int RS = 3;
+    static constexpr int OFF_RV = KEYS * ROW, OFF_RKSF = 2 * KEYS * ROW, OFF_RVSF = OFF_RKSF + KEYS * BLOCKS;
+    static constexpr int RAW = (OFF_RVSF + KEYS * BLOCKS + 1023) / 1024 * 1024;
+    static constexpr int UNITS = KEYS / 16;                  // copies of 16 keys per tile
+    static constexpr int UNIT = 16 * ROW, UNIT_SF = 16 * BLOCKS;
     static constexpr int SUBS = 4 / BLOCKS;                  // groups of 8 keys that a warp expands at once
     static constexpr int PER = KEYS / 16;                    // groups of a tile per warp
     static constexpr int ITEMS = PER / SUBS;
-    static constexpr int OFF_KV = 2 * QTILE;
+    static constexpr int OFF_RAW = 2 * QTILE;
+    static constexpr int OFF_KV = OFF_RAW + RS * RAW;
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
-    static constexpr int NBAR = 1 + 2 * NS + 10;
+    static constexpr int NBAR = 1 + 2 * NS + 10 + 2 * RS;
     static constexpr int OFF_CTL = OFF_BAR + NBAR * 8;       // [0] TMEM base, [1] abort flag
     static constexpr int OFF_ML = OFF_CTL + 8;              // the odd stream's m and l
     static constexpr int SMEM = OFF_ML + kRows * 8 + 1024;
     // TMEM columns: S and P of a stream, then both O
     static constexpr int COL_P = KEYS, COL_STREAM = D == 128 ? 128 : KEYS + KEYS / 2;
     static constexpr int COL_O = 512 - 2 * D;
-    static_assert(SMEM <= 227 * 1024 && PER % SUBS == 0 && PER <= 32, "");
+    static_assert(SMEM <= 227 * 1024 && PER % SUBS == 0 && NBAR <= 64, "");
+    static_assert(4 * UNITS <= 32 && KEYS % 16 == 0 && KEYS * ROW % 512 == 0, "a lane per copy");
     static_assert(KEYS + KEYS / 2 <= COL_STREAM && 2 * COL_STREAM <= COL_O, "");
     static_assert(kRows * D * 4 <= NS * TILE, "the odd stream's O is joined through the ring");
 };
 
-// Registers: the launch gives 512 x 128; the softmax warps take 256 x 192, the others keep 256 x 64.
-IDX_DEVI void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 192;" ::: "memory"); }
-IDX_DEVI void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;" ::: "memory"); }
-static_assert(256 * 192 + 256 * 64 <= 512 * 128, "");
+// Registers: the launch gives 512 x 128.
+constexpr int kSoftmaxRegs = 176, kOtherRegs = 80;
+static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 512 * 128, "");
+template <int N> IDX_DEVI void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory"); }
+template <int N> IDX_DEVI void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory"); }
 
 // The largest scale whose values the type holds, and its NaN twice.
 template <typename T> struct Held;
@@ -76,29 +89,31 @@ IDX_DEVI uint32_t mul2_bf16(uint32_t a, uint32_t b) {
     return d;
 }
 
-// Eight codes times 2^(sf - 127), pairs in order.
+// A pair of codes in fp16 times 2^(sf - 127), in T.  Scales up to EASY take one product; for larger ones, up to
+// MOST, there is a second (of `rest`, times()).
 template <typename T> struct Expand;
 template <> struct Expand<__half> {
+    static constexpr uint32_t EASY = Held<__half>::MOST;
     uint32_t scale;
     IDX_DEVI explicit Expand(uint32_t sf) {
         const int field = (int)sf - 112;  // of an fp16 power of two; at most 28
         const uint32_t bits = field > 0 ? (uint32_t)field << 10 : field >= -9 ? 1u << (9 + field) : 0u;
         scale = bits | bits << 16;
     }
+    IDX_DEVI Expand(uint32_t, bool) : scale(0) {}
     IDX_DEVI uint32_t operator()(uint32_t h) const { return mul2_f16(h, scale); }
+    IDX_DEVI uint32_t times(uint32_t x) const { return x; }
 };
 template <> struct Expand<__nv_bfloat16> {
-    uint32_t scale, more;
-    IDX_DEVI explicit Expand(uint32_t sf) {
-        // an fp16 code moved to bf16's fields stands for 2^-112 of itself
-        const uint32_t field = min(sf + 112u, 254u), rest = sf + 112u - field + 127u;
-        scale = field << 7 | field << 23;
-        more = rest << 7 | rest << 23;  // 1 but for scales above 2^15
-    }
+    // an fp16 code moved to bf16's fields stands for 2^-112 of itself
+    static constexpr uint32_t EASY = 254 - 112;
+    uint32_t scale;
+    IDX_DEVI explicit Expand(uint32_t sf) { scale = (sf + 112u) * 0x00800080u; }
+    IDX_DEVI Expand(uint32_t sf, bool) { scale = (127u + max(sf, EASY) - EASY) * 0x00800080u; }
     IDX_DEVI uint32_t operator()(uint32_t h) const {
-        const uint32_t x = mul2_bf16((h >> 3 & 0x0fff0fffu) | (h & 0x80008000u), scale);
-        return more == 0x3f803f80u ? x : mul2_bf16(x, more);
+        return mul2_bf16((h >> 3 & 0x0fff0fffu) | (h & 0x80008000u), scale);
     }
+    IDX_DEVI uint32_t times(uint32_t x) const { return mul2_bf16(x, scale); }
 };
 template <typename T> IDX_DEVI uint4 expand8(uint32_t w, const Expand<T>& f) {
     uint32_t h[4];
@@ -116,7 +131,8 @@ template <typename T> IDX_DEVI uint4 expand8(uint32_t w, const Expand<T>& f) {
 // blockIdx.x: pair of row tiles (the last, with the most keys, first), split, key head, request.
 template <typename T, int D>
 __global__ void __launch_bounds__(kThreads, 1)
-window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ WindowArgs a) {
+window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_constant__ CUtensorMap tm_k,
+                    const __grid_constant__ CUtensorMap tm_v, const __grid_constant__ WindowArgs a) {
     using C = DenseCfg<D>;
     extern __shared__ __align__(1024) uint8_t smem_raw[];
     uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
@@ -128,6 +144,8 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint64_t* pfull = sfree + 2;      // P is there
     uint64_t* pvdone = pfull + 2;     // O has the tile's P V, P has been read
     uint64_t* done = pvdone + 2;      // every MMA of the stream
+    uint64_t* rfull = done + 2;       // codes and scales of a tile have landed
+    uint64_t* rempty = rfull + C::RS;
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -176,13 +194,16 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     if (warp == 9) {
         if (lane == 0) {
             prefetch_tmap(&tm_q);
+            prefetch_tmap(&tm_k);
+            prefetch_tmap(&tm_v);
             *abort_flag = 0;
         }
         // a barrier per lane, in their order: q; full (the two warps that write a tile), empty (the streams
-        // that read it); per stream S, S free, P (a warp each), P V, done
+        // that read it); per stream S, S free, P (a warp each), P V, done; codes landed, read (a warp each)
         for (int i = lane; i < C::NBAR; i += 32) {
             const int k = (i - 1 - 2 * C::NS) / 2;
-            mbar_init(qfull + i, i == 0 ? 1 : i <= C::NS ? 2 : i <= 2 * C::NS ? (solo ? 1 : 2) : k == 1 || k == 2 ? 4 : 1);
+            const bool read = i >= 1 + 2 * C::NS + 10 + C::RS;
+            mbar_init(qfull + i, i == 0 ? 1 : i <= C::NS ? 2 : i <= 2 * C::NS ? (solo ? 1 : 2) : k == 1 || k == 2 || read ? 4 : 1);
         }
         fence_barrier_init();
         __syncwarp();
@@ -206,90 +227,69 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     tc_fence_after();
     const uint32_t tmem = *tslot;
     const uint32_t kv = smem_u32(smem + C::OFF_KV);
+    const int tiles = a.withhold_step >= 0 ? min(n, a.withhold_step) : n;  // that come
     auto give_up = [&] {
         *abort_flag = 1;
         raise_status(a.d_status, IDX_DEV_TIMEOUT);
     };
 
     if (warp >= 8) {
-        regs_less();
+        regs_less<kOtherRegs>();
         if (warp >= kExpandWarp) {
             // ------------------------------------- codes to values: two warps K, two warps V
             const int is_v = (warp - kExpandWarp) >> 1, part = warp & 1;
-            const uint8_t* const codes = is_v ? a.v_codes : a.k_codes;
-            const uint8_t* const sf = is_v ? a.v_sf : a.k_sf;
-            const uint8_t* const other_sf = is_v ? a.k_sf : a.v_sf;
             const int key_in = lane & 7, block = lane >> 3 & (C::BLOCKS - 1), sub = lane / (8 * C::BLOCKS);
-            const int* const table = a.table + b * a.table_stride;
-            const int tiles = a.withhold_step >= 0 ? min(n, a.withhold_step) : n;  // that come
-            bool bad = false;
-            // a lane's group of 8 keys of tile i: its first row in the cache, -1 for keys that no row sees
-            auto look_up = [&](int i) {
-                int row = -1;
-                if (lane < C::PER && i < tiles) {
-                    const int key = base_of(i) + (part * C::PER + lane) * 8;
-                    if (key < hi && (key < sink || key + 8 > wlo)) {
-                        const int page = table[key >> a.page_shift];
-                        if (page < 0 || page >= a.pages)
-                            bad = true;
-                        else
-                            row = (page * a.Hkv + hk) * a.page_size + (key & (a.page_size - 1));
-                    }
-                }
-                return row;
-            };
-            uint4 raw[C::ITEMS];
-            uint32_t scale[C::ITEMS];  // and the other's of K and V
-            auto load = [&](int i, int rows) {
-                const int row = __shfl_sync(~0u, rows, i * C::SUBS + sub);
-                raw[i] = make_uint4(0u, 0u, 0u, 0u);
-                scale[i] = 127u | 127u << 8;
-                if (row >= 0) {
-                    const long long r = row + key_in;
-                    raw[i] = *reinterpret_cast<const uint4*>(codes + (r * C::BLOCKS + block) * 16);
-                    scale[i] = sf[r * C::BLOCKS + block] | (uint32_t)(is_v ? 0 : other_sf[r * C::BLOCKS + block]) << 8;
-                }
-            };
-            int rows = look_up(0), next = look_up(1);
-#pragma unroll
-            for (int i = 0; i < C::ITEMS; ++i) load(i, rows);
+            bool ok = true;
             for (int t = 0; t < tiles; ++t) {
-                rows = next;
-                next = look_up(t + 2);
                 const int x = 2 * t + is_v, slot = x % C::NS;
-                bool ok = true;
-                if (x >= C::NS)
-                    ok = __all_sync(~0u, mbar_wait(&empty[slot], ((x / C::NS) & 1) ^ 1, abort_flag, a.wait_limit));
-                if (!ok) {
-                    if (lane == 0) give_up();
-                    break;
-                }
+                ok = mbar_wait(&rfull[t % C::RS], t / C::RS & 1, abort_flag, a.wait_limit);
+                if (x >= C::NS) ok = mbar_wait(&empty[slot], ((x / C::NS) & 1) ^ 1, abort_flag, a.wait_limit) && ok;
+                if (!(ok = __all_sync(~0u, ok))) break;
+                const uint32_t raw = smem_u32(smem + C::OFF_RAW + t % C::RS * C::RAW);
 #pragma unroll
                 for (int i = 0; i < C::ITEMS; ++i) {
-                    const uint32_t own = scale[i] & 0xffu, most = max(own, scale[i] >> 8);
-                    const Expand<T> f(min(own, Held<T>::MOST));
-                    const uint32_t w[4] = {raw[i].x, raw[i].y, raw[i].z, raw[i].w};
-                    const int group = part * C::PER + i * C::SUBS + sub;
+                    const int group = part * C::PER + i * C::SUBS + sub, key = group * 8 + key_in;
+                    uint32_t w[4], own, other = 0;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                                 : "r"(raw + is_v * C::OFF_RV + key * C::ROW +
+                                       16 * (D == 128 ? block ^ (key >> 1 & 3) : block ^ (key >> 2 & 1))));
+                    asm volatile("ld.shared.u8 %0, [%1];"
+                                 : "=r"(own)
+                                 : "r"(raw + (is_v ? C::OFF_RVSF : C::OFF_RKSF) + key * C::BLOCKS + block));
+                    if (!is_v)
+                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(other) : "r"(raw + C::OFF_RVSF + key * C::BLOCKS + block));
                     const uint32_t to = kv + slot * C::TILE + group * C::GROUP + block / 2 * 1024 + key_in * 128;
-#pragma unroll
-                    for (int c = 0; c < 4; ++c) {
-                        uint4 v = expand8<T>(w[c], f);
-                        if (most > Held<T>::MOST) {
-                            const uint32_t as = is_v ? 0u : Held<T>::NANS;
-                            v = make_uint4(as, as, as, as);
-                        }
+                    const uint32_t most = max(own, other);
+                    auto put = [&](int c, uint4 v) {
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
                                          to + ((((block & 1) * 4 + c) ^ key_in) * 16)),
                                      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                                      : "memory");
+                    };
+                    if (!__any_sync(~0u, most > Expand<T>::EASY)) {
+                        const Expand<T> f(own);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) put(c, expand8<T>(w[c], f));
+                    } else {
+                        const Expand<T> f(min(own, Expand<T>::EASY)), more(min(own, Held<T>::MOST), true);
+                        const uint32_t gone = is_v ? 0u : Held<T>::NANS;
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) {
+                            uint4 v = expand8<T>(w[c], f);
+                            v = make_uint4(more.times(v.x), more.times(v.y), more.times(v.z), more.times(v.w));
+                            put(c, most > Held<T>::MOST ? make_uint4(gone, gone, gone, gone) : v);
+                        }
                     }
-                    if (t + 1 < tiles) load(i, rows);
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&full[slot]);
+                if (lane == 0) {
+                    mbar_arrive(&full[slot]);
+                    mbar_arrive(&rempty[t % C::RS]);
+                }
             }
-            if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
+            if (!ok && lane == 0) give_up();
         } else if (warp == 8 || warp == 10) {
             // ------------------------------------------------------------ MMA issuers
             // The whole warp runs the control flow, so that descriptors stay in uniform registers, and one
@@ -356,11 +356,59 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             }
             __syncwarp();
         } else if (warp == 9) {
-            mbar_wait(qfull, 0, nullptr, 1ll << 28);  // no copy may be in flight when the CTA ends
+            // ------------------------------- codes and scales as they lie: a copy of 16 keys per lane and array
+            const int unit = lane >> 2, what = lane & 3;  // K, V, K's scales, V's
+            const int* const table = a.table + b * a.table_stride;
+            bool bad = false;
+            // first row of this lane's copy of tile i in the cache; -1: no row of the pair sees its keys
+            auto look_up = [&](int i) {
+                int row = -1;
+                if (unit < C::UNITS && i < tiles) {
+                    const int key = base_of(i) + unit * 16;
+                    if (key < hi && (key < sink || key + 16 > wlo)) {
+                        const int page = table[key >> a.page_shift];
+                        if (page < 0 || page >= a.pages)
+                            bad = true;
+                        else
+                            row = (page * a.Hkv + hk) * a.page_size + (key & (a.page_size - 1));
+                    }
+                }
+                return row;
+            };
+            int row = look_up(0), t = 0;
+            for (; t < tiles; ++t) {
+                const int next = look_up(t + 1);
+                uint64_t* const bar = &rfull[t % C::RS];
+                bool ok = true;
+                if (t >= C::RS)
+                    ok = __all_sync(~0u, mbar_wait(&rempty[t % C::RS], (t / C::RS & 1) ^ 1, abort_flag, a.wait_limit));
+                if (!ok) {
+                    if (lane == 0) give_up();
+                    break;
+                }
+                const uint32_t copies = __ballot_sync(~0u, row >= 0);
+                if (lane == 0)
+                    mbar_arrive_expect_tx(bar, __popc(copies & 0x33333333u) * C::UNIT + __popc(copies & 0xccccccccu) * C::UNIT_SF);
+                __syncwarp();
+                if (row >= 0) {
+                    const uint32_t raw = smem_u32(smem + C::OFF_RAW + t % C::RS * C::RAW);
+                    if (what < 2)
+                        tma_rows(raw + what * C::OFF_RV + unit * C::UNIT, what ? &tm_v : &tm_k, bar, row);
+                    else
+                        bulk_rows(raw + (what == 3 ? C::OFF_RVSF : C::OFF_RKSF) + unit * C::UNIT_SF,
+                                  (what == 3 ? a.v_sf : a.k_sf) + (long long)row * C::BLOCKS, C::UNIT_SF, bar);
+                }
+                __syncwarp();
+                row = next;
+            }
+            if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
+            // no copy may be in flight when the CTA ends
+            mbar_wait(qfull, 0, nullptr, 1ll << 28);
+            for (int y = max(0, t - C::RS); y < t; ++y) mbar_wait(&rfull[y % C::RS], y / C::RS & 1, nullptr, 1ll << 28);
             __syncwarp();
         }
     } else {
-        regs_more();
+        regs_more<kSoftmaxRegs>();
         // ------------------------------------------------------- softmax, one thread per row
         const int s = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
@@ -449,8 +497,8 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             tc_fence_after();
 #pragma unroll
             for (int c = 0; c < C::KEYS / 64; ++c) tmem_st32x32b<32>(ts + C::COL_P + c * 32, p + c * 32);
-            if constexpr (C::KEYS % 64 != 0)
-                tmem_st32x32b<C::KEYS % 64 / 2>(ts + C::COL_P + C::KEYS / 64 * 32, p + C::KEYS / 64 * 32);
+#pragma unroll
+            for (int c = C::KEYS / 64 * 32; c < C::KEYS / 2; c += 8) tmem_st32x32b<8>(ts + C::COL_P + c, p + c);
             tmem_st_wait();
             tc_fence_before();
             __syncwarp();
@@ -555,23 +603,26 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
 
 template <typename T, int D> cudaError_t launch_t(const WindowArgs& a, cudaStream_t s) {
     using C = DenseCfg<D>;
-    CUtensorMap tq;
+    CUtensorMap tq, tk, tv;
     const int tokens = kRows / a.G;
     // q: 64 columns, the heads of a group, groups, tokens
     const cuuint64_t qd[4] = {(uint64_t)D, (uint64_t)a.G, (uint64_t)a.Hkv, (uint64_t)a.T};
     const cuuint64_t qs[3] = {(uint64_t)D * 2, (uint64_t)D * 2 * a.G, (uint64_t)(a.T > 1 ? a.q_stride : (long long)a.Hq * D) * 2};
     const cuuint32_t qb[4] = {64, (uint32_t)a.G, 1, (uint32_t)tokens};
-    if (make_map<4>(&tq, a.q, qd, qs, qb) != CUDA_SUCCESS) return cudaErrorInvalidValue;
+    const long long rows = (long long)a.pages * a.Hkv * a.page_size;
+    if (make_map<4>(&tq, a.q, qd, qs, qb) != CUDA_SUCCESS || code_map(&tk, a.k_codes, D, rows, 16) != CUDA_SUCCESS ||
+        code_map(&tv, a.v_codes, D, rows, 16) != CUDA_SUCCESS)
+        return cudaErrorInvalidValue;
     static PerDevice ready;
     const cudaError_t e = allow_smem(ready, window_dense_kernel<T, D>, C::SMEM);
     if (e != cudaSuccess) return e;
     return launch_k(window_dense_kernel<T, D>, dim3((unsigned)(a.row_tiles * a.splits * a.Hkv * a.B)), dim3(kThreads),
-                    C::SMEM, s, true, tq, a);
+                    C::SMEM, s, true, tq, tk, tv, a);
 }
 
 }  // namespace
 
-int window_dense_keys(int D) { return attn_prefix_keys(D); }
+int window_dense_keys(int D) { return dense_keys(D); }
 
 cudaError_t launch_window_dense(const WindowArgs& a, idx_dtype dt, cudaStream_t s) {
     if (dt == IDX_BF16) return a.D == 128 ? launch_t<__nv_bfloat16, 128>(a, s) : launch_t<__nv_bfloat16, 64>(a, s);
