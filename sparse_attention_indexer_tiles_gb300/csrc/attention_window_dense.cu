@@ -5,7 +5,7 @@
 // tile S = Q K^T (128 rows x tile keys, over D) and O += P V, as the shared prefix's parts are taken
 // (attention_prefix.cu: two streams of 128 rows with S, P and O in TMEM columns of their own, a softmax thread per
 // row, an issuing warp per stream, K and V tiles in turn through one ring).  What differs is how tiles come: TMA
-// brings codes and scales to a small ring of their own, and four warps write the values that they stand for, in q's
+// brings codes and scales to a small ring of their own, and five warps write the values that they stand for, in q's
 // type, where the matrix instructions read them (rows of 64 columns, 128-byte swizzled).  (Codes that these warps
 // loaded into registers a tile ahead were late: 4096 tokens behind one another 381 us.)  The values are the codes times powers of two, so
 // bf16 holds them exactly; fp16 does from 2^-24 to 2^15 (below, they count as 0).  A value that q's type
@@ -23,8 +23,8 @@ namespace {
 
 constexpr int kRows = 128;                 // rows per tile
 constexpr int kHalfQ = kRows * 128;        // 64 columns of a row tile, 128-byte swizzled
-constexpr int kThreads = 16 * 32;          // 8 softmax warps, 2 issuers (of 4), 4 that expand codes
-constexpr int kExpandWarp = 12;            // the first of them: two for K, two for V
+constexpr int kThreads = 16 * 32;          // 8 softmax warps, 2 issuers, one for copies, 5 that expand codes
+constexpr int kExpandWarp = 11, kExpandWarps = 5;  // the first of them, and how many
 
 // Keys per tile: what TMEM holds at D = 128, what a softmax thread's registers hold at D = 64.
 __host__ __device__ constexpr int dense_keys(int D) { return D == 128 ? 80 : 96; }
@@ -45,8 +45,7 @@ template <int D> struct DenseCfg {
     static constexpr int UNITS = KEYS / 16;                  // copies of 16 keys per tile
     static constexpr int UNIT = 16 * ROW, UNIT_SF = 16 * BLOCKS;
     static constexpr int SUBS = 4 / BLOCKS;                  // groups of 8 keys that a warp expands at once
-    static constexpr int PER = KEYS / 16;                    // groups of a tile per warp
-    static constexpr int ITEMS = PER / SUBS;
+    static constexpr int ITEMS = (KEYS / 8 / SUBS + kExpandWarps - 1) / kExpandWarps;  // of them, per warp
     static constexpr int OFF_RAW = 2 * QTILE;
     static constexpr int OFF_KV = OFF_RAW + RS * RAW;
     static constexpr int OFF_BAR = OFF_KV + NS * TILE;
@@ -57,7 +56,7 @@ template <int D> struct DenseCfg {
     // TMEM columns: S and P of a stream, then both O
     static constexpr int COL_P = KEYS, COL_STREAM = D == 128 ? 128 : KEYS + KEYS / 2;
     static constexpr int COL_O = 512 - 2 * D;
-    static_assert(SMEM <= 227 * 1024 && PER % SUBS == 0 && NBAR <= 64, "");
+    static_assert(SMEM <= 227 * 1024 && KEYS / 8 % SUBS == 0 && NBAR <= 64, "");
     static_assert(4 * UNITS <= 32 && KEYS % 16 == 0 && KEYS * ROW % 512 == 0, "a lane per copy");
     static_assert(KEYS + KEYS / 2 <= COL_STREAM && 2 * COL_STREAM <= COL_O, "");
     static_assert(kRows * D * 4 <= NS * TILE, "the odd stream's O is joined through the ring");
@@ -198,12 +197,16 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             prefetch_tmap(&tm_v);
             *abort_flag = 0;
         }
-        // a barrier per lane, in their order: q; full (the two warps that write a tile), empty (the streams
+        // a barrier per lane, in their order: q; full (the warps that write a tile), empty (the streams
         // that read it); per stream S, S free, P (a warp each), P V, done; codes landed, read (a warp each)
         for (int i = lane; i < C::NBAR; i += 32) {
             const int k = (i - 1 - 2 * C::NS) / 2;
             const bool read = i >= 1 + 2 * C::NS + 10 + C::RS;
-            mbar_init(qfull + i, i == 0 ? 1 : i <= C::NS ? 2 : i <= 2 * C::NS ? (solo ? 1 : 2) : k == 1 || k == 2 || read ? 4 : 1);
+            mbar_init(qfull + i, i == 0                 ? 1
+                                 : i <= C::NS || read   ? kExpandWarps
+                                 : i <= 2 * C::NS       ? (solo ? 1 : 2)
+                                 : k == 1 || k == 2     ? 4
+                                                        : 1);
         }
         fence_barrier_init();
         __syncwarp();
@@ -236,47 +239,47 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     if (warp >= 8) {
         regs_less<kOtherRegs>();
         if (warp >= kExpandWarp) {
-            // ------------------------------------- codes to values: two warps K, two warps V
-            const int is_v = (warp - kExpandWarp) >> 1, part = warp & 1;
+            // -------------------------- codes to values: K's items of a tile dealt to the warps, then V's
             const int key_in = lane & 7, block = lane >> 3 & (C::BLOCKS - 1), sub = lane / (8 * C::BLOCKS);
+            const int turn = warp - kExpandWarp;
             bool ok = true;
-            for (int t = 0; t < tiles; ++t) {
-                const int x = 2 * t + is_v, slot = x % C::NS;
-                ok = mbar_wait(&rfull[t % C::RS], t / C::RS & 1, abort_flag, a.wait_limit);
-                if (x >= C::NS) ok = mbar_wait(&empty[slot], ((x / C::NS) & 1) ^ 1, abort_flag, a.wait_limit) && ok;
-                if (!(ok = __all_sync(~0u, ok))) break;
-                const uint32_t raw = smem_u32(smem + C::OFF_RAW + t % C::RS * C::RAW);
+            // one array of a tile: codes at `codes`, scales at `scales`; a NaN scale makes K (seen: also V's, at
+            // `others`) NaN and V 0
+            auto expand = [&](uint32_t codes, uint32_t scales, uint32_t others, bool is_v, uint32_t to) {
+                uint32_t w[C::ITEMS][4], own[C::ITEMS], other[C::ITEMS];
+#pragma unroll
+                for (int i = 0; i < C::ITEMS; ++i) {  // all loads before the first use
+                    const int key = ((i * kExpandWarps + turn) * C::SUBS + sub) * 8 + key_in;
+                    if ((i * kExpandWarps + turn) * C::SUBS >= C::KEYS / 8) break;
+                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                                 : "=r"(w[i][0]), "=r"(w[i][1]), "=r"(w[i][2]), "=r"(w[i][3])
+                                 : "r"(codes + key * C::ROW +
+                                       16 * (D == 128 ? block ^ (key >> 1 & 3) : block ^ (key >> 2 & 1))));
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(own[i]) : "r"(scales + key * C::BLOCKS + block));
+                    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(other[i]) : "r"(others + key * C::BLOCKS + block));
+                }
 #pragma unroll
                 for (int i = 0; i < C::ITEMS; ++i) {
-                    const int group = part * C::PER + i * C::SUBS + sub, key = group * 8 + key_in;
-                    uint32_t w[4], own, other = 0;
-                    asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
-                                 : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
-                                 : "r"(raw + is_v * C::OFF_RV + key * C::ROW +
-                                       16 * (D == 128 ? block ^ (key >> 1 & 3) : block ^ (key >> 2 & 1))));
-                    asm volatile("ld.shared.u8 %0, [%1];"
-                                 : "=r"(own)
-                                 : "r"(raw + (is_v ? C::OFF_RVSF : C::OFF_RKSF) + key * C::BLOCKS + block));
-                    if (!is_v)
-                        asm volatile("ld.shared.u8 %0, [%1];" : "=r"(other) : "r"(raw + C::OFF_RVSF + key * C::BLOCKS + block));
-                    const uint32_t to = kv + slot * C::TILE + group * C::GROUP + block / 2 * 1024 + key_in * 128;
-                    const uint32_t most = max(own, other);
+                    const int group = (i * kExpandWarps + turn) * C::SUBS + sub;
+                    if ((i * kExpandWarps + turn) * C::SUBS >= C::KEYS / 8) break;
+                    const uint32_t row = to + group * C::GROUP + block / 2 * 1024 + key_in * 128;
+                    const uint32_t most = max(own[i], other[i]);
                     auto put = [&](int c, uint4 v) {
                         asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(
-                                         to + ((((block & 1) * 4 + c) ^ key_in) * 16)),
+                                         row + ((((block & 1) * 4 + c) ^ key_in) * 16)),
                                      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                                      : "memory");
                     };
                     if (!__any_sync(~0u, most > Expand<T>::EASY)) {
-                        const Expand<T> f(own);
+                        const Expand<T> f(own[i]);
 #pragma unroll
-                        for (int c = 0; c < 4; ++c) put(c, expand8<T>(w[c], f));
+                        for (int c = 0; c < 4; ++c) put(c, expand8<T>(w[i][c], f));
                     } else {
-                        const Expand<T> f(min(own, Expand<T>::EASY)), more(min(own, Held<T>::MOST), true);
+                        const Expand<T> f(min(own[i], Expand<T>::EASY)), more(min(own[i], Held<T>::MOST), true);
                         const uint32_t gone = is_v ? 0u : Held<T>::NANS;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
-                            uint4 v = expand8<T>(w[c], f);
+                            uint4 v = expand8<T>(w[i][c], f);
                             v = make_uint4(more.times(v.x), more.times(v.y), more.times(v.z), more.times(v.w));
                             put(c, most > Held<T>::MOST ? make_uint4(gone, gone, gone, gone) : v);
                         }
@@ -284,10 +287,21 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                 __syncwarp();
-                if (lane == 0) {
-                    mbar_arrive(&full[slot]);
-                    mbar_arrive(&rempty[t % C::RS]);
+            };
+            for (int t = 0; t < tiles; ++t) {
+                const uint32_t raw = smem_u32(smem + C::OFF_RAW + t % C::RS * C::RAW);
+                ok = mbar_wait(&rfull[t % C::RS], t / C::RS & 1, abort_flag, a.wait_limit);
+#pragma unroll
+                for (int is_v = 0; is_v < 2; ++is_v) {
+                    const int x = 2 * t + is_v, slot = x % C::NS;
+                    if (x >= C::NS) ok = mbar_wait(&empty[slot], ((x / C::NS) & 1) ^ 1, abort_flag, a.wait_limit) && ok;
+                    if (!(ok = __all_sync(~0u, ok))) break;
+                    expand(raw + is_v * C::OFF_RV, raw + (is_v ? C::OFF_RVSF : C::OFF_RKSF), raw + C::OFF_RVSF, is_v,
+                           kv + slot * C::TILE);
+                    if (lane == 0) mbar_arrive(&full[slot]);
                 }
+                if (!ok) break;
+                if (lane == 0) mbar_arrive(&rempty[t % C::RS]);
             }
             if (!ok && lane == 0) give_up();
         } else if (warp == 8 || warp == 10) {
