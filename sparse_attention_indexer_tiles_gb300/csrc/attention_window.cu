@@ -3,11 +3,10 @@
 // Row (token at position p, head) sees the keys j <= p with j < sink or j > p - window (all of
 // them when window is 0), z_j = scale * q . k_j:
 //     o = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse = log sum_j exp(z_j).
-// k and v are e2m1 codes c times a power of two per 32 elements, so with K's block b of a key
-//     q . k_j = sum_b 2^(e_jb) sum_{d in b} q_d c_jd,
-// and the codes are the operand of the matrix instructions as fp16, which holds them exactly.
-// The powers of K's blocks multiply the fp32 sums.  V's multiply its codes in fp16, relative to a
-// running power 2^E per block of columns; sums against V stay in units of 2^E.
+// k and v are e2m1 codes c times a power of two per 32 elements.  The operands of the matrix instructions are codes as
+// fp16, which holds them exactly, times the powers of two relative to running ones: 2^EK for all of K, 2^E for
+// each block of V's columns.  Sums come in units of 2^EK, o in units of 2^E.  Blocks whose power lies outside the 26
+// powers below the running one, or above it, are rare: their step takes another path, a pass per 26 powers.
 //
 // bf16 queries are made fp16 by a power of two per row (the largest element just below 2^15): an
 // element below 2^-32 of the row's largest loses bits, 2^-40 of that one at most.  The weights
@@ -15,11 +14,10 @@
 // past it by 2^8.  Weights below 2^-21 of a row's largest have fewer bits than fp16, those below
 // 2^-31 count as 0.  Maxima, sums and o are fp32, exponentials base 2 on z * log2(e).
 //
-// HBM-bound in theory (68 bytes per key row of 128); in practice the instructions that expand the
-// codes come close.  A block's warps each take 32 keys at a time through a ring of their own, which
-// TMA fills (rows swizzled, so that the warp's reads of 4-byte words meet no bank conflicts).  The
-// products are taken transposed, S^T = K Q^T and O^T += V^T P^T: keys and D are the long axes of the
-// matrix instructions, the rows (8 or 16) the short one.
+// HBM-bound in theory (68 bytes per key row of 128); in practice the instructions that expand the codes come close. A
+// block's warps each take 32 keys at a time through a ring of their own, four bulk copies a step (of 64 and 4
+// bytes per key: tensor copies of swizzled rows took 9 % longer).  The products are taken transposed, S^T = K Q^T
+// and O^T += V^T P^T: keys and D are the long axes of the matrix instructions, the rows (8 or 16) the short one.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -35,23 +33,26 @@ namespace idx {
 namespace {
 
 constexpr int kWarps = 4;
-constexpr int kStages = 3;
+constexpr int kStages = 2;
 constexpr float kLift = 7.f;    // weights are taken times 2^kLift
 constexpr float kRenew = 8.f;   // growth of a row's maximum that renews it; 2^(kLift + kRenew) fits fp16
-// Fields of an fp16 power of two 2^(field - 15) that V's codes take: 28 for a block at E, so that
-// 6 * 2^13 is the largest value; blocks below 2^-26 of it are taken in another pass over the step.
+// Fields of an fp16 power of two 2^(field - 15) that codes take: 28 for a block at the running power, so that 6 * 2^13
+// is the largest value; blocks below 2^-26 of it are taken in another pass over the step.
 constexpr int kTopField = 28, kBand = 26;
-constexpr int kMargin = 3;      // E is set this far above what asked for it
+constexpr int kMargin = 3;      // running powers are set this far above what asked for them
 
 template <int D> struct Ring {
     static constexpr int ROW = D / 2;                        // bytes of codes
     static constexpr int CODES = kWindowStep * ROW;
     static constexpr int SF = kWindowStep * (D / 32);
     static constexpr int OFF_V = CODES, OFF_KSF = 2 * CODES, OFF_VSF = 2 * CODES + SF;
-    static constexpr int STAGE = (2 * CODES + 2 * SF + 511) / 512 * 512;
+    static constexpr int STAGE = 2 * CODES + 2 * SF;
     static constexpr int BYTES = 2 * CODES + 2 * SF;         // that land per stage
     static constexpr int OFF_BAR = kWarps * kStages * STAGE;
-    static constexpr int SMEM = OFF_BAR + kWarps * kStages * 8 + 1024;  // with room to align
+    static_assert(STAGE % 128 == 0, "");
+    static constexpr int JOIN = kWarps * 16 * (D + 6) * 4;   // of 16 rows
+    static constexpr int OFF_ROWS = OFF_BAR > JOIN ? OFF_BAR : JOIN;  // per row: its logits' factor, its position
+    static constexpr int SMEM = OFF_ROWS + 16 * 8 + kWarps * kStages * 8;
 };
 
 // Eight e2m1 codes as fp16, pairs in order.
@@ -89,10 +90,19 @@ IDX_DEVI uint32_t transpose8(uint32_t v) {
 template <int N> IDX_DEVI void lds(uint32_t addr, uint32_t (&w)[N]) {
     if constexpr (N == 1) {
         asm volatile("ld.shared.b32 %0, [%1];" : "=r"(w[0]) : "r"(addr));
-    } else {
-        static_assert(N == 2, "one or two words");
+    } else if constexpr (N == 2) {
         asm volatile("ld.shared.v2.b32 {%0, %1}, [%2];" : "=r"(w[0]), "=r"(w[1]) : "r"(addr));
+    } else {
+        static_assert(N == 4, "one, two or four words");
+        asm volatile("ld.shared.v4.b32 {%0, %1, %2, %3}, [%4];"
+                     : "=r"(w[0]), "=r"(w[1]), "=r"(w[2]), "=r"(w[3])
+                     : "r"(addr));
     }
+}
+IDX_DEVI uint32_t lds8(uint32_t addr) {
+    uint32_t v;
+    asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
 }
 // 2^n for any n that a scale can need, as two factors.
 IDX_DEVI float times_pow2(float x, int n) {
@@ -105,16 +115,14 @@ IDX_DEVI float times_pow2(float x, int n) {
 // blockIdx.x: split, row tile, key head; blockIdx.y: request.
 template <typename T, int D, int NT>
 __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 3)
-window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ CUtensorMap tm_v,
-              const __grid_constant__ WindowArgs a) {
+window_kernel(const __grid_constant__ WindowArgs a) {
     using R = Ring<D>;
     constexpr int BLOCKS = D / 32;      // of K's and V's scales in a row
-    constexpr int VW = D / 64;          // words of a V row that a lane takes
+    constexpr int KW = D / 32, VW = D / 64;  // words of a K row and of a V row that a lane takes
     constexpr int TILES = D / 16;       // of O^T: 16 columns of D each
     constexpr int kRows = 8 * NT;
-    extern __shared__ uint8_t smem_raw[];
-    const uint32_t smem0 = (smem_u32(smem_raw) + 1023u) & ~1023u;
-    uint8_t* smem = smem_raw + (smem0 - smem_u32(smem_raw));
+    extern __shared__ __align__(128) uint8_t smem[];
+    const uint32_t smem0 = smem_u32(smem);
     pdl_wait();
     pdl_trigger();
 
@@ -151,7 +159,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         return kWindowStep * (v < sink_steps ? v : v - sink_steps + from);
     };
 
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::OFF_BAR) + warp * kStages;
+    uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::SMEM) - (warp + 1) * kStages;
     const uint32_t ring = smem0 + warp * kStages * R::STAGE;
     if (lane < kStages) mbar_init(full + lane, 1);
     fence_barrier_init();
@@ -193,11 +201,12 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 if (h == 1 && whole) break;
-                const int row = (pages[h] * a.Hkv + hk) * a.page_size + ((base + 16 * h) & (a.page_size - 1));
-                tma_rows(dst + h * 16 * R::ROW, &tm_k, bar, row);
-                tma_rows(dst + R::OFF_V + h * 16 * R::ROW, &tm_v, bar, row);
-                bulk_rows(dst + R::OFF_KSF + h * 16 * BLOCKS, a.k_sf + (long long)row * BLOCKS, unit * BLOCKS, bar);
-                bulk_rows(dst + R::OFF_VSF + h * 16 * BLOCKS, a.v_sf + (long long)row * BLOCKS, unit * BLOCKS, bar);
+                const long long row =
+                    (pages[h] * a.Hkv + hk) * a.page_size + ((base + 16 * h) & (a.page_size - 1));
+                bulk_rows(dst + h * 16 * R::ROW, a.k_codes + row * R::ROW, unit * R::ROW, bar);
+                bulk_rows(dst + R::OFF_V + h * 16 * R::ROW, a.v_codes + row * R::ROW, unit * R::ROW, bar);
+                bulk_rows(dst + R::OFF_KSF + h * 16 * BLOCKS, a.k_sf + row * BLOCKS, unit * BLOCKS, bar);
+                bulk_rows(dst + R::OFF_VSF + h * 16 * BLOCKS, a.v_sf + row * BLOCKS, unit * BLOCKS, bar);
             }
         }
         __syncwarp();
@@ -206,34 +215,36 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     for (int i = 0; i < kStages; ++i)
         if (i < mine) fetch(i);
 
-    // q as the products' second operand: row g of each eight; block b's two steps of 16 columns take
-    // columns 8 t .. 8 t + 7 of it (in the order of a word of codes)
-    uint32_t qf[NT][BLOCKS][4];
-    float zscale[NT][2];   // of this thread's columns of S^T: rows 2 t and 2 t + 1
-    int see[NT][2], wl[NT][2];
+    // q as the products' second operand: row g of each eight, a quarter of its columns per lane; the i-th step of 16
+    // columns takes 4 i .. 4 i + 3 of each quarter (as the words of codes have them)
+    uint32_t qf[NT][KW][4];
+    float2* const row_info = reinterpret_cast<float2*>(smem + R::OFF_ROWS);  // read in steps that are not plain
+    float zscale[NT][2];  // the logits' factors at 2^EK, of this thread's columns of S^T: rows 2 t and 2 t + 1
+    const float scale = a.scale_log2;
 #pragma unroll
     for (int n = 0; n < NT; ++n) {
         const int i = n * 8 + g;
         const bool live = row0 + i < rows;
         const long long row = live ? query_row(i) : 0;
-        const T* q = static_cast<const T*>(a.q) + row / a.Hq * a.q_stride + row % a.Hq * D + t * 8;
-        uint4 raw[BLOCKS];
+        const T* q = static_cast<const T*>(a.q) + row / a.Hq * a.q_stride + row % a.Hq * D + t * (D / 4);
+        uint4 raw[KW];
 #pragma unroll
-        for (int k = 0; k < BLOCKS; ++k)
-            raw[k] = live ? *reinterpret_cast<const uint4*>(q + k * 32) : make_uint4(0u, 0u, 0u, 0u);
+        for (int k = 0; k < KW; ++k)
+            raw[k] = live ? *reinterpret_cast<const uint4*>(q + k * 8) : make_uint4(0u, 0u, 0u, 0u);
         float factor = 1.f;
+        const uint32_t flip = scale < 0.f ? 0x80008000u : 0u;  // the scale's sign goes to q
         if constexpr (std::is_same<T, __half>::value) {
 #pragma unroll
-            for (int k = 0; k < BLOCKS; ++k) {
-                qf[n][k][0] = raw[k].x;
-                qf[n][k][1] = raw[k].y;
-                qf[n][k][2] = raw[k].z;
-                qf[n][k][3] = raw[k].w;
+            for (int k = 0; k < KW; ++k) {
+                qf[n][k][0] = raw[k].x ^ flip;
+                qf[n][k][1] = raw[k].y ^ flip;
+                qf[n][k][2] = raw[k].z ^ flip;
+                qf[n][k][3] = raw[k].w ^ flip;
             }
         } else {
             uint32_t top = 0;  // the largest magnitude's bits
 #pragma unroll
-            for (int k = 0; k < BLOCKS; ++k) {
+            for (int k = 0; k < KW; ++k) {
                 const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) top = max(top, max(w[j] << 16 & 0x7fff0000u, w[j] & 0x7fff0000u));
@@ -247,38 +258,24 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
             // a row that is not finite has no results
             factor = ex == 255 ? NAN : __int_as_float((127 - up) << 23);
 #pragma unroll
-            for (int k = 0; k < BLOCKS; ++k) {
+            for (int k = 0; k < KW; ++k) {
                 const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    qf[n][k][j] = pack2<__half>(__uint_as_float(w[j] << 16) * f, __uint_as_float(w[j] & 0xffff0000u) * f);
+                    qf[n][k][j] = flip ^ pack2<__half>(__uint_as_float(w[j] << 16) * f,
+                                                       __uint_as_float(w[j] & 0xffff0000u) * f);
             }
         }
-#pragma unroll
-        for (int j = 0; j < 2; ++j) {
-            const int r = row0 + n * 8 + 2 * t + j;
-            // K's powers are taken 1.5 times what they are (see there)
-            zscale[n][j] = __shfl_sync(~0u, factor, (2 * t + j) * 4) * (a.scale_log2 * (2.f / 3.f));
-            const int p = pos0 + r / a.G;
-            see[n][j] = r < rows ? min(p + 1, sp.len) : 0;
-            wl[n][j] = a.window > 0 ? p - a.window + 1 : 0;
-        }
+        if (warp == 0 && t == 0)
+            row_info[i] = make_float2(factor * fabsf(scale), __int_as_float(live ? pos0 + (row0 + i) / a.G : -1));
     }
+    __syncthreads();
     const int all_see = low + 1, all_from = a.window > 0 ? high - a.window + 1 : 0;  // of every row
 
-    // This lane's key of row g of the products, and its keys of V: kv0, + kvd, + 8, + 8 + kvd.  The first
-    // product's transpose hands over the weights of keys key_of(2 t), key_of(2 t + 1).
-    constexpr int kvd = D == 128 ? 2 : 4;
-    const int kg = D == 128 ? (g & 4) | (g & 1) << 1 | (g >> 1 & 1) : (g >> 1) | (g & 1) << 2;
-    const int kv0 = D == 128 ? (t & 1) | (t & 2) << 1 : t;
-    const int vblock = g / (8 / BLOCKS);  // of this lane's columns of V
-    auto k_at = [&](int key, int block) {
-        return key * R::ROW + 16 * (D == 128 ? block ^ (key >> 1 & 3) : block ^ (key >> 2 & 1)) + 4 * t;
-    };
-    auto v_at = [&](int key) {
-        return D == 128 ? key * 64 + 16 * ((g >> 1) ^ (key >> 1 & 3)) + 8 * (g & 1)
-                        : key * 32 + 16 * ((g >> 2) ^ (key >> 2 & 1)) + 4 * (g & 3);
-    };
+    // This lane's key of row g of the products, kg, and its keys of V: t, t + 4, + 8 and + 12.  The first product's
+    // transpose hands over the weights of the keys of rows 2 t and 2 t + 1.
+    const int kg = g >> 1 | (g & 1) << 2;
+    const int kblock = t / (4 / BLOCKS), vblock = g / (8 / BLOCKS);  // of this lane's columns
 
     float o[NT][TILES][4], m[NT][2], l[NT][2];
 #pragma unroll
@@ -290,7 +287,18 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         m[n][0] = m[n][1] = -INFINITY;
         l[n][0] = l[n][1] = 0.f;
     }
-    int E = 0;  // o's unit is 2^E (biased as the scales) over 2^13
+    int E = 0, EK = 0;  // units of o and of S are 2^E and 2^EK (biased as the scales) over 2^13
+    auto scale_logits = [&] {
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                // within the normal numbers: a masked logit times it stays -inf, a logit of 0 stays 0
+                const float z = times_pow2(row_info[n * 8 + 2 * t + j].x, EK - 140);
+                zscale[n][j] = z > 0x1p-126f ? fminf(z, 0x1p127f) : z <= 0x1p-126f ? 0x1p-126f : z;
+            }
+    };
+    scale_logits();
     bool ok = true;
     int i = 0;
     for (; i < mine; ++i) {
@@ -300,80 +308,116 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         const int base = base_of(i);
         const bool plain = base + kWindowStep <= all_see && (base >= all_from || base + kWindowStep <= a.sink);
 
-        // ---- S^T of the two halves of 16 keys
-        float s[2][NT][4];
-#pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            uint32_t sf[2];  // of keys kg and kg + 8
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                if constexpr (BLOCKS == 4) {
-                    asm volatile("ld.shared.b32 %0, [%1];" : "=r"(sf[k]) : "r"(at + R::OFF_KSF + (h * 16 + kg + 8 * k) * 4));
-                } else {
-                    uint16_t x;
-                    asm volatile("ld.shared.u16 %0, [%1];" : "=h"(x) : "r"(at + R::OFF_KSF + (h * 16 + kg + 8 * k) * 2));
-                    sf[k] = x;
-                }
-            }
-#pragma unroll
-            for (int k = 0; k < BLOCKS; ++k) {
-                uint32_t w[2][1], x0[4], x1[4];
-                lds<1>(at + h * 16 * R::ROW + k_at(kg, k), w[0]);
-                lds<1>(at + h * 16 * R::ROW + k_at(kg, k) + 8 * R::ROW, w[1]);
-                expand8(w[0][0], x0);
-                expand8(w[1][0], x1);
-                // 1.5 * 2^(sf - 127): the fraction bit makes a scale of 255 a NaN (0 becomes 2^-127)
-                float f[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    f[j] = __uint_as_float(((k < 3 ? sf[j] << (23 - 8 * k) : sf[j] >> 1) & 0x7f800000u) | 0x00400000u);
-#pragma unroll
-                for (int n = 0; n < NT; ++n) {
-                    float c[4] = {0.f, 0.f, 0.f, 0.f};
-                    mma_f16(c, x0[0], x1[0], x0[1], x1[1], qf[n][k][0], qf[n][k][1]);
-                    mma_f16(c, x0[2], x1[2], x0[3], x1[3], qf[n][k][2], qf[n][k][3]);
-#pragma unroll
-                    for (int j = 0; j < 4; ++j) s[h][n][j] = k == 0 ? c[j] * f[j >> 1] : fmaf(c[j], f[j >> 1], s[h][n][j]);
-                }
-            }
-        }
-
-        // ---- V's scales: pairs of this lane's keys, and whether E and its band hold them
-        uint32_t vs[2][2];  // [half][keys kv0, kv0 + kvd; then both + 8]
+        // ---- scales: whether the running powers and their bands hold them
+        uint32_t ks[2][2];  // [half][keys kg, kg + 8]
+        uint32_t vs[2][2];  // [half][keys t, t + 4; then both + 8]
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
             for (int k = 0; k < 2; ++k) {
-                uint32_t x[2];
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-                    asm volatile("ld.shared.u8 %0, [%1];"
-                                 : "=r"(x[j])
-                                 : "r"(at + R::OFF_VSF + (h * 16 + kv0 + 8 * k + kvd * j) * BLOCKS + vblock));
-                vs[h][k] = x[0] | x[1] << 16;
+                ks[h][k] = lds8(at + R::OFF_KSF + kblock + kg * BLOCKS + (h * 16 + 8 * k) * BLOCKS);
+                const uint32_t v = at + R::OFF_VSF + vblock + t * BLOCKS + (h * 16 + 8 * k) * BLOCKS;
+                vs[h][k] = lds8(v) | lds8(v + 4 * BLOCKS) << 16;
             }
-        uint32_t pending = 0xffu;  // bit 4 h + 2 k + j: a key that a row sees and whose V is still to be added
-        if (!plain) {
-            pending = 0;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                const int key = base + (j >> 2) * 16 + (j >> 1 & 1) * 8 + (j & 1) * kvd + kv0;
-                if (key < hi && (key < sink || key >= wlo)) pending |= 1u << j;
-            }
+        bool slow;
+        {
+            const uint32_t k0 = ks[0][0] | ks[0][1] << 16, k1 = ks[1][0] | ks[1][1] << 16;
+            const uint32_t mostk = __vmaxu2(k0, k1), leastk = __vminu2(k0, k1);
+            const uint32_t most = __vmaxu2(__vmaxu2(vs[0][0], vs[0][1]), __vmaxu2(vs[1][0], vs[1][1]));
+            const uint32_t least = __vminu2(__vminu2(vs[0][0], vs[0][1]), __vminu2(vs[1][0], vs[1][1]));
+            slow = __any_sync(~0u, !plain || (int)max(most & 0xffffu, most >> 16) > E ||
+                                       (int)min(least & 0xffffu, least >> 16) < E - kBand ||
+                                       (int)max(mostk & 0xffffu, mostk >> 16) > EK ||
+                                       (int)min(leastk & 0xffffu, leastk >> 16) < EK - kBand);
         }
-        const uint32_t most = __vmaxu2(__vmaxu2(vs[0][0], vs[0][1]), __vmaxu2(vs[1][0], vs[1][1]));
-        const uint32_t least = __vminu2(__vminu2(vs[0][0], vs[0][1]), __vminu2(vs[1][0], vs[1][1]));
-        const bool slow = __any_sync(~0u, !plain || (int)max(most & 0xffffu, most >> 16) > E ||
-                                              (int)min(least & 0xffffu, least >> 16) < E - kBand);
+        // a key of the step that a row of the tile sees
+        auto seen = [&](int in) {
+            const int key = base + in;
+            return plain || (key < hi && (key < sink || key >= wlo));
+        };
+
+        // ---- S^T of the two halves of 16 keys: K's codes times 2^(field - 15), both halves of `sc` the same
+        float s[2][NT][4];
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[h][n][j] = 0.f;
+        auto add_s = [&](const uint32_t (&sc)[2][2], auto direct, float unit) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                uint32_t w[2][KW];
+                lds<KW>(at + (h * 16 + kg) * R::ROW + t * (R::ROW / 4), w[0]);
+                lds<KW>(at + (h * 16 + kg) * R::ROW + t * (R::ROW / 4) + 8 * R::ROW, w[1]);
+                float c[NT][4];
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) c[n][j] = 0.f;
+#pragma unroll
+                for (int k = 0; k < KW; ++k) {
+                    uint32_t x0[4], x1[4];
+                    expand8(w[0][k], x0);
+                    expand8(w[1][k], x1);
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        x0[j] = hmul2(x0[j], sc[h][0]);
+                        x1[j] = hmul2(x1[j], sc[h][1]);
+                    }
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        mma_f16(c[n], x0[0], x1[0], x0[1], x1[1], qf[n][k][0], qf[n][k][1]);
+                        mma_f16(c[n], x0[2], x1[2], x0[3], x1[3], qf[n][k][2], qf[n][k][3]);
+                    }
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        s[h][n][j] = decltype(direct)::value ? c[n][j] : fmaf(c[n][j], unit, s[h][n][j]);
+            }
+        };
+        if (!slow) {
+            uint32_t sc[2][2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int k = 0; k < 2; ++k) sc[h][k] = ks[h][k] * 0x04000400u + (uint32_t)(kTopField - EK) * 0x04000400u;
+            add_s(sc, std::true_type{}, 1.f);
+        } else {
+            uint32_t pending = 0;  // bit 2 h + k: a key that a row sees and whose block is still to be added
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (seen((j >> 1) * 16 + kg + 8 * (j & 1))) pending |= 1u << j;
+            do {
+                int top = 0;
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    if (pending >> j & 1 && ks[j >> 1][j & 1] != 255u) top = max(top, (int)ks[j >> 1][j & 1]);
+                top = __reduce_max_sync(~0u, top);
+                if (top > EK) EK = min(top + kMargin, 254);  // (in the first pass: nothing has been added)
+                const int Eb = top < EK - kBand / 2 ? top : EK;  // this pass's unit
+                uint32_t sc[2][2];
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int k = 0; k < 2; ++k) {
+                        const int bit = 2 * h + k, x = (int)ks[h][k];
+                        const bool in = pending >> bit & 1 && x >= Eb - kBand;
+                        // a scale of 255: the key's logits are NaN
+                        sc[h][k] = !in ? 0u : x == 255 ? 0x7e007e00u : (uint32_t)(x - Eb + kTopField) * 0x04000400u;
+                        if (in) pending &= ~(1u << bit);
+                    }
+                add_s(sc, std::false_type{}, times_pow2(1.f, max(Eb - EK, -250)));
+            } while (__any_sync(~0u, pending != 0));
+            scale_logits();
+        }
 
         // ---- softmax
         uint32_t p[2][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[h][n][j] *= zscale[n][j & 1];
             if (slow) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
@@ -383,17 +427,15 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                         // a V scale of 255 counts as a NaN logit of the rows that see it
                         uint32_t x = 0;
 #pragma unroll
-                        for (int k = 0; k < BLOCKS; ++k) {
-                            uint32_t y;
-                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(y) : "r"(at + R::OFF_VSF + in * BLOCKS + k));
-                            x = max(x, y);
-                        }
+                        for (int k = 0; k < BLOCKS; ++k) x = max(x, lds8(at + R::OFF_VSF + in * BLOCKS + k));
                         if (x == 255u) s[h][n][j] = NAN;
-                        if (!(key < see[n][j & 1] && (key < a.sink || key >= wl[n][j & 1]))) s[h][n][j] = -INFINITY;
+                        const int pos = __float_as_int(row_info[n * 8 + 2 * t + (j & 1)].y);
+                        if (key > pos || key >= sp.len || (a.window > 0 && key >= a.sink && key <= pos - a.window))
+                            s[h][n][j] = -INFINITY;
                     }
             }
-            float x0 = fmaxf(fmaxf(s[0][n][0], s[0][n][2]), fmaxf(s[1][n][0], s[1][n][2]));
-            float x1 = fmaxf(fmaxf(s[0][n][1], s[0][n][3]), fmaxf(s[1][n][1], s[1][n][3]));
+            float x0 = fmaxf(fmaxf(s[0][n][0], s[0][n][2]), fmaxf(s[1][n][0], s[1][n][2])) * zscale[n][0];
+            float x1 = fmaxf(fmaxf(s[0][n][1], s[0][n][3]), fmaxf(s[1][n][1], s[1][n][3])) * zscale[n][1];
             if (__any_sync(~0u, x0 > m[n][0] + kRenew || x1 > m[n][1] + kRenew)) {
 #pragma unroll
                 for (int d = 4; d < 32; d *= 2) {
@@ -416,14 +458,14 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 }
             }
             // rows that have seen no key yet keep m = -inf: their weights are 0
-            const float b0 = m[n][0] == -INFINITY ? 0.f : m[n][0] - kLift;
-            const float b1 = m[n][1] == -INFINITY ? 0.f : m[n][1] - kLift;
+            const float b0 = m[n][0] == -INFINITY ? 0.f : kLift - m[n][0];
+            const float b1 = m[n][1] == -INFINITY ? 0.f : kLift - m[n][1];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                s[h][n][0] = exp2_approx(s[h][n][0] - b0);
-                s[h][n][1] = exp2_approx(s[h][n][1] - b1);
-                s[h][n][2] = exp2_approx(s[h][n][2] - b0);
-                s[h][n][3] = exp2_approx(s[h][n][3] - b1);
+                s[h][n][0] = exp2_approx(fmaf(s[h][n][0], zscale[n][0], b0));
+                s[h][n][1] = exp2_approx(fmaf(s[h][n][1], zscale[n][1], b1));
+                s[h][n][2] = exp2_approx(fmaf(s[h][n][2], zscale[n][0], b0));
+                s[h][n][3] = exp2_approx(fmaf(s[h][n][3], zscale[n][1], b1));
                 l[n][0] += s[h][n][0] + s[h][n][2];
                 l[n][1] += s[h][n][1] + s[h][n][3];
                 p[h][n][0] = transpose8(pack2<__half>(s[h][n][0], s[h][n][1]));
@@ -436,10 +478,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
         auto add_v = [&](const uint32_t (&sc)[2][2], auto direct, float unit) {
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                uint32_t w[4][VW];  // keys kv0, kv0 + kvd, and both + 8
+                uint32_t w[4][VW];  // keys t, t + 4, t + 8, t + 12
 #pragma unroll
                 for (int k = 0; k < 4; ++k)
-                    lds<VW>(at + R::OFF_V + h * 16 * R::ROW + v_at(kv0 + (k & 1) * kvd + (k >> 1) * 8), w[k]);
+                    lds<VW>(at + R::OFF_V + t * R::ROW + g * (R::ROW / 8) + (h * 16 + 4 * k) * R::ROW, w[k]);
 #pragma unroll
                 for (int v = 0; v < VW; ++v) {
                     // nibbles of two keys side by side: even and odd columns
@@ -481,6 +523,10 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
                 for (int k = 0; k < 2; ++k) sc[h][k] = (vs[h][k] + c) << 10;
             add_v(sc, std::true_type{}, 1.f);
         } else {
+            uint32_t pending = 0;  // bit 4 h + 2 k + j: a key that a row sees and whose V is still to be added
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                if (seen((j >> 2) * 16 + (j >> 1 & 1) * 8 + (j & 1) * 4 + t)) pending |= 1u << j;
             do {
                 // the largest scale still to be taken, of the block's four lanes
                 int top = 0;
@@ -538,7 +584,7 @@ window_kernel(const __grid_constant__ CUtensorMap tm_k, const __grid_constant__ 
     float* so = reinterpret_cast<float*>(smem);       // [warps][rows][kPitch]
     float* sm = so + kWarps * kRows * kPitch;         // [warps][rows] maxima, then sums
     float* sl = sm + kWarps * kRows;
-    static_assert(kWarps * kRows * (kPitch + 2) * 4 <= R::OFF_BAR, "");
+    static_assert(kWarps * kRows * (kPitch + 2) * 4 <= R::JOIN, "");
 #pragma unroll
     for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -644,16 +690,11 @@ __global__ void __launch_bounds__(kJoinThreads) window_join_kernel(const __grid_
 }
 
 template <typename T, int D, int NT> cudaError_t launch_rows(const WindowArgs& a, cudaStream_t s) {
-    const int unit = a.page_size >= kWindowStep ? kWindowStep : 16;
-    const long long rows = (long long)a.pages * a.Hkv * a.page_size;
-    CUtensorMap k, v;
-    if (code_map(&k, a.k_codes, D, rows, unit) != CUDA_SUCCESS || code_map(&v, a.v_codes, D, rows, unit) != CUDA_SUCCESS)
-        return cudaErrorInvalidValue;
     static PerDevice ready;
     const cudaError_t e = allow_smem(ready, window_kernel<T, D, NT>, Ring<D>::SMEM);
     if (e != cudaSuccess) return e;
     return launch_k(window_kernel<T, D, NT>, dim3((unsigned)(a.splits * a.row_tiles * a.Hkv), (unsigned)a.B),
-                    dim3(kWarps * 32), Ring<D>::SMEM, s, true, k, v, a);
+                    dim3(kWarps * 32), Ring<D>::SMEM, s, true, a);
 }
 
 template <typename T, int D>
