@@ -98,7 +98,9 @@ typedef struct idx_options {
                              at; default sqrt(cap/topk).  Test knob to force short or
                              overflowing rows. */
     int sample_stride;    /* odd stride S of the threshold sample; 0 = automatic */
-    int row_split;        /* standalone top-k row split, see below */
+    int row_split;        /* standalone top-k row split, see below;
+                             idx_window_attention_mxfp4: 0 the cheaper path, -1 tiles of few
+                             rows, 1 the tensor cores' dense path */
     int* d_status;        /* optional device int receiving IDX_DEV_* bits */
     idx_stats* d_stats;   /* optional device counters */
     int relative_rows;    /* idx_topk_from_scores: row r's visible scores start at
@@ -112,8 +114,8 @@ typedef struct idx_options {
                              *d_status, leaving no copy or MMA in flight; the call
                              returns and its results are meaningless.  The parts of
                              idx_prefix_attention on the tensor cores' dense path (the
-                             prefix's, and private ones that take it) do the same with
-                             their key tile 1.  It exists to run the timeout unwind on
+                             prefix's, and private ones that take it) and the dense path of
+                             idx_window_attention_mxfp4 do the same with their key tile 1.  It exists to run the timeout unwind on
                              purpose. */
     void* const* stage_events; /* optional array of cudaEvent_t, recorded on `stream`
                              at stage boundaries (NULL entries are skipped).
@@ -542,6 +544,11 @@ idx_status idx_cache_append_mxfp4(const void* k, long long k_stride, const void*
                                   idx_dtype dt, const idx_options* opt, void* stream);
 size_t idx_window_attention_mxfp4_workspace(int B, int T, int max_q, int Hq, int Hkv, int D,
                                             int max_len, int window, int sink);
+/* How such a call is cut on the current device: plan[0] splits of the keys that a tile of rows sees, plan[1]
+ * keys each, plan[2] 1 when the rows take the tensor cores' dense path (many rows per request and key head),
+ * plan[3] the most rows of a tile.  Nothing is launched. */
+idx_status idx_window_attention_mxfp4_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window,
+                                           int sink, int* plan);
 idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const uint8_t* k_codes,
                                       const uint8_t* k_sf, const uint8_t* v_codes,
                                       const uint8_t* v_sf, const int* table, const int* lens,

@@ -41,7 +41,8 @@ __all__ = [
     "idx_score_topk_mxfp4", "idx_score_materialise_mxfp4", "idx_add_rmsnorm_quant",
     "idx_prefix_attention", "idx_prefix_attention_workspace", "idx_prefix_attention_plan",
     "idx_cache_evict", "idx_cache_evict_workspace", "idx_cache_append_mxfp4",
-    "idx_window_attention_mxfp4", "idx_window_attention_mxfp4_workspace", "idx_cache_fork",
+    "idx_window_attention_mxfp4", "idx_window_attention_mxfp4_workspace",
+    "idx_window_attention_mxfp4_plan", "idx_cache_fork",
     "idx_cache_fork_workspace", "idx_cache_resize", "idx_cache_resize_workspace",
     "idx_cache_compact", "idx_cache_compact_workspace",
 ]
@@ -162,6 +163,8 @@ def load(path: str | None = None):
     lib.idx_cache_append_mxfp4.restype = I
     lib.idx_window_attention_mxfp4_workspace.argtypes = [I] * 9
     lib.idx_window_attention_mxfp4_workspace.restype = SZ
+    lib.idx_window_attention_mxfp4_plan.argtypes = [I] * 9 + [P]
+    lib.idx_window_attention_mxfp4_plan.restype = I
     lib.idx_window_attention_mxfp4.argtypes = [P, LL] + [P] * 7 + [I] * 8 + [LL, I, I, I, F, I, P, P, P, SZ, P, P]
     lib.idx_window_attention_mxfp4.restype = I
     lib.idx_cache_fork_workspace.argtypes = [I, LL]
@@ -724,6 +727,16 @@ def idx_window_attention_mxfp4_workspace(B: int, T: int, max_q: int, Hq: int, Hk
                                          max_len: int, window: int, sink: int) -> int:
     return int(load().idx_window_attention_mxfp4_workspace(B, T, max_q, Hq, Hkv, D, max_len,
                                                            window, sink))
+
+
+def idx_window_attention_mxfp4_plan(B: int, T: int, max_q: int, Hq: int, Hkv: int, D: int,
+                                    max_len: int, window: int, sink: int) -> dict:
+    """How such a call is cut: splits of the keys that a tile of rows sees, keys each, whether the
+    rows take the tensor cores' dense path, and the most rows of a tile."""
+    plan = (ctypes.c_int * 4)()
+    _check("idx_window_attention_mxfp4_plan", load().idx_window_attention_mxfp4_plan(
+        B, T, max_q, Hq, Hkv, D, max_len, window, sink, plan))
+    return dict(splits=plan[0], keys=plan[1], dense=bool(plan[2]), rows=plan[3])
 
 
 def idx_window_attention_mxfp4(q, k_codes, k_sf, v_codes, v_sf, table, lens, *, q_start=None,

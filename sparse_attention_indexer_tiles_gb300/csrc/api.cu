@@ -1298,7 +1298,20 @@ idx_status idx_cache_append_mxfp4(const void* k, long long k_stride, const void*
 size_t idx_window_attention_mxfp4_workspace(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window,
                                             int sink) {
     if (!window_sizes_ok(B, T, max_q, Hq, Hkv, D, max_len, window, sink)) return 0;
-    return window_plan(B, T, window_most_tokens(T, max_q), Hq, Hkv, D, max_len, window, sink, sm_count()).total;
+    return window_plan(B, T, window_most_tokens(T, max_q), Hq, Hkv, D, max_len, window, sink, 0, sm_count()).total;
+}
+
+idx_status idx_window_attention_mxfp4_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window,
+                                           int sink, int* plan) {
+    if (!plan) return IDX_EINVAL;
+    if (!window_sizes_ok(B, T, max_q, Hq, Hkv, D, max_len, window, sink)) return IDX_EUNSUPPORTED;
+    const WindowPlan p =
+        window_plan(B, T, window_most_tokens(T, max_q), Hq, Hkv, D, max_len, window, sink, 0, sm_count());
+    plan[0] = p.splits;
+    plan[1] = p.chunk * (p.dense ? window_dense_keys(D) : kWindowStep);
+    plan[2] = p.dense;
+    plan[3] = p.dense ? 2 * (128 / (Hq / Hkv)) * (Hq / Hkv) : p.tile_rows;
+    return IDX_OK;
 }
 
 idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const uint8_t* k_codes, const uint8_t* k_sf,
@@ -1324,7 +1337,7 @@ idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const u
         !aligned(k_sf, 16) || !aligned(v_codes, 16) || !aligned(v_sf, 16) || !aligned(table, 4) || !aligned(lens, 4) ||
         !aligned(q_start, 4) || !aligned(lse, 4))
         return IDX_EALIGN;
-    const WindowPlan p = window_plan(B, T, max_q, Hq, Hkv, D, max_len, window, sink, sm_count());
+    const WindowPlan p = window_plan(B, T, max_q, Hq, Hkv, D, max_len, window, sink, opt ? opt->row_split : 0, sm_count());
     if ((double)p.splits * p.row_tiles * Hkv * (p.dense ? B : 1) > 0x7fffffff) return IDX_EUNSUPPORTED;
     if (p.total > 0 && (!ws || ws_bytes < p.total)) return IDX_EWORKSPACE;
     if (!aligned(ws, 256)) return IDX_EALIGN;

@@ -15,8 +15,8 @@
 // 2^-31 count as 0.  Maxima, sums and o are fp32, exponentials base 2 on z * log2(e).
 //
 // HBM-bound in theory (68 bytes per key row of 128); in practice the instructions that expand the codes come close. A
-// block's warps each take 32 keys at a time through a ring of their own, four bulk copies a step (of 64 and 4
-// bytes per key: tensor copies of swizzled rows took 9 % longer).  The products are taken transposed, S^T = K Q^T
+// block's warps each take 32 keys at a time through a ring of their own, filled by the lanes' 16-byte copies (bulk
+// copies of a step's rows cost more instructions to issue; tensor copies of swizzled rows took 9 % longer still).  The products are taken transposed, S^T = K Q^T
 // and O^T += V^T P^T: keys and D are the long axes of the matrix instructions, the rows (8 or 16) the short one.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -47,12 +47,11 @@ template <int D> struct Ring {
     static constexpr int SF = kWindowStep * (D / 32);
     static constexpr int OFF_V = CODES, OFF_KSF = 2 * CODES, OFF_VSF = 2 * CODES + SF;
     static constexpr int STAGE = 2 * CODES + 2 * SF;
-    static constexpr int BYTES = 2 * CODES + 2 * SF;         // that land per stage
-    static constexpr int OFF_BAR = kWarps * kStages * STAGE;
+    static constexpr int RING = kWarps * kStages * STAGE;
     static_assert(STAGE % 128 == 0, "");
     static constexpr int JOIN = kWarps * 16 * (D + 6) * 4;   // of 16 rows
-    static constexpr int OFF_ROWS = OFF_BAR > JOIN ? OFF_BAR : JOIN;  // per row: its logits' factor, its position
-    static constexpr int SMEM = OFF_ROWS + 16 * 8 + kWarps * kStages * 8;
+    static constexpr int OFF_ROWS = RING > JOIN ? RING : JOIN;  // per row: its logits' factor, its position
+    static constexpr int SMEM = OFF_ROWS + 16 * 8;
 };
 
 // Eight e2m1 codes as fp16, pairs in order.
@@ -99,6 +98,12 @@ template <int N> IDX_DEVI void lds(uint32_t addr, uint32_t (&w)[N]) {
                      : "r"(addr));
     }
 }
+// 16-byte asynchronous copies, past L1, in groups.
+IDX_DEVI void copy16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
+}
+IDX_DEVI void copies_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N> IDX_DEVI void copies_wait() { asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory"); }
 IDX_DEVI uint32_t lds8(uint32_t addr) {
     uint32_t v;
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
@@ -159,12 +164,7 @@ window_kernel(const __grid_constant__ WindowArgs a) {
         return kWindowStep * (v < sink_steps ? v : v - sink_steps + from);
     };
 
-    uint64_t* full = reinterpret_cast<uint64_t*>(smem + R::SMEM) - (warp + 1) * kStages;
     const uint32_t ring = smem0 + warp * kStages * R::STAGE;
-    if (lane < kStages) mbar_init(full + lane, 1);
-    fence_barrier_init();
-    __syncwarp();
-
     // Pages of the warp's next steps, one 16-key half per lane: 16 steps at a time.  A half that no
     // row sees is not looked up (its page may be gone): page 0 is read for it, and masked.
     const int* table = a.table + b * a.table_stride;
@@ -186,34 +186,44 @@ window_kernel(const __grid_constant__ WindowArgs a) {
         }
     };
     const bool whole = a.page_size >= kWindowStep;  // a step lies in one page
+    // The copies of a step: codes of 16 keys are kHalf adjacent 16-byte chunks, dealt to the lanes; scales a chunk for
+    // each of the first lanes, K's and then V's.
+    constexpr int kHalf = R::ROW, kSfChunks = R::SF / 16;
+    const uint8_t* const sf = lane < kSfChunks ? a.k_sf : a.v_sf;
+    const int sf_chunk = lane & (kSfChunks - 1);
     auto fetch = [&](int i) {
         if (i - pages_from >= 16 || i == 0) look_up(i);
         const int base = base_of(i);
-        const int p0 = __shfl_sync(~0u, page_of, 2 * (i - pages_from));
-        const int p1 = __shfl_sync(~0u, page_of, 2 * (i - pages_from) + 1);
-        // (a page that only its second half is seen of)
-        const int pages[2] = {whole ? max(p0, p1) : p0, p1};
-        if (lane == 0 && i != a.withhold_step) {
-            uint64_t* bar = full + i % kStages;
-            const uint32_t dst = ring + i % kStages * R::STAGE;
-            const int unit = whole ? kWindowStep : 16;
-            mbar_arrive_expect_tx(bar, R::BYTES);
+        int p0 = __shfl_sync(~0u, page_of, 2 * (i - pages_from));
+        int p1 = __shfl_sync(~0u, page_of, 2 * (i - pages_from) + 1);
+        if (whole) p0 = p1 = max(p0, p1);  // (a page that only its second half is seen of)
+        const int in_page = base & (a.page_size - 1);
+        const long long row0 = (long long)(p0 * a.Hkv + hk) * a.page_size + in_page;
+        const long long row1 = whole ? row0 + 16 : (long long)(p1 * a.Hkv + hk) * a.page_size;
+        const uint32_t dst = ring + i % kStages * R::STAGE + lane * 16;
+        const uint8_t* const k0 = a.k_codes + row0 * R::ROW + lane * 16;
+        const uint8_t* const k1 = a.k_codes + row1 * R::ROW + lane * 16;
+        const uint8_t* const v0 = a.v_codes + row0 * R::ROW + lane * 16;
+        const uint8_t* const v1 = a.v_codes + row1 * R::ROW + lane * 16;
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                if (h == 1 && whole) break;
-                const long long row =
-                    (pages[h] * a.Hkv + hk) * a.page_size + ((base + 16 * h) & (a.page_size - 1));
-                bulk_rows(dst + h * 16 * R::ROW, a.k_codes + row * R::ROW, unit * R::ROW, bar);
-                bulk_rows(dst + R::OFF_V + h * 16 * R::ROW, a.v_codes + row * R::ROW, unit * R::ROW, bar);
-                bulk_rows(dst + R::OFF_KSF + h * 16 * BLOCKS, a.k_sf + row * BLOCKS, unit * BLOCKS, bar);
-                bulk_rows(dst + R::OFF_VSF + h * 16 * BLOCKS, a.v_sf + row * BLOCKS, unit * BLOCKS, bar);
-            }
+        for (int j = 0; j < kHalf; j += 32) {
+            copy16(dst + j * 16, k0 + j * 16);
+            copy16(dst + (kHalf + j) * 16, k1 + j * 16);
+            copy16(dst + R::OFF_V + j * 16, v0 + j * 16);
+            copy16(dst + R::OFF_V + (kHalf + j) * 16, v1 + j * 16);
         }
-        __syncwarp();
+        if (lane < 2 * kSfChunks) {
+            constexpr int kPerHalf = kSfChunks / 2;
+            const bool second = sf_chunk >= kPerHalf;
+            copy16(ring + i % kStages * R::STAGE + R::OFF_KSF + lane * 16,
+                   sf + (second ? row1 : row0) * BLOCKS + (second ? sf_chunk - kPerHalf : sf_chunk) * 16);
+        }
     };
 #pragma unroll
-    for (int i = 0; i < kStages; ++i)
+    for (int i = 0; i < kStages; ++i) {
         if (i < mine) fetch(i);
+        copies_commit();
+    }
 
     // q as the products' second operand: row g of each eight, a quarter of its columns per lane; the i-th step of 16
     // columns takes 4 i .. 4 i + 3 of each quarter (as the words of codes have them)
@@ -298,13 +308,23 @@ window_kernel(const __grid_constant__ WindowArgs a) {
                 zscale[n][j] = z > 0x1p-126f ? fminf(z, 0x1p127f) : z <= 0x1p-126f ? 0x1p-126f : z;
             }
     };
-    scale_logits();
-    bool ok = true;
-    int i = 0;
-    for (; i < mine; ++i) {
-        ok = __all_sync(~0u, mbar_wait(full + i % kStages, i / kStages & 1, nullptr, a.wait_limit));
-        if (!ok) break;
+    for (int i = 0; i < mine; ++i) {
+        copies_wait<kStages - 1>();
+        __syncwarp();
         const uint32_t at = ring + i % kStages * R::STAGE;
+        if (i == 0) {
+            // the first powers are a little above the first step's (of keys that no row sees, too: any will do)
+            int k = 0, v = 0;
+            for (int j = lane & 3; j < kWindowStep; j += 4) v = max(v, (int)lds8(at + R::OFF_VSF + j * BLOCKS + vblock));
+            v = max(v, __shfl_xor_sync(~0u, v, 1));
+            v = max(v, __shfl_xor_sync(~0u, v, 2));
+#pragma unroll
+            for (int j = 0; j < BLOCKS; ++j) k = max(k, (int)lds8(at + R::OFF_KSF + lane * BLOCKS + j));
+            k = __reduce_max_sync(~0u, k);
+            E = v < 255 ? min(v + kMargin, 254) : 0;
+            EK = k < 255 ? min(k + kMargin, 254) : 0;
+            scale_logits();
+        }
         const int base = base_of(i);
         const bool plain = base + kWindowStep <= all_see && (base >= all_from || base + kWindowStep <= a.sink);
 
@@ -319,17 +339,15 @@ window_kernel(const __grid_constant__ WindowArgs a) {
                 const uint32_t v = at + R::OFF_VSF + vblock + t * BLOCKS + (h * 16 + 8 * k) * BLOCKS;
                 vs[h][k] = lds8(v) | lds8(v + 4 * BLOCKS) << 16;
             }
-        bool slow;
-        {
-            const uint32_t k0 = ks[0][0] | ks[0][1] << 16, k1 = ks[1][0] | ks[1][1] << 16;
-            const uint32_t mostk = __vmaxu2(k0, k1), leastk = __vminu2(k0, k1);
-            const uint32_t most = __vmaxu2(__vmaxu2(vs[0][0], vs[0][1]), __vmaxu2(vs[1][0], vs[1][1]));
-            const uint32_t least = __vminu2(__vminu2(vs[0][0], vs[0][1]), __vminu2(vs[1][0], vs[1][1]));
-            slow = __any_sync(~0u, !plain || (int)max(most & 0xffffu, most >> 16) > E ||
-                                       (int)min(least & 0xffffu, least >> 16) < E - kBand ||
-                                       (int)max(mostk & 0xffffu, mostk >> 16) > EK ||
-                                       (int)min(leastk & 0xffffu, leastk >> 16) < EK - kBand);
-        }
+        bool out = !plain;
+#pragma unroll
+        for (int h = 0; h < 2; ++h)
+#pragma unroll
+            for (int k = 0; k < 2; ++k) out |= ks[h][k] - (uint32_t)(EK - kBand) > (uint32_t)kBand;
+        const uint32_t most = __vmaxu2(__vmaxu2(vs[0][0], vs[0][1]), __vmaxu2(vs[1][0], vs[1][1]));
+        const uint32_t least = __vminu2(__vminu2(vs[0][0], vs[0][1]), __vminu2(vs[1][0], vs[1][1]));
+        const uint32_t top = (uint32_t)E * 0x10001u, low_end = (uint32_t)max(E - kBand, 0) * 0x10001u;
+        const bool slow = __any_sync(~0u, out || __vmaxu2(most, top) != top || __vminu2(least, low_end) != low_end);
         // a key of the step that a row of the tile sees
         auto seen = [&](int in) {
             const int key = base + in;
@@ -516,11 +534,11 @@ window_kernel(const __grid_constant__ WindowArgs a) {
         };
         uint32_t sc[2][2];
         if (!slow) {
-            const uint32_t c = (uint32_t)(kTopField - E) * 0x10001u;
+            const uint32_t c = (uint32_t)(kTopField - E) * 0x04000400u;
 #pragma unroll
             for (int h = 0; h < 2; ++h)
 #pragma unroll
-                for (int k = 0; k < 2; ++k) sc[h][k] = (vs[h][k] + c) << 10;
+                for (int k = 0; k < 2; ++k) sc[h][k] = vs[h][k] * 1024u + c;
             add_v(sc, std::true_type{}, 1.f);
         } else {
             uint32_t pending = 0;  // bit 4 h + 2 k + j: a key that a row sees and whose V is still to be added
@@ -569,14 +587,10 @@ window_kernel(const __grid_constant__ WindowArgs a) {
         }
         __syncwarp();  // the stage has been read
         if (i + kStages < mine) fetch(i + kStages);
+        copies_commit();
     }
+    copies_wait<0>();
     if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
-    if (!ok) {
-        if (lane == 0) raise_status(a.d_status, IDX_DEV_TIMEOUT);
-        // nothing may be in flight when the block ends
-        for (const int sent = min(mine, i + kStages); i < sent; ++i)
-            if (i != a.withhold_step) mbar_wait(full + i % kStages, i / kStages & 1, nullptr, 1ll << 28);
-    }
 
     // ---- join the warps' states through shared memory
     __syncthreads();
@@ -718,7 +732,7 @@ cudaError_t launch_typed(const WindowArgs& a, const WindowPlan& p, cudaStream_t 
 constexpr size_t kRowSplits = 65536;
 constexpr int kMostSplits = 64;
 
-WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window, int sink,
+WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window, int sink, int path,
                        int sm_count) {
     WindowPlan p;
     const int G = Hq / Hkv;
@@ -727,6 +741,12 @@ WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_
     // keys that a tile of `tokens` tokens sees at most
     auto keys_of = [&](long long tokens) {
         return window == 0 ? (long long)max_len : std::min<long long>(max_len, (long long)window + sink + tokens);
+    };
+    // steps of `keys` keys that they lie in at most: those of the first tokens, and one more at either end of the window
+    auto steps_of = [&](long long tokens, int keys) {
+        const long long all = std::max<long long>(1, ((long long)max_len + keys - 1) / keys);
+        return window == 0 ? all
+                           : std::min(all, ((long long)sink + keys - 1) / keys + ((long long)window + tokens) / keys + 2);
     };
     // row tiles over the batch: of requests with max_q tokens, but no more than the call's tokens fill
     auto tiles_over = [&](long long per_request, double rows_per_tile) {
@@ -756,13 +776,13 @@ WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_
         p.chunk = (int)t * unit;
     };
     auto more = [](int s) { return s + (s < 8 ? 1 : s / 4); };
-    {
+    if (path <= 0) {
         // Tiles of 8 or 16 rows: `slots` blocks on an SM together take 128 keys of each of them in `unit_us` times
         // their number, or in the 0.4 us that one takes by itself; 3 us to start and end.
         const int tile_rows = most_rows <= 8 ? 8 : 16, slots = tile_rows == 8 ? 4 : 3;
         const double unit_us = (tile_rows == 8 ? 0.69 : 1.14) * D / 128;
         const long long tiles = (most_rows + tile_rows - 1) / tile_rows, tokens = (tile_rows + G - 1) / G + 1;
-        const long long units = std::max<long long>(1, (keys_of(tokens) + 3 * kWindowStep + 127) / 128);
+        const long long units = (steps_of(tokens, kWindowStep) + kWarps - 1) / kWarps;
         for (int s = 1; s <= kMostSplits && s <= units; s = more(s))
             consider(false, tile_rows, tiles, tiles_over(tiles, tile_rows), units, kWarps, s,
                      [&](long long t, double blocks) {
@@ -772,16 +792,15 @@ WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_
                                 (rest > 0 ? t * std::max(0.4, rest * unit_us) + 3.0 : 0.0);
                      });
     }
-    {
+    if (path > 0 || (path == 0 && most_rows > 16)) {
         // Dense: a CTA per SM takes a key tile for 256 rows in about 1 us, for 128 (two streams in turn) in 0.6.
         const int tokens = 128 / G;
         const long long pairs = ((max_q + tokens - 1) / tokens + 1) / 2;
-        const long long units = std::max<long long>(1, (keys_of(2 * tokens) + 2 * dense_keys - 1) / dense_keys);
+        const long long units = steps_of(2 * tokens, dense_keys);
         const double tile_us = max_q > tokens ? 1.0 : 0.6;
-        if (most_rows > 16)
-            for (int s = 1; s <= kMostSplits && s <= units; s = more(s))
-                consider(true, 128, pairs, tiles_over(pairs, 2.0 * tokens * G), units, 1, s,
-                         [&](long long t, double blocks) { return std::ceil(blocks / sm_count) * (t * tile_us + 9.0); });
+        for (int s = 1; s <= kMostSplits && s <= units; s = more(s))
+            consider(true, 128, pairs, tiles_over(pairs, 2.0 * tokens * G), units, 1, s,
+                     [&](long long t, double blocks) { return std::ceil(blocks / sm_count) * (t * tile_us + 9.0); });
     }
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     p.part = 0;

@@ -34,8 +34,8 @@ struct WindowArgs {
     int row_tiles;           // per request and key head (dense: pairs of them)
     int splits, chunk;       // steps of kWindowStep keys per split (dense: key tiles)
     float scale_log2;        // scale * log2(e)
-    long long wait_limit;    // SM clocks that a wait may take
-    int withhold_step;       // test only: a warp's step (dense: the key tile) that is never loaded, or -1
+    long long wait_limit;    // SM clocks that a wait of the dense path may take
+    int withhold_step;       // test only: the dense path's key tile that is never loaded, or -1
     int* d_status;
 };
 
@@ -45,7 +45,8 @@ struct WindowPlan {
     size_t part, part_lse, total;
 };
 
-WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window, int sink,
+// path: 0 the cheaper one, -1 tiles of few rows, 1 the dense path
+WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_len, int window, int sink, int path,
                        int sm_count);
 
 // The dense path: keys per tile, and the launch.

@@ -103,11 +103,12 @@ def test_requests_without_tokens_and_tokens_behind_the_last(idx):
     check_attention(got, attention(p["q"], p["cache"], p["table"], p["lens"], p["q_start"], 20, 2), torch.bfloat16, 70, 128)
 
 
-def test_rows_that_see_nothing(idx):
+@pytest.mark.parametrize("path", [-1, 1])
+def test_rows_that_see_nothing(idx, path):
     """More new tokens than slots: the first ones have no position."""
     p = problem([2, 0], [5, 3], 3, 1, 64, 16, "fp16")
-    check(idx, p)
-    check(idx, p, window=2, sink=1)
+    check(idx, p, options={"row_split": path})
+    check(idx, p, window=2, sink=1, options={"row_split": path})
 
 
 def test_long_rows_take_splits(idx):
@@ -219,8 +220,69 @@ def test_the_bound_on_the_new_tokens_does_not_matter(idx):
             check(idx, p, 64, 4, max_q=max_q, max_len=max_len)
 
 
+DENSE = {"row_split": 1}
+
+
 def test_a_wait_that_runs_out_is_reported(idx):
-    p = problem([2000], [1], 2, 1, 64, 64, "bf16")
-    got, st = call(idx, p, options={"test_stall_us": 2000})
+    """Only the dense path waits for copies."""
+    made = idx.idx_window_attention_mxfp4_plan(1, 600, 600, 64, 8, 64, 640, 0, 0)
+    assert made["dense"] and made["splits"] == 1     # every part has a second tile
+    got, st = call(idx, problem([600], [600], 8, 8, 64, 64, "bf16"), options={"test_stall_us": 2000})
     assert st & 1
-    check(idx, p)
+    check(idx, problem([300], [64], 8, 1, 64, 64, "bf16"), options=DENSE)
+
+
+@pytest.mark.parametrize("D,dt,window,sink", list(itertools.product([64, 128], ["bf16", "fp16"], [0, 1, 100], [0, 3, 90])))
+def test_the_dense_path(idx, D, dt, window, sink):
+    """Ragged requests, an odd and an even number of row tiles, tiles at the end of a page."""
+    p = problem([330, 61, 100], [130, 61, 70], 6, 2, D, 16, dt, seed=D + window, behind=2)
+    check(idx, p, window, sink, max_q=130, max_len=330, options=DENSE)
+
+
+@pytest.mark.parametrize("group", [1, 3, 40, 64, 128])
+def test_groups_on_the_dense_path(idx, group):
+    new = [200 if group == 1 else 70]
+    p = problem([600], new, group, 1, 64, 32, "bf16", seed=group)
+    check(idx, p, 64, 5, options=DENSE)
+
+
+def test_splits_of_the_dense_path(idx):
+    made = idx.idx_window_attention_mxfp4_plan(1, 20, 20, 16, 1, 128, 20000, 0, 0)
+    assert made["dense"] and made["splits"] > 1
+    check(idx, problem([20000], [20], 16, 1, 128, 64, "bf16", seed=6))
+    p = problem([6000], [20], 8, 1, 128, 64, "bf16", seed=6)
+    check(idx, p, options=DENSE)
+    check(idx, p, 2500, 100, options=DENSE)
+
+
+@pytest.mark.parametrize("where", ["k", "v"])
+def test_nan_scales_on_the_dense_path(idx, where):
+    p = problem([200, 150], [70, 90], 4, 2, 128, 16, "bf16", seed=4)
+    sf = p["cache"][1 if where == "k" else 3]
+    for b, slot in ((0, 150), (1, 149), (0, 3)):
+        sf[int(p["table"][b, slot // 16]), 1, slot % 16, 2] = 255
+    sf[int(p["table"][0, 12]), :, 8:] = 255      # past the last slot
+    check(idx, p, 30, 0, options=DENSE)
+    check(idx, p, 30, 4, options=DENSE)
+
+
+@pytest.mark.parametrize("dt,spread", [("bf16", 10), ("bf16", 40), ("fp16", 8)])
+def test_large_scales_on_the_dense_path(idx, dt, spread):
+    """Scales up to 2^(spread + 4): bf16 takes two products above 2^15."""
+    p = problem([200], [90], 4, 1, 128, 16, dt, seed=spread)
+    g = torch.Generator().manual_seed(spread)
+    sf = p["cache"][3]
+    sf[torch.rand(sf.shape, generator=g) < 0.3] = 127 + spread
+    p["cache"][1][:] -= 5
+    check(idx, p, options=DENSE)
+
+
+def test_a_prompt_in_chunks(idx):
+    """The same rows whether a prompt comes at once or in chunks: each chunk attends to what is in the cache."""
+    p = problem([400], [400], 4, 2, 64, 32, "fp16", seed=9)
+    whole = check(idx, p, 90, 7)
+    for lo, hi, path in ((0, 100, 1), (100, 101, 0), (101, 390, 1), (390, 400, -1)):
+        part = dict(p, q=p["q"][lo:hi].contiguous(), lens=torch.tensor([hi], dtype=torch.int32), q_start=starts([hi - lo]))
+        got = check(idx, part, 90, 7, max_len=400, options={"row_split": path})
+        err = (got[0].float() - whole[0][lo:hi].float()).abs().max()
+        assert err <= 2e-2
