@@ -81,10 +81,41 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
     const int lane = threadIdx.x & 31;
     const int token = (int)(((long long)blockIdx.x * kAppendThreads + threadIdx.x) >> 5);
     if (token >= a.T) return;
-    int b, end, first = 0;
+    const int per_head = a.D / 8, shift = a.D == 128 ? 4 : 3, units = a.Hkv * per_head;
+    const T* k = static_cast<const T*>(a.k) + token * a.k_stride;
+    const T* v = static_cast<const T*>(a.v) + token * a.v_stride;
+    auto load = [&](const T* x, int u) {
+        uint4 r;
+        if constexpr (WIDE) {
+            r = *reinterpret_cast<const uint4*>(x + u * 8);
+        } else {
+            const uint16_t* e = reinterpret_cast<const uint16_t*>(x) + u * 8;
+            r.x = e[0] | (uint32_t)e[1] << 16;
+            r.y = e[2] | (uint32_t)e[3] << 16;
+            r.z = e[4] | (uint32_t)e[5] << 16;
+            r.w = e[6] | (uint32_t)e[7] << 16;
+        }
+        return r;
+    };
+    // units is a multiple of 8 (D >= 64): four lanes of a block are in it together
+    constexpr int kDeep = WIDE ? 4 : 1;
+    uint4 rk[kDeep], rv[kDeep];
+    auto load_from = [&](int u0) {
+#pragma unroll
+        for (int i = 0; i < kDeep; ++i) {
+            const int u = u0 + i * 32 + lane;
+            rk[i] = u < units ? load(k, u) : make_uint4(0u, 0u, 0u, 0u);
+            rv[i] = u < units ? load(v, u) : make_uint4(0u, 0u, 0u, 0u);
+        }
+    };
+    // where the token goes takes a chain of loads: the row's first elements are on their way meanwhile (35k
+    // tokens 47 us with the chain first)
+    int b = 0, end = a.T, first = 0;
+    if (a.q_start && (token < a.q_start[0] || token >= a.q_start[a.B])) return;  // of no request
+    load_from(0);
     if (a.q_start) {
         b = request_of(a.q_start, a.B, token, lane);
-        if (b >= a.B) return;  // behind the last request
+        if (b >= a.B) return;  // (q_start out of order)
         first = a.q_start[b];
         end = a.q_start[b + 1];
     } else {
@@ -103,40 +134,16 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         if (lane == 0) raise_status(a.d_status, IDX_DEV_RANGE);
         return;
     }
-    const int per_head = a.D / 8, units = a.Hkv * per_head;
-    const T* k = static_cast<const T*>(a.k) + token * a.k_stride;
-    const T* v = static_cast<const T*>(a.v) + token * a.v_stride;
     const long long row0 = (long long)page * a.Hkv * a.page_size + (at & (a.page_size - 1));
-    auto load = [&](const T* x, int u) {
-        uint4 r;
-        if constexpr (WIDE) {
-            r = *reinterpret_cast<const uint4*>(x + u * 8);
-        } else {
-            const uint16_t* e = reinterpret_cast<const uint16_t*>(x) + u * 8;
-            r.x = e[0] | (uint32_t)e[1] << 16;
-            r.y = e[2] | (uint32_t)e[3] << 16;
-            r.z = e[4] | (uint32_t)e[5] << 16;
-            r.w = e[6] | (uint32_t)e[7] << 16;
-        }
-        return r;
-    };
-    // units is a multiple of 8 (D >= 64): four lanes of a block are in it together
-    constexpr int kDeep = WIDE ? 4 : 1;
     for (int u0 = 0; u0 < units; u0 += 32 * kDeep) {
-        uint4 rk[kDeep], rv[kDeep];
-#pragma unroll
-        for (int i = 0; i < kDeep; ++i) {
-            const int u = u0 + i * 32 + lane;
-            rk[i] = u < units ? load(k, u) : make_uint4(0u, 0u, 0u, 0u);
-            rv[i] = u < units ? load(v, u) : make_uint4(0u, 0u, 0u, 0u);
-        }
+        if (u0 > 0) load_from(u0);
 #pragma unroll
         for (int i = 0; i < kDeep; ++i) {
             const int u = u0 + i * 32 + lane;
             uint32_t sk, sv;
             const uint32_t ck = quantise8<T>(rk[i], sk), cv = quantise8<T>(rv[i], sv);
             if (u < units) {
-                const int h = u / per_head, d8 = u - h * per_head;
+                const int h = u >> shift, d8 = u & (per_head - 1);
                 const long long row = row0 + (long long)h * a.page_size;
                 reinterpret_cast<uint32_t*>(a.k_codes)[row * per_head + d8] = ck;
                 reinterpret_cast<uint32_t*>(a.v_codes)[row * per_head + d8] = cv;

@@ -68,8 +68,14 @@ __global__ void __launch_bounds__(256) fork_stage_kernel(const __grid_constant__
     }
 }
 
-// A block per row: counts off the row's own pages, counts on its parent's, and takes them over.
-__global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ PagesArgs a) {
+// A block per row, which takes over its parent's pages.  Counts: the row's own pages gain one for each row that it is
+// the parent of and lose its own entry, so a row whose only child is one row (itself or another) changes no count.  Up to
+// kScanRows rows a block finds its row's children among all parents; for more, a row counts off its own pages
+// and counts on its parent's (two sums for an entry: 1024 rows of 256-2048 pages 14.5 us).
+constexpr int kScanRows = 4096;
+
+template <bool SCAN> __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ PagesArgs a) {
+    __shared__ int children_of;
     pdl_wait();
     const int i = blockIdx.x;
     const int* const lens = a.ws ? staged_lens(a) : a.lens;
@@ -83,17 +89,35 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
     }
     int n1 = parent < 0 ? 0 : lens[parent];
     if (!len_ok(a, n1)) n1 = 0;
+    int more = 0;  // of the row's own pages
+    if constexpr (SCAN) {
+        if (threadIdx.x == 0) children_of = 0;
+        __syncthreads();
+        int n = 0;
+        for (int j = threadIdx.x; j < a.B; j += 256) {
+            const int p = a.arg[j];
+            n += p == i || (j == i && (p < -1 || p >= a.B));
+        }
+        n = __reduce_add_sync(~0u, n);
+        if ((threadIdx.x & 31) == 0 && n) atomicAdd(&children_of, n);
+        __syncthreads();
+        more = children_of - 1;
+    }
     const int own = pages_of(a, n0), use = pages_of(a, n1);
     const int* const mine = table + i * a.table_stride;
     const int* const from = table + max(parent, 0) * a.table_stride;
     int* const out = a.table_out + i * a.table_stride;
+#pragma unroll 4
     for (int j = threadIdx.x; j < max(own, use); j += 256) {
-        const int p0 = j < own ? mine[j] : -1, p1 = j < use ? from[j] : -1;
-        bad |= (j < own && !page_ok(a, p0)) || (j < use && !page_ok(a, p1));
-        if (p0 != p1) {
+        const int p1 = j < use ? from[j] : -1;
+        const int p0 = j < own && (!SCAN || more != 0 || parent != i) ? mine[j] : -1;
+        if constexpr (SCAN) {
+            if (more != 0 && page_ok(a, p0)) atomicAdd(a.refs_out + p0, more);
+        } else if (p0 != p1) {
             if (page_ok(a, p0)) atomicSub(a.refs_out + p0, 1);
             if (page_ok(a, p1)) atomicAdd(a.refs_out + p1, 1);
         }
+        bad |= (j < own && !page_ok(a, parent == i ? p1 : p0)) || (j < use && !page_ok(a, p1));
         if (j < use) out[j] = p1;
     }
     if (threadIdx.x == 0) a.lens_out[i] = n1;
@@ -102,10 +126,10 @@ __global__ void __launch_bounds__(256) fork_kernel(const __grid_constant__ Pages
 
 // --------------------------------------------------------- ranking by a cluster
 
-// What a CTA has counted of its pages, of two kinds.
+// What a CTA has counted of its pages.
 struct Counts {
-    int before[kWarps][2];  // in the warps before one
-    int total[2];
+    int before[kWarps];  // in the warps before one
+    int total;
 };
 
 // The CTAs of a ranking: kCluster of them, or one.
@@ -115,13 +139,20 @@ template <bool CLUSTER> struct Team {
     IDX_DEVI Team() : rank(0) {
         if constexpr (CLUSTER) rank = (int)cg::this_cluster().block_rank();
     }
-    // Everything written before is visible after (to loads past L1).
+    // Everything written before is visible after (to loads past L1): the cluster's barrier releases and
+    // acquires.
     IDX_DEVI void sync() const {
-        __threadfence();
         if constexpr (CLUSTER)
             cg::this_cluster().sync();
         else
             __syncthreads();
+    }
+    // A barrier in two halves: a CTA that has arrived reads no other's shared memory any more.
+    IDX_DEVI void arrive() const {
+        if constexpr (CLUSTER) asm volatile("barrier.cluster.arrive.aligned;" ::: "memory");
+    }
+    IDX_DEVI void wait() const {
+        if constexpr (CLUSTER) asm volatile("barrier.cluster.wait.aligned;" ::: "memory");
     }
     template <typename S> IDX_DEVI const S& of(S& mine, int r) const {
         if constexpr (CLUSTER) return *cg::this_cluster().map_shared_rank(&mine, r);
@@ -139,63 +170,56 @@ template <bool CLUSTER> IDX_DEVI Range warp_pages(const Team<CLUSTER>& team, int
     return {(int)min(first, (long long)pages), (int)min(first + per, (long long)pages)};
 }
 
-// Counts the pages of the CTA for which f gives bit 0, and bit 1; published by the next team.sync().
+constexpr int kBatch = 8;  // groups of 32 pages whose loads are in flight together
+
+// Counts the pages of the CTA for which f holds; published by the next team.sync().
 template <typename F> IDX_DEVI void count_pages(Counts& sh, Range r, int warp, int lane, F f) {
-    int c0 = 0, c1 = 0;
+    int c = 0;
 #pragma unroll 8
-    for (int p = r.first + lane; p < r.end; p += 32) {
-        const int x = f(p);
-        c0 += x & 1;
-        c1 += x >> 1;
-    }
-    c0 = warp_sum(c0);
-    c1 = warp_sum(c1);
-    if (lane == 0) {
-        sh.before[warp][0] = c0;
-        sh.before[warp][1] = c1;
-    }
+    for (int p = r.first + lane; p < r.end; p += 32) c += f(p);
+    c = warp_sum(c);
+    if (lane == 0) sh.before[warp] = c;
     __syncthreads();
     if (warp == 0) {
-        const int s0 = sh.before[lane][0], s1 = sh.before[lane][1];
-        const int i0 = warp_scan(s0, lane), i1 = warp_scan(s1, lane);
-        sh.before[lane][0] = i0 - s0;
-        sh.before[lane][1] = i1 - s1;
-        if (lane == 31) {
-            sh.total[0] = i0;
-            sh.total[1] = i1;
-        }
+        const int s = sh.before[lane], i = warp_scan(s, lane);
+        sh.before[lane] = i - s;
+        if (lane == 31) sh.total = i;
     }
 }
 // What the CTAs before this one counted, and all of them.
-template <bool CLUSTER> IDX_DEVI void totals(const Team<CLUSTER>& team, Counts& sh, int (&before)[2], int (&all)[2]) {
-    before[0] = before[1] = all[0] = all[1] = 0;
+template <bool CLUSTER> IDX_DEVI void totals(const Team<CLUSTER>& team, Counts& sh, int& before, int& all) {
+    before = all = 0;
 #pragma unroll
-    for (int r = 0; r < Team<CLUSTER>::CTAS; ++r)
-#pragma unroll
-        for (int k = 0; k < 2; ++k) {
-            const int n = team.of(sh, r).total[k];
-            if (r < team.rank) before[k] += n;
-            all[k] += n;
-        }
+    for (int r = 0; r < Team<CLUSTER>::CTAS; ++r) {
+        const int n = team.of(sh, r).total;
+        if (r < team.rank) before += n;
+        all += n;
+    }
 }
 
 // -------------------------------------------------------------------- resize
 
-// Workspace: a record per row, the rows that copy a page (their number first), and the pages that rows
-// take, by rank.
+// Workspace: per row what it asks for, then its new length as served and the rank of its first page; the rows that copy
+// a page (their number first); the pages that rows take, by rank.
 struct Row {
-    int old_len, new_len;  // new_len as served
-    int rank;              // of its first page
-    int from;              // the page that it copies, or -1
+    int old_len, new_len;
+    int rank;
+    int from;  // the page that it copies, or -1
 };
-IDX_DEVI Row* row_records(const PagesArgs& a) { return reinterpret_cast<Row*>(a.ws); }
-IDX_DEVI int* copy_rows(const PagesArgs& a) { return a.ws + 4ll * a.B; }
-IDX_DEVI int* taken_pages(const PagesArgs& a) { return a.ws + 5ll * a.B + 1; }
+IDX_DEVI int4* row_wants(const PagesArgs& a) { return reinterpret_cast<int4*>(a.ws); }  // old, new, from
+IDX_DEVI int2* row_places(const PagesArgs& a) { return reinterpret_cast<int2*>(a.ws + 4ll * a.B); }
+IDX_DEVI int* copy_rows(const PagesArgs& a) { return a.ws + 6ll * a.B; }
+IDX_DEVI int* taken_pages(const PagesArgs& a) { return a.ws + 7ll * a.B + 1; }
+IDX_DEVI Row served_row(const PagesArgs& a, long long i) {
+    const int4 want = row_wants(a)[i];
+    const int2 place = row_places(a)[i];
+    return {want.x, place.x, place.y, place.x > want.x ? want.z : -1};
+}
 
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kThreads) resize_rank_kernel(const __grid_constant__ PagesArgs a) {
+__global__ void __launch_bounds__(kThreads, 1) resize_rank_kernel(const __grid_constant__ PagesArgs a) {
     __shared__ Counts sh;
-    __shared__ int served, copies;  // CTA 0's: pages that rows take, rows that copy
+    __shared__ int served, copies;  // pages that rows take, rows that copy
     const Team<CLUSTER> team;
     constexpr int kAll = Team<CLUSTER>::CTAS * kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, at = team.rank * kThreads + tid;
@@ -223,7 +247,6 @@ __global__ void __launch_bounds__(kThreads) resize_rank_kernel(const __grid_cons
     }
     team.sync();
     // what rows that grow copy, and which pages are free
-    Row* const rows = row_records(a);
     for (int i = at; i < a.B; i += kAll) {
         Row row = {a.lens[i], a.arg[i], 0, -1};
         if (!len_ok(a, row.old_len) || !len_ok(a, row.new_len)) {
@@ -236,15 +259,17 @@ __global__ void __launch_bounds__(kThreads) resize_rank_kernel(const __grid_cons
             else if (__ldcg(a.refs_out + p) > 1)
                 row.from = p;
         }
-        rows[i] = row;
+        row_wants(a)[i] = make_int4(row.old_len, row.new_len, row.from, 0);
     }
     if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
     count_pages(sh, r, warp, lane, [&](int p) { return __ldcg(a.refs_out + p) <= 0 ? 1 : 0; });
     team.sync();
-    int before[2], all[2];
+    int before, all;
     totals(team, sh, before, all);
-    if (team.rank == 0) {
-        // rows in their order, until the free pages do not suffice for one
+    team.arrive();
+    {
+        // rows in their order, until the free pages do not suffice for one: every CTA goes through them (a barrier
+        // costs more), the first writes
         __shared__ long long part[kWarps];
         __shared__ int part_copies[kWarps];
         long long taken = 0;  // by the rows before these, served or not
@@ -253,8 +278,8 @@ __global__ void __launch_bounds__(kThreads) resize_rank_kernel(const __grid_cons
             const int i = i0 + tid;
             Row row = {0, 0, 0, -1};
             if (i < a.B) {
-                const int4 x = __ldcg(reinterpret_cast<const int4*>(rows + i));
-                row = {x.x, x.y, x.z, x.w};
+                const int4 x = __ldcg(row_wants(a) + i);
+                row = {x.x, x.y, 0, x.z};
             }
             const bool copy = row.from >= 0;
             const int want =
@@ -282,43 +307,46 @@ __global__ void __launch_bounds__(kThreads) resize_rank_kernel(const __grid_cons
                 copied += part_copies[w];
             }
             // (what is served of the rows that want pages comes before all that is not)
-            const bool ok = want == 0 || upto <= all[0];
+            const bool ok = want == 0 || upto <= all;
             if (i < a.B) {
                 if (!ok) {
                     row.new_len = row.old_len;
                     row.from = -1;
-                    raise_status(a.d_status, IDX_DEV_PAGES);
                 } else if (want > 0) {
                     row.rank = (int)(upto - want);
-                    if (copy) {
-                        copy_rows(a)[nth + 1] = i;
-                        atomicMax(&copies, nth + 1);
-                    }
+                    if (copy) atomicMax(&copies, nth + 1);
                     atomicMax(&served, (int)upto);
                 }
-                rows[i] = row;
-                a.lens_out[i] = row.new_len;
+                if (team.rank == 0) {
+                    if (!ok) raise_status(a.d_status, IDX_DEV_PAGES);
+                    if (row.from >= 0) copy_rows(a)[nth + 1] = i;
+                    row_places(a)[i] = make_int2(row.new_len, row.rank);
+                    a.lens_out[i] = row.new_len;
+                }
             }
             __syncthreads();
         }
-        if (tid == 0) copy_rows(a)[0] = copies;
+        if (team.rank == 0 && tid == 0) copy_rows(a)[0] = copies;
     }
-    team.sync();
     // the free pages by rank, as many as rows take
-    const int most = team.of(served, 0);
-    int rank = before[0] + sh.before[warp][0];
-    for (int p0 = r.first; p0 < r.end && rank < most; p0 += 32) {
-        const int p = p0 + lane;
-        const bool is_free = p < r.end && __ldcg(a.refs_out + p) <= 0;
-        const unsigned m = __ballot_sync(~0u, is_free);
-        const int k = rank + __popc(m & ((1u << lane) - 1));
-        if (is_free && k < most) {
-            taken_pages(a)[k] = p;
-            a.refs_out[p] = 1;
+    const int most = served;
+    int rank = before + sh.before[warp];
+    for (int p0 = r.first; p0 < r.end && rank < most; p0 += 32 * kBatch) {
+        int n[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) n[i] = p0 + i * 32 + lane < r.end ? __ldcg(a.refs_out + p0 + i * 32 + lane) : 1;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const unsigned m = __ballot_sync(~0u, n[i] <= 0);
+            const int k = rank + __popc(m & ((1u << lane) - 1)), p = p0 + i * 32 + lane;
+            if (n[i] <= 0 && k < most) {
+                taken_pages(a)[k] = p;
+                a.refs_out[p] = 1;
+            }
+            rank += __popc(m);
         }
-        rank += __popc(m);
     }
-    if constexpr (CLUSTER) team.sync();  // no CTA leaves while another reads its counts
+    team.wait();
 }
 
 // Copies pages pair(k) = (from, to) for k < n, a unit of one of them per block at a time.
@@ -352,17 +380,16 @@ template <typename F> IDX_DEVI void copy_pages(const PageArrays& c, int n, F pai
 
 __global__ void __launch_bounds__(kCopyThreads) resize_move_kernel(const __grid_constant__ PagesArgs a) {
     pdl_wait();
-    const Row* const rows = row_records(a);
     const int* const taken = taken_pages(a);
     const int lane = threadIdx.x & 31;
     const long long step = (long long)gridDim.x * (kCopyThreads / 32);
     for (long long i = ((long long)blockIdx.x * kCopyThreads + threadIdx.x) >> 5; i < a.B; i += step) {
-        const Row row = rows[i];
+        const Row row = served_row(a, i);
         if (!len_ok(a, row.old_len)) continue;
         const int* in = a.table + i * a.table_stride;
         int* out = a.table_out + i * a.table_stride;
         const int had = pages_of(a, row.old_len), has = pages_of(a, row.new_len);
-        const bool copy = row.from >= 0 && row.new_len > row.old_len;
+        const bool copy = row.from >= 0;
         const int kept = min(had - copy, has);
         if (out != in)
             for (int j = lane; j < kept; j += 32) out[j] = in[j];
@@ -371,77 +398,78 @@ __global__ void __launch_bounds__(kCopyThreads) resize_move_kernel(const __grid_
     }
     const int* const list = copy_rows(a);
     copy_pages(a.caches, list[0], [&](int k) {
-        const Row row = rows[list[k + 1]];
+        const Row row = served_row(a, list[k + 1]);
         return make_int2(row.from, taken[row.rank]);
     });
 }
 
 // ------------------------------------------------------------------- compact
 
-// Workspace: the number of moves and of live pages; the pages to fill and the pages that move, by rank;
-// where a page from the live count on goes.
+// Workspace: the number of moves and of live pages; the pages to fill, by rank; the pages that move, the last one
+// first; where a page from the live count on goes.
 IDX_DEVI int* holes_of(const PagesArgs& a) { return a.ws + 4; }
 IDX_DEVI int* movers_of(const PagesArgs& a) { return a.ws + 4 + (a.pages / 2 + 1); }
 IDX_DEVI int* moved_to(const PagesArgs& a) { return a.ws + 4 + 2ll * (a.pages / 2 + 1); }
 
+// One count of the live pages ranks both kinds: page p with l live pages before it is the (p - l)-th free one, and as
+// many live pages follow it as the live count says; the page at the live count knows how many move.
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kThreads) compact_rank_kernel(const __grid_constant__ PagesArgs a) {
-    __shared__ Counts sh[2];
+__global__ void __launch_bounds__(kThreads, 1) compact_rank_kernel(const __grid_constant__ PagesArgs a) {
+    __shared__ Counts sh;
     const Team<CLUSTER> team;
     constexpr int kAll = Team<CLUSTER>::CTAS * kThreads;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, at = team.rank * kThreads + tid;
     pdl_wait();
     pdl_trigger();
     const Range r = warp_pages(team, a.pages, warp);
-    int before[2], all[2];
-    count_pages(sh[0], r, warp, lane, [&](int p) { return a.refs[p] > 0 ? 1 : 0; });
+    count_pages(sh, r, warp, lane, [&](int p) { return a.refs[p] > 0; });
     team.sync();
-    totals(team, sh[0], before, all);
-    const int live = all[0];
-    count_pages(sh[1], r, warp, lane, [&](int p) {
-        const bool used = a.refs[p] > 0;
-        return p < live ? !used : 2 * used;
-    });
-    team.sync();
-    totals(team, sh[1], before, all);
-    const int moves = all[0];  // as many holes below the live count as live pages from it on
-    int nth[2] = {before[0] + sh[1].before[warp][0], before[1] + sh[1].before[warp][1]};
-    for (int p0 = r.first; p0 < r.end; p0 += 32) {
-        const int p = p0 + lane, n = p < r.end ? a.refs[p] : 0;
-        const bool hole = p < r.end && p < live && n <= 0, mover = p >= live && n > 0;
-        const unsigned holes = __ballot_sync(~0u, hole), movers = __ballot_sync(~0u, mover), under = (1u << lane) - 1;
-        if (hole) holes_of(a)[nth[0] + __popc(holes & under)] = p;
-        if (mover) movers_of(a)[nth[1] + __popc(movers & under)] = p;
-        if (p < r.end && !hole && !mover) {
-            if (p >= live) {
+    int before, live;
+    totals(team, sh, before, live);
+    int rank = before + sh.before[warp];  // live pages before the warp's
+    for (int p0 = r.first; p0 < r.end; p0 += 32 * kBatch) {
+        int n[kBatch];
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) n[i] = p0 + i * 32 + lane < r.end ? a.refs[p0 + i * 32 + lane] : 0;
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i) {
+            const int p = p0 + i * 32 + lane;
+            const unsigned m = __ballot_sync(~0u, n[i] > 0);
+            const int l = rank + __popc(m & ((1u << lane) - 1));
+            rank += __popc(m);
+            if (p >= r.end) continue;
+            if (p == live - 1) a.ws[0] = live - (l + (n[i] > 0));  // live pages from the live count on
+            if (p < live) {
+                if (n[i] <= 0)
+                    holes_of(a)[p - l] = p;
+                else if (a.refs_out != a.refs)
+                    a.refs_out[p] = n[i];
+            } else if (n[i] > 0) {
+                movers_of(a)[live - 1 - l] = p;
+            } else {
                 moved_to(a)[p] = p;
                 a.refs_out[p] = 0;
-            } else if (a.refs_out != a.refs) {
-                a.refs_out[p] = n;
             }
         }
-        nth[0] += __popc(holes);
-        nth[1] += __popc(movers);
     }
     team.sync();
+    const int moves = live > 0 ? __ldcg(a.ws) : 0;
     for (int k = at; k < moves; k += kAll) {
-        const int to = __ldcg(holes_of(a) + k), from = __ldcg(movers_of(a) + k);
+        const int to = __ldcg(holes_of(a) + k), from = __ldcg(movers_of(a) + moves - 1 - k);
         moved_to(a)[from] = to;
         const int n = a.refs[from];
         a.refs_out[to] = n;
         a.refs_out[from] = 0;
     }
     if (at == 0) {
-        a.ws[0] = moves;
         a.ws[1] = live;
         *a.live = live;
     }
-    if constexpr (CLUSTER) team.sync();  // no CTA leaves while another reads its counts
 }
 
 __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const __grid_constant__ PagesArgs a) {
     pdl_wait();
-    const int moves = a.ws[0], live = a.ws[1];
+    const int live = a.ws[1], moves = live > 0 ? a.ws[0] : 0;
     const int lane = threadIdx.x & 31;
     const long long step = (long long)gridDim.x * (kCopyThreads / 32);
     bool bad = false;
@@ -461,7 +489,7 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const __grid
         }
     }
     if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
-    copy_pages(a.caches, moves, [&](int k) { return make_int2(movers_of(a)[k], holes_of(a)[k]); });
+    copy_pages(a.caches, moves, [&](int k) { return make_int2(movers_of(a)[moves - 1 - k], holes_of(a)[k]); });
 }
 
 // A ranking kernel: a cluster when its pages or rows are many (see kClusterFrom), one CTA otherwise.
@@ -494,7 +522,7 @@ size_t fork_workspace_ints(int B, long long table_stride) {
     return (size_t)(B + 3) / 4 * 4 + (size_t)B * (size_t)table_stride;
 }
 size_t resize_workspace_ints(int B, int pages, long long table_stride) {
-    return 5 * (size_t)B + 1 + (size_t)std::min<long long>(pages, (long long)B * (table_stride + 1));
+    return 7 * (size_t)B + 1 + (size_t)std::min<long long>(pages, (long long)B * (table_stride + 1));
 }
 size_t compact_workspace_ints(int, int pages) { return 4 + 2 * (size_t)(pages / 2 + 1) + (size_t)pages; }
 
@@ -508,7 +536,7 @@ cudaError_t launch_fork(const PagesArgs& a, int sm_count, cudaStream_t s, int* l
         ++*launched;
     }
     if (a.B == 0) return e;
-    e = launch_k(fork_kernel, dim3((unsigned)a.B), dim3(256), 0, s, true, a);
+    e = launch_k(a.B <= kScanRows ? fork_kernel<true> : fork_kernel<false>, dim3((unsigned)a.B), dim3(256), 0, s, true, a);
     if (e == cudaSuccess) ++*launched;
     return e;
 }

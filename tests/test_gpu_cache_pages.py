@@ -50,7 +50,7 @@ def used(table, lens, page):
 
 
 @pytest.mark.parametrize("in_place", [False, True])
-@pytest.mark.parametrize("B,hi,page", [(1, 5, 16), (4, 100, 16), (37, 700, 32), (300, 5000, 64)])
+@pytest.mark.parametrize("B,hi,page", [(1, 5, 16), (4, 100, 16), (37, 700, 32), (300, 5000, 64), (5000, 40, 16)])
 def test_fork(idx, B, hi, page, in_place):
     pages = B * pages_of(hi, page) + 7
     table, lens, refs = pool(B, page, hi, pages, B, shared=B // 3, zeros=0.1)
