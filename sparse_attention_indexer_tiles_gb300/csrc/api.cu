@@ -1374,6 +1374,7 @@ idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const u
     a.row_tiles = p.row_tiles;
     a.splits = p.splits;
     a.chunk = p.chunk;
+    a.clustered = p.clustered;
     a.scale_log2 = scale * 1.4426950408889634f;
     const int stall_us = opt ? opt->test_stall_us : 0;
     a.wait_limit = stall_us > 0 ? 2100LL * stall_us : (1LL << 32);

@@ -21,12 +21,16 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <cooperative_groups.h>
+
 #include <algorithm>
 #include <cmath>
 #include <type_traits>
 
 #include "serve.cuh"
 #include "window_span.cuh"
+
+namespace cg = cooperative_groups;
 
 namespace idx {
 
@@ -51,7 +55,8 @@ template <int D> struct Ring {
     static_assert(STAGE % 128 == 0, "");
     static constexpr int JOIN = kWarps * 16 * (D + 6) * 4;   // of 16 rows
     static constexpr int OFF_ROWS = RING > JOIN ? RING : JOIN;  // per row: its logits' factor, its position
-    static constexpr int SMEM = OFF_ROWS + 16 * 8;
+    static constexpr int OFF_RESULT = OFF_ROWS + 16 * 8;  // of a split in a cluster: rows of D, then their sums
+    static constexpr int SMEM = OFF_RESULT + 16 * (D + 1) * 4;
 };
 
 // Eight e2m1 codes as fp16, pairs in order.
@@ -155,9 +160,10 @@ window_kernel(const __grid_constant__ WindowArgs a) {
     const int mine = first + warp < end ? (end - 1 - first - warp) / kWarps + 1 : 0;
     if (first >= end) {
         for (int i = tid; i < kRows && row0 + i < rows; i += kWarps * 32) {
-            if (a.splits > 1) a.part_lse[query_row(i) * a.splits + split] = -INFINITY;
+            if (a.splits > 1 && !a.clustered) a.part_lse[query_row(i) * a.splits + split] = -INFINITY;
         }
-        if (a.splits > 1) return;
+        // (a cluster's barrier does not wait for blocks that have ended, and its first block stays)
+        if (a.splits > 1 && !(a.clustered && split == 0)) return;
     }
     auto base_of = [&](int i) {  // first key of the warp's i-th step
         const int v = first + i * kWarps + warp;
@@ -620,6 +626,12 @@ window_kernel(const __grid_constant__ WindowArgs a) {
             }
         }
     __syncthreads();
+    auto write = [&](int r, int d, const float4& acc, float lse) {
+        const long long row = query_row(r);
+        *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + d) =
+            make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
+        if (d == 0 && a.lse) a.lse[row] = lse * 0.6931471805599453f;
+    };
     for (int x = tid; x < kRows * (D / 4); x += kWarps * 32) {
         const int r = x / (D / 4), d = x % (D / 4) * 4;
         if (row0 + r >= rows) break;
@@ -642,17 +654,51 @@ window_kernel(const __grid_constant__ WindowArgs a) {
             acc.w += f * v.w;
         }
         const float lse = sum == 0.f ? -INFINITY : top + log2f(sum);
-        const long long row = query_row(r);
-        if (a.splits > 1) {
-            const long long to = row * a.splits + split;
+        if (a.clustered) {
+            float* result = reinterpret_cast<float*>(smem + R::OFF_RESULT);
+            *reinterpret_cast<float4*>(result + r * D + d) = acc;
+            if (d == 0) result[16 * D + r] = lse;
+        } else if (a.splits > 1) {
+            const long long to = query_row(r) * a.splits + split;
             *reinterpret_cast<float4*>(a.part + to * D + d) = acc;
             if (d == 0) a.part_lse[to] = lse;
         } else {
-            *reinterpret_cast<uint2*>(static_cast<T*>(a.out) + row * D + d) =
-                make_uint2(pack2<T>(acc.x, acc.y), pack2<T>(acc.z, acc.w));
-            if (d == 0 && a.lse) a.lse[row] = lse * 0.6931471805599453f;
+            write(r, d, acc, lse);
         }
     }
+    if (!a.clustered) return;
+    // The cluster's blocks with keys join a share of the tile's columns each.
+    const cg::cluster_group cluster = cg::this_cluster();
+    cluster.sync();
+    const int parts = max(1, min(a.splits, (total + a.chunk - 1) / a.chunk));
+    for (int x = split * (kWarps * 32) + tid; x < kRows * (D / 4); x += parts * (kWarps * 32)) {
+        const int r = x / (D / 4), d = x % (D / 4) * 4;
+        if (row0 + r >= rows) break;
+        const float* result = reinterpret_cast<const float*>(smem + R::OFF_RESULT);
+        float lse[kWindowCluster], top = -INFINITY;
+#pragma unroll
+        for (int p = 0; p < kWindowCluster; ++p) {
+            lse[p] = p < parts ? cluster.map_shared_rank(result, p)[16 * D + r] : -INFINITY;
+            top = max_nan(top, lse[p]);
+        }
+        float sum = 0.f;
+        float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int p = 0; p < kWindowCluster; ++p) sum += lse[p] = lse[p] == -INFINITY ? 0.f : exp2_approx(lse[p] - top);
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;  // NaN stays one
+#pragma unroll
+        for (int p = 0; p < kWindowCluster; ++p) {
+            if (p >= parts) break;
+            const float4 v = *reinterpret_cast<const float4*>(cluster.map_shared_rank(result, p) + r * D + d);
+            const float f = lse[p] * inv;
+            acc.x += f * v.x;
+            acc.y += f * v.y;
+            acc.z += f * v.z;
+            acc.w += f * v.w;
+        }
+        write(r, d, acc, sum == 0.f ? -INFINITY : top + log2f(sum));
+    }
+    cluster.sync();  // no block ends while another reads its results
 }
 
 // Joins a row's splits: a warp per row, lane l holds D / 32 columns.
@@ -707,8 +753,21 @@ template <typename T, int D, int NT> cudaError_t launch_rows(const WindowArgs& a
     static PerDevice ready;
     const cudaError_t e = allow_smem(ready, window_kernel<T, D, NT>, Ring<D>::SMEM);
     if (e != cudaSuccess) return e;
-    return launch_k(window_kernel<T, D, NT>, dim3((unsigned)(a.splits * a.row_tiles * a.Hkv), (unsigned)a.B),
-                    dim3(kWarps * 32), Ring<D>::SMEM, s, true, a);
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(a.splits * a.row_tiles * a.Hkv), (unsigned)a.B);
+    cfg.blockDim = dim3(kWarps * 32);
+    cfg.dynamicSmemBytes = Ring<D>::SMEM;
+    cfg.stream = s;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = a.splits;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = a.clustered ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, window_kernel<T, D, NT>, a);
 }
 
 template <typename T, int D>
@@ -717,7 +776,7 @@ cudaError_t launch_typed(const WindowArgs& a, const WindowPlan& p, cudaStream_t 
                     : p.tile_rows == 8 ? launch_rows<T, D, 1>(a, s) : launch_rows<T, D, 2>(a, s);
     if (e != cudaSuccess) return e;
     ++*launched;
-    if (a.splits == 1) return e;
+    if (a.splits == 1 || a.clustered) return e;
     const long long rows = (long long)a.T * a.Hq, per = kJoinThreads / 32;
     e = launch_k(window_join_kernel<T, D>, dim3((unsigned)((rows + per - 1) / per)), dim3(kJoinThreads), 0, s, true, a);
     if (e == cudaSuccess) ++*launched;
@@ -761,15 +820,21 @@ WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_
     const double join_us = (double)rows * D * 8 / 5e6;
     double best = 0;
     // `count` tiles whose keys are `units` units, in s splits; time(t, blocks): that of blocks of t units each
+    // A cluster joins its splits sooner than a second launch does (16 requests behind a window of 4096 in 4 splits: 27
+    // and 30 us), but must find room for all of its blocks at once: where blocks wait for others to end it costs
+    // more (64 requests of 8192-16384 keys in 6 splits: 231 and 203 us).  `resident`: blocks that run at the same time.
     auto consider = [&](bool dense, int tile_rows, long long row_tiles, double count, long long units, int unit, int s,
-                        auto time) {
+                        double resident, auto time) {
         const long long t = (units + s - 1) / s, all = (units + t - 1) / t, half = (units / 2 + t) / t;
         if (all > 1 && all * rows > most) return;
         // lengths are on the device: the mean of the times with all of them at max_len and at half of it
-        const double us = (time(t, count * all) + time(t, count * half)) / 2 + (all > 1 ? all * join_us + 2.5 : 0.0);
+        const bool clustered = !dense && all > 1 && all <= kWindowCluster && count * all <= resident;
+        const double us = (time(t, count * all) + time(t, count * half)) / 2 +
+                          (clustered ? 1.0 : all > 1 ? all * join_us + 3.5 : 0.0);
         if (best != 0 && us >= best) return;
         best = us;
         p.dense = dense;
+        p.clustered = clustered;
         p.tile_rows = tile_rows;
         p.row_tiles = (int)row_tiles;
         p.splits = (int)all;
@@ -777,30 +842,30 @@ WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_
     };
     auto more = [](int s) { return s + (s < 8 ? 1 : s / 4); };
     if (path <= 0) {
-        // Tiles of 8 or 16 rows: `slots` blocks on an SM together take 128 keys of each of them in `unit_us` times
-        // their number, or in the 0.4 us that one takes by itself; 3 us to start and end.
+        // Tiles of 8 or 16 rows: one of n blocks on an SM, four at most (three of 16 rows), takes 128 keys in 0.75 +
+        // 0.3 n us, and 5 us to start and end (D = 128, 8 rows).
         const int tile_rows = most_rows <= 8 ? 8 : 16, slots = tile_rows == 8 ? 4 : 3;
-        const double unit_us = (tile_rows == 8 ? 0.69 : 1.14) * D / 128;
+        const double slower = (tile_rows == 8 ? 1.0 : 1.6) * (D == 128 ? 1.0 : 0.6);
         const long long tiles = (most_rows + tile_rows - 1) / tile_rows, tokens = (tile_rows + G - 1) / G + 1;
         const long long units = (steps_of(tokens, kWindowStep) + kWarps - 1) / kWarps;
         for (int s = 1; s <= kMostSplits && s <= units; s = more(s))
             consider(false, tile_rows, tiles, tiles_over(tiles, tile_rows), units, kWarps, s,
-                     [&](long long t, double blocks) {
+                     (double)slots * sm_count, [&](long long t, double blocks) {
                          const double on_sm = std::ceil(blocks / sm_count), full = std::floor(on_sm / slots);
                          const double rest = on_sm - full * slots;
-                         return full * (t * slots * unit_us + 3.0) +
-                                (rest > 0 ? t * std::max(0.4, rest * unit_us) + 3.0 : 0.0);
+                         auto wave = [&](double n) { return t * (0.75 + 0.3 * n) * slower + 5.0; };
+                         return full * wave(slots) + (rest > 0 ? wave(rest) : 0.0);
                      });
     }
     if (path > 0 || (path == 0 && most_rows > 16)) {
-        // Dense: a CTA per SM takes a key tile for 256 rows in about 1 us, for 128 (two streams in turn) in 0.6.
+        // Dense: a CTA per SM takes a key tile for 256 rows in about 1.7 us, for 128 (two streams in turn) in 1.1.
         const int tokens = 128 / G;
         const long long pairs = ((max_q + tokens - 1) / tokens + 1) / 2;
         const long long units = steps_of(2 * tokens, dense_keys);
-        const double tile_us = max_q > tokens ? 1.0 : 0.6;
+        const double tile_us = max_q > tokens ? 1.7 : 1.1;
         for (int s = 1; s <= kMostSplits && s <= units; s = more(s))
-            consider(true, 128, pairs, tiles_over(pairs, 2.0 * tokens * G), units, 1, s,
-                     [&](long long t, double blocks) { return std::ceil(blocks / sm_count) * (t * tile_us + 9.0); });
+            consider(true, 128, pairs, tiles_over(pairs, 2.0 * tokens * G), units, 1, s, 0.0,
+                     [&](long long t, double blocks) { return std::ceil(blocks / sm_count) * (t * tile_us + 6.0); });
     }
     auto up = [](size_t b) { return (b + 255) / 256 * 256; };
     p.part = 0;

@@ -25,7 +25,7 @@ namespace {
 
 constexpr int kThreads = 1024, kWarps = kThreads / 32;
 constexpr int kCopyThreads = 256;
-constexpr int kCluster = 8;                 // the portable limit
+constexpr int kCluster = 16;                // the most that a launch may ask for (8 are portable)
 constexpr int kUnit = kCopyThreads * 16 * 4;  // bytes of a page that a block copies at a time
 
 IDX_DEVI int warp_sum(int v) { return __reduce_add_sync(~0u, v); }
@@ -237,12 +237,20 @@ __global__ void __launch_bounds__(kThreads, 1) resize_rank_kernel(const __grid_c
     for (int i = at >> 5; i < a.B; i += kAll / 32) {
         const int n0 = a.lens[i], n1 = a.arg[i];
         if (!len_ok(a, n0) || !len_ok(a, n1) || n1 >= n0) continue;
-        for (int j = pages_of(a, n1) + lane; j < pages_of(a, n0); j += 32) {
-            const int p = a.table[i * a.table_stride + j];
-            if (page_ok(a, p))
-                atomicSub(a.refs_out + p, 1);
-            else
-                bad = true;
+        const int* const in = a.table + i * a.table_stride;
+        const int end = pages_of(a, n0);
+        for (int j0 = pages_of(a, n1) + lane; j0 < end; j0 += 32 * kBatch) {
+            int p[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) p[k] = j0 + 32 * k < end ? in[j0 + 32 * k] : 0;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (j0 + 32 * k >= end) break;
+                if (page_ok(a, p[k]))
+                    atomicSub(a.refs_out + p[k], 1);
+                else
+                    bad = true;
+            }
         }
     }
     team.sync();
@@ -493,10 +501,20 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const __grid
 }
 
 // A ranking kernel: a cluster when its pages or rows are many (see kClusterFrom), one CTA otherwise.
-constexpr int kClusterFrom = 16384;
+constexpr int kClusterFrom = 4096;
 
-cudaError_t launch_rank(void (*one)(PagesArgs), void (*many)(PagesArgs), const PagesArgs& a, cudaStream_t s) {
+cudaError_t launch_rank(void (*one)(PagesArgs), void (*many)(PagesArgs), PerDevice& ready, const PagesArgs& a,
+                        cudaStream_t s) {
     const bool cluster = a.pages >= kClusterFrom || a.B * 16ll >= kClusterFrom;
+    if (cluster) {
+        int device = -1;
+        cudaError_t e = cudaGetDevice(&device);
+        if (e != cudaSuccess) return e;
+        e = (cudaError_t)ready.run(device, [&] {
+            return (int)cudaFuncSetAttribute(many, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        });
+        if (e != cudaSuccess) return e;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(cluster ? kCluster : 1);
     cfg.blockDim = dim3(kThreads);
@@ -542,7 +560,8 @@ cudaError_t launch_fork(const PagesArgs& a, int sm_count, cudaStream_t s, int* l
 }
 
 cudaError_t launch_resize(const PagesArgs& a, int sm_count, cudaStream_t s, int* launched) {
-    cudaError_t e = launch_rank(resize_rank_kernel<false>, resize_rank_kernel<true>, a, s);
+    static PerDevice ready;
+    cudaError_t e = launch_rank(resize_rank_kernel<false>, resize_rank_kernel<true>, ready, a, s);
     if (e != cudaSuccess) return e;
     ++*launched;
     e = launch_k(resize_move_kernel, dim3(move_blocks(sm_count)), dim3(kCopyThreads), 0, s, true, a);
@@ -551,7 +570,8 @@ cudaError_t launch_resize(const PagesArgs& a, int sm_count, cudaStream_t s, int*
 }
 
 cudaError_t launch_compact(const PagesArgs& a, int sm_count, cudaStream_t s, int* launched) {
-    cudaError_t e = launch_rank(compact_rank_kernel<false>, compact_rank_kernel<true>, a, s);
+    static PerDevice ready;
+    cudaError_t e = launch_rank(compact_rank_kernel<false>, compact_rank_kernel<true>, ready, a, s);
     if (e != cudaSuccess) return e;
     ++*launched;
     e = launch_k(compact_move_kernel, dim3(move_blocks(sm_count)), dim3(kCopyThreads), 0, s, true, a);

@@ -10,11 +10,12 @@ namespace idx {
 
 constexpr int kWindowMaxGroup = 128;  // query heads per key head
 constexpr int kWindowStep = 32;       // keys that a warp takes at a time
+constexpr int kWindowCluster = 8;     // the largest portable cluster
 
 // One call.  Query row (token, head) = token * Hq + head; the tokens of request b are
 // q_start[b] .. q_start[b + 1] - 1.  The rows of a request and key head are taken in tiles, the
-// keys that a tile sees in splits; a split leaves its mean of V and its log2-sum-exp2 in the
-// workspace, or the results when there is one split.
+// keys that a tile sees in splits; a split's mean of V and log2-sum-exp2 go to the workspace, or stay in a
+// cluster's shared memory, unless there is one split.
 struct WindowArgs {
     const void* q;           // [T, Hq, D], tokens q_stride elements apart
     const uint8_t* k_codes;  // [pages, Hkv, page_size, D / 2]
@@ -33,6 +34,7 @@ struct WindowArgs {
     int max_q, max_len, window, sink;
     int row_tiles;           // per request and key head (dense: pairs of them)
     int splits, chunk;       // steps of kWindowStep keys per split (dense: key tiles)
+    bool clustered;          // a tile's splits are one cluster, which joins them in shared memory
     float scale_log2;        // scale * log2(e)
     long long wait_limit;    // SM clocks that a wait of the dense path may take
     int withhold_step;       // test only: the dense path's key tile that is never loaded, or -1
@@ -41,6 +43,7 @@ struct WindowArgs {
 
 struct WindowPlan {
     bool dense;              // on the tensor cores' dense path (attention_window_dense.cu)
+    bool clustered;
     int tile_rows, row_tiles, splits, chunk;
     size_t part, part_lse, total;
 };
