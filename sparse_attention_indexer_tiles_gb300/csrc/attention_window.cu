@@ -56,7 +56,8 @@ template <int D> struct Ring {
     static constexpr int JOIN = kWarps * 16 * (D + 6) * 4;   // of 16 rows
     static constexpr int OFF_ROWS = RING > JOIN ? RING : JOIN;  // per row: its logits' factor, its position
     static constexpr int OFF_RESULT = OFF_ROWS + 16 * 8;  // of a split in a cluster: rows of D, then their sums
-    static constexpr int SMEM = OFF_RESULT + 16 * (D + 1) * 4;
+    static constexpr int OFF_Q = (OFF_RESULT + 16 * (D + 1) * 4 + 15) / 16 * 16;  // tiles of 16 rows: the operand of q
+    static constexpr int SMEM = OFF_Q + 16 * D * 2;
 };
 
 // Eight e2m1 codes as fp16, pairs in order.
@@ -233,7 +234,10 @@ window_kernel(const __grid_constant__ WindowArgs a) {
 
     // q as the products' second operand: row g of each eight, a quarter of its columns per lane; the i-th step of 16
     // columns takes 4 i .. 4 i + 3 of each quarter (as the words of codes have them)
+    // (of 16 rows they stay in shared memory: the registers would not hold them beside o)
+    constexpr bool kKeepQ = NT == 1;
     uint32_t qf[NT][KW][4];
+    const uint32_t q_at = smem0 + R::OFF_Q + lane * 16;
     float2* const row_info = reinterpret_cast<float2*>(smem + R::OFF_ROWS);  // read in steps that are not plain
     float zscale[NT][2];  // the logits' factors at 2^EK, of this thread's columns of S^T: rows 2 t and 2 t + 1
     const float scale = a.scale_log2;
@@ -280,6 +284,15 @@ window_kernel(const __grid_constant__ WindowArgs a) {
                 for (int j = 0; j < 4; ++j)
                     qf[n][k][j] = flip ^ pack2<__half>(__uint_as_float(w[j] << 16) * f,
                                                        __uint_as_float(w[j] & 0xffff0000u) * f);
+            }
+        }
+        if constexpr (!kKeepQ) {
+            if (warp == 0) {
+#pragma unroll
+                for (int k = 0; k < KW; ++k)
+                    asm volatile("st.shared.v4.b32 [%0], {%1, %2, %3, %4};" ::"r"(q_at + (n * KW + k) * 512), "r"(qf[n][k][0]),
+                                 "r"(qf[n][k][1]), "r"(qf[n][k][2]), "r"(qf[n][k][3])
+                                 : "memory");
             }
         }
         if (warp == 0 && t == 0)
@@ -391,8 +404,10 @@ window_kernel(const __grid_constant__ WindowArgs a) {
                     }
 #pragma unroll
                     for (int n = 0; n < NT; ++n) {
-                        mma_f16(c[n], x0[0], x1[0], x0[1], x1[1], qf[n][k][0], qf[n][k][1]);
-                        mma_f16(c[n], x0[2], x1[2], x0[3], x1[3], qf[n][k][2], qf[n][k][3]);
+                        uint32_t q[4] = {qf[n][k][0], qf[n][k][1], qf[n][k][2], qf[n][k][3]};
+                        if constexpr (!kKeepQ) lds<4>(q_at + (n * KW + k) * 512, q);
+                        mma_f16(c[n], x0[0], x1[0], x0[1], x1[1], q[0], q[1]);
+                        mma_f16(c[n], x0[2], x1[2], x0[3], x1[3], q[2], q[3]);
                     }
                 }
 #pragma unroll
