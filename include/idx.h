@@ -520,7 +520,9 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
  * A row that sees nothing gets out 0 and lse -inf.  A row that sees a slot with a NaN scale
  * (255, in K or V) or a logit that is NaN or +inf gets NaN, and no other row does.  Weights below 2^-31
  * of a row's largest count as 0.  Values 2^120 and more below the largest in their 32 columns, of a slot that
- * a row of the same request sees, lose bits.
+ * a row of the same request sees, lose bits.  Where many rows of a request share a key head (a prompt),
+ * values may be taken in q's type: in fp16 those below 2^-24 then count as 0 and scales above 2^13 as NaN
+ * scales, in bf16 scales above 2^125.
  *   q    [T, Hq, D] bf16 or fp16, tokens q_stride elements apart, rows on 16-byte boundaries
  *   max_q   an upper bound on a request's new tokens (0 = T)
  *   max_len an upper bound on lens (0 = table_stride * page_size)
@@ -532,9 +534,8 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
  * Slots that no row of a request sees are not read, and their pages need not exist (table
  * entries of any value).  Further limits: Hq a multiple of Hkv with Hq / Hkv <= 128; T * Hq <
  * 2^31 - 256; max_len, window, sink < 2^30.  Device errors (IDX_DEV_RANGE): lens[b] outside [0,
- * max_len] is clamped, a request whose q_start is not in order or that has more than max_q
- * tokens is cut or skipped; a page outside [0, pages) that a row sees: the request's results are
- * meaningless.
+ * max_len] is clamped; where q_start is not in order, a request has more than max_q tokens or a row sees a
+ * page outside [0, pages), the request's results are meaningless.
  * ------------------------------------------------------------------------ */
 idx_status idx_cache_append_mxfp4(const void* k, long long k_stride, const void* v,
                                   long long v_stride, uint8_t* k_codes, uint8_t* k_sf,

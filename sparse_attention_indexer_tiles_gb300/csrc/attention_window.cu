@@ -275,15 +275,16 @@ window_kernel(const __grid_constant__ WindowArgs a) {
             const int ex = (int)(top >> 23);
             const int up = top == 0 ? 0 : min(127 + 14 - ex, 114);
             const float f = __int_as_float((up + 127) << 23);
-            // a row that is not finite has no results
-            factor = ex == 255 ? NAN : __int_as_float((127 - up) << 23);
+            factor = __int_as_float((127 - up) << 23);
 #pragma unroll
             for (int k = 0; k < KW; ++k) {
                 const uint32_t w[4] = {raw[k].x, raw[k].y, raw[k].z, raw[k].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    qf[n][k][j] = flip ^ pack2<__half>(__uint_as_float(w[j] << 16) * f,
-                                                       __uint_as_float(w[j] & 0xffff0000u) * f);
+                    // a row that is not finite is NaN for every key that it sees
+                    qf[n][k][j] = ex == 255 ? 0x7e007e00u
+                                            : flip ^ pack2<__half>(__uint_as_float(w[j] << 16) * f,
+                                                                   __uint_as_float(w[j] & 0xffff0000u) * f);
             }
         }
         if constexpr (!kKeepQ) {
@@ -324,7 +325,7 @@ window_kernel(const __grid_constant__ WindowArgs a) {
             for (int j = 0; j < 2; ++j) {
                 // within the normal numbers: a masked logit times it stays -inf, a logit of 0 stays 0
                 const float z = times_pow2(row_info[n * 8 + 2 * t + j].x, EK - 140);
-                zscale[n][j] = z > 0x1p-126f ? fminf(z, 0x1p127f) : z <= 0x1p-126f ? 0x1p-126f : z;
+                zscale[n][j] = fminf(fmaxf(z, 0x1p-126f), 0x1p127f);
             }
     };
     for (int i = 0; i < mine; ++i) {
@@ -811,6 +812,7 @@ WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_
     WindowPlan p;
     const int G = Hq / Hkv;
     const size_t rows = (size_t)T * Hq;
+    if (max_len == 0) path = -1;  // no key at all, perhaps no cache: nothing for the dense path to copy
     const long long most_rows = (long long)max_q * G;  // of a request and key head
     // keys that a tile of `tokens` tokens sees at most
     auto keys_of = [&](long long tokens) {

@@ -111,6 +111,41 @@ def test_rows_that_see_nothing(idx, path):
     check(idx, p, window=2, sink=1, options={"row_split": path})
 
 
+@pytest.mark.parametrize("path", [-1, 1])
+def test_rows_that_see_nothing_do_not_look_at_q(idx, path):
+    p = problem([2, 50], [6, 4], 3, 1, 64, 16, "bf16", seed=3)
+    p["q"][:4] = torch.tensor([float("nan"), float("inf"), -float("inf"), float("nan")])[:, None, None].bfloat16()
+    check(idx, p, options={"row_split": path})
+    check(idx, p, window=9, options={"row_split": path})
+
+
+@pytest.mark.parametrize("T", [1, 300])
+def test_a_table_without_pages(idx, T):
+    """No slot can be cached: every row sees nothing, whatever the path would be, and no cache is needed."""
+    z = lambda *s: torch.zeros(*s, dtype=torch.uint8, device="cuda")  # noqa: E731
+    lens, table = torch.zeros(1, dtype=torch.int32, device="cuda"), torch.zeros(1, 0, dtype=torch.int32, device="cuda")
+    q = torch.randn(T, 64, 128, device="cuda").bfloat16()
+    for pages in (0, 3):
+        for path in (0, 1):
+            out, lse = idx.idx_window_attention_mxfp4(q, z(pages, 8, 16, 64), z(pages, 8, 16, 4), z(pages, 8, 16, 64),
+                                                      z(pages, 8, 16, 4), table, lens, options={"row_split": path})
+            assert (out == 0).all() and (lse == -float("inf")).all()
+
+
+def test_scales_that_fp16_does_not_hold_on_the_dense_path(idx):
+    """A scale of 2^14 and more counts as a NaN scale there; 2^13 is held."""
+    p = problem([120], [60], 4, 1, 64, 16, "fp16", seed=13)
+    page = int(p["table"][0, 5])
+    p["cache"][3][page, 0, 4, 1] = 127 + 13
+    check(idx, p, 30, 2, options=DENSE)
+    p["cache"][3][page, 0, 4, 1] = 127 + 14
+    q = dict(p, cache=[c.clone() for c in p["cache"]])
+    q["cache"][3][page, 0, 4, 1] = 255
+    got, _ = call(idx, p, window=30, sink=2, options=DENSE)
+    check_attention(got, attention(q["q"], q["cache"], q["table"], q["lens"], q["q_start"], 30, 2), torch.float16, 120, 64)
+    check(idx, p, 30, 2, options={"row_split": -1})
+
+
 def test_long_rows_take_splits(idx):
     p = problem([9000, 100], [1, 1], 2, 1, 64, 128, "bf16", seed=3)
     check(idx, p)
