@@ -778,16 +778,17 @@ def idx_cache_fork(refs, table, lens, parent, *, page_size: int, refs_out=None, 
                    lens_out=None, ws=None, options=None, stats: Stats | None = None, stream=None):
     """Row i of the page table takes over the pages and the length of row parent[i] (i: stays, -1:
     ends), all rows at once; refs [pages] counts the entries that name a page.  Returns
-    (refs_out, table_out, lens_out), each of which may be its input (then with a workspace)."""
+    (refs_out, table_out, lens_out), each of which may be its input: a call in place takes a
+    workspace."""
     fn = "idx_cache_fork"
-    with _Launch(stream, refs.device) as on:
-        refs_out, table_out, lens_out = _page_results(on, fn, refs, refs_out, table, table_out,
-                                                      lens, lens_out)
-        if ws is None and (table_out is table or lens_out is lens
-                           or table_out.data_ptr() == table.data_ptr()
-                           or lens_out.data_ptr() == lens.data_ptr()):
-            ws = torch.empty(max(256, idx_cache_fork_workspace(*table.shape)), dtype=torch.uint8,
-                             device=refs.device)
+    in_place = ws is None and (table_out is table or lens_out is lens)
+    if in_place or refs_out is None or table_out is None or lens_out is None:
+        with _Launch(stream, refs.device) as on:
+            refs_out, table_out, lens_out = _page_results(on, fn, refs, refs_out, table, table_out,
+                                                          lens, lens_out)
+            if in_place:
+                ws = torch.empty(max(256, idx_cache_fork_workspace(*table.shape)),
+                                 dtype=torch.uint8, device=refs.device)
     _serve_call(fn, _serve().cache_fork, (
         refs, table, lens, parent, page_size, refs_out, table_out, lens_out, ws), options, stats,
         stream)
@@ -819,12 +820,13 @@ def idx_cache_resize(caches, refs, table, lens, new_lens, *, page_size: int, ref
     copy of it in every one of `caches` ([pages, ...] tensors).  Returns (refs_out, table_out,
     lens_out), each of which may be its input; lens_out tells where the pages did not suffice."""
     fn = "idx_cache_resize"
-    with _Launch(stream, refs.device) as on:
-        refs_out, table_out, lens_out = _page_results(on, fn, refs, refs_out, table, table_out,
-                                                      lens, lens_out)
-        if ws is None:
-            need = idx_cache_resize_workspace(table.shape[0], refs.shape[0], table.shape[1])
-            ws = torch.empty(max(256, need), dtype=torch.uint8, device=refs.device)
+    if refs_out is None or table_out is None or lens_out is None or ws is None:
+        with _Launch(stream, refs.device) as on:
+            refs_out, table_out, lens_out = _page_results(on, fn, refs, refs_out, table, table_out,
+                                                          lens, lens_out)
+            if ws is None:
+                need = idx_cache_resize_workspace(table.shape[0], refs.shape[0], table.shape[1])
+                ws = torch.empty(max(256, need), dtype=torch.uint8, device=refs.device)
     _serve_call(fn, _serve().cache_resize, (
         caches, refs, table, lens, new_lens, page_size, refs_out, table_out, lens_out, ws), options,
         stats, stream)
@@ -840,13 +842,15 @@ def idx_cache_compact(caches, refs, table, lens, *, page_size: int, refs_out=Non
     """Move the live pages (refs above 0) of `caches` ([pages, ...] tensors) to the front, in
     place; returns (refs_out, table_out, live [1]), the first two may be their inputs."""
     fn = "idx_cache_compact"
-    with _Launch(stream, refs.device) as on:
-        refs_out, table_out, _ = _page_results(on, fn, refs, refs_out, table, table_out, lens, lens)
-        if live is None:
-            live = on.result(torch.empty(1, dtype=torch.int32, device=refs.device))
-        if ws is None:
-            need = idx_cache_compact_workspace(table.shape[0], refs.shape[0])
-            ws = torch.empty(max(256, need), dtype=torch.uint8, device=refs.device)
+    if refs_out is None or table_out is None or live is None or ws is None:
+        with _Launch(stream, refs.device) as on:
+            refs_out, table_out, _ = _page_results(on, fn, refs, refs_out, table, table_out, lens,
+                                                   lens)
+            if live is None:
+                live = on.result(torch.empty(1, dtype=torch.int32, device=refs.device))
+            if ws is None:
+                need = idx_cache_compact_workspace(table.shape[0], refs.shape[0])
+                ws = torch.empty(max(256, need), dtype=torch.uint8, device=refs.device)
     _serve_call(fn, _serve().cache_compact, (
         caches, refs, table, lens, page_size, refs_out, table_out, live, ws), options, stats,
         stream)

@@ -12,8 +12,9 @@
 // cannot hold (scales above 2^125, in fp16 above 2^13) counts as a NaN scale.  K of a slot with a NaN scale becomes NaN and its V
 // 0, so that exactly the rows that see it are NaN.
 //
-// A tile that no row of the two streams sees is not taken; the tiles of the first tokens come before those of the
-// window.  Bounded by the tensor core and the softmax's instructions.
+// The keys that rows of the two streams see are taken in units of 16 (a copy each), those of the first tokens before
+// those of the window, and tiles are made of units in this order, so that the first tokens do not cost a tile of their
+// own (ragged prompts behind a window of 1024: 931 us with a tile of their own, 846 without).  Bounded by the tensor core and the softmax's instructions.
 #include "dense.cuh"
 #include "window_span.cuh"
 
@@ -165,9 +166,10 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     const int hi = max(0, min(sp.len, pos0 + last_token + 1));
     const int wlo = a.window > 0 ? max(0, pos0 + token0 - a.window + 1) : 0;
     const int sink = min(a.sink, hi);
-    int sink_tiles = (sink + C::KEYS - 1) / C::KEYS, from = wlo / C::KEYS;
-    if (from <= sink_tiles) sink_tiles = from = 0;  // no gap
-    const int total = sink_tiles + max(0, (hi + C::KEYS - 1) / C::KEYS - from);
+    // in the order of their units: below `sinks` as they are, from there on `skip` further on
+    int sinks = (sink + 15) / 16 * 16, skip = wlo / 16 * 16 - sinks;
+    if (skip <= 0) sinks = skip = 0;  // no gap
+    const int total = (max(0, hi - skip) + C::KEYS - 1) / C::KEYS;
     const int first = split * a.chunk, n = min(total, first + a.chunk) - first;
     auto row_of = [&](int token, int head) { return (long long)(sp.first + token) * a.Hq + hk * a.G + head; };
     if (n <= 0) {  // no keys in this split
@@ -185,11 +187,6 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         return;
     }
-    auto base_of = [&](int i) {  // first key of the split's i-th tile
-        const int v = first + i;
-        return C::KEYS * (v < sink_tiles ? v : v - sink_tiles + from);
-    };
-
     if (warp == 9) {
         if (lane == 0) {
             prefetch_tmap(&tm_q);
@@ -378,7 +375,7 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             auto look_up = [&](int i) {
                 int row = -1;
                 if (unit < C::UNITS && i < tiles) {
-                    const int key = base_of(i) + unit * 16;
+                    const int place = (first + i) * C::KEYS + unit * 16, key = place + (place < sinks ? 0 : skip);
                     if (key < hi && (key < sink || key + 16 > wlo)) {
                         const int page = table[key >> a.page_shift];
                         if (page < 0 || page >= a.pages)
@@ -432,13 +429,13 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         const int pos = pos0 + token;
         const int see = live ? min(pos + 1, hi) : 0, wl = a.window > 0 ? pos - a.window + 1 : 0;
         // what every row of the stream sees
-        const int all_see = min(pos0 + token1 + 1, hi);
-        const int all_from = a.window > 0 ? pos0 + min(sp.count, token1 + tokens) - a.window : 0;
+        const int all_see = min(pos0 + token1 + 1, hi) - skip;
+        const int all_from = a.window > 0 ? max(sinks, pos0 + min(sp.count, token1 + tokens) - a.window - skip) : 0;
         const int mine = solo ? (n + 1 - s) / 2 : n;
         float m = -INFINITY, l = 0.f;
         bool ok = true;
         for (int i = 0; i < mine; ++i) {
-            const int base = base_of(solo ? 2 * i + s : i);
+            const int base = (first + (solo ? 2 * i + s : i)) * C::KEYS;  // the tile's place in the order of units
             ok = __all_sync(~0u, mbar_wait(&sfull[s], i & 1, abort_flag, a.wait_limit));
             if (!ok) break;
             tc_fence_after();
@@ -453,12 +450,19 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             if (lane == 0) mbar_arrive(&sfree[s]);  // the next S may be computed
             float scale = a.scale_log2;
             // uniform; the maximum below wants scale >= 0
-            const bool all = base + C::KEYS <= all_see && (base >= all_from || base + C::KEYS <= a.sink);
+            const bool all = base + C::KEYS <= all_see && base >= all_from;
             if (!all || scale < 0.f) {
-                const int end = see - base, begin = wl - base, firsts = min(a.sink - base, end);
+                // the window's keys from `begin` on, `width` of them (none: 0), and the first tokens below `firsts`
+                const int begin = max(wl - skip, sinks) - base, width = max(0, see - skip - base - begin);
+                if (base < sink) {
+                    const int firsts = min(sink, see) - base;  // (the first tokens keep their places)
 #pragma unroll
-                for (int c = 0; c < C::KEYS; ++c)
-                    z[c] = (c >= begin && c < end) || c < firsts ? z[c] * scale : -INFINITY;
+                    for (int c = 0; c < C::KEYS; ++c)
+                        z[c] = (unsigned)(c - begin) < (unsigned)width || c < firsts ? z[c] * scale : -INFINITY;
+                } else {
+#pragma unroll
+                    for (int c = 0; c < C::KEYS; ++c) z[c] = (unsigned)(c - begin) < (unsigned)width ? z[c] * scale : -INFINITY;
+                }
                 scale = 1.f;
             }
             float x[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};

@@ -124,6 +124,51 @@ template <bool SCAN> __global__ void __launch_bounds__(256) fork_kernel(const __
     if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
 }
 
+// Both steps in one launch for few rows of few pages: a CTA, and a warp per row.  (A second launch costs the host 2
+// us, more than the GPU takes for both.)
+constexpr int kSmallRows = 32, kSmallWidth = 512, kSmallPages = 16384;
+
+__global__ void __launch_bounds__(1024, 1) fork_small_kernel(const __grid_constant__ PagesArgs a) {
+    pdl_wait();
+    const int lane = threadIdx.x & 31, i = threadIdx.x >> 5;
+    if (a.refs_out != a.refs)
+        for (int p = threadIdx.x; p < a.pages; p += 1024) a.refs_out[p] = a.refs[p];
+    const bool mine = i < a.B;
+    int parent = mine ? a.arg[i] : -1, n0 = mine ? a.lens[i] : 0;
+    bool bad = !len_ok(a, n0) || parent < -1 || parent >= a.B;
+    if (!len_ok(a, n0)) n0 = 0;
+    if (parent < -1 || parent >= a.B) parent = i;
+    // a row's children, of at most 32
+    const int other = lane < a.B ? a.arg[lane] : -1;
+    const int more = __popc(__ballot_sync(~0u, other == i || (lane == i && lane < a.B && parent == i))) - 1;
+    int n1 = parent < 0 ? 0 : a.lens[parent];
+    if (!len_ok(a, n1)) n1 = 0;
+    const int own = mine ? pages_of(a, n0) : 0, use = mine ? pages_of(a, n1) : 0;
+    const int* const from = a.table + max(parent, 0) * a.table_stride;
+    int* const out = a.table_out + i * a.table_stride;
+    // what this row will hold, before any row is written (a workspace: the call is in place)
+    if (a.ws)
+        for (int j = lane; j < use; j += 32) staged_table(a)[i * a.table_stride + j] = from[j];
+    __syncthreads();
+    const int* const mine_now = a.table + i * a.table_stride;
+#pragma unroll 4
+    for (int j = lane; j < own; j += 32) {
+        const int p = mine_now[j];
+        bad |= !page_ok(a, p);
+        if (more != 0 && page_ok(a, p)) atomicAdd(a.refs_out + p, more);
+    }
+    __syncthreads();
+    const int* const taken = a.ws ? staged_table(a) + i * a.table_stride : from;
+#pragma unroll 4
+    for (int j = lane; j < use; j += 32) {
+        const int p = taken[j];
+        bad |= !page_ok(a, p);
+        out[j] = p;
+    }
+    if (mine && lane == 0) a.lens_out[i] = n1;
+    if (bad && mine) raise_status(a.d_status, IDX_DEV_RANGE);
+}
+
 // --------------------------------------------------------- ranking by a cluster
 
 // What a CTA has counted of its pages.
@@ -546,6 +591,11 @@ size_t compact_workspace_ints(int, int pages) { return 4 + 2 * (size_t)(pages / 
 
 cudaError_t launch_fork(const PagesArgs& a, int sm_count, cudaStream_t s, int* launched) {
     cudaError_t e = cudaSuccess;
+    if (a.B > 0 && a.B <= kSmallRows && a.table_stride <= kSmallWidth && a.pages <= kSmallPages) {
+        e = launch_k(fork_small_kernel, dim3(1), dim3(1024), 0, s, true, a);
+        if (e == cudaSuccess) ++*launched;
+        return e;
+    }
     if (a.ws || a.refs_out != a.refs) {
         const long long work = std::max<long long>(a.pages, a.ws ? a.B * 32ll : 0);
         const long long blocks = std::min<long long>((work + 255) / 256, sm_count * 8ll);
