@@ -115,6 +115,7 @@ IDX_DEVI uint32_t lds8(uint32_t addr) {
     asm volatile("ld.shared.u8 %0, [%1];" : "=r"(v) : "r"(addr));
     return v;
 }
+IDX_DEVI void sts8(uint32_t addr, uint32_t v) { asm volatile("st.shared.u8 [%0], %1;" ::"r"(addr), "r"(v)); }
 // 2^n for any n that a scale can need, as two factors.
 IDX_DEVI float times_pow2(float x, int n) {
     const int a = n / 2, b = n - a;
@@ -332,8 +333,28 @@ window_kernel(const __grid_constant__ WindowArgs a) {
         copies_wait<kStages - 1>();
         __syncwarp();
         const uint32_t at = ring + i % kStages * R::STAGE;
+        const int base = base_of(i);
+        const bool plain = base + kWindowStep <= all_see && (base >= all_from || base + kWindowStep <= a.sink);
+        // a key of the step that a row of the tile sees
+        auto seen = [&](int in) {
+            const int key = base + in;
+            return plain || (key < hi && (key < sink || key >= wlo));
+        };
+        if (!plain) {
+            // keys that no row sees get the scales of one that is seen: whatever theirs are, they don't count
+            const bool mine = seen(lane);
+            const uint32_t some = __ballot_sync(~0u, mine);
+            const int from = __ffs(some) - 1;
+            if (!mine && from >= 0)
+#pragma unroll 1
+                for (int k = 0; k < BLOCKS; ++k) {
+                    sts8(at + R::OFF_KSF + lane * BLOCKS + k, lds8(at + R::OFF_KSF + from * BLOCKS + k));
+                    sts8(at + R::OFF_VSF + lane * BLOCKS + k, lds8(at + R::OFF_VSF + from * BLOCKS + k));
+                }
+            __syncwarp();
+        }
         if (i == 0) {
-            // the first powers are a little above the first step's (of keys that no row sees, too: any will do)
+            // the first powers are a little above the first step's
             int k = 0, v = 0;
             for (int j = lane & 3; j < kWindowStep; j += 4) v = max(v, (int)lds8(at + R::OFF_VSF + j * BLOCKS + vblock));
             v = max(v, __shfl_xor_sync(~0u, v, 1));
@@ -345,8 +366,6 @@ window_kernel(const __grid_constant__ WindowArgs a) {
             EK = k < 255 ? min(k + kMargin, 254) : 0;
             scale_logits();
         }
-        const int base = base_of(i);
-        const bool plain = base + kWindowStep <= all_see && (base >= all_from || base + kWindowStep <= a.sink);
 
         // ---- scales: whether the running powers and their bands hold them
         uint32_t ks[2][2];  // [half][keys kg, kg + 8]
@@ -359,7 +378,7 @@ window_kernel(const __grid_constant__ WindowArgs a) {
                 const uint32_t v = at + R::OFF_VSF + vblock + t * BLOCKS + (h * 16 + 8 * k) * BLOCKS;
                 vs[h][k] = lds8(v) | lds8(v + 4 * BLOCKS) << 16;
             }
-        bool out = !plain;
+        bool out = false;
 #pragma unroll
         for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -368,11 +387,6 @@ window_kernel(const __grid_constant__ WindowArgs a) {
         const uint32_t least = __vminu2(__vminu2(vs[0][0], vs[0][1]), __vminu2(vs[1][0], vs[1][1]));
         const uint32_t top = (uint32_t)E * 0x10001u, low_end = (uint32_t)max(E - kBand, 0) * 0x10001u;
         const bool slow = __any_sync(~0u, out || __vmaxu2(most, top) != top || __vminu2(least, low_end) != low_end);
-        // a key of the step that a row of the tile sees
-        auto seen = [&](int in) {
-            const int key = base + in;
-            return plain || (key < hi && (key < sink || key >= wlo));
-        };
 
         // ---- S^T of the two halves of 16 keys: K's codes times 2^(field - 15), both halves of `sc` the same
         float s[2][NT][4];
@@ -458,7 +472,7 @@ window_kernel(const __grid_constant__ WindowArgs a) {
         uint32_t p[2][NT][2];
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
-            if (slow) {
+            if (slow || !plain) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h)
 #pragma unroll
@@ -513,7 +527,7 @@ window_kernel(const __grid_constant__ WindowArgs a) {
             }
         }
 
-        // ---- O^T += V^T P^T, V's codes times 2^(field - 15) of each pair of keys; in steps that are not plain
+        // ---- O^T += V^T P^T, V's codes times 2^(field - 15) of each pair of keys; in slow steps
         // the sums come in units of their own, `unit` of o's
         auto add_v = [&](const uint32_t (&sc)[2][2], auto direct, float unit) {
 #pragma unroll
