@@ -124,9 +124,10 @@ template <bool SCAN> __global__ void __launch_bounds__(256) fork_kernel(const __
     if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
 }
 
-// Both steps in one launch for few rows of few pages: a CTA, and a warp per row.  (A second launch costs the host 2
-// us, more than the GPU takes for both.)
-constexpr int kSmallRows = 32, kSmallWidth = 512, kSmallPages = 16384;
+// Both steps in one launch for few rows of few pages: a CTA, and a warp per row.  A second launch costs the host 2 us,
+// one CTA the GPU some: 4 rows of 32 pages take 3.0 us instead of 4.8 (2.0 and 2.4 in a graph), 32 rows of 64 among 4096
+// pages 3.4 and 4.7 (3.4 and 2.9 in a graph), 32 rows of 512 10.5 and 4.7.
+constexpr int kSmallRows = 32, kSmallWidth = 64, kSmallPages = 4096;
 
 __global__ void __launch_bounds__(1024, 1) fork_small_kernel(const __grid_constant__ PagesArgs a) {
     pdl_wait();

@@ -69,6 +69,30 @@ def test_fork(idx, B, hi, page, in_place):
         assert all(torch.equal(a.cpu(), b) for a, b in zip(d, (refs, table, lens)))
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("B,width,pages", [(32, 64, 4096), (33, 64, 4096), (32, 65, 4096), (32, 64, 4097),
+                                           (33, 512, 16384), (32, 1, 40)])
+def test_fork_at_the_limits_of_one_launch(idx, B, width, pages, in_place):
+    g = torch.Generator().manual_seed(B + width + pages)
+    lens = torch.randint(0, 16 * min(width, pages // B) + 1, (B,), generator=g)
+    lens[0] = 16 * min(width, pages // B)
+    ids = torch.randperm(pages, generator=g).tolist()
+    table = laid_out([[ids.pop() for _ in range(pages_of(n, 16))] for n in lens.tolist()],
+                     torch.zeros(B, width, dtype=torch.int32))
+    lens = lens.to(torch.int32)
+    refs = counts(held(table, lens, 16), pages)
+    parent = torch.randint(-1, B, (B,), generator=g).to(torch.int32)
+    parent[B // 2:B // 2 + 5] = 0
+    rows, new = fork(table, lens, parent, 16)
+    d = [x.cuda() for x in (refs, table, lens)]
+    stats = idx.Stats()
+    r, t, n = idx.idx_cache_fork(*d, parent.cuda(), page_size=16, stats=stats, **outputs(in_place, *d))
+    assert stats.read()["status"] == 0
+    assert torch.equal(n.cpu(), new) and used(t, n, 16) == rows and torch.equal(r.cpu(), counts(rows, pages))
+    if not in_place:
+        assert all(torch.equal(a.cpu(), b) for a, b in zip(d, (refs, table, lens)))
+
+
 def test_fork_reports_what_it_cannot_follow(idx):
     table, lens, refs = pool(4, 16, 60, 40, 1)
     parent = torch.tensor([4, -2, 1, 0], dtype=torch.int32)
