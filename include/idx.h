@@ -526,8 +526,8 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
  *   q    [T, Hq, D] bf16 or fp16, tokens q_stride elements apart, rows on 16-byte boundaries
  *   max_q   an upper bound on a request's new tokens (0 = T)
  *   max_len an upper bound on lens (0 = table_stride * page_size)
- *   out  [T, Hq, D] of q's type, contiguous; lse [T, Hq] fp32 or NULL.  Rows of tokens outside
- *        every request are not written.
+ *   out  [T, Hq, D] of q's type, contiguous, apart from q; lse [T, Hq] fp32 or NULL.  Rows of
+ *        tokens outside every request are not written.
  *   ws   idx_window_attention_mxfp4_workspace(...) bytes for the same arguments (max_q and
  *        max_len as the call counts them), 256-byte aligned; needs no clearing between calls.
  *        The size does not shrink when an argument grows (a window of 0 is the largest).
@@ -580,8 +580,8 @@ idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const u
  * before the call and gives its own back; all rows at once (the next step of a beam search).
  * parent[i] = i leaves the row, -1 ends it (length 0).  Nothing is copied: rows share pages
  * until one of them grows (idx_cache_resize).  Other parents outside [0, B): IDX_DEV_RANGE, the
- * row is left.  ws: idx_cache_fork_workspace(...) bytes, 256-byte aligned, when table_out is
- * table or lens_out is lens; NULL and 0 otherwise.
+ * row is left.  lens_out must not be parent (IDX_EINVAL).  ws: idx_cache_fork_workspace(...)
+ * bytes, 256-byte aligned, when table_out is table or lens_out is lens; NULL and 0 otherwise.
  *
  * idx_cache_resize - row i goes from lens[i] to new_lens[i] slots.  First the rows that shrink
  * give back the pages that they no longer need.  Then the rows that grow take free pages, the

@@ -1468,6 +1468,7 @@ idx_status idx_cache_fork(const int* refs, const int* table, const int* lens, co
         if (!aligned(ws, 256)) return IDX_EALIGN;
         a.ws = static_cast<int*>(ws);
     }
+    if (B > 0 && lens_out == parent) return IDX_EINVAL;  // rows still read it
     if (!arch_ok()) return IDX_EUNSUPPORTED;
     return pages_launch(launch_fork, a, opt, stream);
 }

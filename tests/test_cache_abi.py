@@ -156,6 +156,10 @@ def test_fork_checks(idx, kw, code):
     assert fork(idx.load(), **kw) == code
 
 
+def test_a_fork_does_not_write_its_parents(idx):
+    assert fork(idx.load(), parent=P, lens=2 * P, lens_out=P) == EINVAL
+
+
 @pytest.mark.parametrize("kw,code", COMMON + ARRAYS + [
     (dict(new_lens=None), EINVAL), (dict(lens_out=None), EINVAL), (dict(new_lens=P + 2), EALIGN), (dict(ws=None), EWORKSPACE),
     (dict(ws_bytes=8), EWORKSPACE), (dict(ws=P + 16), EALIGN), (dict(B=0, pages=0, n=0), OK)])
