@@ -7,14 +7,15 @@
 // row, an issuing warp per stream, K and V tiles in turn through one ring).  What differs is how tiles come: TMA
 // brings codes and scales to a small ring of their own, and five warps write the values that they stand for, in q's
 // type, where the matrix instructions read them (rows of 64 columns, 128-byte swizzled).  (Codes that these warps
-// loaded into registers a tile ahead were late: 4096 tokens behind one another 381 us.)  The values are the codes times powers of two, so
-// bf16 holds them exactly; fp16 does from 2^-24 to 2^15 (below, they count as 0).  A value that q's type
-// cannot hold (scales above 2^125, in fp16 above 2^13) counts as a NaN scale.  K of a slot with a NaN scale becomes NaN and its V
-// 0, so that exactly the rows that see it are NaN.
+// loaded into registers a tile ahead were late: 4096 tokens behind one another 381 us, 315 from the ring.)  The values
+// are the codes times powers of two, so bf16 holds them exactly; fp16 does from 2^-24 to 2^15 (below, they count as
+// 0).  A value that q's type cannot hold (scales above 2^125, in fp16 above 2^13) counts as a NaN scale.  K of a slot
+// with a NaN scale becomes NaN and its V 0, so that exactly the rows that see it are NaN.
 //
 // The keys that rows of the two streams see are taken in units of 16 (a copy each), those of the first tokens before
 // those of the window, and tiles are made of units in this order, so that the first tokens do not cost a tile of their
-// own (ragged prompts behind a window of 1024: 931 us with a tile of their own, 846 without).  Bounded by the tensor core and the softmax's instructions.
+// own (ragged prompts behind a window of 1024: 931 us with a tile of their own, 846 without).  Bounded by the
+// instructions of the softmax and the expansion.
 #include "dense.cuh"
 #include "window_span.cuh"
 
