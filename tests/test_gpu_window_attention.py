@@ -167,6 +167,29 @@ def test_nan_scales_reach_only_rows_that_see_them(idx, where, new):
     check(idx, p, window=20, sink=1)
 
 
+@pytest.mark.parametrize("path", [-1, 1])
+@pytest.mark.parametrize("D,dt", [(64, "fp16"), (128, "bf16")])
+@pytest.mark.parametrize("new,window,sink", [(1, 37, 0), (1, 37, 5), (1, 1, 0), (1, 0, 0), (3, 20, 33), (7, 70, 1)])
+def test_what_no_row_sees_changes_no_bit(idx, new, window, sink, D, dt, path):
+    lens = [1, 31, 33, 100, 257]
+    p = problem(lens, [min(n, new) for n in lens], 4, 2, D, 16, dt, seed=window + sink)
+    options = {"row_split": path}
+    want = check(idx, p, window, sink, options=options)
+    g = torch.Generator().manual_seed(new)
+    seen = torch.zeros(p["cache"][0].shape[0], 16, dtype=torch.bool)
+    for b, n in enumerate(lens):
+        for j in range(n):
+            if window == 0 or j < sink or j > n - min(n, new) - window:
+                seen[int(p["table"][b, j // 16]), j % 16] = True
+    wild = torch.tensor([0, 1, 90, 254, 255], dtype=torch.uint8)
+    for x in p["cache"]:
+        is_sf = x.shape[-1] == D // 32
+        other = wild[torch.randint(0, 5, x.shape, generator=g)] if is_sf else 255 - x
+        x.copy_(torch.where(seen[:, None, :, None], x, other))
+    got, st = call(idx, p, window=window, sink=sink, options=options)
+    assert st == 0 and torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+
+
 def test_a_later_token_with_huge_values_leaves_the_ones_before(idx):
     p = problem([64], [8], 2, 1, 128, 16, "bf16", seed=11)
     page = int(p["table"][0, 3])
