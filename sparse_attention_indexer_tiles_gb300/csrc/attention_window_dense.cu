@@ -8,9 +8,9 @@
 // brings codes and scales to a small ring of their own, and five warps write the values that they stand for, in q's
 // type, where the matrix instructions read them (rows of 64 columns, 128-byte swizzled).  (Codes that these warps
 // loaded into registers a tile ahead were late: 4096 tokens behind one another 381 us, 315 from the ring.)  The values
-// are the codes times powers of two, so bf16 holds them exactly; fp16 does from 2^-24 to 2^15 (below, they count as
-// 0).  A value that q's type cannot hold (scales above 2^125, in fp16 above 2^13) counts as a NaN scale.  K of a slot
-// with a NaN scale becomes NaN and its V 0, so that exactly the rows that see it are NaN.
+// are the codes times powers of two, so bf16 holds them exactly; fp16 does from 2^-23 on and rounds smaller ones
+// to multiples of 2^-24.  A value that q's type cannot hold (scales above 2^125, in fp16 above 2^13) counts as a NaN
+// scale.  K of a slot with a NaN scale becomes NaN and its V 0, so that exactly the rows that see it are NaN.
 //
 // The keys that rows of the two streams see are taken in units of 16 (a copy each), those of the first tokens before
 // those of the window, and tiles are made of units in this order, so that the first tokens do not cost a tile of their
@@ -90,27 +90,35 @@ IDX_DEVI uint32_t mul2_bf16(uint32_t a, uint32_t b) {
     return d;
 }
 
-// A pair of codes in fp16 times 2^(sf - 127), in T.  Scales up to EASY take one product; for larger ones, up to
-// MOST, there is a second (of `rest`, times()).
+// A pair of codes in fp16 times 2^(sf - 127), in T, rounded once.  Scales from LEAST to EASY take one product; for
+// others, up to MOST, it is the product of two factors.
 template <typename T> struct Expand;
 template <> struct Expand<__half> {
-    static constexpr uint32_t EASY = Held<__half>::MOST;
+    // from 2^-24 on the scale is an fp16 number; below, 2^-12 of a code is one, and the second product rounds
+    static constexpr uint32_t LEAST = 127 - 24, EASY = Held<__half>::MOST;
     uint32_t scale;
-    IDX_DEVI explicit Expand(uint32_t sf) {
-        const int field = (int)sf - 112;  // of an fp16 power of two; at most 28
-        const uint32_t bits = field > 0 ? (uint32_t)field << 10 : field >= -9 ? 1u << (9 + field) : 0u;
+    IDX_DEVI explicit Expand(uint32_t sf) : Expand((int)sf - 127, 0) {}
+    IDX_DEVI static Expand first(uint32_t sf) { return Expand(sf < LEAST ? -12 : (int)min(sf, EASY) - 127, 0); }
+    IDX_DEVI static Expand second(uint32_t sf) { return Expand(sf < LEAST ? max((int)sf - 127 + 12, -25) : 0, 0); }
+    IDX_DEVI uint32_t operator()(uint32_t h) const { return mul2_f16(h, scale); }
+    IDX_DEVI uint32_t times(uint32_t x) const { return mul2_f16(x, scale); }
+
+private:
+    // 2^n, n from -24 to 15; 0 for -25 (no value of a scale below 2^-36 reaches half a step of fp16)
+    IDX_DEVI Expand(int n, int) {
+        const uint32_t bits = n > -15 ? (uint32_t)(n + 15) << 10 : 1u << (n + 25) >> 1;
         scale = bits | bits << 16;
     }
-    IDX_DEVI Expand(uint32_t, bool) : scale(0) {}
-    IDX_DEVI uint32_t operator()(uint32_t h) const { return mul2_f16(h, scale); }
-    IDX_DEVI uint32_t times(uint32_t x) const { return x; }
 };
 template <> struct Expand<__nv_bfloat16> {
     // an fp16 code moved to bf16's fields stands for 2^-112 of itself
-    static constexpr uint32_t EASY = 254 - 112;
+    static constexpr uint32_t LEAST = 0, EASY = 254 - 112;
     uint32_t scale;
     IDX_DEVI explicit Expand(uint32_t sf) { scale = (sf + 112u) * 0x00800080u; }
-    IDX_DEVI Expand(uint32_t sf, bool) { scale = (127u + max(sf, EASY) - EASY) * 0x00800080u; }
+    IDX_DEVI static Expand first(uint32_t sf) { return Expand(min(sf, EASY)); }
+    IDX_DEVI static Expand second(uint32_t sf) {
+        return Expand(15u + max(min(sf, Held<__nv_bfloat16>::MOST), EASY) - EASY);
+    }
     IDX_DEVI uint32_t operator()(uint32_t h) const {
         return mul2_bf16((h >> 3 & 0x0fff0fffu) | (h & 0x80008000u), scale);
     }
@@ -268,12 +276,12 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                                      "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w)
                                      : "memory");
                     };
-                    if (!__any_sync(~0u, most > Expand<T>::EASY)) {
+                    if (!__any_sync(~0u, most > Expand<T>::EASY || own[i] < Expand<T>::LEAST)) {
                         const Expand<T> f(own[i]);
 #pragma unroll
                         for (int c = 0; c < 4; ++c) put(c, expand8<T>(w[i][c], f));
                     } else {
-                        const Expand<T> f(min(own[i], Expand<T>::EASY)), more(min(own[i], Held<T>::MOST), true);
+                        const Expand<T> f = Expand<T>::first(own[i]), more = Expand<T>::second(own[i]);
                         const uint32_t gone = is_v ? 0u : Held<T>::NANS;
 #pragma unroll
                         for (int c = 0; c < 4; ++c) {
