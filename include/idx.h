@@ -522,7 +522,8 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
  * of a row's largest count as 0.  Values 2^120 and more below the largest in their 32 columns, of a slot that
  * a row of the same request sees, lose bits.  Where many rows of a request share a key head (a prompt),
  * values may be taken in q's type: in fp16 those below 2^-23 are then rounded to multiples of 2^-24 and scales above
- * 2^13 count as NaN scales, in bf16 scales above 2^125.
+ * 2^13 count as NaN scales; in bf16 scales above 2^125 do, and values below 2^-60 lose bits beside scales of V
+ * above 2^87 that a row of the same request sees.
  *   q    [T, Hq, D] bf16 or fp16, tokens q_stride elements apart, rows on 16-byte boundaries
  *   max_q   an upper bound on a request's new tokens (0 = T)
  *   max_len an upper bound on lens (0 = table_stride * page_size)

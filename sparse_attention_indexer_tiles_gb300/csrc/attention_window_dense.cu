@@ -54,7 +54,8 @@ template <int D> struct DenseCfg {
     static constexpr int NBAR = 1 + 2 * NS + 10 + 2 * RS;
     static constexpr int OFF_CTL = OFF_BAR + NBAR * 8;       // [0] TMEM base, [1] abort flag
     static constexpr int OFF_ML = OFF_CTL + 8;              // the odd stream's m and l
-    static constexpr int SMEM = OFF_ML + kRows * 8 + 1024;
+    static constexpr int OFF_LARGE = OFF_ML + kRows * 8;     // the last tile of each 8 that holds large values of V
+    static constexpr int SMEM = OFF_LARGE + 8 * 4 + 1024;
     // TMEM columns: S and P of a stream, then both O
     static constexpr int COL_P = KEYS, COL_STREAM = D == 128 ? 128 : KEYS + KEYS / 2;
     static constexpr int COL_O = 512 - 2 * D;
@@ -70,14 +71,20 @@ static_assert(256 * kSoftmaxRegs + 256 * kOtherRegs <= 512 * 128, "");
 template <int N> IDX_DEVI void regs_more() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N) : "memory"); }
 template <int N> IDX_DEVI void regs_less() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N) : "memory"); }
 
-// The largest scale whose values the type holds, and its NaN twice.
+// The largest scale whose values the type holds, and its NaN twice.  LARGE: the largest scale of V with which O stays
+// inside fp32 whatever the keys are: weights of a tile are at most 2^kRenew before a row's maximum is renewed, and
+// 2^30 keys 2^8 6 2^87 < 2^128.  In a tile with larger ones the maximum counts as kLargeLift more, which makes its
+// weights, and through the renewal all the row's others, that much smaller: 2^30 2^(8 - 40) 6 2^125 < 2^126, and the sum
+// of both kinds is below 2^128.  (For all tiles it would cost small values their bits: 2^-40 of those below 2^-60 leaves
+// fp32's 24.)  fp16's values are far inside.
 template <typename T> struct Held;
 template <> struct Held<__nv_bfloat16> {
-    static constexpr uint32_t MOST = 127 + 125, NANS = 0x7fff7fffu;
+    static constexpr uint32_t MOST = 127 + 125, NANS = 0x7fff7fffu, LARGE = 127 + 87;
 };
 template <> struct Held<__half> {
-    static constexpr uint32_t MOST = 127 + 13, NANS = 0x7fff7fffu;
+    static constexpr uint32_t MOST = 127 + 13, NANS = 0x7fff7fffu, LARGE = MOST;
 };
+constexpr float kLargeLift = 40.f;
 
 IDX_DEVI uint32_t mul2_f16(uint32_t a, uint32_t b) {
     uint32_t d;
@@ -157,6 +164,7 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
     uint64_t* rempty = rfull + C::RS;
     volatile uint32_t* tslot = reinterpret_cast<volatile uint32_t*>(smem + C::OFF_CTL);
     volatile int* abort_flag = reinterpret_cast<volatile int*>(smem + C::OFF_CTL + 4);
+    volatile int* large = reinterpret_cast<volatile int*>(smem + C::OFF_LARGE);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
 
@@ -227,6 +235,7 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
         }
         __syncwarp();
     }
+    if (tid < 8) large[tid] = -1;
     if (warp == 8) {
         tmem_alloc(const_cast<uint32_t*>(tslot), 512);
         tmem_relinquish();
@@ -249,9 +258,10 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             const int key_in = lane & 7, block = lane >> 3 & (C::BLOCKS - 1), sub = lane / (8 * C::BLOCKS);
             const int turn = warp - kExpandWarp;
             bool ok = true;
-            // one array of a tile: codes at `codes`, scales at `scales`; a NaN scale makes K (seen: also V's, at
-            // `others`) NaN and V 0
-            auto expand = [&](uint32_t codes, uint32_t scales, uint32_t others, bool is_v, uint32_t to) {
+            // one array of tile t: codes at `codes`, scales at `scales`; a NaN scale makes K (seen: also V's, at
+            // `others`) NaN and V 0.  K's pass tells the softmax of large values of V that a row of the pair sees
+            // (before K is there, and so before S; a place of `large` is free again 8 tiles on, the ring holds 3).
+            auto expand = [&](int t, uint32_t codes, uint32_t scales, uint32_t others, bool is_v, uint32_t to) {
                 uint32_t w[C::ITEMS][4], own[C::ITEMS], other[C::ITEMS];
 #pragma unroll
                 for (int i = 0; i < C::ITEMS; ++i) {  // all loads before the first use
@@ -289,6 +299,12 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                             v = make_uint4(more.times(v.x), more.times(v.y), more.times(v.z), more.times(v.w));
                             put(c, most > Held<T>::MOST ? make_uint4(gone, gone, gone, gone) : v);
                         }
+                        if (Held<T>::LARGE < Held<T>::MOST && !is_v) {
+                            const int place = (first + t) * C::KEYS + group * 8 + key_in;
+                            const int key = place + (place < sinks ? 0 : skip);
+                            const bool seen = key < hi && (key < sink || key >= wlo);
+                            if (seen && other[i] > Held<T>::LARGE && other[i] <= Held<T>::MOST) large[t & 7] = t;
+                        }
                     }
                 }
                 asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
@@ -302,7 +318,7 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
                     const int x = 2 * t + is_v, slot = x % C::NS;
                     if (x >= C::NS) ok = mbar_wait(&empty[slot], ((x / C::NS) & 1) ^ 1, abort_flag, a.wait_limit) && ok;
                     if (!(ok = __all_sync(~0u, ok))) break;
-                    expand(raw + is_v * C::OFF_RV, raw + (is_v ? C::OFF_RVSF : C::OFF_RKSF), raw + C::OFF_RVSF, is_v,
+                    expand(t, raw + is_v * C::OFF_RV, raw + (is_v ? C::OFF_RVSF : C::OFF_RKSF), raw + C::OFF_RVSF, is_v,
                            kv + slot * C::TILE);
                     if (lane == 0) mbar_arrive(&full[slot]);
                 }
@@ -479,7 +495,11 @@ window_dense_kernel(const __grid_constant__ CUtensorMap tm_q, const __grid_const
             for (int c = 0; c < C::KEYS; c += 8)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) x[j] = max3(x[j], z[c + 2 * j], z[c + 2 * j + 1]);
-            const float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale - Elem<T>::LIFT;
+            float top = fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) * scale - Elem<T>::LIFT;
+            if constexpr (Held<T>::LARGE < Held<T>::MOST) {
+                const int tile = solo ? 2 * i + s : i;
+                if (large[tile & 7] == tile) top += kLargeLift;
+            }
             // O is at rest and P has been read once the last P V has completed
             auto last_done = [&] {
                 return i == 0 ||
