@@ -572,10 +572,10 @@ idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const u
  *         [n_caches] bytes of a page in each (HOST): K and V, codes and scales, the indexer's
  *         keys ...  Bases 16-byte aligned and page_bytes a multiple of 16 (IDX_EALIGN);
  *         n_caches <= 8.
- * page_size 16, 32, 64 or 128; table_stride * page_size < 2^31; B <= 2^24.  Results do not depend on
- * the order in which threads run.  Device errors (IDX_DEV_RANGE): a length outside [0, table_stride
- * * page_size] counts as 0 in a fork and leaves its row as it is otherwise; a table entry outside [0, pages)
- * within a row's length is kept and not counted.
+ * page_size 16, 32, 64 or 128; table_stride * page_size < 2^31; B <= 2^24; pages <= 2^31 - 256
+ * (IDX_EUNSUPPORTED).  Results do not depend on the order in which threads run.  Device errors
+ * (IDX_DEV_RANGE): a length outside [0, table_stride * page_size] counts as 0 in a fork and leaves its row
+ * as it is otherwise; a table entry outside [0, pages) within a row's length is kept and not counted.
  *
  * idx_cache_fork - row i takes over the pages and the length of row parent[i] as they were
  * before the call and gives its own back; all rows at once (the next step of a beam search).

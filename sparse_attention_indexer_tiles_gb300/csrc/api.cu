@@ -1395,8 +1395,9 @@ namespace {
 
 size_t ints_bytes(size_t n) { return (n * sizeof(int) + 255) / 256 * 256; }
 
+// Pages: the rankings step through their numbers 256 at a time in 32 bits; a step from below kMostPages ends below 2^31.
 bool pages_sizes_ok(int B, int pages, long long table_stride) {
-    return B >= 0 && B <= 1 << 24 && pages >= 0 && table_stride >= 0 && table_stride <= 0x7fffffffll;
+    return B >= 0 && B <= 1 << 24 && pages >= 0 && pages <= kMostPages && table_stride >= 0 && table_stride <= 0x7fffffffll;
 }
 
 // The arguments that the calls share.

@@ -9,6 +9,7 @@
 namespace idx {
 
 constexpr int kMaxCaches = 8;
+constexpr int kMostPages = 0x7fffff00;
 
 // The arrays whose pages move with the tables: [pages][bytes] each.
 struct PageArrays {
