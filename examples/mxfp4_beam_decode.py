@@ -50,11 +50,13 @@ class Beams:
         grow = self.lens + torch.tensor(new, dtype=torch.int32, device=self.dev)
         idx.idx_cache_resize(self.cache, self.refs, self.table, self.lens, grow, page_size=PAGE, refs_out=self.refs,
                              table_out=self.table, lens_out=self.lens, ws=self.ws, stats=self.stats)
+        # a row for which the pages did not suffice has no slots for its new tokens: it sits this call out
+        lens = torch.where(self.lens == grow, self.lens, 0)
         rows = (x @ self.qkv.t()).to(torch.bfloat16)
         q, k, v = (t.unflatten(1, (-1, DIM)) for t in rows.split([HEADS * DIM, KV_HEADS * DIM, KV_HEADS * DIM], 1))
         start = torch.tensor([0] + list(torch.tensor(new).cumsum(0)), dtype=torch.int32, device=self.dev)
-        idx.idx_cache_append_mxfp4(k, v, *self.cache, self.table, self.lens, q_start=start, stats=self.stats)
-        out, lse = idx.idx_window_attention_mxfp4(q, *self.cache, self.table, self.lens, q_start=start, max_q=max(new),
+        idx.idx_cache_append_mxfp4(k, v, *self.cache, self.table, lens, q_start=start, stats=self.stats)
+        out, lse = idx.idx_window_attention_mxfp4(q, *self.cache, self.table, lens, q_start=start, max_q=max(new),
                                                   max_len=self.longest, window=self.window, sink=self.sink,
                                                   stats=self.stats)
         if self.said is not None:

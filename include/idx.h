@@ -506,7 +506,8 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
  *   k, v  [T, Hkv, D] bf16 or fp16, tokens k_stride, v_stride elements apart (at least
  *         Hkv * D, so both may be slices of one projection); rows on 16-byte boundaries
  *         are read with wide loads, others element by element
- * A token whose page is negative is not kept.  Tokens outside every request are not
+ * A token whose page is negative is not kept.  A request's last slots are written whatever they hold, so lens has to
+ * count its new tokens (after an idx_cache_resize: that served the row, see there).  Tokens outside every request are not
  * read.  No two requests may share the page of a new token.  Device errors
  * (IDX_DEV_RANGE): a position outside [0, table_stride * page_size) or a page from
  * `pages` on: the token is not written.  No workspace.
@@ -592,7 +593,10 @@ idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const u
  * copies, also when all that hold the page grow (it is free from the next call on).  From the
  * first row on for which the free pages do not suffice, rows that want pages keep their pages
  * and length, and IDX_DEV_PAGES is raised; lens_out tells.  A new length outside [0, table_stride
- * * page_size]: IDX_DEV_RANGE, the row is left.
+ * * page_size]: IDX_DEV_RANGE, the row is left.  A row whose lens_out is not its new length has no slots for the
+ * tokens that it was to grow by: an append with that length would write them over its newest slots, and over other
+ * rows' where it shares their page.  Until it is served the append and the attention get 0 as its length
+ * (lens_out[i] == new_lens[i] ? lens_out[i] : 0, on the device): its tokens are not kept, and its rows see nothing.
  * ws: idx_cache_resize_workspace(...) bytes, 256-byte aligned.
  *
  * idx_cache_compact - moves the live pages to the front: with `live` pages whose count is above

@@ -718,7 +718,8 @@ def idx_cache_append_mxfp4(k, v, k_codes, k_sf, v_codes, v_sf, table, lens, *, q
                            options=None, stats: Stats | None = None, stream=None) -> None:
     """Write the new tokens' k, v [T, Hkv, D] (slices of a wider projection may be given) into a
     paged MXFP4 cache: codes [pages, Hkv, page_size, D // 2] and scales [..., D // 32] uint8.
-    lens [B] counts the new tokens; q_start [B + 1] says which are whose (None: T / B each)."""
+    lens [B] counts the new tokens, whose slots they take whatever those hold; q_start [B + 1] says
+    which are whose (None: T / B each)."""
     _serve_call("idx_cache_append_mxfp4", _serve().cache_append_mxfp4, (
         k, v, k_codes, k_sf, v_codes, v_sf, table, lens, q_start), options, stats, stream)
 
@@ -818,7 +819,9 @@ def idx_cache_resize(caches, refs, table, lens, new_lens, *, page_size: int, ref
     """Rows of the page table go from lens to new_lens slots: they give pages back and take free
     ones (refs 0, lowest first), and a row that grows into a page which others hold too takes a
     copy of it in every one of `caches` ([pages, ...] tensors).  Returns (refs_out, table_out,
-    lens_out), each of which may be its input; lens_out tells where the pages did not suffice."""
+    lens_out), each of which may be its input; lens_out tells where the pages did not suffice.  An
+    append after it takes torch.where(lens_out == new_lens, lens_out, 0): a row that was not served
+    has no slots for its new tokens."""
     fn = "idx_cache_resize"
     if refs_out is None or table_out is None or lens_out is None or ws is None:
         with _Launch(stream, refs.device) as on:
