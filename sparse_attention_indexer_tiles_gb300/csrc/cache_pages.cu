@@ -437,6 +437,7 @@ __global__ void __launch_bounds__(kCopyThreads) resize_move_kernel(const __grid_
     const int* const taken = taken_pages(a);
     const int lane = threadIdx.x & 31;
     const long long step = (long long)gridDim.x * (kCopyThreads / 32);
+    bool bad = false;
     for (long long i = ((long long)blockIdx.x * kCopyThreads + threadIdx.x) >> 5; i < a.B; i += step) {
         const Row row = served_row(a, i);
         if (!len_ok(a, row.old_len)) continue;
@@ -445,11 +446,22 @@ __global__ void __launch_bounds__(kCopyThreads) resize_move_kernel(const __grid_
         const int had = pages_of(a, row.old_len), has = pages_of(a, row.new_len);
         const bool copy = row.from >= 0;
         const int kept = min(had - copy, has);
-        if (out != in)
-            for (int j = lane; j < kept; j += 32) out[j] = in[j];
+        // (kept entries are checked here, given back and copied ones by the ranking)
+        for (int j0 = lane; j0 < kept; j0 += 32 * kBatch) {
+            int p[kBatch];
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) p[k] = j0 + 32 * k < kept ? in[j0 + 32 * k] : 0;
+#pragma unroll
+            for (int k = 0; k < kBatch; ++k) {
+                if (j0 + 32 * k >= kept) break;
+                bad |= !page_ok(a, p[k]);
+                if (out != in) out[j0 + 32 * k] = p[k];
+            }
+        }
         for (int j = kept + lane; j < has; j += 32) out[j] = taken[row.rank + j - kept];
         if (copy && lane == 0) atomicSub(a.refs_out + row.from, 1);
     }
+    if (bad) raise_status(a.d_status, IDX_DEV_RANGE);
     const int* const list = copy_rows(a);
     copy_pages(a.caches, list[0], [&](int k) {
         const Row row = served_row(a, list[k + 1]);
