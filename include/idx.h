@@ -509,8 +509,8 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
  * A token whose page is negative is not kept.  A request's last slots are written whatever they hold, so lens has to
  * count its new tokens (after an idx_cache_resize: that served the row, see there).  Tokens outside every request are not
  * read.  No two requests may share the page of a new token.  Device errors
- * (IDX_DEV_RANGE): a position outside [0, table_stride * page_size) or a page from
- * `pages` on: the token is not written.  No workspace.
+ * (IDX_DEV_RANGE): a position outside [0, table_stride * page_size), a page from `pages` on or a request that
+ * ends behind token T: the token is not written.  No workspace.
  *
  * idx_window_attention_mxfp4 - attention of every request's new tokens (one for a decode
  * step, a chunk of a prompt, a few drafted ones) over its cache, causal, with a sliding

@@ -124,7 +124,8 @@ __global__ void __launch_bounds__(kAppendThreads) append_kernel(const __grid_con
         end = (b + 1) * per;
     }
     const long long at = (long long)a.lens[b] - end + token;  // position of the token
-    if (token < first || at < 0 || at >= a.table_stride << a.page_shift) {
+    // (a request that ends behind the call's tokens: where they belong is not known)
+    if (token < first || end > a.T || at < 0 || at >= a.table_stride << a.page_shift) {
         if (lane == 0) raise_status(a.d_status, IDX_DEV_RANGE);
         return;
     }
