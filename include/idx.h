@@ -533,11 +533,12 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
  *   ws   idx_window_attention_mxfp4_workspace(...) bytes for the same arguments (max_q and
  *        max_len as the call counts them), 256-byte aligned; needs no clearing between calls.
  *        The size does not shrink when an argument grows (a window of 0 is the largest).
- * Slots that no row of a request sees are not read, and their pages need not exist (table
- * entries of any value).  Further limits: Hq a multiple of Hkv with Hq / Hkv <= 128; T * Hq <
- * 2^31 - 256; max_len, window, sink < 2^30.  Device errors (IDX_DEV_RANGE): lens[b] outside [0,
- * max_len] is clamped; where q_start is not in order, a request has more than max_q tokens or a row sees a
- * page outside [0, pages), the request's results are meaningless.
+ * Pages without a slot that a row of the request sees are not read and need not exist (table entries of any
+ * value).  Other slots of the pages that are read may be read too, and change no bit of a result, whatever they
+ * hold.  Further limits: Hq a multiple of Hkv with Hq / Hkv <= 128; T * Hq < 2^31 - 256; max_len, window,
+ * sink < 2^30.  Device errors (IDX_DEV_RANGE): lens[b] outside [0, max_len] is clamped; where q_start is not in
+ * order, a request has more than max_q tokens or a row sees a page outside [0, pages), the request's results
+ * are meaningless.
  * ------------------------------------------------------------------------ */
 idx_status idx_cache_append_mxfp4(const void* k, long long k_stride, const void* v,
                                   long long v_stride, uint8_t* k_codes, uint8_t* k_sf,

@@ -174,14 +174,14 @@ window_kernel(const __grid_constant__ WindowArgs a) {
 
     const uint32_t ring = smem0 + warp * kStages * R::STAGE;
     // Pages of the warp's next steps, one 16-key half per lane: 16 steps at a time.  A half that no
-    // row sees is not looked up (its page may be gone): page 0 is read for it, and masked.
+    // row sees is not looked up (its page may be gone): its place is filled from the other half's page, and masked.
     const int* table = a.table + b * a.table_stride;
     bool bad = false;
-    int pages_from = 0, page_of = 0;
+    int pages_from = 0, page_of = -1;
     auto look_up = [&](int i) {
         pages_from = i;
         const int s = i + (lane >> 1);
-        page_of = 0;
+        page_of = -1;
         if (s < mine) {
             const int key = base_of(s) + (lane & 1) * 16;
             if (key < hi && (key < sink || key + 16 > wlo)) {
@@ -204,7 +204,9 @@ window_kernel(const __grid_constant__ WindowArgs a) {
         const int base = base_of(i);
         int p0 = __shfl_sync(~0u, page_of, 2 * (i - pages_from));
         int p1 = __shfl_sync(~0u, page_of, 2 * (i - pages_from) + 1);
-        if (whole) p0 = p1 = max(p0, p1);  // (a page that only its second half is seen of)
+        // (a row sees a key of every step; where a page holds a whole step, both halves name it or one does)
+        if (p0 < 0) p0 = max(p1, 0);
+        if (p1 < 0) p1 = p0;
         const int in_page = base & (a.page_size - 1);
         const long long row0 = (long long)(p0 * a.Hkv + hk) * a.page_size + in_page;
         const long long row1 = whole ? row0 + 16 : (long long)(p1 * a.Hkv + hk) * a.page_size;
