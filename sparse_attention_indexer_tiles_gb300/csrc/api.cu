@@ -4,6 +4,7 @@
 #include <algorithm>
 #include <atomic>
 #include <chrono>
+#include <cfloat>
 #include <cmath>
 #include <cstdint>
 #include <cstring>
@@ -1375,7 +1376,7 @@ idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const u
     a.splits = p.splits;
     a.chunk = p.chunk;
     a.clustered = p.clustered;
-    a.scale_log2 = scale * 1.4426950408889634f;
+    a.scale_log2 = std::fmin(std::fmax(scale * 1.4426950408889634f, -FLT_MAX), FLT_MAX);  // 0 times it stays 0
     const int stall_us = opt ? opt->test_stall_us : 0;
     a.wait_limit = stall_us > 0 ? 2100LL * stall_us : (1LL << 32);
     a.withhold_step = stall_us > 0 ? 1 : -1;
