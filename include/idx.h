@@ -100,7 +100,9 @@ typedef struct idx_options {
     int sample_stride;    /* odd stride S of the threshold sample; 0 = automatic */
     int row_split;        /* standalone top-k row split, see below;
                              idx_window_attention_mxfp4: 0 the cheaper path, -1 tiles of few
-                             rows, 1 the tensor cores' dense path */
+                             rows, 1 the tensor cores' dense path;
+                             idx_cache_resize, idx_cache_compact: -1 ranks pages with one
+                             CTA, as where a device does not place a cluster of 16 */
     int* d_status;        /* optional device int receiving IDX_DEV_* bits */
     idx_stats* d_stats;   /* optional device counters */
     int relative_rows;    /* idx_topk_from_scores: row r's visible scores start at

@@ -1432,6 +1432,7 @@ idx_status pages_args(PagesArgs& a, void* const* caches, const long long* page_b
     a.pages = pages;
     a.page_size = page_size;
     a.page_shift = page_shift(page_size);
+    a.one_cta = opt && opt->row_split == -1;
     a.d_status = opt ? opt->d_status : nullptr;
     return IDX_OK;
 }

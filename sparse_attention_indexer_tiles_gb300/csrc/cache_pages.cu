@@ -13,6 +13,7 @@
 #include <cooperative_groups.h>
 
 #include <algorithm>
+#include <atomic>
 
 #include "cache_pages.cuh"
 #include "serve.cuh"
@@ -561,16 +562,45 @@ __global__ void __launch_bounds__(kCopyThreads) compact_move_kernel(const __grid
 // A ranking kernel: a cluster when its pages or rows are many (see kClusterFrom), one CTA otherwise.
 constexpr int kClusterFrom = 4096;
 
-cudaError_t launch_rank(void (*one)(PagesArgs), void (*many)(PagesArgs), PerDevice& ready, const PagesArgs& a,
-                        cudaStream_t s) {
-    const bool cluster = a.pages >= kClusterFrom || a.B * 16ll >= kClusterFrom;
-    if (cluster) {
-        int device = -1;
-        cudaError_t e = cudaGetDevice(&device);
+// The devices that place a cluster of kCluster CTAs of a kernel: more than the portable eight, so a part of a GPU may
+// not.
+class ClusterDevices {
+    PerDevice asked_;
+    std::atomic<uint64_t> without_{0};
+
+public:
+    cudaError_t place(void (*kernel)(PagesArgs), bool* yes) {
+        int device = -1, clusters = 1;
+        const cudaError_t e = cudaGetDevice(&device);
         if (e != cudaSuccess) return e;
-        e = (cudaError_t)ready.run(device, [&] {
-            return (int)cudaFuncSetAttribute(many, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        asked_.run(device, [&] {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(kCluster);
+            cfg.blockDim = dim3(kThreads);
+            cudaLaunchAttribute attr;
+            attr.id = cudaLaunchAttributeClusterDimension;
+            attr.val.clusterDim.x = kCluster;
+            attr.val.clusterDim.y = attr.val.clusterDim.z = 1;
+            cfg.attrs = &attr;
+            cfg.numAttrs = 1;
+            if (cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) != cudaSuccess ||
+                cudaOccupancyMaxActiveClusters(&clusters, kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                clusters = 0;
+            }
+            if (clusters < 1 && device < 64) without_.fetch_or(1ull << device);
+            return 0;
         });
+        *yes = clusters > 0 && !(device < 64 && without_.load() >> device & 1);
+        return cudaSuccess;
+    }
+};
+
+cudaError_t launch_rank(void (*one)(PagesArgs), void (*many)(PagesArgs), ClusterDevices& devices, const PagesArgs& a,
+                        cudaStream_t s) {
+    bool cluster = !a.one_cta && (a.pages >= kClusterFrom || a.B * 16ll >= kClusterFrom);
+    if (cluster) {
+        const cudaError_t e = devices.place(many, &cluster);
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg = {};
@@ -623,8 +653,8 @@ cudaError_t launch_fork(const PagesArgs& a, int sm_count, cudaStream_t s, int* l
 }
 
 cudaError_t launch_resize(const PagesArgs& a, int sm_count, cudaStream_t s, int* launched) {
-    static PerDevice ready;
-    cudaError_t e = launch_rank(resize_rank_kernel<false>, resize_rank_kernel<true>, ready, a, s);
+    static ClusterDevices devices;
+    cudaError_t e = launch_rank(resize_rank_kernel<false>, resize_rank_kernel<true>, devices, a, s);
     if (e != cudaSuccess) return e;
     ++*launched;
     e = launch_k(resize_move_kernel, dim3(move_blocks(sm_count)), dim3(kCopyThreads), 0, s, true, a);
@@ -633,8 +663,8 @@ cudaError_t launch_resize(const PagesArgs& a, int sm_count, cudaStream_t s, int*
 }
 
 cudaError_t launch_compact(const PagesArgs& a, int sm_count, cudaStream_t s, int* launched) {
-    static PerDevice ready;
-    cudaError_t e = launch_rank(compact_rank_kernel<false>, compact_rank_kernel<true>, ready, a, s);
+    static ClusterDevices devices;
+    cudaError_t e = launch_rank(compact_rank_kernel<false>, compact_rank_kernel<true>, devices, a, s);
     if (e != cudaSuccess) return e;
     ++*launched;
     e = launch_k(compact_move_kernel, dim3(move_blocks(sm_count)), dim3(kCopyThreads), 0, s, true, a);

@@ -32,6 +32,7 @@ struct PagesArgs {
     int B, pages, page_size, page_shift;
     // workspace of the call at hand (see the kernels)
     int* ws;
+    bool one_cta;          // rank with one CTA, whatever the sizes are
     int* d_status;
 };
 
