@@ -1384,7 +1384,7 @@ idx_status idx_window_attention_mxfp4(const void* q, long long q_stride, const u
     cudaStream_t s = static_cast<cudaStream_t>(stream);
     int launched = 0;
     record(opt, 0, s);
-    const cudaError_t e = launch_window(a, p, dt, sm_count(), s, &launched);
+    const cudaError_t e = launch_window(a, p, dt, s, &launched);
     count_launches(launched);
     record(opt, 1, s);
     return cuda_status(e);

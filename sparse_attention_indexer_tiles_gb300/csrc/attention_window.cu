@@ -907,7 +907,7 @@ WindowPlan window_plan(int B, int T, int max_q, int Hq, int Hkv, int D, int max_
     return p;
 }
 
-cudaError_t launch_window(const WindowArgs& a, const WindowPlan& p, idx_dtype dt, int, cudaStream_t s, int* launched) {
+cudaError_t launch_window(const WindowArgs& a, const WindowPlan& p, idx_dtype dt, cudaStream_t s, int* launched) {
     if (dt == IDX_BF16)
         return a.D == 128 ? launch_typed<__nv_bfloat16, 128>(a, p, s, launched)
                           : launch_typed<__nv_bfloat16, 64>(a, p, s, launched);

@@ -57,7 +57,6 @@ int window_dense_keys(int D);
 cudaError_t launch_window_dense(const WindowArgs& a, idx_dtype dt, cudaStream_t s);
 
 // Adds the number of kernels launched to *launched.
-cudaError_t launch_window(const WindowArgs& a, const WindowPlan& p, idx_dtype dt, int sm_count, cudaStream_t s,
-                          int* launched);
+cudaError_t launch_window(const WindowArgs& a, const WindowPlan& p, idx_dtype dt, cudaStream_t s, int* launched);
 
 }  // namespace idx
