@@ -177,7 +177,7 @@ window_kernel(const __grid_constant__ WindowArgs a) {
     // row sees is not looked up (its page may be gone): its place is filled from the other half's page, and masked.
     const int* table = a.table + b * a.table_stride;
     bool bad = false;
-    int pages_from = 0, page_of = -1;
+    int pages_from = 0, page_of = 0;
     auto look_up = [&](int i) {
         pages_from = i;
         const int s = i + (lane >> 1);
@@ -192,6 +192,9 @@ window_kernel(const __grid_constant__ WindowArgs a) {
                 }
             }
         }
+        // (a row sees a key of every step; where a page holds a whole step, both halves name it or one does)
+        const int other = __shfl_xor_sync(~0u, page_of, 1);
+        if (page_of < 0) page_of = max(other, 0);
     };
     const bool whole = a.page_size >= kWindowStep;  // a step lies in one page
     // The copies of a step: codes of 16 keys are kHalf adjacent 16-byte chunks, dealt to the lanes; scales a chunk for
@@ -202,11 +205,8 @@ window_kernel(const __grid_constant__ WindowArgs a) {
     auto fetch = [&](int i) {
         if (i - pages_from >= 16 || i == 0) look_up(i);
         const int base = base_of(i);
-        int p0 = __shfl_sync(~0u, page_of, 2 * (i - pages_from));
-        int p1 = __shfl_sync(~0u, page_of, 2 * (i - pages_from) + 1);
-        // (a row sees a key of every step; where a page holds a whole step, both halves name it or one does)
-        if (p0 < 0) p0 = max(p1, 0);
-        if (p1 < 0) p1 = p0;
+        const int p0 = __shfl_sync(~0u, page_of, 2 * (i - pages_from));
+        const int p1 = __shfl_sync(~0u, page_of, 2 * (i - pages_from) + 1);
         const int in_page = base & (a.page_size - 1);
         const long long row0 = (long long)(p0 * a.Hkv + hk) * a.page_size + in_page;
         const long long row1 = whole ? row0 + 16 : (long long)(p1 * a.Hkv + hk) * a.page_size;
