@@ -413,6 +413,8 @@ idx_status idx_add_rmsnorm_quant(const void* x, long long x_stride, const void* 
  *     out = sum_j exp(z_j) v_j / sum_j exp(z_j),   lse = log sum_j exp(z_j)
  * A row that sees nothing gets out 0 and lse -inf; one that sees a NaN logit or one of +inf
  * gets NaN, and so do the weights of its request and key head.
+ * Sums of weights times v are fp32 before they are divided, and weights reach 2^8: bf16 values of
+ * 2^89 and more may leave it.
  *
  *   q   [B, Q, Hq, D];  k_cache, v_cache [pages, Hkv, page_size, D]; bf16 or fp16
  *   prefix_table [ceil(prefix_len / page_size)] int32: the prefix's pages in order
@@ -526,7 +528,7 @@ idx_status idx_cache_evict(void* k_cache, void* v_cache, const int* table, const
  * a row of the same request sees, lose bits.  Where many rows of a request share a key head (a prompt),
  * values may be taken in q's type: in fp16 those below 2^-23 are then rounded to multiples of 2^-24 and scales above
  * 2^13 count as NaN scales; in bf16 scales above 2^125 do, and values below 2^-60 lose bits beside scales of V
- * above 2^87 that a row of the same request sees.
+ * above 2^87 that a row of the same request sees.  q . k itself, before scale, is fp32 there.
  *   q    [T, Hq, D] bf16 or fp16, tokens q_stride elements apart, rows on 16-byte boundaries
  *   max_q   an upper bound on a request's new tokens (0 = T)
  *   max_len an upper bound on lens (0 = table_stride * page_size)
